@@ -22,6 +22,7 @@ CSRC_DIR = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libgdn_sm103a.so")
 HEADER = os.path.join(REPO_DIR, "include", "gdn.h")
+KV_HEADER = os.path.join(REPO_DIR, "include", "gdn_kv.h")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v"] + ARCH_FLAGS
@@ -44,7 +45,7 @@ def sources() -> list[str]:
 def _digest() -> str:
     h = hashlib.sha256()
     files = sources() + sorted(os.path.join(CSRC_DIR, f) for f in os.listdir(CSRC_DIR)
-                               if f.endswith((".cuh", ".h"))) + [HEADER]
+                               if f.endswith((".cuh", ".h"))) + [HEADER, KV_HEADER]
     for f in files:
         h.update(os.path.basename(f).encode())
         with open(f, "rb") as fh:
@@ -92,7 +93,7 @@ def kernel_source_digest() -> str:
     """Hash of all CUDA sources without their comments, and of the flags: identifies the
     kernels a profile was taken on, and stays put when only commentary changes."""
     return _code_digest(sources() + sorted(os.path.join(CSRC_DIR, f) for f in os.listdir(CSRC_DIR)
-                                           if f.endswith((".cuh", ".h"))) + [HEADER])
+                                           if f.endswith((".cuh", ".h"))) + [HEADER, KV_HEADER])
 
 
 # the translation unit of the verify kernels and everything it includes

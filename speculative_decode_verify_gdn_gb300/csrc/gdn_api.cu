@@ -14,6 +14,7 @@
 
 #include "gdn_common.cuh"
 #include "gdn_kernels.h"
+#include "kv_kernels.h"
 
 namespace {
 
@@ -263,6 +264,8 @@ gdn_status verify_impl(const gdn_dims* dims, const VerifyArgs& v, gdn_stream_t s
 
 namespace gdn {
 gdn_status report_error(gdn_status s, const char* msg) { return fail(s, "%s", msg); }
+gdn_status report_ok() { return ok(); }
+gdn_status device_status_word(uint32_t** out) { return status_word(out); }
 }  // namespace gdn
 
 extern "C" {
