@@ -1,8 +1,25 @@
-// Attention of verify windows over the paged cache (contract in include/gdn_kv.h).
+// Attention of verify windows over the paged cache (contract in include/gdn_kv.h), on the tensor
+// cores.
 //
-// One warp per row (sequence, window token, query head): the lanes hold the query, and the keys
-// of the prefix, of the sequence and of the window pass one by one through an online softmax
-// (running maximum and sum in f32).
+// The work is cut into items: (prefix run, kv head, block of up to 256 rows) for the prefixes, a
+// run being consecutive sequences with the same prefix, and (sequence, kv head, block) for what a
+// sequence does not share.  A row is one query head of one window token; its block's rows all
+// meet the same keys, so the prefix is read and multiplied once for every sequence on it.  An
+// item's keys come in tiles of 128.  All tiles of all items, in order, are dealt to the CTAs (one
+// per SM) in equal contiguous stretches: a CTA's part of an item is a segment, it yields the
+// softmax-weighted sum and the log-sum-exp of its own keys (f32, in the workspace), and a last
+// kernel joins a row's segments.  Which CTA computes what depends on the lengths alone, so
+// results repeat bit for bit.
+//
+// Kernels: plan (one CTA: lengths -> items and stretches), tiles (persistent, tcgen05), join.
+//
+// The tile kernel: a producer warp brings keys and values by TMA (128-byte swizzle) into a ring
+// of tiles; one thread issues S = Q K^T and O += P V (tcgen05, M = 128, accumulators in tensor
+// memory, P read from tensor memory); two groups of four warps, one per stream, turn S into P, a
+// row per thread.  A block of more than 128 rows uses the two streams for its two halves on the
+// same keys; a smaller one gives them alternate tiles of the same rows.  While one stream's
+// softmax runs, the tensor core works for the other.
+#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "gdn_common.cuh"
@@ -12,22 +29,109 @@ namespace gdn {
 
 namespace {
 
-constexpr int kRowWarps = 8;
+constexpr int kCtas = 152;       // one per SM; no CTA waits for another, so any number is correct
+constexpr int kTileKeys = 128;
+constexpr int kBlockRows = 256;  // rows of an item
+constexpr int kPlanThreads = 1024;
+constexpr int kGroupThreads = 128;  // a softmax group: one thread per row of a stream
+constexpr int kTileThreads = 2 * kGroupThreads + 64;
+constexpr int kJoinWarps = 8;
+constexpr float kLn2 = 0.693147180559945f, kLog2e = 1.442695040888963f;
+// A running maximum may lag behind by up to 8 powers of two before O is rescaled: probabilities
+// stay below 2^8, far inside both 16-bit types, and keep their relative precision.
+constexpr float kLag = 8.0f;
 
-template <bool F16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  if (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+// ---------------------------------------------------------------- the plan
+struct SeqRec {     // what a sequence does not share
+  long long off;    // first tile of its items in the order of all tiles
+  int32_t tiles;    // per item (0: nothing to do)
+  int32_t keys;     // cached tokens
+  int32_t run;      // its prefix run, -1 without
+  int32_t win;      // window tokens, clamped to 0..K
+};
+struct RunRec {     // consecutive sequences on one prefix
+  long long off;
+  long long row;    // first row of its partial results
+  int32_t tiles;
+  int32_t keys;
+  int32_t slot;
+  int32_t b0, n;    // sequences b0 .. b0 + n - 1
+  int32_t pad[3];
+};
+struct PlanHead {
+  long long tiles, prefix_tiles;  // in all; those of the runs come first
+  long long own_row;              // first row of the sequences' partial results
+  int32_t runs, pad;
+};
+struct StartRec {
+  int32_t own, idx;  // where a CTA's stretch begins: run or sequence idx
+};
+
+struct AttnWs {
+  PlanHead* head;
+  StartRec* start;  // [kCtas]
+  SeqRec* seq;      // [B]
+  RunRec* run;      // [B]
+  float* lse;       // [rows] log2 units
+  float* o;         // [rows, D]
+};
+
+__host__ __device__ inline size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// Rows of partial results of a block: one per row when the streams hold its halves, else two (one
+// per stream).
+__host__ __device__ inline int block_width(int rows) { return rows > kTileKeys ? rows : 2 * rows; }
+// Rows of partial results of all blocks of `rows` rows.
+__host__ __device__ inline long long rows_width(long long rows) {
+  const long long full = (rows - 1) / kBlockRows;
+  return full * kBlockRows + block_width(int(rows - full * kBlockRows));
 }
 
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if (F16) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
+__host__ __device__ inline AttnWs carve_attn(void* base, const gdn_kv_dims& d, size_t* total) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  size_t o = 0;
+  // a segment of CTA c and item i starts at row 256 c + (rows of the items before i); every row of
+  // the batch has at most two rows here from its prefix and two from its own sequence
+  const size_t rows = size_t(kBlockRows) * kCtas + 4 * size_t(d.B) * d.K * d.Hq;
+  AttnWs w;
+  w.head = reinterpret_cast<PlanHead*>(p + o), o += 256;
+  w.start = reinterpret_cast<StartRec*>(p + o), o += up256(sizeof(StartRec) * kCtas);
+  w.seq = reinterpret_cast<SeqRec*>(p + o), o += up256(sizeof(SeqRec) * size_t(d.B));
+  w.run = reinterpret_cast<RunRec*>(p + o), o += up256(sizeof(RunRec) * size_t(d.B));
+  w.lse = reinterpret_cast<float*>(p + o), o += up256(4 * rows);
+  w.o = reinterpret_cast<float*>(p + o), o += 4 * rows * size_t(d.D);
+  if (total) *total = o;
+  return w;
+}
+
+// CTA c's stretch is tiles [first_tile(c), first_tile(c + 1)); the CTA of tile x.
+__device__ __forceinline__ long long first_tile(long long c, long long tiles) { return c * tiles / kCtas; }
+__device__ __forceinline__ int cta_of(long long x, long long tiles) { return int(((x + 1) * kCtas - 1) / tiles); }
+
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* sums, T& total) {  // exclusive, kPlanThreads threads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
+  __syncthreads();
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  T s = sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  total = __shfl_sync(0xffffffffu, s, 31);
+  const T before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+  return x - v + (warp > 0 ? before : 0);
 }
 
 // A slot's length, 0 (and a status bit) when it is negative or beyond the table's columns.
@@ -40,119 +144,827 @@ __device__ __forceinline__ int slot_len(const AttnParams& p, int slot) {
   return n;
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kRowWarps) attn_row_kernel(const AttnParams p) {
-  constexpr int N = D / 64;  // 32-bit words (pairs of elements) per lane
+__device__ __forceinline__ int prefix_slot(const AttnParams& p, int b) {
+  if (!p.prefix_of) return -1;
+  const int s = p.prefix_of[b];
+  return s < 0 || s >= p.d.n_slots ? -1 : s;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParams p, const AttnWs w) {
+  __shared__ long long sums[32];
+  grid_launch_dependents();
+  grid_wait();
   const gdn_kv_dims& d = p.d;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  if (row >= (long long)d.B * d.K * d.Hq) return;
-  const int h = int(row % d.Hq);
-  const long long tok = row / d.Hq;
-  const int t = int(tok % d.K), b = int(tok / d.K);
-  const int kh = h / (d.Hq / d.Hkv);
-  int win = p.win_len ? p.win_len[b] : d.K;
-  if (win < 0 || win > d.K) {
-    atomicOr(p.err, GDN_DEVERR_KV_WINDOW);
-    win = win < 0 ? 0 : d.K;
-  }
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.out) + row * (D / 2);
-  if (t >= win) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) out[32 * i + lane] = 0;
-    if (p.lse && lane == 0) p.lse[row] = -INFINITY;
-    return;
-  }
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) + tok * d.q_token_stride + (long long)h * D);
-  float2 qv[N], acc[N];
-  const float c = p.scale * 1.44269504f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    qv[i] = unpack2<F16>(q[32 * i + lane]);
-    qv[i].x *= c, qv[i].y *= c;
-    acc[i] = make_float2(0.f, 0.f);
-  }
-  float m = -INFINITY, l = 0.f;
-  auto key = [&](const uint16_t* k, const uint16_t* v) {
-    float s = 0.f;
-    float2 vv[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float2 kk = unpack2<F16>(reinterpret_cast<const uint32_t*>(k)[32 * i + lane]);
-      vv[i] = unpack2<F16>(reinterpret_cast<const uint32_t*>(v)[32 * i + lane]);
-      s += qv[i].x * kk.x + qv[i].y * kk.y;
+  const int tid = int(threadIdx.x), KG = d.K * (d.Hq / d.Hkv);
+  long long n_runs = 0;
+  for (int b0 = 0; b0 < d.B; b0 += kPlanThreads) {  // sequences: lengths, and the runs' ends
+    const int b = b0 + tid;
+    int s = -1;
+    bool first = false, last = false;
+    if (b < d.B) {
+      s = prefix_slot(p, b);
+      if (s < 0 && p.prefix_of && p.prefix_of[b] != -1) atomicOr(p.err, GDN_DEVERR_KV_SLOT);
+      first = s >= 0 && (b == 0 || prefix_slot(p, b - 1) != s);
+      last = s >= 0 && (b == d.B - 1 || prefix_slot(p, b + 1) != s);
     }
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-    l = l * f + w;
-    m = mn;
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i].x = acc[i].x * f + w * vv[i].x, acc[i].y = acc[i].y * f + w * vv[i].y;
-  };
-  auto cached = [&](int slot) {
-    const int n = slot_len(p, slot);
-    const int32_t* pages = p.table + (long long)slot * d.max_pages;
-    for (int at = 0; at < n; at += d.page_size) {
-      const int page = pages[at / d.page_size];
-      if (page < 0 || page >= d.n_pages) {
-        atomicOr(p.err, GDN_DEVERR_KV_PAGE);
+    long long total;
+    const long long r = n_runs + block_scan<long long>(first ? 1 : 0, sums, total) - (first ? 0 : 1);
+    if (b < d.B) {
+      int win = p.win_len ? p.win_len[b] : d.K;
+      if (win < 0 || win > d.K) {
+        atomicOr(p.err, GDN_DEVERR_KV_WINDOW);
+        win = win < 0 ? 0 : d.K;
+      }
+      const int keys = slot_len(p, d.slot0 + b);
+      SeqRec q;
+      q.off = 0;
+      q.keys = keys;
+      q.win = win;
+      q.run = s >= 0 ? int(r) : -1;
+      q.tiles = win > 0 ? ((keys + 15) / 16 + 1 + 7) / 8 : 0;  // units of 16 keys; the window is one unit
+      w.seq[b] = q;
+      if (first) {
+        w.run[r].b0 = b;
+        w.run[r].slot = s;
+        const int n = slot_len(p, s);
+        w.run[r].keys = n;
+        w.run[r].tiles = (n + kTileKeys - 1) / kTileKeys;
+      }
+      if (last) w.run[r].n = b + 1;  // (its end; the length follows)
+    }
+    n_runs += total;
+  }
+  __syncthreads();
+  long long tiles = 0, row = 0;
+  for (int r0 = 0; r0 < n_runs; r0 += kPlanThreads) {
+    const int r = r0 + tid;
+    long long mine = 0, rows = 0;
+    if (r < n_runs) {
+      const int n = w.run[r].n - w.run[r].b0;
+      w.run[r].n = n;
+      const long long block = (long long)n * KG;
+      mine = (block + kBlockRows - 1) / kBlockRows * d.Hkv * w.run[r].tiles;
+      rows = d.Hkv * rows_width(block);
+    }
+    long long total, total_rows;
+    const long long off = tiles + block_scan<long long>(mine, sums, total);
+    const long long at = row + block_scan<long long>(rows, sums, total_rows);
+    if (r < n_runs) w.run[r].off = off, w.run[r].row = at;
+    tiles += total;
+    row += total_rows;
+  }
+  const long long prefix_tiles = tiles;
+  const int own_items = d.Hkv * ((KG + kBlockRows - 1) / kBlockRows);
+  for (int b0 = 0; b0 < d.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    long long total;
+    const long long off = tiles + block_scan<long long>(b < d.B ? (long long)own_items * w.seq[b].tiles : 0, sums, total);
+    if (b < d.B) w.seq[b].off = off;
+    tiles += total;
+  }
+  if (tid == 0) {
+    w.head->tiles = tiles;
+    w.head->prefix_tiles = prefix_tiles;
+    w.head->own_row = row;
+    w.head->runs = int(n_runs);
+  }
+  __syncthreads();
+  if (tid < kCtas) {  // where each stretch begins: the last record that starts at or before it and has tiles
+    const long long x = first_tile(tid, tiles);
+    StartRec s{0, 0};
+    if (x < tiles) {
+      s.own = x >= prefix_tiles;
+      int lo = 0, hi = (s.own ? d.B : int(n_runs)) - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if ((s.own ? w.seq[mid].off : w.run[mid].off) <= x)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      s.idx = lo;
+    }
+    w.start[tid] = s;
+  }
+}
+
+// ---------------------------------------------------------------- segments
+struct Seg {
+  int own, idx, h, row0, rows;  // rows row0 .. row0 + rows - 1 of the run's or sequence's rows
+  int tok0;                     // its first window token (of all B K)
+  int slot, keys, win;          // cached tokens; own: window tokens (prefix: -1)
+  int units;                    // of 16 keys, the window's included
+  int t0, t1;                   // tiles of the item
+  int parity;                   // of tile t0 in the order of all tiles
+  long long part;               // first row of its partial results
+  __device__ __forceinline__ bool paired() const { return rows > kTileKeys; }
+};
+
+// Walks a CTA's stretch segment by segment; every warp of the CTA walks it for itself.
+struct SegWalk {
+  const AttnParams& p;
+  const AttnWs& w;
+  long long x, end;
+  int own, idx, cta;
+  long long own_row;
+  int runs;
+  __device__ __forceinline__ SegWalk(const AttnParams& p_, const AttnWs& w_, int cta_) : p(p_), w(w_), cta(cta_) {
+    const PlanHead h = *w.head;
+    x = first_tile(cta, h.tiles), end = first_tile(cta + 1, h.tiles);
+    own = w.start[cta].own, idx = w.start[cta].idx;
+    own_row = h.own_row, runs = h.runs;
+  }
+  __device__ __forceinline__ bool next(Seg& s) {
+    if (x >= end) return false;
+    const gdn_kv_dims& d = p.d;
+    const int KG = d.K * (d.Hq / d.Hkv);
+    while (true) {
+      if (!own && idx == runs) own = 1, idx = 0;
+      if (own && idx >= d.B) return false;
+      long long off, rows, row;
+      int tiles;
+      if (own) {
+        const SeqRec q = w.seq[idx];
+        off = q.off, tiles = q.tiles, rows = KG;
+        row = own_row + (long long)idx * d.Hkv * rows_width(KG);
+        s.slot = d.slot0 + idx, s.keys = q.keys, s.win = q.win, s.tok0 = idx * d.K;
+        s.units = (q.keys + 15) / 16 + 1;
+      } else {
+        const RunRec r = w.run[idx];
+        off = r.off, tiles = r.tiles, rows = (long long)r.n * KG, row = r.row;
+        s.slot = r.slot, s.keys = r.keys, s.win = -1, s.tok0 = r.b0 * d.K;
+        s.units = (r.keys + 15) / 16;
+      }
+      const int blocks = int((rows + kBlockRows - 1) / kBlockRows);
+      const long long items = (long long)blocks * d.Hkv;
+      if (tiles == 0 || x >= off + items * tiles) {
+        ++idx;
         continue;
       }
-      const long long o = p.layer * d.cache_layer_stride + page * d.cache_page_stride + kh * d.cache_head_stride;
-      const int in = n - at < d.page_size ? n - at : d.page_size;
-      for (int i = 0; i < in; ++i)
-        key(static_cast<const uint16_t*>(p.k_cache) + o + i * d.cache_token_stride,
-            static_cast<const uint16_t*>(p.v_cache) + o + i * d.cache_token_stride);
+      const long long item = (x - off) / tiles;
+      s.own = own, s.idx = idx;
+      s.h = int(item / blocks);
+      const int rb = int(item - (long long)s.h * blocks);
+      s.row0 = rb * kBlockRows;
+      s.rows = int(rows - s.row0 < kBlockRows ? rows - s.row0 : kBlockRows);
+      s.t0 = int(x - off - item * tiles);
+      const long long left = end - x;
+      s.t1 = left < tiles - s.t0 ? s.t0 + int(left) : tiles;
+      s.parity = int(x & 1);
+      s.part = (long long)kBlockRows * cta + row + s.h * rows_width(rows) + s.row0;
+      x += s.t1 - s.t0;
+      return true;
     }
-  };
-  if (p.prefix_of) {
-    const int s = p.prefix_of[b];
-    if (s < -1 || s >= d.n_slots)
-      atomicOr(p.err, GDN_DEVERR_KV_SLOT);
-    else if (s >= 0)
-      cached(s);
   }
-  cached(d.slot0 + b);
-  uint32_t seen = 0;
-  if (p.parent) {
-    for (int j = t; j >= 0;) {
-      seen |= 1u << j;
-      int up = p.parent[(long long)b * d.K + j];
-      if (up < -1 || up >= j) {
-        atomicOr(p.err, GDN_DEVERR_TREE_PARENT);
-        up = -1;
+};
+
+// ---------------------------------------------------------------- tensor-core tiles
+template <int D>
+struct TileLayout {
+  static constexpr int BYTES = kTileKeys * D * 2;  // a tile of keys, values or queries
+  static constexpr int HALF = kTileKeys * 128;     // 64 of the D columns: 128 rows of 128 bytes
+  static constexpr int STAGES = D == 128 ? 5 : 10;  // >= 5: two tiles of values wait while a third of keys is read
+  static constexpr int OFF_Q = 0;                  // one per stream
+  static constexpr int OFF_RING = 2 * BYTES;
+  static constexpr int OFF_BAR = OFF_RING + STAGES * BYTES;
+  static constexpr int NBAR = 2 * STAGES + 8;
+  static constexpr int TOTAL = OFF_BAR + NBAR * 8 + 16 + 1024;  // 1024: the base is aligned by hand
+};
+
+struct TileMaps {
+  CUtensorMap k16, v16;  // boxes of 16 tokens of the cache
+  CUtensorMap kb, vb;    // boxes of `box` tokens
+  CUtensorMap kw, vw;    // boxes of 16 tokens of the window
+};
+
+__device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, int c4, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// Shared-memory descriptor of a 128-byte-swizzled operand: rows of 128 bytes, groups of 8 rows
+// 1024 bytes apart (SBO); LBO is the step between 64-column halves of an MN-major operand and not
+// used by a K-major one.
+__device__ __forceinline__ uint64_t swizzled_desc(uint32_t saddr, uint32_t lbo) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// kind::f16 with A and B both f16 (F16) or bf16, f32 accumulator.
+template <bool F16>
+__device__ __forceinline__ uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (F16 ? 0u : (1u << 7) | (1u << 10)) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if (F16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tmem_st32_words(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+// Tensor-memory columns: S of stream s (P over its first half once S has been read), then O.
+constexpr uint32_t kTmemCols = 512;
+__device__ __forceinline__ uint32_t tmem_s(int s) { return 128u * uint32_t(s); }
+__device__ __forceinline__ uint32_t tmem_o(int s) { return 256u + 128u * uint32_t(s); }
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    attn_tile_kernel(const AttnParams p, const AttnWs w, const int box, const __grid_constant__ TileMaps maps) {
+  using L = TileLayout<D>;
+  constexpr int NS = L::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t gave_up;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t *const full = bars, *const empty = bars + NS, *const q_ready = bars + 2 * NS, *const s_ready = q_ready + 2,
+           *const p_ready = q_ready + 4, *const o_done = q_ready + 6;
+  const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const gdn_kv_dims& d = p.d;
+  const int G = d.Hq / d.Hkv;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 2);  // one arrival per stream; a tile that one stream alone uses arrives twice
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(q_ready + s, kGroupThreads);
+      mbar_init(s_ready + s, 1);
+      mbar_init(p_ready + s, kGroupThreads);
+      mbar_init(o_done + s, 1);
+    }
+    gave_up = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) tmem_alloc(&tmem_slot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  grid_launch_dependents();
+  grid_wait();
+
+  // Bounded wait of one thread; once one has given up, all others of the CTA do too.
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!gave_up) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (global_timer_ns() - t0 > kSpinLimitNs) {
+        gave_up = 1;
+        atomicOr(p.err, kDevErrTimeout);
       }
-      j = up;
     }
-  } else {
-    seen = (2u << t) - 1u;
-  }
-  for (int j = 0; j < win; ++j)
-    if (seen >> j & 1) {
-      const long long o = ((long long)b * d.K + j) * d.win_token_stride + (long long)kh * D;
-      key(static_cast<const uint16_t*>(p.k_win) + o, static_cast<const uint16_t*>(p.v_win) + o);
+    return false;
+  };
+
+  // The same for a whole warp, which goes on or gives up together.
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
+
+  SegWalk walk(p, w, int(blockIdx.x));
+  Seg seg;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    uint32_t n = 0;  // tiles so far; tile n's keys are in ring slot 2n, its values in slot 2n + 1 (mod STAGES)
+    uint32_t issued = 0;
+    bool ok = true;
+    while (ok && walk.next(seg)) {
+      const int32_t* pages = p.table + (long long)seg.slot * d.max_pages;
+      for (int t = seg.t0; ok && t < seg.t1; ++t, ++n) {
+        const int u0 = 8 * t, units = seg.units - u0 < 8 ? seg.units - u0 : 8;
+        const int cached = (seg.keys + 15) / 16 - u0;  // units of this tile from the cache (may exceed 8)
+        const bool whole = cached >= 8;                // and none from the window: boxes of `box` tokens
+        const int rows = whole ? box : 16;
+        const int boxes = whole ? kTileKeys / box : units;
+        const int i = lane / (D / 64), half = lane % (D / 64);
+        int page = 0, in = 0;
+        const bool from_window = !whole && i == cached;  // (the window is the unit behind the cached ones)
+        if (i < boxes && !from_window) {
+          const int token = t * kTileKeys + i * rows, col = token / d.page_size;
+          in = token - col * d.page_size;
+          page = pages[col];
+          if (page < 0 || page >= d.n_pages) {  // reads zeros there
+            atomicOr(p.err, GDN_DEVERR_KV_PAGE);
+            page = d.n_pages;
+          }
+        }
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t use = 2 * n + v, slot = use % NS;
+          if (!wait_warp(empty + slot, ((use / NS) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(full + slot, uint32_t(units) * 16 * D * 2);
+          __syncwarp();
+          if (i < boxes) {
+            const uint32_t dst = base + L::OFF_RING + slot * L::BYTES + half * L::HALF + i * rows * 128;
+            const uint32_t bar = smem_addr(full + slot);
+            if (from_window)
+              tma_load4(dst, v ? &maps.vw : &maps.kw, half * 64, seg.h, 0, seg.idx, bar);
+            else if (whole)
+              tma_load5(dst, v ? &maps.vb : &maps.kb, half * 64, in, seg.h, page, p.layer, bar);
+            else
+              tma_load5(dst, v ? &maps.v16 : &maps.k16, half * 64, in, seg.h, page, p.layer, bar);
+          }
+          __syncwarp();
+          issued = use + 1;
+        }
+      }
     }
-  const float r = 1.f / l;  // a live row sees at least itself: l >= 1
+    // the last uses of the ring: the copies have landed and the tensor core has read them
+    for (uint32_t use = issued > NS ? issued - NS : 0; use < issued; ++use) {
+      if (ok) ok = wait_warp(empty + use % NS, (use / NS) & 1);
+      if (!ok) mbar_drain(full + use % NS, (use / NS) & 1);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ tensor core
+    if (lane == 0) {
+      struct Pending {
+        uint32_t use;
+        int units, twice, first, last;
+      } pend[2];
+      bool has[2] = {false, false}, ok = true;
+      uint32_t n = 0, np[2] = {0, 0}, nq[2] = {0, 0};
+      auto values = [&](int s) -> bool {  // O += P V of the stream's pending tile
+        const Pending q = pend[s];
+        has[s] = false;
+        const uint32_t slot = q.use % NS;
+        if (!wait(p_ready + s, np[s] & 1) || !wait(full + slot, (q.use / NS) & 1)) return false;
+        ++np[s];
+        tc_fence_after();
+        const uint32_t idesc = idesc_f16<F16>(kTileKeys, D) | (1u << 16);  // B (values) MN-major
+        const uint64_t db = swizzled_desc(base + L::OFF_RING + slot * L::BYTES, L::HALF);
+        for (int u = 0; u < q.units; ++u)
+          umma_ts(tmem + tmem_o(s), tmem + tmem_s(s) + 8 * u, db + uint64_t(128 * u), idesc, (q.first && u == 0) ? 0u : 1u);
+        umma_commit(empty + slot);
+        if (q.twice) umma_commit(empty + slot);
+        if (q.last) umma_commit(o_done + s);
+        return true;
+      };
+      while (ok && walk.next(seg)) {
+        const bool paired = seg.paired();
+        for (int t = seg.t0; ok && t < seg.t1; ++t, ++n) {
+          const int units = seg.units - 8 * t < 8 ? seg.units - 8 * t : 8;
+          const int turn = (seg.parity + t - seg.t0) & 1;
+          for (int s = 0; ok && s < 2; ++s) {
+            if (!paired && s != turn) continue;
+            if (has[s] && !values(s)) {
+              ok = false;
+              break;
+            }
+            const bool first = paired ? t == seg.t0 : t - seg.t0 < 2, last = paired ? t == seg.t1 - 1 : seg.t1 - t <= 2;
+            const uint32_t use = 2 * n, slot = use % NS;
+            if (first) {
+              if (!wait(q_ready + s, nq[s] & 1)) {
+                ok = false;
+                break;
+              }
+              ++nq[s];
+            }
+            if (!wait(full + slot, (use / NS) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t idesc = idesc_f16<F16>(kTileKeys, 16 * units);
+            const uint64_t da = swizzled_desc(base + L::OFF_Q + s * L::BYTES, 16);
+            const uint64_t db = swizzled_desc(base + L::OFF_RING + slot * L::BYTES, 16);
 #pragma unroll
-  for (int i = 0; i < N; ++i) out[32 * i + lane] = pack2<F16>(acc[i].x * r, acc[i].y * r);
-  if (p.lse && lane == 0) p.lse[row] = (m + log2f(l)) * 0.693147181f;
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t step = uint64_t((k & 3) * 2 + (k >> 2) * (L::HALF >> 4));
+              umma_bf16(tmem + tmem_s(s), da + step, db + step, idesc, k > 0 ? 1u : 0u);
+            }
+            umma_commit(s_ready + s);
+            umma_commit(empty + slot);
+            if (!paired) umma_commit(empty + slot);
+            pend[s] = Pending{use + 1, units, paired ? 0 : 1, first ? 1 : 0, last ? 1 : 0};
+            has[s] = true;
+          }
+        }
+      }
+      for (int s = 0; s < 2; ++s)
+        if (ok && has[s]) ok = values(s);
+      if (!ok) {  // what is under way finishes before tensor memory is freed
+        umma_commit(o_done);
+        mbar_drain(o_done, 0);
+        mbar_drain(o_done, 1);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax: stream s, one row per thread
+    const int s = warp >> 2, r = tid & 127;
+    const uint32_t lane_sel = uint32_t(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + tmem_s(s) + lane_sel, to = tmem + tmem_o(s) + lane_sel;
+    // a negative scale is the positive one on negated queries; 0 is as good as 1e-30
+    const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);
+    const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+    uint32_t n = 0, ns = 0, no = 0;  // tiles of the CTA, tiles of this stream, its segments
+    bool ok = true;
+    while (ok && walk.next(seg)) {
+      const bool paired = seg.paired();
+      const int count = seg.t1 - seg.t0;
+      const uint32_t n0 = n;
+      n += uint32_t(count);
+      int t = seg.t0;
+      if (!paired && ((seg.parity ^ s) & 1)) ++t;
+      if (t >= seg.t1) continue;
+      const int step = paired ? 1 : 2;
+      const int srow0 = paired ? s * kTileKeys : 0;
+      const int rows = seg.rows - srow0 < kTileKeys ? seg.rows - srow0 : kTileKeys;
+      const bool idle = 32 * (warp & 3) >= rows;  // a warp without rows only keeps the barriers going
+
+      {  // queries: 16 bytes a thread, swizzled; rows that do not exist are zero
+        constexpr int C = D / 8;
+        uint8_t* const q_tile = smem + L::OFF_Q + s * L::BYTES;
+        const uint16_t* const q = static_cast<const uint16_t*>(p.q);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          const int piece = r + i * kGroupThreads, row = piece / C, ch = piece % C;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (row < rows) {
+            const int rr = seg.row0 + srow0 + row, tok = seg.tok0 + rr / G, head = seg.h * G + rr % G;
+            v = *reinterpret_cast<const uint4*>(q + tok * d.q_token_stride + head * D + ch * 8);
+            v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+          }
+          *reinterpret_cast<uint4*>(q_tile + (ch >> 3) * L::HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(q_ready + s);
+      }
+
+      uint32_t seen = 0;  // own: the window tokens that this row sees
+      if (seg.own && seg.t1 == (seg.units + 7) / 8) {
+        // each lane holds a node's parent; four doublings reach every ancestor of 16 nodes
+        uint32_t anc = 0;
+        if (p.parent) {
+          int up = -1;
+          if (lane < d.K) {
+            up = p.parent[(long long)seg.idx * d.K + lane];
+            if (up < -1 || up >= lane) {
+              atomicOr(p.err, kDevErrTreeParent);
+              up = -1;
+            }
+          }
+          anc = 1u << lane;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a = __shfl_sync(0xffffffffu, anc, up & 31);
+            const int g = __shfl_sync(0xffffffffu, up, up & 31);
+            if (up >= 0) anc |= a, up = g;
+          }
+        } else {
+          anc = (2u << lane) - 1u;
+        }
+        const int tok = ((seg.row0 + srow0 + r) / G) % d.K;
+        seen = __shfl_sync(0xffffffffu, anc, tok & 31) & ((1u << seg.win) - 1u);
+      }
+
+      float m = -INFINITY, l = 0.f;  // running maximum (unscaled) and sum
+      bool first = true;
+      for (; ok && t < seg.t1; t += step, ++ns) {
+        if (!wait_warp(s_ready + s, ns & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int units = seg.units - 8 * t < 8 ? seg.units - 8 * t : 8;
+        const int cached = seg.keys - t * kTileKeys;  // keys of this tile from the cache (may exceed 128)
+        if (!idle) {
+          float x[128];
+          tmem_ld32(ts, x);
+          tmem_ld32(ts + 32, x + 32);
+          tmem_ld32(ts + 64, x + 64);
+          tmem_ld32(ts + 96, x + 96);
+          if (cached < kTileKeys) {
+            const int wu = (cached + 15) / 16 * 16;  // the window's unit (own; beyond the tile for a prefix)
+#pragma unroll
+            for (int j = 0; j < 128; ++j) {
+              const bool see = j < cached || (seg.own && j >= wu && j < wu + 16 && (seen >> ((j - wu) & 15) & 1u));
+              x[j] = see ? x[j] : -INFINITY;
+            }
+          }
+          float mx = x[0];
+#pragma unroll
+          for (int j = 1; j < 128; ++j) mx = fmaxf(mx, x[j]);
+          const float up = (mx - m) * c;
+          const bool move = mx > m && !(up <= kLag);  // (m = -inf: up is inf)
+          if (__any_sync(0xffffffffu, move)) {
+            const float f = move ? exp2_fast((m - mx) * c) : 1.f;
+            if (!first) {
+#pragma unroll
+              for (int q = 0; q < D; q += 32) {
+                float o[32];
+                tmem_ld32(to + q, o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] *= f;
+                tmem_st32(to + q, o);
+              }
+            }
+            if (move) l *= f, m = mx;
+          }
+          const float mc = m == -INFINITY ? 0.f : m * c;
+          uint32_t pk[64];
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 64; ++j) {
+            const float a = exp2_fast(fmaf(x[2 * j], c, -mc)), b = exp2_fast(fmaf(x[2 * j + 1], c, -mc));
+            sum += a + b;
+            pk[j] = pack2<F16>(a, b);
+          }
+          l += sum;
+          tmem_st32_words(ts, pk);
+          tmem_st32_words(ts + 32, pk + 32);
+        }
+        first = false;
+        if (cached < kTileKeys && (seg.own || (cached & 15))) {
+          // values behind the last cached token of its unit, and behind the window's last token, are
+          // not the batch's: zero them, for 0 x NaN is NaN
+          const uint32_t use = 2 * (n0 + uint32_t(t - seg.t0)) + 1, slot = use % NS;
+          if (!wait_warp(full + slot, (use / NS) & 1)) {
+            ok = false;
+            break;
+          }
+          const int tail = cached > 0 ? cached : 0, wu = (tail + 15) / 16 * 16;
+          const int end = units * 16;
+          uint8_t* const v_tile = smem + L::OFF_RING + slot * L::BYTES;
+          constexpr int C = D / 8;
+          for (int i = r; i < (end - tail) * C; i += kGroupThreads) {
+            const int row = tail + i / C, ch = i % C;
+            if (row >= wu && row < wu + seg.win) continue;
+            *reinterpret_cast<uint4*>(v_tile + (ch >> 3) * L::HALF + row * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        mbar_arrive(p_ready + s);
+      }
+      if (!ok) break;
+
+      // the segment's result: O / l and the log-sum-exp in powers of two
+      if (!wait_warp(o_done + s, no & 1)) {
+        ok = false;
+        break;
+      }
+      ++no;
+      tc_fence_after();
+      if (!idle) {
+        const long long part = seg.part + (paired ? srow0 : s * seg.rows) + r;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        float* const out = w.o + part * D;
+#pragma unroll
+        for (int q = 0; q < D; q += 32) {
+          float o[32];
+          tmem_ld32(to + q, o);
+          if (r < rows) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4*>(out + q + j) = make_float4(o[j] * inv, o[j + 1] * inv, o[j + 2] * inv, o[j + 3] * inv);
+          }
+        }
+        if (r < rows) w.lse[part] = l == 0.f ? -INFINITY : m * c + log2f(l);
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- join
+// One warp per row: the segments of its sequence and of its prefix, by their log-sum-exps.
+template <int D, bool F16>
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnParams p, const AttnWs w) {
+  constexpr int N = D / 32;
+  grid_launch_dependents();
+  grid_wait();
+  const gdn_kv_dims& d = p.d;
+  const int G = d.Hq / d.Hkv, KG = d.K * G, lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (row >= (long long)d.B * d.K * d.Hq) return;
+  const int hq = int(row % d.Hq), h = hq / G, g = hq - h * G;
+  const int tok = int(row / d.Hq), b = tok / d.K, t = tok - b * d.K;
+  const SeqRec q = w.seq[b];
+  const long long tiles = w.head->tiles;
+  uint16_t* const out = static_cast<uint16_t*>(p.out) + row * D;
+  float acc[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+  float M = -INFINITY, W = 0.f;
+  if (t < q.win) {
+    // the row's item in each of the two parts: tiles [at, at + n), first CTA, and rows
+    struct Part {
+      long long at, base;
+      int n, c0, parts, width, lr;
+      bool paired;
+    };
+    auto part_of = [&](long long off, int n, long long row0, long long rows, int r) {
+      Part x{};
+      if (n == 0) return x;
+      const int blocks = int((rows + kBlockRows - 1) / kBlockRows), rb = r / kBlockRows;
+      const int in = int(rows - (long long)rb * kBlockRows < kBlockRows ? rows - (long long)rb * kBlockRows : kBlockRows);
+      x.at = off + ((long long)h * blocks + rb) * n;
+      x.n = n;
+      x.c0 = cta_of(x.at, tiles);
+      x.paired = in > kTileKeys;
+      x.parts = (cta_of(x.at + n - 1, tiles) - x.c0 + 1) * (x.paired ? 1 : 2);
+      x.width = in;
+      x.lr = r - rb * kBlockRows;
+      x.base = row0 + h * rows_width(rows) + (long long)rb * kBlockRows;
+      return x;
+    };
+    const Part own = part_of(q.off, q.tiles, w.head->own_row + (long long)b * d.Hkv * rows_width(KG), KG, t * G + g);
+    Part pre{};
+    if (q.run >= 0) {
+      const RunRec r = w.run[q.run];
+      pre = part_of(r.off, r.tiles, r.row, (long long)r.n * KG, ((b - r.b0) * d.K + t) * G + g);
+    }
+    const int count = own.parts + pre.parts;
+    for (int i0 = 0; i0 < count; i0 += 32) {
+      long long at = -1;
+      const int i = i0 + lane;
+      if (i < count) {
+        const Part& x = i < own.parts ? own : pre;
+        const int j = i < own.parts ? i : i - own.parts;
+        const int c = x.c0 + (x.paired ? j : j >> 1), s = x.paired ? 0 : j & 1;
+        long long lo = first_tile(c, tiles), hi = first_tile(c + 1, tiles);
+        if (lo < x.at) lo = x.at;
+        if (hi > x.at + x.n) hi = x.at + x.n;
+        if (hi > lo && (x.paired || hi - lo >= 2 || int(lo & 1) == s))  // (a single tile belongs to one stream)
+          at = (long long)kBlockRows * c + x.base + s * x.width + x.lr;
+      }
+      const float e = at >= 0 ? w.lse[at] : -INFINITY;
+      float mx = e;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const bool nan = __any_sync(0xffffffffu, e != e);
+      const float Mn = fmaxf(M, mx), f = M == -INFINITY ? 0.f : exp2f(M - Mn);
+      float wt = e == -INFINITY ? 0.f : exp2f(e - (Mn == -INFINITY ? 0.f : Mn));
+      M = Mn;
+      W = W * f + warp_sum(wt);
+      if (nan) W = NAN;
+#pragma unroll
+      for (int k = 0; k < N; ++k) acc[k] *= f;
+      const int m = count - i0 < 32 ? count - i0 : 32;
+#pragma unroll 4
+      for (int j = 0; j < m; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, wt, j);
+        const long long aj = __shfl_sync(0xffffffffu, at, j);
+        if (wj != 0.f) {
+          const float* o = w.o + aj * D + lane * N;
+          if (N == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(o);
+            acc[0] += wj * v.x, acc[1] += wj * v.y, acc[N - 2] += wj * v.z, acc[N - 1] += wj * v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(o);
+            acc[0] += wj * v.x, acc[1] += wj * v.y;
+          }
+        }
+      }
+    }
+    const float inv = 1.f / W;
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] *= inv;
+  }
+  uint32_t* const o = reinterpret_cast<uint32_t*>(out) + lane * (N / 2);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) o[i] = pack2<F16>(acc[2 * i], acc[2 * i + 1]);
+  if (p.lse && lane == 0) p.lse[row] = t < q.win ? (M + log2f(W)) * kLn2 : -INFINITY;
+}
+
+// ---------------------------------------------------------------- launches
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder (the library does not link against libcuda).
+EncodeTiled encoder() {
+  static const EncodeTiled f = [] {
+    void* sym = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      sym = nullptr;
+    return reinterpret_cast<EncodeTiled>(sym);
+  }();
+  return f;
+}
+
+template <typename... Args>
+cudaError_t launch_pdl(void (*kernel)(Args...), unsigned grid, int threads, int smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(unsigned(threads), 1, 1);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D, bool F16>
+cudaError_t launch(const AttnParams& p, const AttnWs& w, int box, const TileMaps& maps, cudaStream_t stream) {
+  using L = TileLayout<D>;
+  static_assert(L::TOTAL <= 232448 - 64, "shared memory");
+  cudaError_t e = launch_pdl(attn_plan_kernel, 1u, kPlanThreads, 0, stream, p, w);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(attn_tile_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn_tile_kernel<D, F16>, unsigned(kCtas), kTileThreads, L::TOTAL, stream, p, w, box, maps);
+  if (e != cudaSuccess) return e;
+  const long long rows = (long long)p.d.B * p.d.K * p.d.Hq;
+  return launch_pdl(attn_join_kernel<D, F16>, unsigned((rows + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, stream,
+                    p, w);
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(const gdn_kv_dims&) { return 256; }
+size_t attn_workspace_bytes(const gdn_kv_dims& d) {
+  size_t n = 0;
+  carve_attn(nullptr, d, &n);
+  return n;
+}
 
 cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) {
-  const long long rows = (long long)p.d.B * p.d.K * p.d.Hq;
-  const unsigned grid = unsigned((rows + kRowWarps - 1) / kRowWarps);
-  if (p.d.D == 128) {
-    if (p.d.dtype) attn_row_kernel<128, true><<<grid, 32 * kRowWarps, 0, stream>>>(p);
-    else attn_row_kernel<128, false><<<grid, 32 * kRowWarps, 0, stream>>>(p);
-  } else {
-    if (p.d.dtype) attn_row_kernel<64, true><<<grid, 32 * kRowWarps, 0, stream>>>(p);
-    else attn_row_kernel<64, false><<<grid, 32 * kRowWarps, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  const gdn_kv_dims& d = p.d;
+  const EncodeTiled encode = encoder();
+  if (!encode) return cudaErrorNotSupported;
+  // Tokens per copy of a full tile: as many as lie together in a page, a divisor of the tile's 128.
+  int box = 16;
+  while (box < kTileKeys && d.page_size % (2 * box) == 0) box *= 2;
+  const auto type = d.dtype ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  bool ok = true;
+  auto map = [&](CUtensorMap* m, const void* at, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* boxes) {
+    ok = ok && encode(m, type, cuuint32_t(rank), const_cast<void*>(at), dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  TileMaps maps;
+  const cuuint64_t cd[5] = {cuuint64_t(d.D), cuuint64_t(d.page_size), cuuint64_t(d.Hkv), cuuint64_t(d.n_pages), cuuint64_t(d.n_layers)};
+  const cuuint64_t cs[4] = {2ull * d.cache_token_stride, 2ull * d.cache_head_stride, 2ull * d.cache_page_stride, 2ull * d.cache_layer_stride};
+  const cuuint32_t b16[5] = {64, 16, 1, 1, 1}, bb[5] = {64, cuuint32_t(box), 1, 1, 1};
+  map(&maps.k16, p.k_cache, 5, cd, cs, b16);
+  map(&maps.v16, p.v_cache, 5, cd, cs, b16);
+  map(&maps.kb, p.k_cache, 5, cd, cs, bb);
+  map(&maps.vb, p.v_cache, 5, cd, cs, bb);
+  // windows: (D, kv head, token, sequence); rows behind the K-th token read as zeros
+  const cuuint64_t wd[4] = {cuuint64_t(d.D), cuuint64_t(d.Hkv), cuuint64_t(d.K), cuuint64_t(d.B)};
+  const cuuint64_t wst[3] = {2ull * d.D, 2ull * d.win_token_stride, 2ull * d.K * d.win_token_stride};
+  const cuuint32_t bw[4] = {64, 1, 16, 1};
+  map(&maps.kw, p.k_win, 4, wd, wst, bw);
+  map(&maps.vw, p.v_win, 4, wd, wst, bw);
+  if (!ok) return cudaErrorInvalidValue;
+  const AttnWs w = carve_attn(p.ws, d, nullptr);
+  if (d.D == 128) return d.dtype ? launch<128, true>(p, w, box, maps, stream) : launch<128, false>(p, w, box, maps, stream);
+  return d.dtype ? launch<64, true>(p, w, box, maps, stream) : launch<64, false>(p, w, box, maps, stream);
 }
 
 }  // namespace gdn
