@@ -15,8 +15,8 @@
 //
 // The tile kernel: a producer warp brings keys and values by TMA (128-byte swizzle) into a ring
 // of tiles; one thread issues S = Q K^T and O += P V (tcgen05, M = 128, accumulators in tensor
-// memory, P read from tensor memory); two groups of four warps, one per stream, turn S into P, a
-// row per thread.  A block of more than 128 rows uses the two streams for its two halves on the
+// memory, P read from tensor memory); a warp per stream fetches the next segment's queries; two
+// groups of four warps, one per stream, turn S into P, a row per thread.  A block of more than 128 rows uses the two streams for its two halves on the
 // same keys; a smaller one gives them alternate tiles of the same rows.  While one stream's
 // softmax runs, the tensor core works for the other.
 #include <cuda.h>
@@ -34,12 +34,17 @@ constexpr int kTileKeys = 128;
 constexpr int kBlockRows = 256;  // rows of an item
 constexpr int kPlanThreads = 1024;
 constexpr int kGroupThreads = 128;  // a softmax group: one thread per row of a stream
-constexpr int kTileThreads = 2 * kGroupThreads + 64;
+constexpr int kTileThreads = 3 * kGroupThreads;  // two softmax groups; producer, tensor-core and two query warps
+// Registers: 168 a thread at launch (64512 in all), then 224 for the softmax threads, which hold a
+// row of 128 scores, and 56 for the rest: 256 x 224 + 128 x 56 = 64512.
+constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 constexpr int kJoinWarps = 8;
 constexpr float kLn2 = 0.693147180559945f, kLog2e = 1.442695040888963f;
 // A running maximum may lag behind by up to 8 powers of two before O is rescaled: probabilities
 // stay below 2^8, far inside both 16-bit types, and keep their relative precision.
 constexpr float kLag = 8.0f;
+// Longest wait inside the tile kernel: looks of at most about a microsecond each, a few seconds in all.
+constexpr uint32_t kMaxLooks = 1u << 22;
 
 // ---------------------------------------------------------------- the plan
 struct SeqRec {     // what a sequence does not share
@@ -150,7 +155,7 @@ __device__ __forceinline__ int prefix_slot(const AttnParams& p, int b) {
   return s < 0 || s >= p.d.n_slots ? -1 : s;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParams p, const AttnWs w) {
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWs w) {
   __shared__ long long sums[32];
   grid_launch_dependents();
   grid_wait();
@@ -260,7 +265,7 @@ struct Seg {
   __device__ __forceinline__ bool paired() const { return rows > kTileKeys; }
 };
 
-// Walks a CTA's stretch segment by segment; every warp of the CTA walks it for itself.
+// Walks a CTA's stretch segment by segment.
 struct SegWalk {
   const AttnParams& p;
   const AttnWs& w;
@@ -301,13 +306,13 @@ struct SegWalk {
         ++idx;
         continue;
       }
-      const long long item = (x - off) / tiles;
+      const int item = int((x - off) / tiles);
       s.own = own, s.idx = idx;
-      s.h = int(item / blocks);
-      const int rb = int(item - (long long)s.h * blocks);
+      s.h = item / blocks;
+      const int rb = item - s.h * blocks;
       s.row0 = rb * kBlockRows;
       s.rows = int(rows - s.row0 < kBlockRows ? rows - s.row0 : kBlockRows);
-      s.t0 = int(x - off - item * tiles);
+      s.t0 = int(x - off - (long long)item * tiles);
       const long long left = end - x;
       s.t1 = left < tiles - s.t0 ? s.t0 + int(left) : tiles;
       s.parity = int(x & 1);
@@ -319,6 +324,8 @@ struct SegWalk {
 };
 
 // ---------------------------------------------------------------- tensor-core tiles
+constexpr int kSegRing = 4;
+
 template <int D>
 struct TileLayout {
   static constexpr int BYTES = kTileKeys * D * 2;  // a tile of keys, values or queries
@@ -327,11 +334,13 @@ struct TileLayout {
   static constexpr int OFF_Q = 0;                  // one per stream
   static constexpr int OFF_RING = 2 * BYTES;
   static constexpr int OFF_BAR = OFF_RING + STAGES * BYTES;
-  static constexpr int NBAR = 2 * STAGES + 8;
-  static constexpr int TOTAL = OFF_BAR + NBAR * 8 + 16 + 1024;  // 1024: the base is aligned by hand
+  static constexpr int NBAR = 2 * STAGES + 10 + 2 * kSegRing;
+  static constexpr int OFF_SEG = OFF_BAR + NBAR * 8;  // segments on their way from the producer
+  static constexpr int TOTAL = OFF_SEG + kSegRing * int(sizeof(Seg)) + 1024;  // 1024: the base is aligned by hand
 };
 
 struct TileMaps {
+  // (D, token, kv head, page or sequence, layer); a keys' map and the values' behind it
   CUtensorMap k16, v16;  // boxes of 16 tokens of the cache
   CUtensorMap kb, vb;    // boxes of `box` tokens
   CUtensorMap kw, vw;    // boxes of 16 tokens of the window
@@ -343,26 +352,32 @@ __device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* m, in
       "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
       : "memory");
 }
-__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
-
 // Shared-memory descriptor of a 128-byte-swizzled operand: rows of 128 bytes, groups of 8 rows
 // 1024 bytes apart (SBO); LBO is the step between 64-column halves of an MN-major operand and not
 // used by a K-major one.
-__device__ __forceinline__ uint64_t swizzled_desc(uint32_t saddr, uint32_t lbo) {
-  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) | (uint64_t(1024 >> 4) << 32) |
-         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+// Low word of a descriptor; the high word (SBO, version, layout) is the same for all of them.
+__device__ __forceinline__ uint32_t swizzled_desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
 }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+// One step of 16 (elements of D for S, keys for O): S += Q K^T with the operands' descriptors, O += P V
+// with P in tensor memory.  (The descriptors are put together beside each product, from one
+// register: held ready for every step, they would not fit the issuing warp's registers.)
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void umma_ss_step(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b32 a, b;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "add.u32 a, %1, %6;\n\tadd.u32 b, %2, %7;\n\tmov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi), "n"(A_STEP), "n"(B_STEP)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_step(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
       : "memory");
 }
 
@@ -388,26 +403,38 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-__device__ __forceinline__ void tmem_st32_words(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
-      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
+
+// A value that all lanes hold, in a form that the compiler knows to be the same in all of them (the
+// tensor core's operands live in uniform registers).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
 
 // Tensor-memory columns: S of stream s (P over its first half once S has been read), then O.
 constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t tmem_s(int s) { return 128u * uint32_t(s); }
 __device__ __forceinline__ uint32_t tmem_o(int s) { return 256u + 128u * uint32_t(s); }
 
+// One look at a barrier's phase, sleeping for up to about a microsecond.
+__device__ __forceinline__ bool mbar_look(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "n"(1000)
+      : "memory");
+  return ok != 0;
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    attn_tile_kernel(const AttnParams p, const AttnWs w, const int box, const __grid_constant__ TileMaps maps) {
+    attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWs w, const int box, const __grid_constant__ TileMaps maps) {
   using L = TileLayout<D>;
   constexpr int NS = L::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -417,7 +444,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t *const full = bars, *const empty = bars + NS, *const q_ready = bars + 2 * NS, *const s_ready = q_ready + 2,
-           *const p_ready = q_ready + 4, *const o_done = q_ready + 6;
+           *const p_ready = q_ready + 4, *const o_done = q_ready + 6, *const q_free = q_ready + 8, *const seg_full = q_ready + 10,
+           *const seg_empty = seg_full + kSegRing;
+  Seg* const segs = reinterpret_cast<Seg*>(smem + L::OFF_SEG);
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const gdn_kv_dims& d = p.d;
   const int G = d.Hq / d.Hkv;
@@ -428,10 +457,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(empty + i, 2);  // one arrival per stream; a tile that one stream alone uses arrives twice
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(q_ready + s, kGroupThreads);
+      mbar_init(q_ready + s, 32);
+      mbar_init(q_free + s, 1);
       mbar_init(s_ready + s, 1);
       mbar_init(p_ready + s, kGroupThreads);
       mbar_init(o_done + s, 1);
+    }
+    for (int i = 0; i < kSegRing; ++i) {
+      mbar_init(seg_full + i, 1);
+      mbar_init(seg_empty + i, 3 + 2 * kGroupThreads / 32);  // every warp but the producer
     }
     gave_up = 0;
     fence_mbar_init();
@@ -444,32 +478,44 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   grid_launch_dependents();
   grid_wait();
 
-  // Bounded wait of one thread; once one has given up, all others of the CTA do too.
+  // Bounded wait of one thread; once one has given up, all others of the CTA do too.  (Short: the
+  // tile kernel's loops have to stay in the instruction cache.)
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (!gave_up) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if (global_timer_ns() - t0 > kSpinLimitNs) {
+    for (uint32_t i = 0; !mbar_look(bar, parity); ++i) {
+      if (gave_up) return false;
+      if (i > kMaxLooks) {
         gave_up = 1;
         atomicOr(p.err, kDevErrTimeout);
+        return false;
       }
     }
-    return false;
+    return true;
   };
-
   // The same for a whole warp, which goes on or gives up together.
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
 
-  SegWalk walk(p, w, int(blockIdx.x));
-  Seg seg;
-
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 8) {
     // ------------------------------------------------------------ producer
+    SegWalk walk(p, w, int(blockIdx.x));
+    Seg seg;
     uint32_t n = 0;  // tiles so far; tile n's keys are in ring slot 2n, its values in slot 2n + 1 (mod STAGES)
-    uint32_t issued = 0;
+    uint32_t issued = 0, k = 0;  // ring uses; segments handed on
     bool ok = true;
-    while (ok && walk.next(seg)) {
+    while (ok) {
+      const bool more = walk.next(seg);
+      if (!wait_warp(seg_empty + k % kSegRing, ((k / kSegRing) & 1) ^ 1)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        if (!more) seg.t1 = -1;
+        segs[k % kSegRing] = seg;
+        mbar_arrive(seg_full + k % kSegRing);
+      }
+      __syncwarp();
+      ++k;
+      if (!more) break;
       const int32_t* pages = p.table + (long long)seg.slot * d.max_pages;
       for (int t = seg.t0; ok && t < seg.t1; ++t, ++n) {
         const int u0 = 8 * t, units = seg.units - u0 < 8 ? seg.units - u0 : 8;
@@ -489,6 +535,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             page = d.n_pages;
           }
         }
+        const int c3 = from_window ? seg.idx : page, c4 = from_window ? 0 : p.layer;
+        const CUtensorMap* const m = from_window ? &maps.kw : whole ? &maps.kb : &maps.k16;  // the values' map follows
+#pragma unroll 1
         for (int v = 0; v < 2; ++v) {
           const uint32_t use = 2 * n + v, slot = use % NS;
           if (!wait_warp(empty + slot, ((use / NS) & 1) ^ 1)) {
@@ -497,16 +546,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           if (lane == 0) mbar_arrive_expect_tx(full + slot, uint32_t(units) * 16 * D * 2);
           __syncwarp();
-          if (i < boxes) {
-            const uint32_t dst = base + L::OFF_RING + slot * L::BYTES + half * L::HALF + i * rows * 128;
-            const uint32_t bar = smem_addr(full + slot);
-            if (from_window)
-              tma_load4(dst, v ? &maps.vw : &maps.kw, half * 64, seg.h, 0, seg.idx, bar);
-            else if (whole)
-              tma_load5(dst, v ? &maps.vb : &maps.kb, half * 64, in, seg.h, page, p.layer, bar);
-            else
-              tma_load5(dst, v ? &maps.v16 : &maps.k16, half * 64, in, seg.h, page, p.layer, bar);
-          }
+          if (i < boxes)
+            tma_load5(base + L::OFF_RING + slot * L::BYTES + half * L::HALF + i * rows * 128, m + v, half * 64, in, seg.h, c3, c4,
+                      smem_addr(full + slot));
           __syncwarp();
           issued = use + 1;
         }
@@ -519,120 +561,151 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ tensor core
-    if (lane == 0) {
-      struct Pending {
-        uint32_t use;
-        int units, twice, first, last;
-      } pend[2];
-      bool has[2] = {false, false}, ok = true;
-      uint32_t n = 0, np[2] = {0, 0}, nq[2] = {0, 0};
-      auto values = [&](int s) -> bool {  // O += P V of the stream's pending tile
-        const Pending q = pend[s];
-        has[s] = false;
-        const uint32_t slot = q.use % NS;
-        if (!wait(p_ready + s, np[s] & 1) || !wait(full + slot, (q.use / NS) & 1)) return false;
-        ++np[s];
-        tc_fence_after();
-        const uint32_t idesc = idesc_f16<F16>(kTileKeys, D) | (1u << 16);  // B (values) MN-major
-        const uint64_t db = swizzled_desc(base + L::OFF_RING + slot * L::BYTES, L::HALF);
-        for (int u = 0; u < q.units; ++u)
-          umma_ts(tmem + tmem_o(s), tmem + tmem_s(s) + 8 * u, db + uint64_t(128 * u), idesc, (q.first && u == 0) ? 0u : 1u);
-        umma_commit(empty + slot);
-        if (q.twice) umma_commit(empty + slot);
-        if (q.last) umma_commit(o_done + s);
-        return true;
-      };
-      while (ok && walk.next(seg)) {
-        const bool paired = seg.paired();
-        for (int t = seg.t0; ok && t < seg.t1; ++t, ++n) {
-          const int units = seg.units - 8 * t < 8 ? seg.units - 8 * t : 8;
-          const int turn = (seg.parity + t - seg.t0) & 1;
-          for (int s = 0; ok && s < 2; ++s) {
-            if (!paired && s != turn) continue;
-            if (has[s] && !values(s)) {
-              ok = false;
-              break;
-            }
-            const bool first = paired ? t == seg.t0 : t - seg.t0 < 2, last = paired ? t == seg.t1 - 1 : seg.t1 - t <= 2;
-            const uint32_t use = 2 * n, slot = use % NS;
-            if (first) {
-              if (!wait(q_ready + s, nq[s] & 1)) {
+    {
+      const uint32_t tm = uniform(tmem);
+      // The whole warp walks the schedule and one elected lane issues: operands stay warp-uniform.
+      // What a stream's pending tile needs for O += P V, as fields of one word: units (4 bits), then
+      // flags - this stream alone uses the tile, first and last tile of the stream's segment.
+      constexpr uint32_t kAlone = 16, kFirst = 32, kLast = 64, kHas = 128;
+      uint32_t pend0 = 0, pend1 = 0, use0 = 0, use1 = 0;
+      uint32_t phases = 0;  // bit s: of p_ready[s]; bit 2 + s: of q_ready[s]
+      bool ok = true;
+      uint32_t n = 0;
+      const uint32_t scores_idesc = p.scale < 0.f ? 1u << 13 : 0u;  // a negative scale negates the queries
+      for (uint32_t k = 0; ok; ++k) {
+        const Seg& seg = segs[k % kSegRing];
+        if (!wait_warp(seg_full + k % kSegRing, (k / kSegRing) & 1)) {
+          ok = false;
+          break;
+        }
+        int t0 = int(uniform(uint32_t(seg.t0))), t1 = int(uniform(uint32_t(seg.t1)));
+        const int all = int(uniform(uint32_t(seg.units))), parity = int(uniform(uint32_t(seg.parity)));
+        bool paired = uniform(seg.paired() ? 1u : 0u) != 0;
+        const bool end = t1 < 0;  // no further segment: one more turn for the pending tiles
+        if (end) t0 = 0, t1 = 1, paired = true;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_empty + k % kSegRing);
+        for (int t = t0; ok && t < t1; ++t, ++n) {
+          // paired: both streams on this tile; else the one whose turn it is
+          const uint32_t units = uint32_t(all - 8 * t < 8 ? all - 8 * t : 8);
+          const int turn = (parity + t - t0) & 1;
+          const uint32_t q = paired ? units | (t == t0 ? kFirst : 0u) | (t == t1 - 1 ? kLast : 0u)
+                                    : units | kAlone | (t - t0 < 2 ? kFirst : 0u) | (t1 - t <= 2 ? kLast : 0u);
+#pragma unroll 1
+          for (int s = paired ? 0 : turn; s <= (paired ? 1 : turn); ++s) {
+            const uint32_t was = s ? pend1 : pend0;
+            if (was) {  // O += P V of the stream's pending tile
+              const uint32_t use = s ? use1 : use0, slot = use % NS;
+              if (!wait_warp(p_ready + s, (phases >> s) & 1) || !wait_warp(full + slot, (use / NS) & 1)) {
                 ok = false;
                 break;
               }
-              ++nq[s];
+              phases ^= 1u << s;
+              tc_fence_after();
+              const uint32_t idesc = idesc_f16<F16>(kTileKeys, D) | (1u << 16);  // B (values) MN-major
+              const uint32_t steps = was & 15;
+              if (elect_one()) {
+                uint32_t at = tm + tmem_s(s), db = swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, L::HALF);
+                uint32_t more = was & kFirst ? 0u : 1u;
+#pragma unroll 1
+                for (uint32_t u = 0; u < steps; ++u, at += 8, db += 128, more = 1) umma_ts_step(tm + tmem_o(s), at, db, idesc, more);
+                umma_commit(empty + slot);
+                if (was & kAlone) umma_commit(empty + slot);
+                if (was & kLast) umma_commit(o_done + s);
+              }
+              __syncwarp();
+              if (s)
+                pend1 = 0;
+              else
+                pend0 = 0;
             }
-            if (!wait(full + slot, (use / NS) & 1)) {
+            if (end) continue;
+            // S = Q K^T of this tile
+            const uint32_t use = 2 * n, slot = use % NS;
+            if (q & kFirst) {
+              if (!wait_warp(q_ready + s, (phases >> (2 + s)) & 1)) {
+                ok = false;
+                break;
+              }
+              phases ^= 4u << s;
+            }
+            if (!wait_warp(full + slot, (use / NS) & 1)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t idesc = idesc_f16<F16>(kTileKeys, 16 * units);
-            const uint64_t da = swizzled_desc(base + L::OFF_Q + s * L::BYTES, 16);
-            const uint64_t db = swizzled_desc(base + L::OFF_RING + slot * L::BYTES, 16);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint64_t step = uint64_t((k & 3) * 2 + (k >> 2) * (L::HALF >> 4));
-              umma_bf16(tmem + tmem_s(s), da + step, db + step, idesc, k > 0 ? 1u : 0u);
+            const uint32_t idesc = idesc_f16<F16>(kTileKeys, int(16 * units)) | scores_idesc;
+            const uint32_t da = swizzled_desc_lo(base + L::OFF_Q + s * L::BYTES, 16);
+            const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16);
+            if (elect_one()) {
+              const uint32_t to = tm + tmem_s(s);
+              umma_ss_step<0, 0>(to, da, db, idesc, 0);
+              umma_ss_step<2, 2>(to, da, db, idesc, 1);
+              umma_ss_step<4, 4>(to, da, db, idesc, 1);
+              umma_ss_step<6, 6>(to, da, db, idesc, 1);
+              if (D == 128) {
+                constexpr int H = L::HALF >> 4;
+                umma_ss_step<H, H>(to, da, db, idesc, 1);
+                umma_ss_step<H + 2, H + 2>(to, da, db, idesc, 1);
+                umma_ss_step<H + 4, H + 4>(to, da, db, idesc, 1);
+                umma_ss_step<H + 6, H + 6>(to, da, db, idesc, 1);
+              }
+              umma_commit(s_ready + s);
+              umma_commit(empty + slot);
+              if (q & kAlone) umma_commit(empty + slot);
+              if (q & kLast) umma_commit(q_free + s);
             }
-            umma_commit(s_ready + s);
-            umma_commit(empty + slot);
-            if (!paired) umma_commit(empty + slot);
-            pend[s] = Pending{use + 1, units, paired ? 0 : 1, first ? 1 : 0, last ? 1 : 0};
-            has[s] = true;
+            __syncwarp();
+            if (s)
+              pend1 = q | kHas, use1 = use + 1;
+            else
+              pend0 = q | kHas, use0 = use + 1;
           }
         }
+        if (end) break;
       }
-      for (int s = 0; s < 2; ++s)
-        if (ok && has[s]) ok = values(s);
       if (!ok) {  // what is under way finishes before tensor memory is freed
-        umma_commit(o_done);
-        mbar_drain(o_done, 0);
-        mbar_drain(o_done, 1);
+        if (elect_one()) {
+          umma_commit(o_done);
+          mbar_drain(o_done, 0);
+          mbar_drain(o_done, 1);
+        }
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ softmax: stream s, one row per thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int s = warp >> 2, r = tid & 127;
     const uint32_t lane_sel = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + tmem_s(s) + lane_sel, to = tmem + tmem_o(s) + lane_sel;
-    // a negative scale is the positive one on negated queries; 0 is as good as 1e-30
-    const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);
-    const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+    const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);  // (0 is as good as 1e-30)
     uint32_t n = 0, ns = 0, no = 0;  // tiles of the CTA, tiles of this stream, its segments
     bool ok = true;
-    while (ok && walk.next(seg)) {
+    for (uint32_t k = 0; ok; ++k) {
+      const Seg& seg = segs[k % kSegRing];
+      if (!wait_warp(seg_full + k % kSegRing, (k / kSegRing) & 1)) {
+        ok = false;
+        break;
+      }
+      auto done = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_empty + k % kSegRing);
+      };
+      if (seg.t1 < 0) break;
       const bool paired = seg.paired();
-      const int count = seg.t1 - seg.t0;
       const uint32_t n0 = n;
-      n += uint32_t(count);
+      n += uint32_t(seg.t1 - seg.t0);
       int t = seg.t0;
       if (!paired && ((seg.parity ^ s) & 1)) ++t;
-      if (t >= seg.t1) continue;
+      if (t >= seg.t1) {
+        done();
+        continue;
+      }
       const int step = paired ? 1 : 2;
       const int srow0 = paired ? s * kTileKeys : 0;
       const int rows = seg.rows - srow0 < kTileKeys ? seg.rows - srow0 : kTileKeys;
       const bool idle = 32 * (warp & 3) >= rows;  // a warp without rows only keeps the barriers going
-
-      {  // queries: 16 bytes a thread, swizzled; rows that do not exist are zero
-        constexpr int C = D / 8;
-        uint8_t* const q_tile = smem + L::OFF_Q + s * L::BYTES;
-        const uint16_t* const q = static_cast<const uint16_t*>(p.q);
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-          const int piece = r + i * kGroupThreads, row = piece / C, ch = piece % C;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (row < rows) {
-            const int rr = seg.row0 + srow0 + row, tok = seg.tok0 + rr / G, head = seg.h * G + rr % G;
-            v = *reinterpret_cast<const uint4*>(q + tok * d.q_token_stride + head * D + ch * 8);
-            v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-          }
-          *reinterpret_cast<uint4*>(q_tile + (ch >> 3) * L::HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v;
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(q_ready + s);
-      }
 
       uint32_t seen = 0;  // own: the window tokens that this row sees
       if (seg.own && seg.t1 == (seg.units + 7) / 8) {
@@ -678,22 +751,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tmem_ld32(ts + 64, x + 64);
           tmem_ld32(ts + 96, x + 96);
           if (cached < kTileKeys) {
-            const int wu = (cached + 15) / 16 * 16;  // the window's unit (own; beyond the tile for a prefix)
+            const int wu = (cached + 15) & ~15;  // the window's unit (own; behind the tile for a prefix)
 #pragma unroll
-            for (int j = 0; j < 128; ++j) {
-              const bool see = j < cached || (seg.own && j >= wu && j < wu + 16 && (seen >> ((j - wu) & 15) & 1u));
-              x[j] = see ? x[j] : -INFINITY;
+            for (int q = 0; q < 4; ++q) {
+              const int n_seen = cached - 32 * q;
+              uint32_t see = n_seen >= 32 ? 0xffffffffu : n_seen <= 0 ? 0u : (1u << n_seen) - 1u;
+              if (seg.own && (wu >> 5) == q) see |= seen << (wu & 31);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[32 * q + j] = (see >> j) & 1u ? x[32 * q + j] : -INFINITY;
             }
           }
           float mx = x[0];
 #pragma unroll
           for (int j = 1; j < 128; ++j) mx = fmaxf(mx, x[j]);
           const float up = (mx - m) * c;
-          const bool move = mx > m && !(up <= kLag);  // (m = -inf: up is inf)
+          const bool move = mx > m && !(up <= kLag) && r < rows;  // (m = -inf: up is inf)
           if (__any_sync(0xffffffffu, move)) {
             const float f = move ? exp2_fast((m - mx) * c) : 1.f;
             if (!first) {
-#pragma unroll
+#pragma unroll 1
               for (int q = 0; q < D; q += 32) {
                 float o[32];
                 tmem_ld32(to + q, o);
@@ -705,17 +781,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (move) l *= f, m = mx;
           }
           const float mc = m == -INFINITY ? 0.f : m * c;
-          uint32_t pk[64];
           float sum = 0.f;
 #pragma unroll
-          for (int j = 0; j < 64; ++j) {
-            const float a = exp2_fast(fmaf(x[2 * j], c, -mc)), b = exp2_fast(fmaf(x[2 * j + 1], c, -mc));
-            sum += a + b;
-            pk[j] = pack2<F16>(a, b);
+          for (int q = 0; q < 4; ++q) {
+            float pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float a = exp2_fast(fmaf(x[32 * q + 2 * j], c, -mc)), b = exp2_fast(fmaf(x[32 * q + 2 * j + 1], c, -mc));
+              sum += a + b;
+              pk[j] = __uint_as_float(pack2<F16>(a, b));
+            }
+            tmem_st16(ts + 16 * q, pk);
           }
           l += sum;
-          tmem_st32_words(ts, pk);
-          tmem_st32_words(ts + 32, pk + 32);
         }
         first = false;
         if (cached < kTileKeys && (seg.own || (cached & 15))) {
@@ -753,7 +831,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const long long part = seg.part + (paired ? srow0 : s * seg.rows) + r;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         float* const out = w.o + part * D;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < D; q += 32) {
           float o[32];
           tmem_ld32(to + q, o);
@@ -766,6 +844,43 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (r < rows) w.lse[part] = l == 0.f ? -INFINITY : m * c + log2f(l);
       }
       tc_fence_before();
+      done();
+    }
+  }
+  else {
+    // ------------------------------------------------------------ queries of stream s, a segment ahead
+    // Rows behind the block's last keep what they hold: nothing reads their results.
+    constexpr int C = D / 8, STEP = 32 / C;  // a lane keeps its 16-byte column and takes every STEP-th row
+    const int s = warp - 10, ch = lane % C;
+    const int step_tok = STEP / G, step_g = STEP - step_tok * G;
+    uint32_t nq = 0;  // segments of this stream
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+      const Seg& seg = segs[k % kSegRing];
+      if (!wait_warp(seg_full + k % kSegRing, (k / kSegRing) & 1) || seg.t1 < 0) break;
+      const int srow0 = seg.paired() ? s * kTileKeys : 0;
+      const int rows = seg.rows - srow0 < kTileKeys ? seg.rows - srow0 : kTileKeys;
+      if (seg.paired() || seg.t1 - seg.t0 >= 2 || ((seg.parity ^ s) & 1) == 0) {
+        if (nq > 0) ok = wait_warp(q_free + s, (nq - 1) & 1);
+        if (!ok) break;
+        ++nq;
+        int row = lane / C, tok = (seg.row0 + srow0 + row) / G, g = seg.row0 + srow0 + row - tok * G;
+        const uint16_t* const q = static_cast<const uint16_t*>(p.q) + seg.tok0 * d.q_token_stride + (long long)seg.h * G * D + ch * 8;
+        const uint32_t q_tile = base + L::OFF_Q + s * L::BYTES + (ch >> 3) * L::HALF;
+#pragma unroll 2
+        for (; row < rows; row += STEP) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(q_tile + row * 128 + (((ch & 7) ^ (row & 7)) << 4)),
+                       "l"(q + tok * d.q_token_stride + g * D)
+                       : "memory");
+          g += step_g, tok += step_tok;
+          if (g >= G) g -= G, ++tok;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        mbar_arrive(q_ready + s);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(seg_empty + k % kSegRing);
     }
   }
   tc_fence_before();
@@ -779,7 +894,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // ---------------------------------------------------------------- join
 // One warp per row: the segments of its sequence and of its prefix, by their log-sum-exps.
 template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnParams p, const AttnWs w) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWs w) {
   constexpr int N = D / 32;
   grid_launch_dependents();
   grid_wait();
@@ -955,12 +1070,11 @@ cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) {
   map(&maps.v16, p.v_cache, 5, cd, cs, b16);
   map(&maps.kb, p.k_cache, 5, cd, cs, bb);
   map(&maps.vb, p.v_cache, 5, cd, cs, bb);
-  // windows: (D, kv head, token, sequence); rows behind the K-th token read as zeros
-  const cuuint64_t wd[4] = {cuuint64_t(d.D), cuuint64_t(d.Hkv), cuuint64_t(d.K), cuuint64_t(d.B)};
-  const cuuint64_t wst[3] = {2ull * d.D, 2ull * d.win_token_stride, 2ull * d.K * d.win_token_stride};
-  const cuuint32_t bw[4] = {64, 1, 16, 1};
-  map(&maps.kw, p.k_win, 4, wd, wst, bw);
-  map(&maps.vw, p.v_win, 4, wd, wst, bw);
+  // rows behind a window's K-th token read as zeros
+  const cuuint64_t wd[5] = {cuuint64_t(d.D), cuuint64_t(d.K), cuuint64_t(d.Hkv), cuuint64_t(d.B), 1};
+  const cuuint64_t wst[4] = {2ull * d.win_token_stride, 2ull * d.D, 2ull * d.K * d.win_token_stride, 2ull * d.K * d.win_token_stride};
+  map(&maps.kw, p.k_win, 5, wd, wst, b16);
+  map(&maps.vw, p.v_win, 5, wd, wst, b16);
   if (!ok) return cudaErrorInvalidValue;
   const AttnWs w = carve_attn(p.ws, d, nullptr);
   if (d.D == 128) return d.dtype ? launch<128, true>(p, w, box, maps, stream) : launch<128, false>(p, w, box, maps, stream);
