@@ -66,15 +66,16 @@ struct RunRec {     // consecutive sequences on one prefix
 struct PlanHead {
   long long tiles, prefix_tiles;  // in all; those of the runs come first
   long long own_row;              // first row of the sequences' partial results
-  int32_t runs, pad;
+  int32_t runs;
+  int32_t split;                  // prefixes and sequences are dealt out apart from each other
 };
 struct StartRec {
-  int32_t own, idx;  // where a CTA's stretch begins: run or sequence idx
+  int32_t own, idx;  // where a stretch begins: run or sequence idx
 };
 
 struct AttnWs {
   PlanHead* head;
-  StartRec* start;  // [kCtas]
+  StartRec* start;  // [2][kCtas]
   SeqRec* seq;      // [B]
   RunRec* run;      // [B]
   float* lse;       // [rows] log2 units
@@ -97,10 +98,10 @@ __host__ __device__ inline AttnWs carve_attn(void* base, const gdn_kv_dims& d, s
   size_t o = 0;
   // a segment of CTA c and item i starts at row 256 c + (rows of the items before i); every row of
   // the batch has at most two rows here from its prefix and two from its own sequence
-  const size_t rows = size_t(kBlockRows) * kCtas + 4 * size_t(d.B) * d.K * d.Hq;
+  const size_t rows = 2 * size_t(kBlockRows) * kCtas + 4 * size_t(d.B) * d.K * d.Hq;
   AttnWs w;
   w.head = reinterpret_cast<PlanHead*>(p + o), o += 256;
-  w.start = reinterpret_cast<StartRec*>(p + o), o += up256(sizeof(StartRec) * kCtas);
+  w.start = reinterpret_cast<StartRec*>(p + o), o += up256(2 * sizeof(StartRec) * kCtas);
   w.seq = reinterpret_cast<SeqRec*>(p + o), o += up256(sizeof(SeqRec) * size_t(d.B));
   w.run = reinterpret_cast<RunRec*>(p + o), o += up256(sizeof(RunRec) * size_t(d.B));
   w.lse = reinterpret_cast<float*>(p + o), o += up256(4 * rows);
@@ -109,7 +110,14 @@ __host__ __device__ inline AttnWs carve_attn(void* base, const gdn_kv_dims& d, s
   return w;
 }
 
-// CTA c's stretch is tiles [first_tile(c), first_tile(c + 1)); the CTA of tile x.
+// A deal gives CTA c tiles [first_tile(c), first_tile(c + 1)) of `tiles`; the CTA of tile x.
+//
+// With at least kSplitTiles tiles, the prefixes' and the sequences' are two deals, and every CTA
+// gets its share of both - even CTAs in this order, odd ones in the other: a prefix tile costs
+// tensor-core time and a sequence's tile memory time, so a CTA that had one kind alone would end
+// early or late, and at any time half the CTAs wait for memory while half compute.  With fewer,
+// one deal over all tiles puts them on as many CTAs as there are.
+constexpr long long kSplitTiles = 4 * kCtas;
 __device__ __forceinline__ long long first_tile(long long c, long long tiles) { return c * tiles / kCtas; }
 __device__ __forceinline__ int cta_of(long long x, long long tiles) { return int(((x + 1) * kCtas - 1) / tiles); }
 
@@ -227,15 +235,18 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     if (b < d.B) w.seq[b].off = off;
     tiles += total;
   }
+  const bool split = tiles >= kSplitTiles;
   if (tid == 0) {
     w.head->tiles = tiles;
     w.head->prefix_tiles = prefix_tiles;
-    w.head->own_row = row;
+    w.head->own_row = row + (split ? kBlockRows * kCtas : 0);
     w.head->runs = int(n_runs);
+    w.head->split = split;
   }
   __syncthreads();
-  if (tid < kCtas) {  // where each stretch begins: the last record that starts at or before it and has tiles
-    const long long x = first_tile(tid, tiles);
+  if (tid < 2 * kCtas) {  // where each stretch begins: the last record that starts at or before it
+    const int own = tid / kCtas, c = tid % kCtas;
+    const long long x = !split ? first_tile(c, tiles) : own ? prefix_tiles + first_tile(c, tiles - prefix_tiles) : first_tile(c, prefix_tiles);
     StartRec s{0, 0};
     if (x < tiles) {
       s.own = x >= prefix_tiles;
@@ -270,16 +281,28 @@ struct SegWalk {
   const AttnParams& p;
   const AttnWs& w;
   long long x, end;
-  int own, idx, cta;
+  int own, idx, cta, deal;
   long long own_row;
   int runs;
   __device__ __forceinline__ SegWalk(const AttnParams& p_, const AttnWs& w_, int cta_) : p(p_), w(w_), cta(cta_) {
+    own_row = w.head->own_row, runs = w.head->runs;
+    deal = 0;
+    begin();
+  }
+  __device__ __forceinline__ void begin() {  // the CTA's stretch of its first or second deal
     const PlanHead h = *w.head;
-    x = first_tile(cta, h.tiles), end = first_tile(cta + 1, h.tiles);
-    own = w.start[cta].own, idx = w.start[cta].idx;
-    own_row = h.own_row, runs = h.runs;
+    if (h.split) {
+      const int which = deal ^ (cta & 1);
+      const long long o = which ? h.prefix_tiles : 0, n = which ? h.tiles - h.prefix_tiles : h.prefix_tiles;
+      x = o + first_tile(cta, n), end = o + first_tile(cta + 1, n);
+      own = w.start[which * kCtas + cta].own, idx = w.start[which * kCtas + cta].idx;
+    } else {
+      x = deal ? 0 : first_tile(cta, h.tiles), end = deal ? 0 : first_tile(cta + 1, h.tiles);
+      own = w.start[cta].own, idx = w.start[cta].idx;
+    }
   }
   __device__ __forceinline__ bool next(Seg& s) {
+    if (x >= end && deal == 0) deal = 1, begin();
     if (x >= end) return false;
     const gdn_kv_dims& d = p.d;
     const int KG = d.K * (d.Hq / d.Hkv);
@@ -373,11 +396,13 @@ __device__ __forceinline__ void umma_ss_step(uint32_t d_tmem, uint32_t a_lo, uin
       "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi), "n"(A_STEP), "n"(B_STEP)
       : "memory");
 }
+template <int STEP>  // of 16 keys: 8 columns of P, 2048 bytes of values
 __device__ __forceinline__ void umma_ts_step(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
+      "{\n\t.reg .pred p;\n\t.reg .b32 a, b;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "add.u32 a, %1, %6;\n\tadd.u32 b, %2, %7;\n\tmov.b64 db, {b, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi), "n"(8 * STEP), "n"(128 * STEP)
       : "memory");
 }
 
@@ -419,8 +444,8 @@ constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t tmem_s(int s) { return 128u * uint32_t(s); }
 __device__ __forceinline__ uint32_t tmem_o(int s) { return 256u + 128u * uint32_t(s); }
 
-// One look at a barrier's phase, sleeping for up to about a microsecond.
-__device__ __forceinline__ bool mbar_look(uint64_t* bar, uint32_t parity) {
+// A look at a barrier's phase that sleeps for up to about a microsecond, and one that does not.
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -428,6 +453,17 @@ __device__ __forceinline__ bool mbar_look(uint64_t* bar, uint32_t parity) {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_addr(bar)), "r"(parity), "n"(1000)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_look(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -478,21 +514,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   grid_launch_dependents();
   grid_wait();
 
-  // Bounded wait of one thread; once one has given up, all others of the CTA do too.  (Short: the
-  // tile kernel's loops have to stay in the instruction cache.)
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    for (uint32_t i = 0; !mbar_look(bar, parity); ++i) {
-      if (gave_up) return false;
-      if (i > kMaxLooks) {
-        gave_up = 1;
-        atomicOr(p.err, kDevErrTimeout);
+  // Bounded wait of a whole warp, which goes on or gives up together; once one warp has given up,
+  // all of the CTA's do.  (Every branch is on a vote: the tensor-core warp's operands stay in
+  // uniform registers only as long as the compiler can see that its lanes stay together.)
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
+    for (uint32_t i = 0; !__all_sync(0xffffffffu, mbar_sleep(bar, parity)); ++i) {
+      if (__any_sync(0xffffffffu, gave_up || i > kMaxLooks)) {
+        if (i > kMaxLooks) {
+          gave_up = 1;
+          atomicOr(p.err, kDevErrTimeout);
+        }
         return false;
       }
     }
     return true;
   };
-  // The same for a whole warp, which goes on or gives up together.
-  auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
 
   if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 8) {
@@ -564,14 +600,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     {
       const uint32_t tm = uniform(tmem);
       // The whole warp walks the schedule and one elected lane issues: operands stay warp-uniform.
-      // What a stream's pending tile needs for O += P V, as fields of one word: units (4 bits), then
-      // flags - this stream alone uses the tile, first and last tile of the stream's segment.
-      constexpr uint32_t kAlone = 16, kFirst = 32, kLast = 64, kHas = 128;
-      uint32_t pend0 = 0, pend1 = 0, use0 = 0, use1 = 0;
+      // What a stream's pending tile needs for O += P V, as fields of one word: units (4 bits), flags -
+      // this stream alone uses the tile, first and last tile of the stream's segment, there is one, its
+      // values have landed -, ring slot (4 bits), phase.
+      constexpr uint32_t kAlone = 16, kFirst = 32, kLast = 64, kHas = 128, kLanded = 256, kSlot = 512, kPhase = 8192;
+      uint32_t pend0 = 0, pend1 = 0;
       uint32_t phases = 0;  // bit s: of p_ready[s]; bit 2 + s: of q_ready[s]
-      bool ok = true;
-      uint32_t n = 0;
+      uint32_t slot = 0, phase = 0;  // of the tile's keys; its values are in the slot behind
+      bool ok = true, landed = false;  // (landed: the tile's keys were there when last looked at)
       const uint32_t scores_idesc = p.scale < 0.f ? 1u << 13 : 0u;  // a negative scale negates the queries
+      const uint32_t values_idesc = idesc_f16<F16>(kTileKeys, D) | (1u << 16);  // B (values) MN-major
       for (uint32_t k = 0; ok; ++k) {
         const Seg& seg = segs[k % kSegRing];
         if (!wait_warp(seg_full + k % kSegRing, (k / kSegRing) & 1)) {
@@ -585,32 +623,43 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (end) t0 = 0, t1 = 1, paired = true;
         __syncwarp();
         if (lane == 0) mbar_arrive(seg_empty + k % kSegRing);
-        for (int t = t0; ok && t < t1; ++t, ++n) {
+        for (int t = t0; ok && t < t1; ++t) {
           // paired: both streams on this tile; else the one whose turn it is
           const uint32_t units = uint32_t(all - 8 * t < 8 ? all - 8 * t : 8);
           const int turn = (parity + t - t0) & 1;
-          const uint32_t q = paired ? units | (t == t0 ? kFirst : 0u) | (t == t1 - 1 ? kLast : 0u)
-                                    : units | kAlone | (t - t0 < 2 ? kFirst : 0u) | (t1 - t <= 2 ? kLast : 0u);
+          uint32_t q = kHas | (paired ? units | (t == t0 ? kFirst : 0u) | (t == t1 - 1 ? kLast : 0u)
+                                      : units | kAlone | (t - t0 < 2 ? kFirst : 0u) | (t1 - t <= 2 ? kLast : 0u));
+          const uint32_t vslot = slot + 1 < NS ? slot + 1 : 0, vphase = slot + 1 < NS ? phase : phase ^ 1;
+          q |= vslot * kSlot | vphase * kPhase;
 #pragma unroll 1
           for (int s = paired ? 0 : turn; s <= (paired ? 1 : turn); ++s) {
             const uint32_t was = s ? pend1 : pend0;
             if (was) {  // O += P V of the stream's pending tile
-              const uint32_t use = s ? use1 : use0, slot = use % NS;
-              if (!wait_warp(p_ready + s, (phases >> s) & 1) || !wait_warp(full + slot, (use / NS) & 1)) {
+              const uint32_t at = (was / kSlot) & 15;
+              if ((!(was & kLanded) && !wait_warp(full + at, (was / kPhase) & 1)) || !wait_warp(p_ready + s, (phases >> s) & 1)) {
                 ok = false;
                 break;
               }
               phases ^= 1u << s;
               tc_fence_after();
-              const uint32_t idesc = idesc_f16<F16>(kTileKeys, D) | (1u << 16);  // B (values) MN-major
-              const uint32_t steps = was & 15;
               if (elect_one()) {
-                uint32_t at = tm + tmem_s(s), db = swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, L::HALF);
-                uint32_t more = was & kFirst ? 0u : 1u;
+                const uint32_t tp = tm + tmem_s(s), to = tm + tmem_o(s);
+                const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + at * L::BYTES, L::HALF);
+                umma_ts_step<0>(to, tp, db, values_idesc, was & kFirst ? 0u : 1u);
+                if ((was & 15) == 8) {
+                  umma_ts_step<1>(to, tp, db, values_idesc, 1);
+                  umma_ts_step<2>(to, tp, db, values_idesc, 1);
+                  umma_ts_step<3>(to, tp, db, values_idesc, 1);
+                  umma_ts_step<4>(to, tp, db, values_idesc, 1);
+                  umma_ts_step<5>(to, tp, db, values_idesc, 1);
+                  umma_ts_step<6>(to, tp, db, values_idesc, 1);
+                  umma_ts_step<7>(to, tp, db, values_idesc, 1);
+                } else {
 #pragma unroll 1
-                for (uint32_t u = 0; u < steps; ++u, at += 8, db += 128, more = 1) umma_ts_step(tm + tmem_o(s), at, db, idesc, more);
-                umma_commit(empty + slot);
-                if (was & kAlone) umma_commit(empty + slot);
+                  for (uint32_t u = 1; u < (was & 15); ++u) umma_ts_step<0>(to, tp + 8 * u, db + 128 * u, values_idesc, 1);
+                }
+                umma_commit(empty + at);
+                if (was & kAlone) umma_commit(empty + at);
                 if (was & kLast) umma_commit(o_done + s);
               }
               __syncwarp();
@@ -621,7 +670,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             if (end) continue;
             // S = Q K^T of this tile
-            const uint32_t use = 2 * n, slot = use % NS;
             if (q & kFirst) {
               if (!wait_warp(q_ready + s, (phases >> (2 + s)) & 1)) {
                 ok = false;
@@ -629,15 +677,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               }
               phases ^= 4u << s;
             }
-            if (!wait_warp(full + slot, (use / NS) & 1)) {
+            if (!landed && !wait_warp(full + slot, phase)) {
               ok = false;
               break;
             }
+            landed = paired && s == 0;
             tc_fence_after();
-            const uint32_t idesc = idesc_f16<F16>(kTileKeys, int(16 * units)) | scores_idesc;
-            const uint32_t da = swizzled_desc_lo(base + L::OFF_Q + s * L::BYTES, 16);
-            const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16);
             if (elect_one()) {
+              const uint32_t idesc = idesc_f16<F16>(kTileKeys, int(16 * units)) | scores_idesc;
+              const uint32_t da = swizzled_desc_lo(base + L::OFF_Q + s * L::BYTES, 16);
+              const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16);
               const uint32_t to = tm + tmem_s(s);
               umma_ss_step<0, 0>(to, da, db, idesc, 0);
               umma_ss_step<2, 2>(to, da, db, idesc, 1);
@@ -656,11 +705,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               if (q & kLast) umma_commit(q_free + s);
             }
             __syncwarp();
+            // While the tensor core is at it, a look whether the values have landed and, once the tile's
+            // last scores are issued, the next keys: waits that are not needed later, when it would idle.
+            const uint32_t now = q | (__all_sync(0xffffffffu, mbar_look(full + vslot, vphase)) ? kLanded : 0u);
             if (s)
-              pend1 = q | kHas, use1 = use + 1;
+              pend1 = now;
             else
-              pend0 = q | kHas, use0 = use + 1;
+              pend0 = now;
           }
+          slot += 2, phase ^= slot >= NS ? 1u : 0u, slot -= slot >= NS ? NS : 0;
+          landed = !end && ok && __all_sync(0xffffffffu, mbar_look(full + slot, phase));
         }
         if (end) break;
       }
@@ -905,7 +959,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
   const int hq = int(row % d.Hq), h = hq / G, g = hq - h * G;
   const int tok = int(row / d.Hq), b = tok / d.K, t = tok - b * d.K;
   const SeqRec q = w.seq[b];
-  const long long tiles = w.head->tiles;
   uint16_t* const out = static_cast<uint16_t*>(p.out) + row * D;
   float acc[N];
 #pragma unroll
@@ -914,30 +967,34 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
   if (t < q.win) {
     // the row's item in each of the two parts: tiles [at, at + n), first CTA, and rows
     struct Part {
-      long long at, base;
+      long long at, base, deal, tiles;  // (the deal's first tile and size)
       int n, c0, parts, width, lr;
       bool paired;
     };
-    auto part_of = [&](long long off, int n, long long row0, long long rows, int r) {
+    const bool split = w.head->split;
+    const long long all = w.head->tiles, shared = w.head->prefix_tiles;
+    auto part_of = [&](long long off, int n, long long row0, long long rows, int r, bool is_own) {
       Part x{};
       if (n == 0) return x;
+      x.deal = split && is_own ? shared : 0;
+      x.tiles = !split ? all : is_own ? all - shared : shared;
       const int blocks = int((rows + kBlockRows - 1) / kBlockRows), rb = r / kBlockRows;
       const int in = int(rows - (long long)rb * kBlockRows < kBlockRows ? rows - (long long)rb * kBlockRows : kBlockRows);
       x.at = off + ((long long)h * blocks + rb) * n;
       x.n = n;
-      x.c0 = cta_of(x.at, tiles);
+      x.c0 = cta_of(x.at - x.deal, x.tiles);
       x.paired = in > kTileKeys;
-      x.parts = (cta_of(x.at + n - 1, tiles) - x.c0 + 1) * (x.paired ? 1 : 2);
+      x.parts = (cta_of(x.at - x.deal + n - 1, x.tiles) - x.c0 + 1) * (x.paired ? 1 : 2);
       x.width = in;
       x.lr = r - rb * kBlockRows;
       x.base = row0 + h * rows_width(rows) + (long long)rb * kBlockRows;
       return x;
     };
-    const Part own = part_of(q.off, q.tiles, w.head->own_row + (long long)b * d.Hkv * rows_width(KG), KG, t * G + g);
+    const Part own = part_of(q.off, q.tiles, w.head->own_row + (long long)b * d.Hkv * rows_width(KG), KG, t * G + g, true);
     Part pre{};
     if (q.run >= 0) {
       const RunRec r = w.run[q.run];
-      pre = part_of(r.off, r.tiles, r.row, (long long)r.n * KG, ((b - r.b0) * d.K + t) * G + g);
+      pre = part_of(r.off, r.tiles, r.row, (long long)r.n * KG, ((b - r.b0) * d.K + t) * G + g, false);
     }
     const int count = own.parts + pre.parts;
     for (int i0 = 0; i0 < count; i0 += 32) {
@@ -947,7 +1004,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid
         const Part& x = i < own.parts ? own : pre;
         const int j = i < own.parts ? i : i - own.parts;
         const int c = x.c0 + (x.paired ? j : j >> 1), s = x.paired ? 0 : j & 1;
-        long long lo = first_tile(c, tiles), hi = first_tile(c + 1, tiles);
+        long long lo = x.deal + first_tile(c, x.tiles), hi = x.deal + first_tile(c + 1, x.tiles);
         if (lo < x.at) lo = x.at;
         if (hi > x.at + x.n) hi = x.at + x.n;
         if (hi > lo && (x.paired || hi - lo >= 2 || int(lo & 1) == s))  // (a single tile belongs to one stream)
