@@ -14,8 +14,8 @@
 // Kernels: plan (one CTA: lengths -> items and stretches), tiles (persistent, tcgen05), join.
 //
 // The tile kernel: a producer warp brings keys and values by TMA (128-byte swizzle) into a ring
-// of tiles; one thread issues S = Q K^T and O += P V (tcgen05, M = 128, accumulators in tensor
-// memory, P read from tensor memory); a warp per stream fetches the next segment's queries; two
+// of tiles; a warp per stream issues S = Q K^T and O += P V (tcgen05, M = 128, accumulators in
+// tensor memory, P read from tensor memory); one warp fetches the next segment's queries; two
 // groups of four warps, one per stream, turn S into P, a row per thread.  A block of more than 128 rows uses the two streams for its two halves on the
 // same keys; a smaller one gives them alternate tiles of the same rows.  While one stream's
 // softmax runs, the tensor core works for the other.
@@ -34,7 +34,7 @@ constexpr int kTileKeys = 128;
 constexpr int kBlockRows = 256;  // rows of an item
 constexpr int kPlanThreads = 1024;
 constexpr int kGroupThreads = 128;  // a softmax group: one thread per row of a stream
-constexpr int kTileThreads = 3 * kGroupThreads;  // two softmax groups; producer, tensor-core and two query warps
+constexpr int kTileThreads = 3 * kGroupThreads;  // two softmax groups; producer, two tensor-core warps, query warp
 // Registers: 168 a thread at launch (64512 in all), then 224 for the softmax threads, which hold a
 // row of 128 scores, and 56 for the rest: 256 x 224 + 128 x 56 = 64512.
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
@@ -444,7 +444,7 @@ constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t tmem_s(int s) { return 128u * uint32_t(s); }
 __device__ __forceinline__ uint32_t tmem_o(int s) { return 256u + 128u * uint32_t(s); }
 
-// A look at a barrier's phase that sleeps for up to about a microsecond, and one that does not.
+// A look at a barrier's phase that sleeps for up to about a microsecond.
 __device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -456,18 +456,6 @@ __device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool mbar_look(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 template <int D, bool F16>
 __global__ void __launch_bounds__(kTileThreads, 1)
     attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWs w, const int box, const __grid_constant__ TileMaps maps) {
@@ -490,7 +478,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full + i, 1);
-      mbar_init(empty + i, 2);  // one arrival per stream; a tile that one stream alone uses arrives twice
+      mbar_init(empty + i, 2);  // one arrival per stream
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(q_ready + s, 32);
@@ -595,136 +583,120 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (ok) ok = wait_warp(empty + use % NS, (use / NS) & 1);
       if (!ok) mbar_drain(full + use % NS, (use / NS) & 1);
     }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ tensor core
-    {
-      const uint32_t tm = uniform(tmem);
-      // The whole warp walks the schedule and one elected lane issues: operands stay warp-uniform.
-      // What a stream's pending tile needs for O += P V, as fields of one word: units (4 bits), flags -
-      // this stream alone uses the tile, first and last tile of the stream's segment, there is one, its
-      // values have landed -, ring slot (4 bits), phase.
-      constexpr uint32_t kAlone = 16, kFirst = 32, kLast = 64, kHas = 128, kLanded = 256, kSlot = 512, kPhase = 8192;
-      uint32_t pend0 = 0, pend1 = 0;
-      uint32_t phases = 0;  // bit s: of p_ready[s]; bit 2 + s: of q_ready[s]
-      uint32_t slot = 0, phase = 0;  // of the tile's keys; its values are in the slot behind
-      bool ok = true, landed = false;  // (landed: the tile's keys were there when last looked at)
-      const uint32_t scores_idesc = p.scale < 0.f ? 1u << 13 : 0u;  // a negative scale negates the queries
-      const uint32_t values_idesc = idesc_f16<F16>(kTileKeys, D) | (1u << 16);  // B (values) MN-major
-      for (uint32_t k = 0; ok; ++k) {
-        const Seg& seg = segs[k % kSegRing];
-        if (!wait_warp(seg_full + k % kSegRing, (k / kSegRing) & 1)) {
+  } else if (warp == 9 || warp == 10) {
+    // ------------------------------------------------------------ tensor core, stream s
+    // (A warp each: a product takes the tensor core 64 cycles and this warp nearly as long to issue
+    // beside the softmax warps; with one for both streams the tensor core waited for it.)  The whole
+    // warp walks the schedule and one elected lane issues: operands stay warp-uniform.
+    const int s = warp - 9;
+    const uint32_t ts = uniform(tmem) + tmem_s(s), to = uniform(tmem) + tmem_o(s);
+    const uint32_t q_desc = swizzled_desc_lo(base + L::OFF_Q + s * L::BYTES, 16);
+    const uint32_t values_idesc = idesc_f16<F16>(kTileKeys, D) | (1u << 16);  // B (values) MN-major
+    const uint32_t scores_idesc = p.scale < 0.f ? 1u << 13 : 0u;              // a negative scale negates the queries
+    //
+    // Each of the two warps sees every tile land, in order, and releases each of its slots once - the
+    // stream that does not use a tile by a plain arrival.  A wait on a phase's parity is sound only
+    // within one phase of the barrier, and copies do not land in the order they were asked for:
+    // this way no slot can be filled again, or be a use behind, where either stream waits for it.
+    uint32_t slot = 0, phase = 0;  // of a tile's keys; its values are in the slot behind
+    uint32_t np = 0, nq = 0;       // P tiles, segments of this stream
+    bool ok = true;
+    // The tile whose O += P V is still to be issued.
+    bool pending = false, p_first = false, p_last = false;
+    uint32_t p_units = 0, p_slot = 0, p_phase = 0;
+    auto values = [&]() -> bool {
+      pending = false;
+      if (!wait_warp(full + p_slot, p_phase) || !wait_warp(p_ready + s, np & 1)) return false;
+      ++np;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + p_slot * L::BYTES, L::HALF);
+        umma_ts_step<0>(to, ts, db, values_idesc, p_first ? 0u : 1u);
+        if (p_units == 8) {
+          umma_ts_step<1>(to, ts, db, values_idesc, 1);
+          umma_ts_step<2>(to, ts, db, values_idesc, 1);
+          umma_ts_step<3>(to, ts, db, values_idesc, 1);
+          umma_ts_step<4>(to, ts, db, values_idesc, 1);
+          umma_ts_step<5>(to, ts, db, values_idesc, 1);
+          umma_ts_step<6>(to, ts, db, values_idesc, 1);
+          umma_ts_step<7>(to, ts, db, values_idesc, 1);
+        } else {
+#pragma unroll 1
+          for (uint32_t u = 1; u < p_units; ++u) umma_ts_step<0>(to, ts + 8 * u, db + 128 * u, values_idesc, 1);
+        }
+        umma_commit(empty + p_slot);
+        if (p_last) umma_commit(o_done + s);
+      }
+      __syncwarp();
+      return true;
+    };
+    for (uint32_t k = 0; ok; ++k) {
+      const Seg& seg = segs[k % kSegRing];
+      if (!wait_warp(seg_full + k % kSegRing, (k / kSegRing) & 1)) {
+        ok = false;
+        break;
+      }
+      const int t0 = int(uniform(uint32_t(seg.t0))), t1 = int(uniform(uint32_t(seg.t1)));
+      const int all = int(uniform(uint32_t(seg.units))), parity = int(uniform(uint32_t(seg.parity)));
+      const bool paired = uniform(seg.paired() ? 1u : 0u) != 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(seg_empty + k % kSegRing);
+      const bool end = t1 < 0;
+      bool first = true;
+      for (int t = t0; ok && (end || t < t1); ++t) {
+        const uint32_t vslot = slot + 1 < NS ? slot + 1 : 0, vphase = slot + 1 < NS ? phase : phase ^ 1;
+        if (!end && !paired && ((parity + t - t0) & 1) != s) {  // the other stream's tile
+          ok = wait_warp(full + slot, phase);
+          if (ok && lane == 0) mbar_arrive(empty + slot);
+          if (ok && pending) ok = values();
+          if (ok) ok = wait_warp(full + vslot, vphase);
+          if (ok && lane == 0) mbar_arrive(empty + vslot);
+          slot += 2, phase ^= slot >= NS ? 1u : 0u, slot -= slot >= NS ? NS : 0;
+          continue;
+        }
+        if (pending && !values()) ok = false;
+        if (end || !ok) break;
+        // S = Q K^T of this tile
+        if (first) {
+          if (!wait_warp(q_ready + s, nq & 1)) ok = false;
+          ++nq;
+        }
+        if (!ok || !wait_warp(full + slot, phase)) {
           ok = false;
           break;
         }
-        int t0 = int(uniform(uint32_t(seg.t0))), t1 = int(uniform(uint32_t(seg.t1)));
-        const int all = int(uniform(uint32_t(seg.units))), parity = int(uniform(uint32_t(seg.parity)));
-        bool paired = uniform(seg.paired() ? 1u : 0u) != 0;
-        const bool end = t1 < 0;  // no further segment: one more turn for the pending tiles
-        if (end) t0 = 0, t1 = 1, paired = true;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(seg_empty + k % kSegRing);
-        for (int t = t0; ok && t < t1; ++t) {
-          // paired: both streams on this tile; else the one whose turn it is
-          const uint32_t units = uint32_t(all - 8 * t < 8 ? all - 8 * t : 8);
-          const int turn = (parity + t - t0) & 1;
-          uint32_t q = kHas | (paired ? units | (t == t0 ? kFirst : 0u) | (t == t1 - 1 ? kLast : 0u)
-                                      : units | kAlone | (t - t0 < 2 ? kFirst : 0u) | (t1 - t <= 2 ? kLast : 0u));
-          const uint32_t vslot = slot + 1 < NS ? slot + 1 : 0, vphase = slot + 1 < NS ? phase : phase ^ 1;
-          q |= vslot * kSlot | vphase * kPhase;
-#pragma unroll 1
-          for (int s = paired ? 0 : turn; s <= (paired ? 1 : turn); ++s) {
-            const uint32_t was = s ? pend1 : pend0;
-            if (was) {  // O += P V of the stream's pending tile
-              const uint32_t at = (was / kSlot) & 15;
-              if ((!(was & kLanded) && !wait_warp(full + at, (was / kPhase) & 1)) || !wait_warp(p_ready + s, (phases >> s) & 1)) {
-                ok = false;
-                break;
-              }
-              phases ^= 1u << s;
-              tc_fence_after();
-              if (elect_one()) {
-                const uint32_t tp = tm + tmem_s(s), to = tm + tmem_o(s);
-                const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + at * L::BYTES, L::HALF);
-                umma_ts_step<0>(to, tp, db, values_idesc, was & kFirst ? 0u : 1u);
-                if ((was & 15) == 8) {
-                  umma_ts_step<1>(to, tp, db, values_idesc, 1);
-                  umma_ts_step<2>(to, tp, db, values_idesc, 1);
-                  umma_ts_step<3>(to, tp, db, values_idesc, 1);
-                  umma_ts_step<4>(to, tp, db, values_idesc, 1);
-                  umma_ts_step<5>(to, tp, db, values_idesc, 1);
-                  umma_ts_step<6>(to, tp, db, values_idesc, 1);
-                  umma_ts_step<7>(to, tp, db, values_idesc, 1);
-                } else {
-#pragma unroll 1
-                  for (uint32_t u = 1; u < (was & 15); ++u) umma_ts_step<0>(to, tp + 8 * u, db + 128 * u, values_idesc, 1);
-                }
-                umma_commit(empty + at);
-                if (was & kAlone) umma_commit(empty + at);
-                if (was & kLast) umma_commit(o_done + s);
-              }
-              __syncwarp();
-              if (s)
-                pend1 = 0;
-              else
-                pend0 = 0;
-            }
-            if (end) continue;
-            // S = Q K^T of this tile
-            if (q & kFirst) {
-              if (!wait_warp(q_ready + s, (phases >> (2 + s)) & 1)) {
-                ok = false;
-                break;
-              }
-              phases ^= 4u << s;
-            }
-            if (!landed && !wait_warp(full + slot, phase)) {
-              ok = false;
-              break;
-            }
-            landed = paired && s == 0;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint32_t idesc = idesc_f16<F16>(kTileKeys, int(16 * units)) | scores_idesc;
-              const uint32_t da = swizzled_desc_lo(base + L::OFF_Q + s * L::BYTES, 16);
-              const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16);
-              const uint32_t to = tm + tmem_s(s);
-              umma_ss_step<0, 0>(to, da, db, idesc, 0);
-              umma_ss_step<2, 2>(to, da, db, idesc, 1);
-              umma_ss_step<4, 4>(to, da, db, idesc, 1);
-              umma_ss_step<6, 6>(to, da, db, idesc, 1);
-              if (D == 128) {
-                constexpr int H = L::HALF >> 4;
-                umma_ss_step<H, H>(to, da, db, idesc, 1);
-                umma_ss_step<H + 2, H + 2>(to, da, db, idesc, 1);
-                umma_ss_step<H + 4, H + 4>(to, da, db, idesc, 1);
-                umma_ss_step<H + 6, H + 6>(to, da, db, idesc, 1);
-              }
-              umma_commit(s_ready + s);
-              umma_commit(empty + slot);
-              if (q & kAlone) umma_commit(empty + slot);
-              if (q & kLast) umma_commit(q_free + s);
-            }
-            __syncwarp();
-            // While the tensor core is at it, a look whether the values have landed and, once the tile's
-            // last scores are issued, the next keys: waits that are not needed later, when it would idle.
-            const uint32_t now = q | (__all_sync(0xffffffffu, mbar_look(full + vslot, vphase)) ? kLanded : 0u);
-            if (s)
-              pend1 = now;
-            else
-              pend0 = now;
-          }
-          slot += 2, phase ^= slot >= NS ? 1u : 0u, slot -= slot >= NS ? NS : 0;
-          landed = !end && ok && __all_sync(0xffffffffu, mbar_look(full + slot, phase));
-        }
-        if (end) break;
-      }
-      if (!ok) {  // what is under way finishes before tensor memory is freed
+        tc_fence_after();
+        const uint32_t units = uint32_t(all - 8 * t < 8 ? all - 8 * t : 8);
+        const bool last = paired ? t == t1 - 1 : t1 - t <= 2;
         if (elect_one()) {
-          umma_commit(o_done);
-          mbar_drain(o_done, 0);
-          mbar_drain(o_done, 1);
+          const uint32_t idesc = idesc_f16<F16>(kTileKeys, int(16 * units)) | scores_idesc;
+          const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16);
+          umma_ss_step<0, 0>(ts, q_desc, db, idesc, 0);
+          umma_ss_step<2, 2>(ts, q_desc, db, idesc, 1);
+          umma_ss_step<4, 4>(ts, q_desc, db, idesc, 1);
+          umma_ss_step<6, 6>(ts, q_desc, db, idesc, 1);
+          if (D == 128) {
+            constexpr int H = L::HALF >> 4;
+            umma_ss_step<H, H>(ts, q_desc, db, idesc, 1);
+            umma_ss_step<H + 2, H + 2>(ts, q_desc, db, idesc, 1);
+            umma_ss_step<H + 4, H + 4>(ts, q_desc, db, idesc, 1);
+            umma_ss_step<H + 6, H + 6>(ts, q_desc, db, idesc, 1);
+          }
+          umma_commit(s_ready + s);
+          umma_commit(empty + slot);
+          if (last) umma_commit(q_free + s);
         }
+        __syncwarp();
+        pending = true, p_units = units, p_first = first, p_last = last, p_slot = vslot, p_phase = vphase;
+        first = false;
+        slot += 2, phase ^= slot >= NS ? 1u : 0u, slot -= slot >= NS ? NS : 0;
       }
+      if (end) break;
+    }
+    if (!ok && elect_one()) {  // what is under way finishes before tensor memory is freed
+      umma_commit(o_done + s);
+      mbar_drain(o_done + s, 0);
+      mbar_drain(o_done + s, 1);
     }
     __syncwarp();
   } else if (warp < 8) {
@@ -902,22 +874,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   }
   else {
-    // ------------------------------------------------------------ queries of stream s, a segment ahead
+    // ------------------------------------------------------------ queries, a segment ahead
     // Rows behind the block's last keep what they hold: nothing reads their results.
     constexpr int C = D / 8, STEP = 32 / C;  // a lane keeps its 16-byte column and takes every STEP-th row
-    const int s = warp - 10, ch = lane % C;
-    const int step_tok = STEP / G, step_g = STEP - step_tok * G;
-    uint32_t nq = 0;  // segments of this stream
+    const int ch = lane % C, step_tok = STEP / G, step_g = STEP - step_tok * G;
+    uint32_t nq0 = 0, nq1 = 0;  // segments of each stream
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       const Seg& seg = segs[k % kSegRing];
       if (!wait_warp(seg_full + k % kSegRing, (k / kSegRing) & 1) || seg.t1 < 0) break;
-      const int srow0 = seg.paired() ? s * kTileKeys : 0;
-      const int rows = seg.rows - srow0 < kTileKeys ? seg.rows - srow0 : kTileKeys;
-      if (seg.paired() || seg.t1 - seg.t0 >= 2 || ((seg.parity ^ s) & 1) == 0) {
+      const bool paired = seg.paired();
+#pragma unroll 1
+      for (int i = 0; ok && i < 2; ++i) {
+        const int s = paired ? i : (seg.parity + i) & 1;  // in the order of their first tiles
+        if (!paired && i >= seg.t1 - seg.t0) continue;
+        const int srow0 = paired ? s * kTileKeys : 0;
+        const int rows = seg.rows - srow0 < kTileKeys ? seg.rows - srow0 : kTileKeys;
+        const uint32_t nq = s ? nq1++ : nq0++;
         if (nq > 0) ok = wait_warp(q_free + s, (nq - 1) & 1);
         if (!ok) break;
-        ++nq;
         int row = lane / C, tok = (seg.row0 + srow0 + row) / G, g = seg.row0 + srow0 + row - tok * G;
         const uint16_t* const q = static_cast<const uint16_t*>(p.q) + seg.tok0 * d.q_token_stride + (long long)seg.h * G * D + ch * 8;
         const uint32_t q_tile = base + L::OFF_Q + s * L::BYTES + (ch >> 3) * L::HALF;
