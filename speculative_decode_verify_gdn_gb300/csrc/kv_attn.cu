@@ -384,25 +384,57 @@ __device__ __forceinline__ uint32_t swizzled_desc_lo(uint32_t saddr, uint32_t lb
 }
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 
-// One step of 16 (elements of D for S, keys for O): S += Q K^T with the operands' descriptors, O += P V
-// with P in tensor memory.  (The descriptors are put together beside each product, from one
-// register: held ready for every step, they would not fit the issuing warp's registers.)
-template <int A_STEP, int B_STEP>
-__device__ __forceinline__ void umma_ss_step(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+// S = Q K^T of a tile: steps of 16 of the D elements (32 bytes of a swizzled row, then the other
+// 64-column half, H 16-byte units on).  The whole warp runs it and one elected lane issues: a
+// branch to one lane would cost every step its operands' way into uniform registers.
+template <int D>
+__device__ __forceinline__ void umma_scores(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+#define GDN_STEP(off, acc)                                                                        \
+  "add.u32 a, %1, " off ";\n\tadd.u32 b, %2, " off ";\n\tmov.b64 da, {a, %4};\n\tmov.b64 db, {b, %4};\n\t" \
+  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, " acc ";\n\t"
+#define GDN_HEAD "{\n\t.reg .pred q, t, f;\n\t.reg .b32 a, b;\n\t.reg .b64 da, db;\n\telect.sync _|q, 0xffffffff;\n\t" \
+  "setp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 f, 0, 0;\n\t"
+  if (D == 128)
+    asm volatile(GDN_HEAD GDN_STEP("0", "f") GDN_STEP("2", "t") GDN_STEP("4", "t") GDN_STEP("6", "t") GDN_STEP("1024", "t")
+                     GDN_STEP("1026", "t") GDN_STEP("1028", "t") GDN_STEP("1030", "t") "}" ::"r"(d_tmem),
+                 "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kDescHi)
+                 : "memory");
+  else
+    asm volatile(GDN_HEAD GDN_STEP("0", "f") GDN_STEP("2", "t") GDN_STEP("4", "t") GDN_STEP("6", "t") "}" ::"r"(d_tmem),
+                 "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kDescHi)
+                 : "memory");
+#undef GDN_STEP
+#undef GDN_HEAD
+}
+
+// O += P V (O = P V unless `more`): steps of 16 keys, 8 columns of P and 2048 bytes of values each;
+// the first one, and the other seven of a whole tile.
+__device__ __forceinline__ void umma_values_first(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t more) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b32 a, b;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "add.u32 a, %1, %6;\n\tadd.u32 b, %2, %7;\n\tmov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi), "n"(A_STEP), "n"(B_STEP)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 db, {%2, %5};\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(more), "n"(kDescHi)
       : "memory");
 }
-template <int STEP>  // of 16 keys: 8 columns of P, 2048 bytes of values
-__device__ __forceinline__ void umma_ts_step(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma_values_rest(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc) {
+#define GDN_STEP(acol, boff)                                                        \
+  "add.u32 a, %1, " acol ";\n\tadd.u32 b, %2, " boff ";\n\tmov.b64 db, {b, %4};\n\t" \
+  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, t;\n\t"
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b32 a, b;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "add.u32 a, %1, %6;\n\tadd.u32 b, %2, %7;\n\tmov.b64 db, {b, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi), "n"(8 * STEP), "n"(128 * STEP)
+      "{\n\t.reg .pred q, t;\n\t.reg .b32 a, b;\n\t.reg .b64 db;\n\telect.sync _|q, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+      GDN_STEP("8", "128") GDN_STEP("16", "256") GDN_STEP("24", "384") GDN_STEP("32", "512") GDN_STEP("40", "640")
+      GDN_STEP("48", "768") GDN_STEP("56", "896") "}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kDescHi)
+      : "memory");
+#undef GDN_STEP
+}
+
+// The elected lane's arrival on `bar` once the products issued so far are done, if `yes`.
+__device__ __forceinline__ void umma_commit_one(uint64_t* bar, bool yes = true) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.and.b32 p, %1, 0, q;\n\t"
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(uint32_t(yes))
       : "memory");
 }
 
@@ -428,23 +460,78 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// One lane of a converged warp, the same each time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
+// 64 consecutive columns of this thread's tensor-memory lane, one load and one wait.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int q = 0; q < 64; ++q) v[q] = __uint_as_float(r[q]);
+}
+
+// 16 words to this thread's lane; tmem_st_wait() before anything relies on them.
+__device__ __forceinline__ void tmem_st16_words(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two f32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 // A value that all lanes hold, in a form that the compiler knows to be the same in all of them (the
 // tensor core's operands live in uniform registers).
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Tensor-memory columns: S of stream s (P over its first half once S has been read), then O.
 constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t tmem_s(int s) { return 128u * uint32_t(s); }
 __device__ __forceinline__ uint32_t tmem_o(int s) { return 256u + 128u * uint32_t(s); }
 
-// A look at a barrier's phase that sleeps for up to about a microsecond.
+// A look at a barrier's phase, and one that sleeps for up to about a microsecond.
+__device__ __forceinline__ bool mbar_look(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -471,7 +558,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
            *const p_ready = q_ready + 4, *const o_done = q_ready + 6, *const q_free = q_ready + 8, *const seg_full = q_ready + 10,
            *const seg_empty = seg_full + kSegRing;
   Seg* const segs = reinterpret_cast<Seg*>(smem + L::OFF_SEG);
-  const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int tid = int(threadIdx.x), warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const gdn_kv_dims& d = p.d;
   const int G = d.Hq / d.Hkv;
 
@@ -609,25 +696,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!wait_warp(full + p_slot, p_phase) || !wait_warp(p_ready + s, np & 1)) return false;
       ++np;
       tc_fence_after();
-      if (elect_one()) {
-        const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + p_slot * L::BYTES, L::HALF);
-        umma_ts_step<0>(to, ts, db, values_idesc, p_first ? 0u : 1u);
-        if (p_units == 8) {
-          umma_ts_step<1>(to, ts, db, values_idesc, 1);
-          umma_ts_step<2>(to, ts, db, values_idesc, 1);
-          umma_ts_step<3>(to, ts, db, values_idesc, 1);
-          umma_ts_step<4>(to, ts, db, values_idesc, 1);
-          umma_ts_step<5>(to, ts, db, values_idesc, 1);
-          umma_ts_step<6>(to, ts, db, values_idesc, 1);
-          umma_ts_step<7>(to, ts, db, values_idesc, 1);
-        } else {
+      const uint32_t db = uniform(swizzled_desc_lo(base + L::OFF_RING + p_slot * L::BYTES, L::HALF));
+      umma_values_first(to, ts, db, values_idesc, p_first ? 0u : 1u);
+      if (p_units == 8) {
+        umma_values_rest(to, ts, db, values_idesc);
+      } else {
 #pragma unroll 1
-          for (uint32_t u = 1; u < p_units; ++u) umma_ts_step<0>(to, ts + 8 * u, db + 128 * u, values_idesc, 1);
-        }
-        umma_commit(empty + p_slot);
-        if (p_last) umma_commit(o_done + s);
+        for (uint32_t u = 1; u < p_units; ++u) umma_values_first(to, ts + 8 * u, db + 128 * u, values_idesc, 1);
       }
-      __syncwarp();
+      umma_commit_one(empty + p_slot);
+      umma_commit_one(o_done + s, p_last);
       return true;
     };
     for (uint32_t k = 0; ok; ++k) {
@@ -654,6 +732,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           slot += 2, phase ^= slot >= NS ? 1u : 0u, slot -= slot >= NS ? NS : 0;
           continue;
         }
+        // (whether the keys are there is seen before the wait for P: one wait less between the products)
+        const bool landed = pending && !end && __all_sync(0xffffffffu, mbar_look(full + slot, phase));
         if (pending && !values()) ok = false;
         if (end || !ok) break;
         // S = Q K^T of this tile
@@ -661,44 +741,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (!wait_warp(q_ready + s, nq & 1)) ok = false;
           ++nq;
         }
-        if (!ok || !wait_warp(full + slot, phase)) {
+        if (!ok || (!landed && !wait_warp(full + slot, phase))) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t units = uint32_t(all - 8 * t < 8 ? all - 8 * t : 8);
         const bool last = paired ? t == t1 - 1 : t1 - t <= 2;
-        if (elect_one()) {
-          const uint32_t idesc = idesc_f16<F16>(kTileKeys, int(16 * units)) | scores_idesc;
-          const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16);
-          umma_ss_step<0, 0>(ts, q_desc, db, idesc, 0);
-          umma_ss_step<2, 2>(ts, q_desc, db, idesc, 1);
-          umma_ss_step<4, 4>(ts, q_desc, db, idesc, 1);
-          umma_ss_step<6, 6>(ts, q_desc, db, idesc, 1);
-          if (D == 128) {
-            constexpr int H = L::HALF >> 4;
-            umma_ss_step<H, H>(ts, q_desc, db, idesc, 1);
-            umma_ss_step<H + 2, H + 2>(ts, q_desc, db, idesc, 1);
-            umma_ss_step<H + 4, H + 4>(ts, q_desc, db, idesc, 1);
-            umma_ss_step<H + 6, H + 6>(ts, q_desc, db, idesc, 1);
-          }
-          umma_commit(s_ready + s);
-          umma_commit(empty + slot);
-          if (last) umma_commit(q_free + s);
-        }
-        __syncwarp();
+        umma_scores<D>(ts, q_desc, uniform(swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16)),
+                       idesc_f16<F16>(kTileKeys, int(16 * units)) | scores_idesc);
+        umma_commit_one(s_ready + s);
+        umma_commit_one(empty + slot);
+        umma_commit_one(q_free + s, last);
         pending = true, p_units = units, p_first = first, p_last = last, p_slot = vslot, p_phase = vphase;
         first = false;
         slot += 2, phase ^= slot >= NS ? 1u : 0u, slot -= slot >= NS ? NS : 0;
       }
       if (end) break;
     }
-    if (!ok && elect_one()) {  // what is under way finishes before tensor memory is freed
-      umma_commit(o_done + s);
+    if (!ok) {  // what is under way finishes before tensor memory is freed
+      umma_commit_one(o_done + s);
       mbar_drain(o_done + s, 0);
       mbar_drain(o_done + s, 1);
     }
-    __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax: stream s, one row per thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -772,10 +837,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int cached = seg.keys - t * kTileKeys;  // keys of this tile from the cache (may exceed 128)
         if (!idle) {
           float x[128];
-          tmem_ld32(ts, x);
-          tmem_ld32(ts + 32, x + 32);
-          tmem_ld32(ts + 64, x + 64);
-          tmem_ld32(ts + 96, x + 96);
+          tmem_ld64(ts, x);
+          tmem_ld64(ts + 64, x + 64);
           if (cached < kTileKeys) {
             const int wu = (cached + 15) & ~15;  // the window's unit (own; behind the tile for a prefix)
 #pragma unroll
@@ -787,9 +850,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               for (int j = 0; j < 32; ++j) x[32 * q + j] = (see >> j) & 1u ? x[32 * q + j] : -INFINITY;
             }
           }
-          float mx = x[0];
+          float m4[4] = {x[0], x[1], x[2], x[3]};  // (four chains, two values a step)
 #pragma unroll
-          for (int j = 1; j < 128; ++j) mx = fmaxf(mx, x[j]);
+          for (int j = 4; j < 124; j += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m4[q] = fmaxf(fmaxf(m4[q], x[j + q]), x[j + 4 + q]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) m4[q] = fmaxf(m4[q], x[124 + q]);
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           const float up = (mx - m) * c;
           const bool move = mx > m && !(up <= kLag) && r < rows;  // (m = -inf: up is inf)
           if (__any_sync(0xffffffffu, move)) {
@@ -807,19 +875,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (move) l *= f, m = mx;
           }
           const float mc = m == -INFINITY ? 0.f : m * c;
-          float sum = 0.f;
+          const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+          float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            float pk[16];
+            uint32_t pk[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const float a = exp2_fast(fmaf(x[32 * q + 2 * j], c, -mc)), b = exp2_fast(fmaf(x[32 * q + 2 * j + 1], c, -mc));
-              sum += a + b;
-              pk[j] = __uint_as_float(pack2<F16>(a, b));
+              const float2 e = fma2(make_float2(x[32 * q + 2 * j], x[32 * q + 2 * j + 1]), c2, mc2);
+              const float2 w2 = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+              sum = add2(sum, w2);
+              pk[j] = pack2<F16>(w2.x, w2.y);
             }
-            tmem_st16(ts + 16 * q, pk);
+            tmem_st16_words(ts + 16 * q, pk);
           }
-          l += sum;
+          l += sum.x + sum.y;
+          tmem_st_wait();
         }
         first = false;
         if (cached < kTileKeys && (seg.own || (cached & 15))) {
