@@ -14,8 +14,8 @@
 // Kernels: plan (one CTA: lengths -> items and stretches), tiles (persistent, tcgen05), join.
 //
 // The tile kernel: a producer warp brings keys and values by TMA (128-byte swizzle) into a ring
-// of tiles; a warp per stream issues S = Q K^T and O += P V (tcgen05, M = 128, accumulators in
-// tensor memory, P read from tensor memory); one warp fetches the next segment's queries; two
+// of tiles; one warp issues S = Q K^T and O += P V (tcgen05, M = 128, accumulators in tensor
+// memory, P read from tensor memory); another fetches the next segment's queries; two
 // groups of four warps, one per stream, turn S into P, a row per thread.  A block of more than 128 rows uses the two streams for its two halves on the
 // same keys; a smaller one gives them alternate tiles of the same rows.  While one stream's
 // softmax runs, the tensor core works for the other.
@@ -34,7 +34,7 @@ constexpr int kTileKeys = 128;
 constexpr int kBlockRows = 256;  // rows of an item
 constexpr int kPlanThreads = 1024;
 constexpr int kGroupThreads = 128;  // a softmax group: one thread per row of a stream
-constexpr int kTileThreads = 3 * kGroupThreads;  // two softmax groups; producer, two tensor-core warps, query warp
+constexpr int kTileThreads = 3 * kGroupThreads;  // two softmax groups; producer, tensor-core, query and an idle warp
 // Registers: 168 a thread at launch (64512 in all), then 224 for the softmax threads, which hold a
 // row of 128 scores, and 56 for the rest: 256 x 224 + 128 x 56 = 64512.
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full + i, 1);
-      mbar_init(empty + i, 2);  // one arrival per stream
+      mbar_init(empty + i, 2);  // one arrival per stream; a tile that one stream alone uses arrives twice
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(q_ready + s, 32);
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(seg_full + i, 1);
-      mbar_init(seg_empty + i, 3 + 2 * kGroupThreads / 32);  // every warp but the producer
+      mbar_init(seg_empty + i, 2 + 2 * kGroupThreads / 32);  // tensor-core, query and softmax warps
     }
     gave_up = 0;
     fence_mbar_init();
@@ -670,99 +670,117 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (ok) ok = wait_warp(empty + use % NS, (use / NS) & 1);
       if (!ok) mbar_drain(full + use % NS, (use / NS) & 1);
     }
-  } else if (warp == 9 || warp == 10) {
-    // ------------------------------------------------------------ tensor core, stream s
-    // (A warp each: a product takes the tensor core 64 cycles and this warp nearly as long to issue
-    // beside the softmax warps; with one for both streams the tensor core waited for it.)  The whole
-    // warp walks the schedule and one elected lane issues: operands stay warp-uniform.
-    const int s = warp - 9;
-    const uint32_t ts = uniform(tmem) + tmem_s(s), to = uniform(tmem) + tmem_o(s);
-    const uint32_t q_desc = swizzled_desc_lo(base + L::OFF_Q + s * L::BYTES, 16);
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ tensor core
+    // One warp issues for both streams, the O += P V of a stream's tile before and the S = Q K^T of its
+    // next in one go: 1024 cycles of the tensor core, during which the other stream's softmax runs.
+    // (A warp per stream lets the two interleave and take twice as long each: 497 us where this
+    // takes 440, B=64 behind 32768 tokens.)  The whole warp walks the schedule, in uniform registers.
+    //
+    // A wait on a phase's parity is sound only within one phase of the barrier: a slot's use before this
+    // one has to have been waited for.  Before keys t that is values t - STAGES / 2 - 1 or so, of either
+    // stream, which are done by then, or done first where a stream had no turn for so long (a CTA
+    // changes deals, or from one stream a tile to both).
+    constexpr uint32_t kAlone = 16, kFirst = 32, kLast = 64, kHas = 128, kSlot = 256, kPhase = 4096;
+    const uint32_t tm = uniform(tmem);
     const uint32_t values_idesc = idesc_f16<F16>(kTileKeys, D) | (1u << 16);  // B (values) MN-major
     const uint32_t scores_idesc = p.scale < 0.f ? 1u << 13 : 0u;              // a negative scale negates the queries
-    //
-    // Each of the two warps sees every tile land, in order, and releases each of its slots once - the
-    // stream that does not use a tile by a plain arrival.  A wait on a phase's parity is sound only
-    // within one phase of the barrier, and copies do not land in the order they were asked for:
-    // this way no slot can be filled again, or be a use behind, where either stream waits for it.
     uint32_t slot = 0, phase = 0;  // of a tile's keys; its values are in the slot behind
-    uint32_t np = 0, nq = 0;       // P tiles, segments of this stream
+    uint32_t phases = 0;           // bit s: of p_ready[s]; bit 2 + s: of q_ready[s]
+    uint32_t pend0 = 0, pend1 = 0;  // the streams' tiles whose O += P V is still to be issued: units, flags, slot, phase
     bool ok = true;
-    // The tile whose O += P V is still to be issued.
-    bool pending = false, p_first = false, p_last = false;
-    uint32_t p_units = 0, p_slot = 0, p_phase = 0;
-    auto values = [&]() -> bool {
-      pending = false;
-      if (!wait_warp(full + p_slot, p_phase) || !wait_warp(p_ready + s, np & 1)) return false;
-      ++np;
-      tc_fence_after();
-      const uint32_t db = uniform(swizzled_desc_lo(base + L::OFF_RING + p_slot * L::BYTES, L::HALF));
-      umma_values_first(to, ts, db, values_idesc, p_first ? 0u : 1u);
-      if (p_units == 8) {
-        umma_values_rest(to, ts, db, values_idesc);
-      } else {
-#pragma unroll 1
-        for (uint32_t u = 1; u < p_units; ++u) umma_values_first(to, ts + 8 * u, db + 128 * u, values_idesc, 1);
-      }
-      umma_commit_one(empty + p_slot);
-      umma_commit_one(o_done + s, p_last);
-      return true;
-    };
     for (uint32_t k = 0; ok; ++k) {
       const Seg& seg = segs[k % kSegRing];
       if (!wait_warp(seg_full + k % kSegRing, (k / kSegRing) & 1)) {
         ok = false;
         break;
       }
-      const int t0 = int(uniform(uint32_t(seg.t0))), t1 = int(uniform(uint32_t(seg.t1)));
+      int t0 = int(uniform(uint32_t(seg.t0))), t1 = int(uniform(uint32_t(seg.t1)));
       const int all = int(uniform(uint32_t(seg.units))), parity = int(uniform(uint32_t(seg.parity)));
-      const bool paired = uniform(seg.paired() ? 1u : 0u) != 0;
+      bool paired = uniform(seg.paired() ? 1u : 0u) != 0;
+      const bool end = t1 < 0;  // no further segment: one more turn for the pending tiles
+      if (end) t0 = 0, t1 = 1, paired = true;
       __syncwarp();
       if (lane == 0) mbar_arrive(seg_empty + k % kSegRing);
-      const bool end = t1 < 0;
-      bool first = true;
-      for (int t = t0; ok && (end || t < t1); ++t) {
-        const uint32_t vslot = slot + 1 < NS ? slot + 1 : 0, vphase = slot + 1 < NS ? phase : phase ^ 1;
-        if (!end && !paired && ((parity + t - t0) & 1) != s) {  // the other stream's tile
-          ok = wait_warp(full + slot, phase);
-          if (ok && lane == 0) mbar_arrive(empty + slot);
-          if (ok && pending) ok = values();
-          if (ok) ok = wait_warp(full + vslot, vphase);
-          if (ok && lane == 0) mbar_arrive(empty + vslot);
-          slot += 2, phase ^= slot >= NS ? 1u : 0u, slot -= slot >= NS ? NS : 0;
-          continue;
-        }
-        // (whether the keys are there is seen before the wait for P: one wait less between the products)
-        const bool landed = pending && !end && __all_sync(0xffffffffu, mbar_look(full + slot, phase));
-        if (pending && !values()) ok = false;
-        if (end || !ok) break;
-        // S = Q K^T of this tile
-        if (first) {
-          if (!wait_warp(q_ready + s, nq & 1)) ok = false;
-          ++nq;
-        }
-        if (!ok || (!landed && !wait_warp(full + slot, phase))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+      for (int t = t0; ok && t < t1; ++t) {
+        // paired: both streams on this tile; else the one whose turn it is
         const uint32_t units = uint32_t(all - 8 * t < 8 ? all - 8 * t : 8);
-        const bool last = paired ? t == t1 - 1 : t1 - t <= 2;
-        umma_scores<D>(ts, q_desc, uniform(swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16)),
-                       idesc_f16<F16>(kTileKeys, int(16 * units)) | scores_idesc);
-        umma_commit_one(s_ready + s);
-        umma_commit_one(empty + slot);
-        umma_commit_one(q_free + s, last);
-        pending = true, p_units = units, p_first = first, p_last = last, p_slot = vslot, p_phase = vphase;
-        first = false;
+        const int turn = (parity + t - t0) & 1;
+        const uint32_t q = kHas | (paired ? units | (t == t0 ? kFirst : 0u) | (t == t1 - 1 ? kLast : 0u)
+                                          : units | kAlone | (t - t0 < 2 ? kFirst : 0u) | (t1 - t <= 2 ? kLast : 0u));
+        const uint32_t vslot = slot + 1 < NS ? slot + 1 : 0, vphase = slot + 1 < NS ? phase : phase ^ 1;
+#pragma unroll 1
+        for (int s = paired ? 0 : turn; ok && s <= (paired ? 1 : turn); ++s) {
+          bool landed = false;
+          // O += P V of this stream's tile before; ahead of it the other stream's, if its values still hold
+          // the slot that these keys are to come to (it had no turn for three tiles).
+          const uint32_t other = s ? pend0 : pend1;
+#pragma unroll 1
+          for (int v = !end && other && ((other / kSlot) & 15) == slot ? s ^ 1 : s;; v = s) {
+            const uint32_t was = v ? pend1 : pend0;
+            if (was) {
+              const uint32_t at = (was / kSlot) & 15;
+              ok = wait_warp(full + at, (was / kPhase) & 1);
+              // (whether the next keys are there is seen before the wait for P: one wait less between the products)
+              landed = v == s && !end && __all_sync(0xffffffffu, mbar_look(full + slot, phase));
+              ok = ok && wait_warp(p_ready + v, (phases >> v) & 1);
+              if (!ok) break;
+              phases ^= 1u << v;
+              tc_fence_after();
+              const uint32_t db = uniform(swizzled_desc_lo(base + L::OFF_RING + at * L::BYTES, L::HALF));
+              umma_values_first(tm + tmem_o(v), tm + tmem_s(v), db, values_idesc, was & kFirst ? 0u : 1u);
+              if ((was & 15) == 8) {
+                umma_values_rest(tm + tmem_o(v), tm + tmem_s(v), db, values_idesc);
+              } else {
+#pragma unroll 1
+                for (uint32_t u = 1; u < (was & 15); ++u)
+                  umma_values_first(tm + tmem_o(v), tm + tmem_s(v) + 8 * u, db + 128 * u, values_idesc, 1);
+              }
+              umma_commit_one(empty + at);
+              umma_commit_one(empty + at, (was & kAlone) != 0);
+              umma_commit_one(o_done + v, (was & kLast) != 0);
+              if (v)
+                pend1 = 0;
+              else
+                pend0 = 0;
+            }
+            if (v == s) break;
+          }
+          if (!ok) break;
+          if (end) continue;
+          if (q & kFirst) {
+            if (!wait_warp(q_ready + s, (phases >> (2 + s)) & 1)) {
+              ok = false;
+              break;
+            }
+            phases ^= 4u << s;
+          }
+          if (!landed && !wait_warp(full + slot, phase)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          umma_scores<D>(tm + tmem_s(s), swizzled_desc_lo(base + L::OFF_Q + s * L::BYTES, 16),
+                         uniform(swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16)),
+                         idesc_f16<F16>(kTileKeys, int(16 * units)) | scores_idesc);
+          umma_commit_one(s_ready + s);
+          umma_commit_one(empty + slot);
+          umma_commit_one(empty + slot, (q & kAlone) != 0);
+          umma_commit_one(q_free + s, (q & kLast) != 0);
+          const uint32_t now = q | vslot * kSlot | vphase * kPhase;
+          if (s)
+            pend1 = now;
+          else
+            pend0 = now;
+        }
         slot += 2, phase ^= slot >= NS ? 1u : 0u, slot -= slot >= NS ? NS : 0;
       }
       if (end) break;
     }
     if (!ok) {  // what is under way finishes before tensor memory is freed
-      umma_commit_one(o_done + s);
-      mbar_drain(o_done + s, 0);
-      mbar_drain(o_done + s, 1);
+      umma_commit_one(o_done);
+      mbar_drain(o_done, 0);
+      mbar_drain(o_done, 1);
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax: stream s, one row per thread
@@ -944,7 +962,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       done();
     }
   }
-  else {
+  else if (warp == 11) {
     // ------------------------------------------------------------ queries, a segment ahead
     // Rows behind the block's last keep what they hold: nothing reads their results.
     constexpr int C = D / 8, STEP = 32 / C;  // a lane keeps its 16-byte column and takes every STEP-th row

@@ -234,6 +234,24 @@ def test_large(B, K, Hq, Hkv, D, ps, lens, prefix, dtype):
     assert ((lse.double() - ref_lse).abs() <= 1e-4).all()
 
 
+@pytest.mark.parametrize("B,K,Hq,Hkv,D,plen,own", [
+    (60, 1, 8, 4, 64, 20000, 100), (60, 1, 8, 4, 128, 19999, 300), (33, 3, 4, 4, 128, 21000, 500),
+    (90, 5, 4, 2, 64, 17000, 260), (7, 16, 6, 6, 128, 15000, 2000), (150, 2, 8, 4, 64, 9000, 129)])
+def test_many_tiles_of_both_kinds(B, K, Hq, Hkv, D, plen, own):
+    """Enough tiles that prefixes and sequences are dealt out apart: CTAs change from the one to the
+    other at any parity, with one or both streams on either side, and several prefixes in turn."""
+    lens = [(37 * i) % own for i in range(B)] + [plen, 300]
+    pool = Pool(30, lens, Hkv=Hkv, D=D, ps=32)
+    pre = [B if i % 20 < 18 else B + 1 if i % 20 == 18 else -1 for i in range(B)]
+    q, k, v = window(pool, B, K, Hq)
+    out, lse = attend(pool, B, K, Hq, q, k, v, prefix_of=pre)
+    ref, ref_lse, mag = torch_reference(pool, B, K, Hq, q, k, v, pre)
+    assert ((out.double() - ref).abs() <= ROUND[BF] * (mag + ref.abs()) + 2e-4 * mag).all()
+    assert ((lse.double() - ref_lse).abs() <= 1e-4).all()
+    again, _ = attend(pool, B, K, Hq, q, k, v, prefix_of=pre)
+    assert torch.equal(again, out)
+
+
 def test_cache_offsets_beyond_32_bits():
     """Pages whose elements lie past 2^32 elements of the pool."""
     ps, Hkv, D = 64, 8, 128
