@@ -38,7 +38,7 @@ constexpr int kTileThreads = 3 * kGroupThreads;  // two softmax groups; producer
 // Registers: 168 a thread at launch (64512 in all), then 224 for the softmax threads, which hold a
 // row of 128 scores, and 56 for the rest: 256 x 224 + 128 x 56 = 64512.
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 4, kJoinRowsMax = 32;
 constexpr float kLn2 = 0.693147180559945f, kLog2e = 1.442695040888963f;
 // A running maximum may lag behind by up to 8 powers of two before O is rescaled: probabilities
 // stay below 2^8, far inside both 16-bit types, and keep their relative precision.
@@ -47,20 +47,24 @@ constexpr float kLag = 8.0f;
 constexpr uint32_t kMaxLooks = 1u << 22;
 
 // ---------------------------------------------------------------- the plan
-struct SeqRec {     // what a sequence does not share
-  long long off;    // first tile of its items in the order of all tiles
-  int32_t tiles;    // per item (0: nothing to do)
-  int32_t keys;     // cached tokens
-  int32_t run;      // its prefix run, -1 without
-  int32_t win;      // window tokens, clamped to 0..K
+struct SeqRec {       // a sequence: what it does not share, and where its rows are in its prefix run
+  long long off;      // first tile of its items in the order of all tiles
+  long long pre_off;  // the run's first tile
+  long long pre_row;  // the run's first row of partial results
+  long long pre_rows; // the run's rows per kv head
+  long long pre_at;   // the sequence's first of them
+  int32_t tiles;      // per item (0: nothing to do)
+  int32_t pre_tiles;  // per item of the run (0: no prefix)
+  int32_t keys;       // cached tokens
+  int32_t win;        // window tokens, clamped to 0..K
 };
-struct RunRec {     // consecutive sequences on one prefix
+struct RunRec {       // consecutive sequences on one prefix
   long long off;
-  long long row;    // first row of its partial results
+  long long row;
   int32_t tiles;
   int32_t keys;
   int32_t slot;
-  int32_t b0, n;    // sequences b0 .. b0 + n - 1
+  int32_t b0, n;      // sequences b0 .. b0 + n - 1
   int32_t pad[3];
 };
 struct PlanHead {
@@ -119,7 +123,13 @@ __host__ __device__ inline AttnWs carve_attn(void* base, const gdn_kv_dims& d, s
 // one deal over all tiles puts them on as many CTAs as there are.
 constexpr long long kSplitTiles = 4 * kCtas;
 __device__ __forceinline__ long long first_tile(long long c, long long tiles) { return c * tiles / kCtas; }
-__device__ __forceinline__ int cta_of(long long x, long long tiles) { return int(((x + 1) * kCtas - 1) / tiles); }
+__device__ __forceinline__ int cta_of(long long x, long long tiles) {
+  int c = int(float(x) * (float(kCtas) / float(tiles)));  // (within one of it)
+  c = c < 0 ? 0 : c > kCtas - 1 ? kCtas - 1 : c;
+  while (c > 0 && first_tile(c, tiles) > x) --c;
+  while (c < kCtas - 1 && first_tile(c + 1, tiles) <= x) ++c;
+  return c;
+}
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -165,45 +175,51 @@ __device__ __forceinline__ int prefix_slot(const AttnParams& p, int b) {
 
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWs w) {
   __shared__ long long sums[32];
+  __shared__ long long run_off[kPlanThreads], seq_off[kPlanThreads];  // first tiles, where they fit here
   grid_launch_dependents();
   grid_wait();
   const gdn_kv_dims& d = p.d;
   const int tid = int(threadIdx.x), KG = d.K * (d.Hq / d.Hkv);
   long long n_runs = 0;
+  // (one step of threads, the usual case, keeps what it knows of its sequence for the steps below)
+  const bool once = d.B <= kPlanThreads;
+  int win = 0, keys = 0, slot = -1;
+  long long run = -1;
   for (int b0 = 0; b0 < d.B; b0 += kPlanThreads) {  // sequences: lengths, and the runs' ends
     const int b = b0 + tid;
-    int s = -1;
     bool first = false, last = false;
+    int run_keys = 0;
+    win = 0, keys = 0, slot = -1;
     if (b < d.B) {
-      s = prefix_slot(p, b);
-      if (s < 0 && p.prefix_of && p.prefix_of[b] != -1) atomicOr(p.err, GDN_DEVERR_KV_SLOT);
-      first = s >= 0 && (b == 0 || prefix_slot(p, b - 1) != s);
-      last = s >= 0 && (b == d.B - 1 || prefix_slot(p, b + 1) != s);
-    }
-    long long total;
-    const long long r = n_runs + block_scan<long long>(first ? 1 : 0, sums, total) - (first ? 0 : 1);
-    if (b < d.B) {
-      int win = p.win_len ? p.win_len[b] : d.K;
+      const int before = b > 0 ? prefix_slot(p, b - 1) : -1, after = b + 1 < d.B ? prefix_slot(p, b + 1) : -1;
+      slot = prefix_slot(p, b);
+      keys = slot_len(p, d.slot0 + b);
+      win = p.win_len ? p.win_len[b] : d.K;
       if (win < 0 || win > d.K) {
         atomicOr(p.err, GDN_DEVERR_KV_WINDOW);
         win = win < 0 ? 0 : d.K;
       }
-      const int keys = slot_len(p, d.slot0 + b);
-      SeqRec q;
-      q.off = 0;
-      q.keys = keys;
-      q.win = win;
-      q.run = s >= 0 ? int(r) : -1;
-      q.tiles = win > 0 ? ((keys + 15) / 16 + 1 + 7) / 8 : 0;  // units of 16 keys; the window is one unit
-      w.seq[b] = q;
-      if (first) {
-        w.run[r].b0 = b;
-        w.run[r].slot = s;
-        const int n = slot_len(p, s);
-        w.run[r].keys = n;
-        w.run[r].tiles = (n + kTileKeys - 1) / kTileKeys;
+      if (slot < 0 && p.prefix_of && p.prefix_of[b] != -1) atomicOr(p.err, GDN_DEVERR_KV_SLOT);
+      first = slot >= 0 && before != slot;
+      last = slot >= 0 && after != slot;
+      if (first) run_keys = slot_len(p, slot);
+    }
+    long long total;
+    run = n_runs + block_scan<long long>(first ? 1 : 0, sums, total) - (first ? 0 : 1);
+    if (slot < 0) run = -1;
+    if (b < d.B) {
+      if (!once) {
+        w.seq[b].keys = keys;
+        w.seq[b].win = win;
+        w.seq[b].pre_off = run;  // (for now)
       }
-      if (last) w.run[r].n = b + 1;  // (its end; the length follows)
+      if (first) {
+        w.run[run].b0 = b;
+        w.run[run].slot = slot;
+        w.run[run].keys = run_keys;
+        w.run[run].tiles = (run_keys + kTileKeys - 1) / kTileKeys;
+      }
+      if (last) w.run[run].n = b + 1;  // (its end; the length follows)
     }
     n_runs += total;
   }
@@ -223,16 +239,34 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     const long long off = tiles + block_scan<long long>(mine, sums, total);
     const long long at = row + block_scan<long long>(rows, sums, total_rows);
     if (r < n_runs) w.run[r].off = off, w.run[r].row = at;
+    if (n_runs <= kPlanThreads) run_off[tid] = off;
     tiles += total;
     row += total_rows;
   }
+  __syncthreads();
   const long long prefix_tiles = tiles;
   const int own_items = d.Hkv * ((KG + kBlockRows - 1) / kBlockRows);
   for (int b0 = 0; b0 < d.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
+    SeqRec q{};
+    if (b < d.B) {
+      if (!once) win = w.seq[b].win, keys = w.seq[b].keys, run = w.seq[b].pre_off;
+      q.keys = keys;
+      q.win = win;
+      q.tiles = win > 0 ? ((keys + 15) / 16 + 1 + 7) / 8 : 0;  // units of 16 keys; the window is one unit
+      if (run >= 0) {
+        const RunRec r = w.run[run];
+        q.pre_off = r.off;
+        q.pre_row = r.row;
+        q.pre_rows = (long long)r.n * KG;
+        q.pre_at = (long long)(b - r.b0) * KG;
+        q.pre_tiles = r.tiles;
+      }
+    }
     long long total;
-    const long long off = tiles + block_scan<long long>(b < d.B ? (long long)own_items * w.seq[b].tiles : 0, sums, total);
-    if (b < d.B) w.seq[b].off = off;
+    q.off = tiles + block_scan<long long>((long long)own_items * q.tiles, sums, total);
+    if (b < d.B) w.seq[b] = q;
+    if (once) seq_off[tid] = q.off;
     tiles += total;
   }
   const bool split = tiles >= kSplitTiles;
@@ -250,10 +284,12 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     StartRec s{0, 0};
     if (x < tiles) {
       s.own = x >= prefix_tiles;
+      const bool here = s.own ? once : n_runs <= kPlanThreads;
+      const long long* const offs = s.own ? seq_off : run_off;
       int lo = 0, hi = (s.own ? d.B : int(n_runs)) - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if ((s.own ? w.seq[mid].off : w.run[mid].off) <= x)
+        if ((here ? offs[mid] : s.own ? w.seq[mid].off : w.run[mid].off) <= x)
           lo = mid;
         else
           hi = mid - 1;
@@ -1010,107 +1046,136 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 }
 
 // ---------------------------------------------------------------- join
-// One warp per row: the segments of its sequence and of its prefix, by their log-sum-exps.
+// One CTA per (sequence, kv head, 4 to 32 of its rows): the segments of the sequence and of its prefix,
+// weighted by their log-sum-exps.  Where the segments are follows from the plan and is listed once
+// per CTA; then a warp takes a row at a time.  Bound by the latency of its loads (lengths, then
+// log-sum-exps, then sums): the sums of a row are read together, and a CTA takes as many rows as
+// leave two CTAs to an SM (32 rows at B=64 K=16: 24 us where 4 take 62; 4 rows at B=1 K=16 with 40
+// segments a row: 12 us where 32 take 63).
 template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWs w) {
-  constexpr int N = D / 32;
+__global__ void __launch_bounds__(32 * kJoinWarps, 8)
+    attn_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWs w, const int join_rows) {
+  constexpr int N = D / 32, U = 4;
+  // the partial results of a block's first row: of the sequence, and of the prefix's block that
+  // holds the CTA's first row and the one behind it
+  __shared__ long long list[3][2 * kCtas];
+  __shared__ int counts[3];
+  __shared__ int row_at[kJoinWarps][32];
+  __shared__ float row_w[kJoinWarps][32];
   grid_launch_dependents();
   grid_wait();
   const gdn_kv_dims& d = p.d;
-  const int G = d.Hq / d.Hkv, KG = d.K * G, lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= (long long)d.B * d.K * d.Hq) return;
-  const int hq = int(row % d.Hq), h = hq / G, g = hq - h * G;
-  const int tok = int(row / d.Hq), b = tok / d.K, t = tok - b * d.K;
+  const int G = d.Hq / d.Hkv, KG = d.K * G, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunks = (KG + join_rows - 1) / join_rows;
+  const int r0 = int(blockIdx.x % unsigned(chunks)) * join_rows, bh = int(blockIdx.x / unsigned(chunks));
+  const int h = bh % d.Hkv, b = bh / d.Hkv;
   const SeqRec q = w.seq[b];
-  uint16_t* const out = static_cast<uint16_t*>(p.out) + row * D;
-  float acc[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = 0.f;
-  float M = -INFINITY, W = 0.f;
-  if (t < q.win) {
-    // the row's item in each of the two parts: tiles [at, at + n), first CTA, and rows
-    struct Part {
-      long long at, base, deal, tiles;  // (the deal's first tile and size)
-      int n, c0, parts, width, lr;
-      bool paired;
-    };
-    const bool split = w.head->split;
-    const long long all = w.head->tiles, shared = w.head->prefix_tiles;
-    auto part_of = [&](long long off, int n, long long row0, long long rows, int r, bool is_own) {
-      Part x{};
-      if (n == 0) return x;
-      x.deal = split && is_own ? shared : 0;
-      x.tiles = !split ? all : is_own ? all - shared : shared;
-      const int blocks = int((rows + kBlockRows - 1) / kBlockRows), rb = r / kBlockRows;
-      const int in = int(rows - (long long)rb * kBlockRows < kBlockRows ? rows - (long long)rb * kBlockRows : kBlockRows);
-      x.at = off + ((long long)h * blocks + rb) * n;
-      x.n = n;
-      x.c0 = cta_of(x.at - x.deal, x.tiles);
-      x.paired = in > kTileKeys;
-      x.parts = (cta_of(x.at - x.deal + n - 1, x.tiles) - x.c0 + 1) * (x.paired ? 1 : 2);
-      x.width = in;
-      x.lr = r - rb * kBlockRows;
-      x.base = row0 + h * rows_width(rows) + (long long)rb * kBlockRows;
-      return x;
-    };
-    const Part own = part_of(q.off, q.tiles, w.head->own_row + (long long)b * d.Hkv * rows_width(KG), KG, t * G + g, true);
-    Part pre{};
-    if (q.run >= 0) {
-      const RunRec r = w.run[q.run];
-      pre = part_of(r.off, r.tiles, r.row, (long long)r.n * KG, ((b - r.b0) * d.K + t) * G + g, false);
-    }
-    const int count = own.parts + pre.parts;
-    for (int i0 = 0; i0 < count; i0 += 32) {
-      long long at = -1;
-      const int i = i0 + lane;
-      if (i < count) {
-        const Part& x = i < own.parts ? own : pre;
-        const int j = i < own.parts ? i : i - own.parts;
-        const int c = x.c0 + (x.paired ? j : j >> 1), s = x.paired ? 0 : j & 1;
-        long long lo = x.deal + first_tile(c, x.tiles), hi = x.deal + first_tile(c + 1, x.tiles);
-        if (lo < x.at) lo = x.at;
-        if (hi > x.at + x.n) hi = x.at + x.n;
-        if (hi > lo && (x.paired || hi - lo >= 2 || int(lo & 1) == s))  // (a single tile belongs to one stream)
-          at = (long long)kBlockRows * c + x.base + s * x.width + x.lr;
+  const PlanHead head = *w.head;
+  const int rows = KG - r0 < join_rows ? KG - r0 : join_rows;
+  const long long pre0 = q.pre_at + r0;  // the CTA's first row in the prefix's
+  if (warp < 3) {
+    const bool own = warp == 0;
+    const long long all = own ? KG : q.pre_rows;
+    const int n = own ? q.tiles : q.pre_tiles;
+    const long long rb = own ? r0 / kBlockRows : pre0 / kBlockRows + (warp - 1);
+    int count = 0;
+    if (n > 0 && (warp < 2 || rb * kBlockRows < pre0 + rows)) {
+      const long long deal = head.split && own ? head.prefix_tiles : 0;
+      const long long size = !head.split ? head.tiles : own ? head.tiles - head.prefix_tiles : head.prefix_tiles;
+      const long long blocks = (all + kBlockRows - 1) / kBlockRows;
+      const int width = int(all - rb * kBlockRows < kBlockRows ? all - rb * kBlockRows : kBlockRows);
+      const bool paired = width > kTileKeys;
+      const long long from = (own ? q.off : q.pre_off) + (h * blocks + rb) * n;
+      const int c0 = cta_of(from - deal, size), c1 = cta_of(from - deal + n - 1, size);
+      const long long base = (own ? head.own_row + (long long)b * d.Hkv * rows_width(KG) : q.pre_row) + h * rows_width(all) + rb * kBlockRows;
+      const int parts = (c1 - c0 + 1) * (paired ? 1 : 2);
+      for (int i0 = 0; i0 < parts; i0 += 32) {
+        const int i = i0 + lane, c = c0 + (paired ? i : i >> 1), s = paired ? 0 : i & 1;
+        bool there = i < parts;
+        if (there) {
+          long long lo = deal + first_tile(c, size), hi = deal + first_tile(c + 1, size);
+          lo = lo < from ? from : lo;
+          hi = hi > from + n ? from + n : hi;
+          there = hi > lo && (paired || hi - lo >= 2 || int(lo & 1) == s);  // (a single tile belongs to one stream)
+        }
+        const uint32_t some = __ballot_sync(0xffffffffu, there);
+        if (there) list[warp][count + __popc(some & ((1u << lane) - 1u))] = (long long)kBlockRows * c + base + s * width;
+        count += __popc(some);
       }
-      const float e = at >= 0 ? w.lse[at] : -INFINITY;
-      float mx = e;
+    }
+    if (lane == 0) counts[warp] = count;
+  }
+  __syncthreads();
+  const int n_own = counts[0];
+  for (int i = warp; i < rows; i += kJoinWarps) {
+    const int r = r0 + i, t = r / G;
+    float acc[N];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const bool nan = __any_sync(0xffffffffu, e != e);
-      const float Mn = fmaxf(M, mx), f = M == -INFINITY ? 0.f : exp2f(M - Mn);
-      float wt = e == -INFINITY ? 0.f : exp2f(e - (Mn == -INFINITY ? 0.f : Mn));
-      M = Mn;
-      W = W * f + warp_sum(wt);
-      if (nan) W = NAN;
+    for (int k = 0; k < N; ++k) acc[k] = 0.f;
+    float M = -INFINITY, W = 0.f;
+    const bool live = t < q.win;
+    if (live) {
+      const int side = (pre0 + i) / kBlockRows != pre0 / kBlockRows ? 2 : 1;
+      const int count = n_own + counts[side];
+      const int lr_own = r % kBlockRows, lr_pre = int((pre0 + i) % kBlockRows);
+      for (int j0 = 0; j0 < count; j0 += 32) {
+        const int j = j0 + lane;
+        long long at = 0;
+        float e = -INFINITY;
+        if (j < count) {
+          at = j < n_own ? list[0][j] + lr_own : list[side][j - n_own] + lr_pre;
+          e = w.lse[at];
+        }
+        float mx = e;
 #pragma unroll
-      for (int k = 0; k < N; ++k) acc[k] *= f;
-      const int m = count - i0 < 32 ? count - i0 : 32;
-#pragma unroll 4
-      for (int j = 0; j < m; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, wt, j);
-        const long long aj = __shfl_sync(0xffffffffu, at, j);
-        if (wj != 0.f) {
-          const float* o = w.o + aj * D + lane * N;
-          if (N == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(o);
-            acc[0] += wj * v.x, acc[1] += wj * v.y, acc[N - 2] += wj * v.z, acc[N - 1] += wj * v.w;
-          } else {
-            const float2 v = *reinterpret_cast<const float2*>(o);
-            acc[0] += wj * v.x, acc[1] += wj * v.y;
-          }
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float Mn = fmaxf(M, mx), f = M == -INFINITY ? 0.f : exp2f(M - Mn);
+        const float wt = e == -INFINITY ? 0.f : exp2f(e - (Mn == -INFINITY ? 0.f : Mn));  // (NaN stays NaN)
+        M = Mn;
+        W = W * f + warp_sum(wt);
+#pragma unroll
+        for (int k = 0; k < N; ++k) acc[k] *= f;
+        const uint32_t some = __ballot_sync(0xffffffffu, wt != 0.f);
+        __syncwarp();
+        if (wt != 0.f) {
+          const int k = __popc(some & ((1u << lane) - 1u));
+          row_at[warp][k] = int(at);  // (rows of partial results: below 2^31)
+          row_w[warp][k] = wt;
+        }
+        __syncwarp();
+        const int m = __popc(some);
+        for (int k0 = 0; k0 < m; k0 += U) {
+          float v[U][N];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (k0 + u < m) {
+              const float* o = w.o + (long long)row_at[warp][k0 + u] * D + lane * N;
+              if (N == 4)
+                *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(o);
+              else
+                *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(o);
+            }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (k0 + u < m) {
+              const float wj = row_w[warp][k0 + u];
+#pragma unroll
+              for (int k = 0; k < N; ++k) acc[k] += wj * v[u][k];
+            }
         }
       }
+      const float inv = 1.f / W;
+#pragma unroll
+      for (int k = 0; k < N; ++k) acc[k] *= inv;
     }
-    const float inv = 1.f / W;
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] *= inv;
+    const long long row = ((long long)b * d.K + t) * d.Hq + h * G + (r - t * G);
+    uint32_t* const o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D) + lane * (N / 2);
+    if (N == 4)
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack2<F16>(acc[0], acc[1]), pack2<F16>(acc[N - 2], acc[N - 1]));
+    else
+      *o = pack2<F16>(acc[0], acc[1]);
+    if (p.lse && lane == 0) p.lse[row] = live ? (M + log2f(W)) * kLn2 : -INFINITY;
   }
-  uint32_t* const o = reinterpret_cast<uint32_t*>(out) + lane * (N / 2);
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) o[i] = pack2<F16>(acc[2 * i], acc[2 * i + 1]);
-  if (p.lse && lane == 0) p.lse[row] = t < q.win ? (M + log2f(W)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------- launches
@@ -1156,9 +1221,12 @@ cudaError_t launch(const AttnParams& p, const AttnWs& w, int box, const TileMaps
   if (e != cudaSuccess) return e;
   e = launch_pdl(attn_tile_kernel<D, F16>, unsigned(kCtas), kTileThreads, L::TOTAL, stream, p, w, box, maps);
   if (e != cudaSuccess) return e;
-  const long long rows = (long long)p.d.B * p.d.K * p.d.Hq;
-  return launch_pdl(attn_join_kernel<D, F16>, unsigned((rows + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, stream,
-                    p, w);
+  const int KG = p.d.K * (p.d.Hq / p.d.Hkv);
+  const long long heads = (long long)p.d.B * p.d.Hkv;
+  int join_rows = kJoinRowsMax;  // a power of two: a CTA's rows are in one block of its sequence
+  while (join_rows > kJoinWarps && heads * ((KG + join_rows - 1) / join_rows) < 2 * kCtas) join_rows /= 2;
+  return launch_pdl(attn_join_kernel<D, F16>, unsigned(heads * ((KG + join_rows - 1) / join_rows)), 32 * kJoinWarps, 0,
+                    stream, p, w, join_rows);
 }
 
 }  // namespace
