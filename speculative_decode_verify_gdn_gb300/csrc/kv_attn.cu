@@ -465,12 +465,11 @@ __device__ __forceinline__ void umma_values_rest(uint32_t d_tmem, uint32_t a_tme
 #undef GDN_STEP
 }
 
-// The elected lane's arrival on `bar` once the products issued so far are done, if `yes`.
-__device__ __forceinline__ void umma_commit_one(uint64_t* bar, bool yes = true) {
+// The elected lane's arrival on `bar` once the products issued so far are done.
+__device__ __forceinline__ void umma_commit_one(uint64_t* bar) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.and.b32 p, %1, 0, q;\n\t"
-      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
-      "r"(uint32_t(yes))
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
       : "memory");
 }
 
@@ -717,13 +716,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // one has to have been waited for.  Before keys t that is values t - STAGES / 2 - 1 or so, of either
     // stream, which are done by then, or done first where a stream had no turn for so long (a CTA
     // changes deals, or from one stream a tile to both).
-    constexpr uint32_t kAlone = 16, kFirst = 32, kLast = 64, kHas = 128, kSlot = 256, kPhase = 4096;
+    constexpr uint32_t kAlone = 16, kFirst = 32, kLast = 64, kHas = 128, kSlot = 256, kPhase = 4096, kSeen = 8192;
     const uint32_t tm = uniform(tmem);
     const uint32_t values_idesc = idesc_f16<F16>(kTileKeys, D) | (1u << 16);  // B (values) MN-major
     const uint32_t scores_idesc = p.scale < 0.f ? 1u << 13 : 0u;              // a negative scale negates the queries
     uint32_t slot = 0, phase = 0;  // of a tile's keys; its values are in the slot behind
     uint32_t phases = 0;           // bit s: of p_ready[s]; bit 2 + s: of q_ready[s]
-    uint32_t pend0 = 0, pend1 = 0;  // the streams' tiles whose O += P V is still to be issued: units, flags, slot, phase
+    uint32_t pend0 = 0, pend1 = 0;  // the streams' tiles whose O += P V is still to be issued: units, flags, slot, phase, values seen
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       const Seg& seg = segs[k % kSegRing];
@@ -747,23 +746,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t vslot = slot + 1 < NS ? slot + 1 : 0, vphase = slot + 1 < NS ? phase : phase ^ 1;
 #pragma unroll 1
         for (int s = paired ? 0 : turn; ok && s <= (paired ? 1 : turn); ++s) {
-          bool landed = false;
+          bool landed = paired && s == 1;  // (stream 0 has waited for the tile's keys)
           // O += P V of this stream's tile before; ahead of it the other stream's, if its values still hold
-          // the slot that these keys are to come to (it had no turn for three tiles).
+          // the slot that these keys are to come to (it had no turn for three tiles).  As few waits and
+          // commits as there can be: the tensor core idles for whatever passes here between its products.
           const uint32_t other = s ? pend0 : pend1;
 #pragma unroll 1
           for (int v = !end && other && ((other / kSlot) & 15) == slot ? s ^ 1 : s;; v = s) {
             const uint32_t was = v ? pend1 : pend0;
             if (was) {
               const uint32_t at = (was / kSlot) & 15;
-              ok = wait_warp(full + at, (was / kPhase) & 1);
-              // (whether the next keys are there is seen before the wait for P: one wait less between the products)
-              landed = v == s && !end && __all_sync(0xffffffffu, mbar_look(full + slot, phase));
+              if (!(was & kSeen)) {
+                ok = wait_warp(full + at, (was / kPhase) & 1);
+                if (v == 0 && pend1 && ((pend1 / kSlot) & 15) == at) pend1 |= kSeen;
+                // (whether the next keys are there is seen before the wait for P: one wait less between the products)
+                if (v == s && !end) landed = __all_sync(0xffffffffu, mbar_look(full + slot, phase));
+              }
               ok = ok && wait_warp(p_ready + v, (phases >> v) & 1);
               if (!ok) break;
               phases ^= 1u << v;
               tc_fence_after();
-              const uint32_t db = uniform(swizzled_desc_lo(base + L::OFF_RING + at * L::BYTES, L::HALF));
+              const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + at * L::BYTES, L::HALF);
               umma_values_first(tm + tmem_o(v), tm + tmem_s(v), db, values_idesc, was & kFirst ? 0u : 1u);
               if ((was & 15) == 8) {
                 umma_values_rest(tm + tmem_o(v), tm + tmem_s(v), db, values_idesc);
@@ -773,8 +776,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                   umma_values_first(tm + tmem_o(v), tm + tmem_s(v) + 8 * u, db + 128 * u, values_idesc, 1);
               }
               umma_commit_one(empty + at);
-              umma_commit_one(empty + at, (was & kAlone) != 0);
-              umma_commit_one(o_done + v, (was & kLast) != 0);
+              if (was & (kAlone | kLast)) {
+                if (was & kAlone) umma_commit_one(empty + at);
+                if (was & kLast) umma_commit_one(o_done + v);
+              }
               if (v)
                 pend1 = 0;
               else
@@ -797,12 +802,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           tc_fence_after();
           umma_scores<D>(tm + tmem_s(s), swizzled_desc_lo(base + L::OFF_Q + s * L::BYTES, 16),
-                         uniform(swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16)),
+                         swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16),
                          idesc_f16<F16>(kTileKeys, int(16 * units)) | scores_idesc);
           umma_commit_one(s_ready + s);
           umma_commit_one(empty + slot);
-          umma_commit_one(empty + slot, (q & kAlone) != 0);
-          umma_commit_one(q_free + s, (q & kLast) != 0);
+          if (q & (kAlone | kLast)) {
+            if (q & kAlone) umma_commit_one(empty + slot);
+            if (q & kLast) umma_commit_one(q_free + s);
+          }
           const uint32_t now = q | vslot * kSlot | vphase * kPhase;
           if (s)
             pend1 = now;
