@@ -52,7 +52,7 @@ extern "C" {
 typedef struct {
   int32_t B;          /* sequences in the batch: slots slot0 .. slot0 + B - 1 */
   int32_t K;          /* window tokens, 1..16 (gdn_kv_commit of chains: 1..1048576) */
-  int32_t Hq;         /* query heads, a multiple of Hkv (query head h reads kv head h / (Hq/Hkv)) */
+  int32_t Hq;         /* query heads, a multiple of Hkv, at most 128 Hkv (query head h reads kv head h / (Hq/Hkv)) */
   int32_t Hkv;        /* key/value heads */
   int32_t D;          /* head dim, 64 or 128 */
   int32_t page_size;  /* tokens per page, a multiple of 16, 16..1024 */

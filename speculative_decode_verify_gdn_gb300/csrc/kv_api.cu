@@ -49,6 +49,7 @@ gdn_status check_dims(const gdn_kv_dims* d, Use use, bool tree) {
   if (use == kAttn) {
     if (d->Hq < 1 || d->Hq > 65536 || d->Hq % d->Hkv)
       return fail(d->Hq < 1 ? GDN_ERR_INVALID_ARG : GDN_ERR_UNSUPPORTED, "Hq=%d (a multiple of Hkv=%d)", d->Hq, d->Hkv);
+    if (d->Hq / d->Hkv > 128) return fail(GDN_ERR_UNSUPPORTED, "Hq/Hkv=%d (at most 128)", d->Hq / d->Hkv);
     if (d->q_token_stride < (int64_t)d->Hq * d->D || d->q_token_stride % 8 || d->q_token_stride >= (1LL << 36))
       return fail(GDN_ERR_INVALID_ARG, "q_token_stride=%lld (a multiple of 8, at least Hq * D)", (long long)d->q_token_stride);
     if ((long long)d->B * d->K * d->Hq > (1LL << 30)) return fail(GDN_ERR_UNSUPPORTED, "more than 2^30 rows");
@@ -210,7 +211,7 @@ gdn_status gdn_attn_verify(const gdn_kv_dims* dims, int32_t layer, const void* q
   uint32_t* err = nullptr;
   GDN_RETURN_IF(gdn::device_status_word(&err));
   const gdn::AttnParams p{d, layer, q, k_win, v_win, k_cache, v_cache, page_table, seq_len, prefix_of, win_len, parent,
-                          scale, out, lse, workspace, err};
+                          scale, out, lse, workspace, err, 0, 0};
   const cudaError_t e = gdn::launch_attn(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
   return gdn::report_ok();

@@ -14,8 +14,8 @@
 // Kernels: plan (one CTA: lengths -> items and stretches), tiles (persistent, tcgen05), join.
 //
 // The tile kernel: a producer warp brings keys and values by TMA (128-byte swizzle) into a ring
-// of tiles; one warp issues S = Q K^T and O += P V (tcgen05, M = 128, accumulators in tensor
-// memory, P read from tensor memory); another fetches the next segment's queries; two
+// of tiles; a warp per stream issues S = Q K^T and O += P V (tcgen05, M = 128, accumulators in
+// tensor memory, P read from tensor memory); one warp fetches the next segment's queries; two
 // groups of four warps, one per stream, turn S into P, a row per thread.  A block of more than 128 rows uses the two streams for its two halves on the
 // same keys; a smaller one gives them alternate tiles of the same rows.  While one stream's
 // softmax runs, the tensor core works for the other.
@@ -31,20 +31,22 @@ namespace {
 
 constexpr int kCtas = 152;       // one per SM; no CTA waits for another, so any number is correct
 constexpr int kTileKeys = 128;
-constexpr int kBlockRows = 256;  // rows of an item
+constexpr int kTileRows = 128;   // rows of a stream's tile, whole tokens of G query heads: 128 / G * G are used
+constexpr int kBlockRows = 256;  // rows of an item, at most
 constexpr int kPlanThreads = 1024;
 constexpr int kGroupThreads = 128;  // a softmax group: one thread per row of a stream
-constexpr int kTileThreads = 3 * kGroupThreads;  // two softmax groups; producer, tensor-core, query and an idle warp
+constexpr int kTileThreads = 3 * kGroupThreads;  // two softmax groups; producer, two tensor-core warps, query warp
 // Registers: 168 a thread at launch (64512 in all), then 224 for the softmax threads, which hold a
 // row of 128 scores, and 56 for the rest: 256 x 224 + 128 x 56 = 64512.
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
-constexpr int kJoinWarps = 4, kJoinRowsMax = 32;
+constexpr int kJoinWarps = 4, kJoinRowsMax = 32;  // (four warps: four lists)
 constexpr float kLn2 = 0.693147180559945f, kLog2e = 1.442695040888963f;
 // A running maximum may lag behind by up to 8 powers of two before O is rescaled: probabilities
 // stay below 2^8, far inside both 16-bit types, and keep their relative precision.
 constexpr float kLag = 8.0f;
 // Longest wait inside the tile kernel: looks of at most about a microsecond each, a few seconds in all.
 constexpr uint32_t kMaxLooks = 1u << 22;
+constexpr uint32_t kMaxTurnLooks = 1u << 14;
 
 // ---------------------------------------------------------------- the plan
 struct SeqRec {       // a sequence: what it does not share, and where its rows are in its prefix run
@@ -88,13 +90,13 @@ struct AttnWs {
 
 __host__ __device__ inline size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Rows of partial results of a block: one per row when the streams hold its halves, else two (one
-// per stream).
-__host__ __device__ inline int block_width(int rows) { return rows > kTileKeys ? rows : 2 * rows; }
+// Rows of partial results of a block, with `tile` rows to a stream: one per row when the streams
+// hold its halves, else two (one per stream).
+__host__ __device__ inline int block_width(int rows, int tile) { return rows > tile ? rows : 2 * rows; }
 // Rows of partial results of all blocks of `rows` rows.
-__host__ __device__ inline long long rows_width(long long rows) {
-  const long long full = (rows - 1) / kBlockRows;
-  return full * kBlockRows + block_width(int(rows - full * kBlockRows));
+__host__ __device__ inline long long rows_width(long long rows, int tile) {
+  const long long full = (rows - 1) / (2 * tile);
+  return full * 2 * tile + block_width(int(rows - full * 2 * tile), tile);
 }
 
 __host__ __device__ inline AttnWs carve_attn(void* base, const gdn_kv_dims& d, size_t* total) {
@@ -232,8 +234,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
       const int n = w.run[r].n - w.run[r].b0;
       w.run[r].n = n;
       const long long block = (long long)n * KG;
-      mine = (block + kBlockRows - 1) / kBlockRows * d.Hkv * w.run[r].tiles;
-      rows = d.Hkv * rows_width(block);
+      mine = (block + 2 * p.tile_rows - 1) / (2 * p.tile_rows) * d.Hkv * w.run[r].tiles;
+      rows = d.Hkv * rows_width(block, p.tile_rows);
     }
     long long total, total_rows;
     const long long off = tiles + block_scan<long long>(mine, sums, total);
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
   }
   __syncthreads();
   const long long prefix_tiles = tiles;
-  const int own_items = d.Hkv * ((KG + kBlockRows - 1) / kBlockRows);
+  const int own_items = d.Hkv * ((KG + 2 * p.tile_rows - 1) / (2 * p.tile_rows));
   for (int b0 = 0; b0 < d.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
     SeqRec q{};
@@ -303,13 +305,14 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 // ---------------------------------------------------------------- segments
 struct Seg {
   int own, idx, h, row0, rows;  // rows row0 .. row0 + rows - 1 of the run's or sequence's rows
+  int pair;                     // they fill more than one row tile: both streams take every tile of keys
   int tok0;                     // its first window token (of all B K)
   int slot, keys, win;          // cached tokens; own: window tokens (prefix: -1)
   int units;                    // of 16 keys, the window's included
   int t0, t1;                   // tiles of the item
   int parity;                   // of tile t0 in the order of all tiles
   long long part;               // first row of its partial results
-  __device__ __forceinline__ bool paired() const { return rows > kTileKeys; }
+  __device__ __forceinline__ bool paired() const { return pair != 0; }
 };
 
 // Walks a CTA's stretch segment by segment.
@@ -350,7 +353,7 @@ struct SegWalk {
       if (own) {
         const SeqRec q = w.seq[idx];
         off = q.off, tiles = q.tiles, rows = KG;
-        row = own_row + (long long)idx * d.Hkv * rows_width(KG);
+        row = own_row + (long long)idx * d.Hkv * rows_width(KG, p.tile_rows);
         s.slot = d.slot0 + idx, s.keys = q.keys, s.win = q.win, s.tok0 = idx * d.K;
         s.units = (q.keys + 15) / 16 + 1;
       } else {
@@ -359,7 +362,8 @@ struct SegWalk {
         s.slot = r.slot, s.keys = r.keys, s.win = -1, s.tok0 = r.b0 * d.K;
         s.units = (r.keys + 15) / 16;
       }
-      const int blocks = int((rows + kBlockRows - 1) / kBlockRows);
+      const int block = 2 * p.tile_rows;
+      const int blocks = int((rows + block - 1) / block);
       const long long items = (long long)blocks * d.Hkv;
       if (tiles == 0 || x >= off + items * tiles) {
         ++idx;
@@ -369,13 +373,14 @@ struct SegWalk {
       s.own = own, s.idx = idx;
       s.h = item / blocks;
       const int rb = item - s.h * blocks;
-      s.row0 = rb * kBlockRows;
-      s.rows = int(rows - s.row0 < kBlockRows ? rows - s.row0 : kBlockRows);
+      s.row0 = rb * block;
+      s.rows = int(rows - s.row0 < block ? rows - s.row0 : block);
+      s.pair = s.rows > p.tile_rows;
       s.t0 = int(x - off - (long long)item * tiles);
       const long long left = end - x;
       s.t1 = left < tiles - s.t0 ? s.t0 + int(left) : tiles;
       s.parity = int(x & 1);
-      s.part = (long long)kBlockRows * cta + row + s.h * rows_width(rows) + s.row0;
+      s.part = (long long)kBlockRows * cta + row + s.h * rows_width(rows, p.tile_rows) + s.row0;
       x += s.t1 - s.t0;
       return true;
     }
@@ -403,6 +408,8 @@ struct TileMaps {
   CUtensorMap k16, v16;  // boxes of 16 tokens of the cache
   CUtensorMap kb, vb;    // boxes of `box` tokens
   CUtensorMap kw, vw;    // boxes of 16 tokens of the window
+  // queries, (D, query head, token): boxes of G heads x the tokens of a row tile, and of a sequence's
+  CUtensorMap qt, qs;
 };
 
 __device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, int c4, uint32_t bar) {
@@ -411,6 +418,13 @@ __device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* m, in
       "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
       : "memory");
 }
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 // Shared-memory descriptor of a 128-byte-swizzled operand: rows of 128 bytes, groups of 8 rows
 // 1024 bytes apart (SBO); LBO is the step between 64-column halves of an MN-major operand and not
 // used by a K-major one.
@@ -528,6 +542,13 @@ __device__ __forceinline__ void tmem_st16_words(uint32_t taddr, const uint32_t (
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 32 bytes (a sector) a thread.
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 // Two f32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -585,7 +606,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   constexpr int NS = L::STAGES;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_slot;
-  __shared__ volatile uint32_t gave_up;
+  __shared__ volatile uint32_t gave_up, turns[2];  // (turns: taken so far by each tensor-core warp)
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
@@ -600,18 +621,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full + i, 1);
-      mbar_init(empty + i, 2);  // one arrival per stream; a tile that one stream alone uses arrives twice
+      mbar_init(empty + i, 2);  // one arrival per stream
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(q_ready + s, 32);
+      mbar_init(q_ready + s, 1);
       mbar_init(q_free + s, 1);
+      turns[s] = 0;
       mbar_init(s_ready + s, 1);
       mbar_init(p_ready + s, kGroupThreads);
       mbar_init(o_done + s, 1);
     }
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(seg_full + i, 1);
-      mbar_init(seg_empty + i, 2 + 2 * kGroupThreads / 32);  // tensor-core, query and softmax warps
+      mbar_init(seg_empty + i, 3 + 2 * kGroupThreads / 32);  // every warp but the producer
     }
     gave_up = 0;
     fence_mbar_init();
@@ -705,125 +727,115 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (ok) ok = wait_warp(empty + use % NS, (use / NS) & 1);
       if (!ok) mbar_drain(full + use % NS, (use / NS) & 1);
     }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ tensor core
-    // One warp issues for both streams, the O += P V of a stream's tile before and the S = Q K^T of its
-    // next in one go: 1024 cycles of the tensor core, during which the other stream's softmax runs.
-    // (A warp per stream lets the two interleave and take twice as long each: 497 us where this
-    // takes 440, B=64 behind 32768 tokens.)  The whole warp walks the schedule, in uniform registers.
+  } else if (warp == 9 || warp == 10) {
+    // ------------------------------------------------------------ tensor core, stream s
+    // A warp per stream, taking turns: the O += P V of the stream's tile before and the S = Q K^T of its
+    // next go out in one go, 1024 cycles of the tensor core, during which the other stream's softmax
+    // runs and the other warp does its waiting.  (Without turns the two streams' products interleave
+    // and take twice as long each; one warp for both leaves the tensor core idle while it waits.)  The
+    // whole warp walks the schedule, in uniform registers.
     //
-    // A wait on a phase's parity is sound only within one phase of the barrier: a slot's use before this
-    // one has to have been waited for.  Before keys t that is values t - STAGES / 2 - 1 or so, of either
-    // stream, which are done by then, or done first where a stream had no turn for so long (a CTA
-    // changes deals, or from one stream a tile to both).
-    constexpr uint32_t kAlone = 16, kFirst = 32, kLast = 64, kHas = 128, kSlot = 256, kPhase = 4096, kSeen = 8192;
-    const uint32_t tm = uniform(tmem);
+    // Each of the two warps sees every tile land, in order, and releases each of its slots once - the
+    // stream that does not use a tile by a plain arrival.  A wait on a phase's parity is sound only
+    // within one phase of the barrier, and copies do not land in the order they were asked for:
+    // this way no slot can be filled again, or be a use behind, where either stream waits for it.
+    const int s = warp - 9;
+    const uint32_t tm = uniform(tmem), ts = tm + tmem_s(s), to = tm + tmem_o(s);
+    const uint32_t q_desc = swizzled_desc_lo(base + L::OFF_Q + s * L::BYTES, 16);
     const uint32_t values_idesc = idesc_f16<F16>(kTileKeys, D) | (1u << 16);  // B (values) MN-major
     const uint32_t scores_idesc = p.scale < 0.f ? 1u << 13 : 0u;              // a negative scale negates the queries
-    uint32_t slot = 0, phase = 0;  // of a tile's keys; its values are in the slot behind
-    uint32_t phases = 0;           // bit s: of p_ready[s]; bit 2 + s: of q_ready[s]
-    uint32_t pend0 = 0, pend1 = 0;  // the streams' tiles whose O += P V is still to be issued: units, flags, slot, phase, values seen
+    uint32_t slot = 0, phase = 0;     // of a tile's keys; its values are in the slot behind
+    uint32_t np = 0, nq = 0;          // P tiles, segments of this stream
+    uint32_t theirs = 0, ours = 0;    // the other stream's turns ahead of this warp's next; this warp's
+    // The tile whose O += P V is still to be issued; tiles of the other stream since.
+    bool pending = false, p_first = false, p_last = false;
+    uint32_t p_units = 0, p_slot = 0, p_phase = 0, since = 0;
     bool ok = true;
+    auto values_ready = [&]() -> bool { return wait_warp(full + p_slot, p_phase) && wait_warp(p_ready + s, np++ & 1); };
+    auto values = [&] {
+      pending = false;
+      tc_fence_after();
+      const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + p_slot * L::BYTES, L::HALF);
+      umma_values_first(to, ts, db, values_idesc, p_first ? 0u : 1u);
+      if (p_units == 8) {
+        umma_values_rest(to, ts, db, values_idesc);
+      } else {
+#pragma unroll 1
+        for (uint32_t u = 1; u < p_units; ++u) umma_values_first(to, ts + 8 * u, db + 128 * u, values_idesc, 1);
+      }
+      umma_commit_one(empty + p_slot);
+      if (p_last) umma_commit_one(o_done + s);
+    };
     for (uint32_t k = 0; ok; ++k) {
       const Seg& seg = segs[k % kSegRing];
       if (!wait_warp(seg_full + k % kSegRing, (k / kSegRing) & 1)) {
         ok = false;
         break;
       }
-      int t0 = int(uniform(uint32_t(seg.t0))), t1 = int(uniform(uint32_t(seg.t1)));
+      const int t0 = int(uniform(uint32_t(seg.t0))), t1 = int(uniform(uint32_t(seg.t1)));
       const int all = int(uniform(uint32_t(seg.units))), parity = int(uniform(uint32_t(seg.parity)));
-      bool paired = uniform(seg.paired() ? 1u : 0u) != 0;
-      const bool end = t1 < 0;  // no further segment: one more turn for the pending tiles
-      if (end) t0 = 0, t1 = 1, paired = true;
+      const bool paired = uniform(seg.paired() ? 1u : 0u) != 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(seg_empty + k % kSegRing);
-      for (int t = t0; ok && t < t1; ++t) {
-        // paired: both streams on this tile; else the one whose turn it is
-        const uint32_t units = uint32_t(all - 8 * t < 8 ? all - 8 * t : 8);
-        const int turn = (parity + t - t0) & 1;
-        const uint32_t q = kHas | (paired ? units | (t == t0 ? kFirst : 0u) | (t == t1 - 1 ? kLast : 0u)
-                                          : units | kAlone | (t - t0 < 2 ? kFirst : 0u) | (t1 - t <= 2 ? kLast : 0u));
+      const bool end = t1 < 0;
+      bool first = true;
+#pragma unroll 1
+      for (int t = t0; ok && (end || t < t1); ++t) {
         const uint32_t vslot = slot + 1 < NS ? slot + 1 : 0, vphase = slot + 1 < NS ? phase : phase ^ 1;
-#pragma unroll 1
-        for (int s = paired ? 0 : turn; ok && s <= (paired ? 1 : turn); ++s) {
-          bool landed = paired && s == 1;  // (stream 0 has waited for the tile's keys)
-          // O += P V of this stream's tile before; ahead of it the other stream's, if its values still hold
-          // the slot that these keys are to come to (it had no turn for three tiles).  As few waits and
-          // commits as there can be: the tensor core idles for whatever passes here between its products.
-          const uint32_t other = s ? pend0 : pend1;
-#pragma unroll 1
-          for (int v = !end && other && ((other / kSlot) & 15) == slot ? s ^ 1 : s;; v = s) {
-            const uint32_t was = v ? pend1 : pend0;
-            if (was) {
-              const uint32_t at = (was / kSlot) & 15;
-              if (!(was & kSeen)) {
-                ok = wait_warp(full + at, (was / kPhase) & 1);
-                if (v == 0 && pend1 && ((pend1 / kSlot) & 15) == at) pend1 |= kSeen;
-                // (whether the next keys are there is seen before the wait for P: one wait less between the products)
-                if (v == s && !end) landed = __all_sync(0xffffffffu, mbar_look(full + slot, phase));
-              }
-              ok = ok && wait_warp(p_ready + v, (phases >> v) & 1);
-              if (!ok) break;
-              phases ^= 1u << v;
-              tc_fence_after();
-              const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + at * L::BYTES, L::HALF);
-              umma_values_first(tm + tmem_o(v), tm + tmem_s(v), db, values_idesc, was & kFirst ? 0u : 1u);
-              if ((was & 15) == 8) {
-                umma_values_rest(tm + tmem_o(v), tm + tmem_s(v), db, values_idesc);
-              } else {
-#pragma unroll 1
-                for (uint32_t u = 1; u < (was & 15); ++u)
-                  umma_values_first(tm + tmem_o(v), tm + tmem_s(v) + 8 * u, db + 128 * u, values_idesc, 1);
-              }
-              umma_commit_one(empty + at);
-              if (was & (kAlone | kLast)) {
-                if (was & kAlone) umma_commit_one(empty + at);
-                if (was & kLast) umma_commit_one(o_done + v);
-              }
-              if (v)
-                pend1 = 0;
-              else
-                pend0 = 0;
-            }
-            if (v == s) break;
+        const bool skip = !end && !paired && ((parity + t - t0) & 1) != s;  // the other stream's tile
+        bool landed = false;
+        // what has to be there before this warp's turn
+        if (pending && (!skip || since)) {  // (a second tile of the other stream: its keys may need this slot)
+          ok = values_ready();
+          if (ok && !skip && !end) {
+            landed = __all_sync(0xffffffffu, mbar_look(full + slot, phase) && (!first || mbar_look(q_ready + s, nq & 1)));
           }
-          if (!ok) break;
-          if (end) continue;
-          if (q & kFirst) {
-            if (!wait_warp(q_ready + s, (phases >> (2 + s)) & 1)) {
-              ok = false;
-              break;
-            }
-            phases ^= 4u << s;
-          }
-          if (!landed && !wait_warp(full + slot, phase)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          umma_scores<D>(tm + tmem_s(s), swizzled_desc_lo(base + L::OFF_Q + s * L::BYTES, 16),
-                         swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16),
-                         idesc_f16<F16>(kTileKeys, int(16 * units)) | scores_idesc);
-          umma_commit_one(s_ready + s);
-          umma_commit_one(empty + slot);
-          if (q & (kAlone | kLast)) {
-            if (q & kAlone) umma_commit_one(empty + slot);
-            if (q & kLast) umma_commit_one(q_free + s);
-          }
-          const uint32_t now = q | vslot * kSlot | vphase * kPhase;
-          if (s)
-            pend1 = now;
-          else
-            pend0 = now;
         }
+        if (skip) {
+          if (ok && pending && since) values();
+          ++theirs, ++since;
+          ok = ok && wait_warp(full + slot, phase);
+          if (ok && lane == 0) mbar_arrive(empty + slot);
+          ok = ok && wait_warp(full + vslot, vphase);
+          if (ok && lane == 0) mbar_arrive(empty + vslot);
+          slot += 2, phase ^= slot >= NS ? 1u : 0u, slot -= slot >= NS ? NS : 0;
+          continue;
+        }
+        if (!ok) break;
+        if (paired && s == 1) ++theirs;
+        // (turns are about time alone: nothing breaks should this look give up)
+        for (uint32_t i = 0; !end && i < kMaxTurnLooks && __any_sync(0xffffffffu, turns[s ^ 1] < theirs); ++i) {
+        }
+        if (pending) values();
+        if (end) break;
+        // S = Q K^T of this tile; a turn does not wait for keys that are late
+        if (!landed) {
+          if (lane == 0) turns[s] = ++ours;
+          if (first) ok = wait_warp(q_ready + s, nq & 1);
+          ok = ok && wait_warp(full + slot, phase);
+          if (!ok) break;
+        }
+        tc_fence_after();
+        const uint32_t units = uint32_t(all - 8 * t < 8 ? all - 8 * t : 8);
+        const bool last = paired ? t == t1 - 1 : t1 - t <= 2;
+        umma_scores<D>(ts, q_desc, swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16),
+                       idesc_f16<F16>(kTileKeys, int(16 * units)) | scores_idesc);
+        if (landed && lane == 0) turns[s] = ++ours;
+        umma_commit_one(s_ready + s);
+        umma_commit_one(empty + slot);
+        if (last) umma_commit_one(q_free + s);
+        if (paired && s == 0) ++theirs;
+        if (first) ++nq;
+        pending = true, p_units = units, p_first = first, p_last = last, p_slot = vslot, p_phase = vphase, since = 0;
+        first = false;
         slot += 2, phase ^= slot >= NS ? 1u : 0u, slot -= slot >= NS ? NS : 0;
       }
       if (end) break;
     }
     if (!ok) {  // what is under way finishes before tensor memory is freed
-      umma_commit_one(o_done);
-      mbar_drain(o_done, 0);
-      mbar_drain(o_done, 1);
+      umma_commit_one(o_done + s);
+      mbar_drain(o_done + s, 0);
+      mbar_drain(o_done + s, 1);
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax: stream s, one row per thread
@@ -855,8 +867,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         continue;
       }
       const int step = paired ? 1 : 2;
-      const int srow0 = paired ? s * kTileKeys : 0;
-      const int rows = seg.rows - srow0 < kTileKeys ? seg.rows - srow0 : kTileKeys;
+      const int srow0 = paired ? s * p.tile_rows : 0;
+      const int rows = seg.rows - srow0 < p.tile_rows ? seg.rows - srow0 : p.tile_rows;
       const bool idle = 32 * (warp & 3) >= rows;  // a warp without rows only keeps the barriers going
 
       uint32_t seen = 0;  // own: the window tokens that this row sees
@@ -995,8 +1007,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tmem_ld32(to + q, o);
           if (r < rows) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<float4*>(out + q + j) = make_float4(o[j] * inv, o[j + 1] * inv, o[j + 2] * inv, o[j + 3] * inv);
+            for (int j = 0; j < 32; ++j) o[j] *= inv;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) store8(out + q + j, o + j);
           }
         }
         if (r < rows) w.lse[part] = l == 0.f ? -INFINITY : m * c + log2f(l);
@@ -1007,41 +1020,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   else if (warp == 11) {
     // ------------------------------------------------------------ queries, a segment ahead
-    // Rows behind the block's last keep what they hold: nothing reads their results.
-    constexpr int C = D / 8, STEP = 32 / C;  // a lane keeps its 16-byte column and takes every STEP-th row
-    const int ch = lane % C, step_tok = STEP / G, step_g = STEP - step_tok * G;
+    // By TMA, whole tokens of G heads.  Rows behind the block's last hold other tokens' queries or what
+    // was there: nothing reads their results.
     uint32_t nq0 = 0, nq1 = 0;  // segments of each stream
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       const Seg& seg = segs[k % kSegRing];
       if (!wait_warp(seg_full + k % kSegRing, (k / kSegRing) & 1) || seg.t1 < 0) break;
       const bool paired = seg.paired();
+      const int toks = seg.own && d.K < p.tile_toks ? d.K : p.tile_toks;
 #pragma unroll 1
       for (int i = 0; ok && i < 2; ++i) {
         const int s = paired ? i : (seg.parity + i) & 1;  // in the order of their first tiles
         if (!paired && i >= seg.t1 - seg.t0) continue;
-        const int srow0 = paired ? s * kTileKeys : 0;
-        const int rows = seg.rows - srow0 < kTileKeys ? seg.rows - srow0 : kTileKeys;
         const uint32_t nq = s ? nq1++ : nq0++;
         if (nq > 0) ok = wait_warp(q_free + s, (nq - 1) & 1);
         if (!ok) break;
-        int row = lane / C, tok = (seg.row0 + srow0 + row) / G, g = seg.row0 + srow0 + row - tok * G;
-        const uint16_t* const q = static_cast<const uint16_t*>(p.q) + seg.tok0 * d.q_token_stride + (long long)seg.h * G * D + ch * 8;
-        const uint32_t q_tile = base + L::OFF_Q + s * L::BYTES + (ch >> 3) * L::HALF;
-#pragma unroll 2
-        for (; row < rows; row += STEP) {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(q_tile + row * 128 + (((ch & 7) ^ (row & 7)) << 4)),
-                       "l"(q + tok * d.q_token_stride + g * D)
-                       : "memory");
-          g += step_g, tok += step_tok;
-          if (g >= G) g -= G, ++tok;
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
-        mbar_arrive(q_ready + s);
+        if (lane == 0) mbar_arrive_expect_tx(q_ready + s, uint32_t(toks * G) * D * 2);
+        __syncwarp();
+        if (lane < D / 64)
+          tma_load3(base + L::OFF_Q + s * L::BYTES + lane * L::HALF, seg.own ? &maps.qs : &maps.qt, lane * 64, seg.h * G,
+                    seg.tok0 + seg.row0 / G + (paired ? s * p.tile_toks : 0), smem_addr(q_ready + s));
+        __syncwarp();
       }
-      __syncwarp();
       if (lane == 0) mbar_arrive(seg_empty + k % kSegRing);
+    }
+    // (the tensor core waits for every tile of queries; after a wait that gave up, they land first)
+    if (!ok || gave_up) {
+      if (nq0 > 0) mbar_drain(q_ready, (nq0 - 1) & 1);
+      if (nq1 > 0) mbar_drain(q_ready + 1, (nq1 - 1) & 1);
     }
   }
   tc_fence_before();
@@ -1063,10 +1070,10 @@ template <int D, bool F16>
 __global__ void __launch_bounds__(32 * kJoinWarps, 8)
     attn_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWs w, const int join_rows) {
   constexpr int N = D / 32, U = 4;
-  // the partial results of a block's first row: of the sequence, and of the prefix's block that
-  // holds the CTA's first row and the one behind it
-  __shared__ long long list[3][2 * kCtas];
-  __shared__ int counts[3];
+  // the partial results of a block's first row: of the sequence (0, 1) and of the prefix (2, 3), the
+  // block that holds the CTA's first row and the one behind it
+  __shared__ long long list[4][2 * kCtas];
+  __shared__ int counts[4];
   __shared__ int row_at[kJoinWarps][32];
   __shared__ float row_w[kJoinWarps][32];
   grid_launch_dependents();
@@ -1080,21 +1087,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 8)
   const PlanHead head = *w.head;
   const int rows = KG - r0 < join_rows ? KG - r0 : join_rows;
   const long long pre0 = q.pre_at + r0;  // the CTA's first row in the prefix's
-  if (warp < 3) {
-    const bool own = warp == 0;
-    const long long all = own ? KG : q.pre_rows;
+  const int tile = p.tile_rows, block = 2 * tile;
+  {
+    const bool own = warp < 2;
+    const long long all = own ? KG : q.pre_rows, first = own ? r0 : pre0;
     const int n = own ? q.tiles : q.pre_tiles;
-    const long long rb = own ? r0 / kBlockRows : pre0 / kBlockRows + (warp - 1);
+    const long long rb = first / block + (warp & 1);
     int count = 0;
-    if (n > 0 && (warp < 2 || rb * kBlockRows < pre0 + rows)) {
+    if (n > 0 && ((warp & 1) == 0 || rb * block < first + rows)) {
       const long long deal = head.split && own ? head.prefix_tiles : 0;
       const long long size = !head.split ? head.tiles : own ? head.tiles - head.prefix_tiles : head.prefix_tiles;
-      const long long blocks = (all + kBlockRows - 1) / kBlockRows;
-      const int width = int(all - rb * kBlockRows < kBlockRows ? all - rb * kBlockRows : kBlockRows);
-      const bool paired = width > kTileKeys;
+      const long long blocks = (all + block - 1) / block;
+      const int width = int(all - rb * block < block ? all - rb * block : block);
+      const bool paired = width > tile;
       const long long from = (own ? q.off : q.pre_off) + (h * blocks + rb) * n;
       const int c0 = cta_of(from - deal, size), c1 = cta_of(from - deal + n - 1, size);
-      const long long base = (own ? head.own_row + (long long)b * d.Hkv * rows_width(KG) : q.pre_row) + h * rows_width(all) + rb * kBlockRows;
+      const long long base = (own ? head.own_row + (long long)b * d.Hkv * rows_width(KG, tile) : q.pre_row) + h * rows_width(all, tile) + rb * block;
       const int parts = (c1 - c0 + 1) * (paired ? 1 : 2);
       for (int i0 = 0; i0 < parts; i0 += 32) {
         const int i = i0 + lane, c = c0 + (paired ? i : i >> 1), s = paired ? 0 : i & 1;
@@ -1113,7 +1121,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 8)
     if (lane == 0) counts[warp] = count;
   }
   __syncthreads();
-  const int n_own = counts[0];
   for (int i = warp; i < rows; i += kJoinWarps) {
     const int r = r0 + i, t = r / G;
     float acc[N];
@@ -1122,15 +1129,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 8)
     float M = -INFINITY, W = 0.f;
     const bool live = t < q.win;
     if (live) {
-      const int side = (pre0 + i) / kBlockRows != pre0 / kBlockRows ? 2 : 1;
-      const int count = n_own + counts[side];
-      const int lr_own = r % kBlockRows, lr_pre = int((pre0 + i) % kBlockRows);
+      const int side_own = r / block != r0 / block ? 1 : 0, side = (pre0 + i) / block != pre0 / block ? 3 : 2;
+      const int n_own = counts[side_own], count = n_own + counts[side];
+      const int lr_own = r % block, lr_pre = int((pre0 + i) % block);
       for (int j0 = 0; j0 < count; j0 += 32) {
         const int j = j0 + lane;
         long long at = 0;
         float e = -INFINITY;
         if (j < count) {
-          at = j < n_own ? list[0][j] + lr_own : list[side][j - n_own] + lr_pre;
+          at = j < n_own ? list[side_own][j] + lr_own : list[side][j - n_own] + lr_pre;
           e = w.lse[at];
         }
         float mx = e;
@@ -1230,7 +1237,7 @@ cudaError_t launch(const AttnParams& p, const AttnWs& w, int box, const TileMaps
   if (e != cudaSuccess) return e;
   const int KG = p.d.K * (p.d.Hq / p.d.Hkv);
   const long long heads = (long long)p.d.B * p.d.Hkv;
-  int join_rows = kJoinRowsMax;  // a power of two: a CTA's rows are in one block of its sequence
+  int join_rows = kJoinRowsMax;
   while (join_rows > kJoinWarps && heads * ((KG + join_rows - 1) / join_rows) < 2 * kCtas) join_rows /= 2;
   return launch_pdl(attn_join_kernel<D, F16>, unsigned(heads * ((KG + join_rows - 1) / join_rows)), 32 * kJoinWarps, 0,
                     stream, p, w, join_rows);
@@ -1244,8 +1251,12 @@ size_t attn_workspace_bytes(const gdn_kv_dims& d) {
   return n;
 }
 
-cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) {
+cudaError_t launch_attn(const AttnParams& params, cudaStream_t stream) {
+  AttnParams p = params;
   const gdn_kv_dims& d = p.d;
+  const int G = d.Hq / d.Hkv;
+  p.tile_toks = kTileRows / G;
+  p.tile_rows = p.tile_toks * G;
   const EncodeTiled encode = encoder();
   if (!encode) return cudaErrorNotSupported;
   // Tokens per copy of a full tile: as many as lie together in a page, a divisor of the tile's 128.
@@ -1271,6 +1282,11 @@ cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) {
   const cuuint64_t wst[4] = {2ull * d.win_token_stride, 2ull * d.D, 2ull * d.K * d.win_token_stride, 2ull * d.K * d.win_token_stride};
   map(&maps.kw, p.k_win, 5, wd, wst, b16);
   map(&maps.vw, p.v_win, 5, wd, wst, b16);
+  const cuuint64_t qd[3] = {cuuint64_t(d.D), cuuint64_t(d.Hq), cuuint64_t(d.B) * d.K};
+  const cuuint64_t qst[2] = {2ull * d.D, 2ull * d.q_token_stride};
+  const cuuint32_t bt[3] = {64, cuuint32_t(G), cuuint32_t(p.tile_toks)}, bs[3] = {64, cuuint32_t(G), cuuint32_t(d.K < p.tile_toks ? d.K : p.tile_toks)};
+  map(&maps.qt, p.q, 3, qd, qst, bt);
+  map(&maps.qs, p.q, 3, qd, qst, bs);
   if (!ok) return cudaErrorInvalidValue;
   const AttnWs w = carve_attn(p.ws, d, nullptr);
   if (d.D == 128) return d.dtype ? launch<128, true>(p, w, box, maps, stream) : launch<128, false>(p, w, box, maps, stream);

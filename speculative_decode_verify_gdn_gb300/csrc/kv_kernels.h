@@ -30,6 +30,7 @@ struct AttnParams {
   float* lse;  // [B, K, Hq] or null
   void* ws;
   uint32_t* err;
+  int tile_toks, tile_rows;  // tokens and rows (tokens x query heads per kv head) of a row tile; set by launch_attn
 };
 
 size_t attn_workspace_bytes(const gdn_kv_dims& d);
