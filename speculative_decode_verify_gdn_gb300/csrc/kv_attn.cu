@@ -571,6 +571,18 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // tensor core's operands live in uniform registers).
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+// Maximum of a row's 128 scores, in four chains of two values a step (NaN counts for nothing).
+__device__ __forceinline__ float row_max(const float (&x)[128]) {
+  float m[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int j = 4; j < 124; j += 8)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) m[q] = fmaxf(fmaxf(m[q], x[j + q]), x[j + 4 + q]);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) m[q] = fmaxf(m[q], x[124 + q]);
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
 // Tensor-memory columns: S of stream s (P over its first half once S has been read), then O.
 constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t tmem_s(int s) { return 128u * uint32_t(s); }
@@ -751,7 +763,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool pending = false, p_first = false, p_last = false;
     uint32_t p_units = 0, p_slot = 0, p_phase = 0, since = 0;
     bool ok = true;
-    auto values_ready = [&]() -> bool { return wait_warp(full + p_slot, p_phase) && wait_warp(p_ready + s, np++ & 1); };
     auto values = [&] {
       pending = false;
       tc_fence_after();
@@ -786,10 +797,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         bool landed = false;
         // what has to be there before this warp's turn
         if (pending && (!skip || since)) {  // (a second tile of the other stream: its keys may need this slot)
-          ok = values_ready();
-          if (ok && !skip && !end) {
-            landed = __all_sync(0xffffffffu, mbar_look(full + slot, phase) && (!first || mbar_look(q_ready + s, nq & 1)));
-          }
+          ok = wait_warp(full + p_slot, p_phase);
+          landed = ok && !skip && !end &&
+                   __all_sync(0xffffffffu, mbar_look(full + slot, phase) && (!first || mbar_look(q_ready + s, nq & 1)));
+          ok = ok && wait_warp(p_ready + s, np++ & 1);
         }
         if (skip) {
           if (ok && pending && since) values();
@@ -923,17 +934,32 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               for (int j = 0; j < 32; ++j) x[32 * q + j] = (see >> j) & 1u ? x[32 * q + j] : -INFINITY;
             }
           }
-          float m4[4] = {x[0], x[1], x[2], x[3]};  // (four chains, two values a step)
+          // The exponentials take the maximum that is known and the tile's own is found beside them: only
+          // if a row lies more than kLag above is O rescaled and the tile's P done again.  (A pass for the
+          // maximum ahead of them adds a third to the softmax, which the tensor core waits for.)
+          if (first) m = row_max(x);
+          while (true) {
+            const float mc = m == -INFINITY ? 0.f : m * c;
+            const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int j = 4; j < 124; j += 8)
+            for (int q = 0; q < 4; ++q) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) m4[q] = fmaxf(fmaxf(m4[q], x[j + q]), x[j + 4 + q]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) m4[q] = fmaxf(m4[q], x[124 + q]);
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          const float up = (mx - m) * c;
-          const bool move = mx > m && !(up <= kLag) && r < rows;  // (m = -inf: up is inf)
-          if (__any_sync(0xffffffffu, move)) {
+              for (int j = 0; j < 16; ++j) {
+                const float2 e = fma2(make_float2(x[32 * q + 2 * j], x[32 * q + 2 * j + 1]), c2, mc2);
+                const float2 w2 = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+                sum = add2(sum, w2);
+                pk[j] = pack2<F16>(w2.x, w2.y);
+              }
+              tmem_st16_words(ts + 16 * q, pk);
+            }
+            const float mx = row_max(x);
+            const bool move = mx > m && !((mx - m) * c <= kLag) && r < rows;  // (m = -inf: infinitely far)
+            if (!__any_sync(0xffffffffu, move)) {
+              l += sum.x + sum.y;
+              break;
+            }
             const float f = move ? exp2_fast((m - mx) * c) : 1.f;
             if (!first) {
 #pragma unroll 1
@@ -947,22 +973,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             if (move) l *= f, m = mx;
           }
-          const float mc = m == -INFINITY ? 0.f : m * c;
-          const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
-          float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float2 e = fma2(make_float2(x[32 * q + 2 * j], x[32 * q + 2 * j + 1]), c2, mc2);
-              const float2 w2 = make_float2(exp2_fast(e.x), exp2_fast(e.y));
-              sum = add2(sum, w2);
-              pk[j] = pack2<F16>(w2.x, w2.y);
-            }
-            tmem_st16_words(ts + 16 * q, pk);
-          }
-          l += sum.x + sum.y;
           tmem_st_wait();
         }
         first = false;
