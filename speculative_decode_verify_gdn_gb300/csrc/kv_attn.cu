@@ -15,7 +15,7 @@
 //
 // The tile kernel: a producer warp brings keys and values by TMA (128-byte swizzle) into a ring
 // of tiles; a warp per stream issues S = Q K^T and O += P V (tcgen05, M = 128, accumulators in
-// tensor memory, P read from tensor memory); one warp fetches the next segment's queries; two
+// tensor memory, P read from tensor memory); one warp deals out segments and fetches their queries; two
 // groups of four warps, one per stream, turn S into P, a row per thread.  A block of more than 128 rows uses the two streams for its two halves on the
 // same keys; a smaller one gives them alternate tiles of the same rows.  While one stream's
 // softmax runs, the tensor core works for the other.
@@ -35,7 +35,7 @@ constexpr int kTileRows = 128;   // rows of a stream's tile, whole tokens of G q
 constexpr int kBlockRows = 256;  // rows of an item, at most
 constexpr int kPlanThreads = 1024;
 constexpr int kGroupThreads = 128;  // a softmax group: one thread per row of a stream
-constexpr int kTileThreads = 3 * kGroupThreads;  // two softmax groups; producer, two tensor-core warps, query warp
+constexpr int kTileThreads = 3 * kGroupThreads;  // two softmax groups; producer, two tensor-core warps, scheduler
 // Registers: 168 a thread at launch (64512 in all), then 224 for the softmax threads, which hold a
 // row of 128 scores, and 56 for the rest: 256 x 224 + 128 x 56 = 64512.
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
@@ -46,7 +46,7 @@ constexpr float kLn2 = 0.693147180559945f, kLog2e = 1.442695040888963f;
 constexpr float kLag = 8.0f;
 // Longest wait inside the tile kernel: looks of at most about a microsecond each, a few seconds in all.
 constexpr uint32_t kMaxLooks = 1u << 22;
-constexpr uint32_t kMaxTurnLooks = 1u << 14;
+constexpr uint32_t kMaxTurnLooks = 1u << 14, kMaxIdle = 1u << 25;
 
 // ---------------------------------------------------------------- the plan
 struct SeqRec {       // a sequence: what it does not share, and where its rows are in its prefix run
@@ -399,7 +399,7 @@ struct TileLayout {
   static constexpr int OFF_RING = 2 * BYTES;
   static constexpr int OFF_BAR = OFF_RING + STAGES * BYTES;
   static constexpr int NBAR = 2 * STAGES + 10 + 2 * kSegRing;
-  static constexpr int OFF_SEG = OFF_BAR + NBAR * 8;  // segments on their way from the producer
+  static constexpr int OFF_SEG = OFF_BAR + NBAR * 8;  // segments on their way from the scheduler
   static constexpr int TOTAL = OFF_SEG + kSegRing * int(sizeof(Seg)) + 1024;  // 1024: the base is aligned by hand
 };
 
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(seg_full + i, 1);
-      mbar_init(seg_empty + i, 3 + 2 * kGroupThreads / 32);  // every warp but the producer
+      mbar_init(seg_empty + i, 4 + 2 * kGroupThreads / 32);  // every warp, the one that hands them on included
     }
     gave_up = 0;
     fence_mbar_init();
@@ -677,62 +677,80 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 8) {
     // ------------------------------------------------------------ producer
-    SegWalk walk(p, w, int(blockIdx.x));
-    Seg seg;
-    uint32_t n = 0;  // tiles so far; tile n's keys are in ring slot 2n, its values in slot 2n + 1 (mod STAGES)
-    uint32_t issued = 0, k = 0;  // ring uses; segments handed on
-    bool ok = true;
-    while (ok) {
-      const bool more = walk.next(seg);
-      if (!wait_warp(seg_empty + k % kSegRing, ((k / kSegRing) & 1) ^ 1)) {
-        ok = false;
-        break;
+    // Copies go out as slots fall free; the page numbers of the tile behind are on their way meanwhile.
+    uint32_t n = 0, issued = 0;  // tiles and ring uses so far; tile n's keys are use 2n, its values 2n + 1
+    uint32_t k = 0;              // segments so far
+    int t = 0, t1 = 0;           // of the present segment: next tile, end
+    bool ok = true, more = true;
+    // the tile at hand (of a lane: its box), and how to get the one behind
+    int units = 0, boxes = 0, page = 0, in = 0, c4 = 0, h = 0;
+    uint32_t step = 0;  // bytes between boxes
+    const CUtensorMap* m = nullptr;
+    const int i = lane / (D / 64), half = lane % (D / 64);
+    auto next_tile = [&]() {
+      while (ok && t == t1) {
+        if (k > 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(seg_empty + (k - 1) % kSegRing);
+        }
+        ok = wait_warp(seg_full + k % kSegRing, (k / kSegRing) & 1);
+        t = segs[k % kSegRing].t0, t1 = segs[k % kSegRing].t1;
+        ++k;
+        if (t1 < 0) more = false;
+        if (t1 < 0 || !ok) return;
       }
-      if (lane == 0) {
-        if (!more) seg.t1 = -1;
-        segs[k % kSegRing] = seg;
-        mbar_arrive(seg_full + k % kSegRing);
-      }
-      __syncwarp();
-      ++k;
-      if (!more) break;
-      const int32_t* pages = p.table + (long long)seg.slot * d.max_pages;
-      for (int t = seg.t0; ok && t < seg.t1; ++t, ++n) {
-        const int u0 = 8 * t, units = seg.units - u0 < 8 ? seg.units - u0 : 8;
-        const int cached = (seg.keys + 15) / 16 - u0;  // units of this tile from the cache (may exceed 8)
-        const bool whole = cached >= 8;                // and none from the window: boxes of `box` tokens
-        const int rows = whole ? box : 16;
-        const int boxes = whole ? kTileKeys / box : units;
-        const int i = lane / (D / 64), half = lane % (D / 64);
-        int page = 0, in = 0;
-        const bool from_window = !whole && i == cached;  // (the window is the unit behind the cached ones)
-        if (i < boxes && !from_window) {
+      if (!ok) return;
+      const Seg& seg = segs[(k - 1) % kSegRing];
+      const int left = seg.units - 8 * t;
+      units = left < 8 ? left : 8;
+      const int cached = ((seg.keys + 15) >> 4) - 8 * t;  // units of this tile from the cache (may exceed 8)
+      const bool whole = cached >= 8;                     // and none from the window: boxes of `box` tokens
+      const int rows = whole ? box : 16;
+      boxes = whole ? kTileKeys / box : units;
+      step = uint32_t(rows) * 128;
+      m = whole ? &maps.kb : &maps.k16;
+      h = seg.h;
+      c4 = p.layer;
+      if (i < boxes) {
+        if (!whole && i == cached) {  // the window is the unit behind the cached ones
+          m = &maps.kw;
+          page = seg.idx, in = 0, c4 = 0;
+        } else {
           const int token = t * kTileKeys + i * rows, col = token / d.page_size;
           in = token - col * d.page_size;
-          page = pages[col];
-          if (page < 0 || page >= d.n_pages) {  // reads zeros there
-            atomicOr(p.err, GDN_DEVERR_KV_PAGE);
-            page = d.n_pages;
-          }
-        }
-        const int c3 = from_window ? seg.idx : page, c4 = from_window ? 0 : p.layer;
-        const CUtensorMap* const m = from_window ? &maps.kw : whole ? &maps.kb : &maps.k16;  // the values' map follows
-#pragma unroll 1
-        for (int v = 0; v < 2; ++v) {
-          const uint32_t use = 2 * n + v, slot = use % NS;
-          if (!wait_warp(empty + slot, ((use / NS) & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(full + slot, uint32_t(units) * 16 * D * 2);
-          __syncwarp();
-          if (i < boxes)
-            tma_load5(base + L::OFF_RING + slot * L::BYTES + half * L::HALF + i * rows * 128, m + v, half * 64, in, seg.h, c3, c4,
-                      smem_addr(full + slot));
-          __syncwarp();
-          issued = use + 1;
+          page = p.table[(long long)seg.slot * d.max_pages + col];
         }
       }
+      ++t;
+    };
+    next_tile();
+    while (ok && more) {
+      const int now_units = units, now_boxes = boxes, now_in = in, now_c4 = c4, now_h = h;
+      const uint32_t now_step = step;
+      const CUtensorMap* const now_m = m;
+      int now_page = page;
+      if (i < now_boxes && now_m != &maps.kw && (now_page < 0 || now_page >= d.n_pages)) {  // reads zeros there
+        atomicOr(p.err, GDN_DEVERR_KV_PAGE);
+        now_page = d.n_pages;
+      }
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {
+        const uint32_t use = 2 * n + v, slot = use % NS;
+        if (!wait_warp(empty + slot, ((use / NS) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(full + slot, uint32_t(now_units) * 16 * D * 2);
+        __syncwarp();
+        if (i < now_boxes)
+          tma_load5(base + L::OFF_RING + slot * L::BYTES + half * L::HALF + i * now_step, now_m + v, half * 64, now_in, now_h,
+                    now_page, now_c4, smem_addr(full + slot));
+        __syncwarp();
+        issued = use + 1;
+        if (v == 0) next_tile();
+        if (!ok) break;
+      }
+      ++n;
     }
     // the last uses of the ring: the copies have landed and the tensor core has read them
     for (uint32_t use = issued > NS ? issued - NS : 0; use < issued; ++use) {
@@ -741,7 +759,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp == 9 || warp == 10) {
     // ------------------------------------------------------------ tensor core, stream s
-    // A warp per stream, taking turns: the O += P V of the stream's tile before and the S = Q K^T of its
+    // A warp per stream, taking turns on the tiles they share: the O += P V of the stream's tile before and the S = Q K^T of its
     // next go out in one go, 1024 cycles of the tensor core, during which the other stream's softmax
     // runs and the other warp does its waiting.  (Without turns the two streams' products interleave
     // and take twice as long each; one warp for both leaves the tensor core idle while it waits.)  The
@@ -759,9 +777,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint32_t slot = 0, phase = 0;     // of a tile's keys; its values are in the slot behind
     uint32_t np = 0, nq = 0;          // P tiles, segments of this stream
     uint32_t theirs = 0, ours = 0;    // the other stream's turns ahead of this warp's next; this warp's
-    // The tile whose O += P V is still to be issued; tiles of the other stream since.
+    // The tile whose O += P V is still to be issued.
     bool pending = false, p_first = false, p_last = false;
-    uint32_t p_units = 0, p_slot = 0, p_phase = 0, since = 0;
+    uint32_t p_units = 0, p_slot = 0, p_phase = 0;
     bool ok = true;
     auto values = [&] {
       pending = false;
@@ -796,17 +814,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool skip = !end && !paired && ((parity + t - t0) & 1) != s;  // the other stream's tile
         bool landed = false;
         // what has to be there before this warp's turn
-        if (pending && (!skip || since)) {  // (a second tile of the other stream: its keys may need this slot)
+        if (pending) {
           ok = wait_warp(full + p_slot, p_phase);
-          landed = ok && !skip && !end &&
-                   __all_sync(0xffffffffu, mbar_look(full + slot, phase) && (!first || mbar_look(q_ready + s, nq & 1)));
+          landed = ok && !end && __all_sync(0xffffffffu, mbar_look(full + slot, phase) &&
+                                                             (skip || !first || mbar_look(q_ready + s, nq & 1)));
+          if (skip && landed && lane == 0) mbar_arrive(empty + slot);
           ok = ok && wait_warp(p_ready + s, np++ & 1);
         }
         if (skip) {
-          if (ok && pending && since) values();
-          ++theirs, ++since;
-          ok = ok && wait_warp(full + slot, phase);
-          if (ok && lane == 0) mbar_arrive(empty + slot);
+          // (tiles in alternation wait for memory: the values go at once, and their slot with them)
+          if (ok && pending) values();
+          ++theirs;
+          if (!landed) {
+            ok = ok && wait_warp(full + slot, phase);
+            if (ok && lane == 0) mbar_arrive(empty + slot);
+          }
           ok = ok && wait_warp(full + vslot, vphase);
           if (ok && lane == 0) mbar_arrive(empty + vslot);
           slot += 2, phase ^= slot >= NS ? 1u : 0u, slot -= slot >= NS ? NS : 0;
@@ -815,7 +837,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!ok) break;
         if (paired && s == 1) ++theirs;
         // (turns are about time alone: nothing breaks should this look give up)
-        for (uint32_t i = 0; !end && i < kMaxTurnLooks && __any_sync(0xffffffffu, turns[s ^ 1] < theirs); ++i) {
+        for (uint32_t i = 0; paired && !end && i < kMaxTurnLooks && __any_sync(0xffffffffu, turns[s ^ 1] < theirs); ++i) {
         }
         if (pending) values();
         if (end) break;
@@ -837,7 +859,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (last) umma_commit_one(q_free + s);
         if (paired && s == 0) ++theirs;
         if (first) ++nq;
-        pending = true, p_units = units, p_first = first, p_last = last, p_slot = vslot, p_phase = vphase, since = 0;
+        pending = true, p_units = units, p_first = first, p_last = last, p_slot = vslot, p_phase = vphase;
         first = false;
         slot += 2, phase ^= slot >= NS ? 1u : 0u, slot -= slot >= NS ? NS : 0;
       }
@@ -1029,34 +1051,67 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   }
   else if (warp == 11) {
-    // ------------------------------------------------------------ queries, a segment ahead
-    // By TMA, whole tokens of G heads.  Rows behind the block's last hold other tokens' queries or what
-    // was there: nothing reads their results.
-    uint32_t nq0 = 0, nq1 = 0;  // segments of each stream
-    bool ok = true;
-    for (uint32_t k = 0; ok; ++k) {
-      const Seg& seg = segs[k % kSegRing];
-      if (!wait_warp(seg_full + k % kSegRing, (k / kSegRing) & 1) || seg.t1 < 0) break;
-      const bool paired = seg.paired();
-      const int toks = seg.own && d.K < p.tile_toks ? d.K : p.tile_toks;
-#pragma unroll 1
-      for (int i = 0; ok && i < 2; ++i) {
-        const int s = paired ? i : (seg.parity + i) & 1;  // in the order of their first tiles
-        if (!paired && i >= seg.t1 - seg.t0) continue;
-        const uint32_t nq = s ? nq1++ : nq0++;
-        if (nq > 0) ok = wait_warp(q_free + s, (nq - 1) & 1);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(q_ready + s, uint32_t(toks * G) * D * 2);
+    // ------------------------------------------------------------ segments and queries, ahead of the rest
+    // Walks the CTA's stretches and hands segments on as the ring has room, and fetches a segment's
+    // queries as soon as the products with the ones before are done - whichever comes first.  Queries
+    // come by TMA, whole tokens of G heads: rows behind the block's last hold other tokens' queries or
+    // what was there, and nothing reads their results.
+    SegWalk walk(p, w, int(blockIdx.x));
+    uint32_t k = 0, kq = 0;      // segments handed on; segment whose queries are next
+    uint32_t nq0 = 0, nq1 = 0;   // segments of each stream
+    int part = 0;                // of segment kq: its first or second stream
+    uint32_t idle = 0;
+    bool more = true, ok = true;
+    while (ok && (more || kq < k)) {
+      bool did = false;
+      if (more && __all_sync(0xffffffffu, mbar_look(seg_empty + k % kSegRing, ((k / kSegRing) & 1) ^ 1))) {
+        Seg seg;
+        more = walk.next(seg);
+        if (lane == 0) {
+          if (!more) seg.t1 = -1;
+          segs[k % kSegRing] = seg;
+          mbar_arrive(seg_full + k % kSegRing);
+        }
         __syncwarp();
-        if (lane < D / 64)
-          tma_load3(base + L::OFF_Q + s * L::BYTES + lane * L::HALF, seg.own ? &maps.qs : &maps.qt, lane * 64, seg.h * G,
-                    seg.tok0 + seg.row0 / G + (paired ? s * p.tile_toks : 0), smem_addr(q_ready + s));
-        __syncwarp();
+        if (more) ++k;
+        did = true;
       }
-      if (lane == 0) mbar_arrive(seg_empty + k % kSegRing);
+      if (kq < k) {
+        const Seg& seg = segs[kq % kSegRing];
+        const bool paired = seg.paired();
+        const int s = paired ? part : (seg.parity + part) & 1;  // in the order of their first tiles
+        const uint32_t nq = s ? nq1 : nq0;
+        if (nq == 0 || __all_sync(0xffffffffu, mbar_look(q_free + s, (nq - 1) & 1))) {
+          const int toks = seg.own && d.K < p.tile_toks ? d.K : p.tile_toks;
+          if (lane == 0) mbar_arrive_expect_tx(q_ready + s, uint32_t(toks * G) * D * 2);
+          __syncwarp();
+          if (lane < D / 64)
+            tma_load3(base + L::OFF_Q + s * L::BYTES + lane * L::HALF, seg.own ? &maps.qs : &maps.qt, lane * 64, seg.h * G,
+                      seg.tok0 + seg.row0 / G + (paired ? s * p.tile_toks : 0), smem_addr(q_ready + s));
+          if (s)
+            ++nq1;
+          else
+            ++nq0;
+          if (++part == 2 || (!paired && seg.t1 - seg.t0 == 1)) {
+            part = 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(seg_empty + kq % kSegRing);
+            ++kq;
+          }
+          did = true;
+        }
+      }
+      idle = did ? 0 : idle + 1;
+      if (__any_sync(0xffffffffu, gave_up || idle > kMaxIdle)) {
+        if (idle > kMaxIdle) {
+          gave_up = 1;
+          atomicOr(p.err, kDevErrTimeout);
+        }
+        ok = false;
+      }
     }
     // (the tensor core waits for every tile of queries; after a wait that gave up, they land first)
-    if (!ok || gave_up) {
+    if (!ok) {
       if (nq0 > 0) mbar_drain(q_ready, (nq0 - 1) & 1);
       if (nq1 > 0) mbar_drain(q_ready + 1, (nq1 - 1) & 1);
     }
