@@ -618,6 +618,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   constexpr int NS = L::STAGES;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_slot;
+  __shared__ int page_of_box[32][2];
   __shared__ volatile uint32_t gave_up, turns[2];  // (turns: taken so far by each tensor-core warp)
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
@@ -677,14 +678,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 8) {
     // ------------------------------------------------------------ producer
-    // Copies go out as slots fall free; the page numbers of the tile behind are on their way meanwhile.
+    // Copies go out as slots fall free; the page numbers of the tile behind are on their way to shared
+    // memory meanwhile (into a register, the warp would wait for them at its next instruction).
     uint32_t n = 0, issued = 0;  // tiles and ring uses so far; tile n's keys are use 2n, its values 2n + 1
     uint32_t k = 0;              // segments so far
     int t = 0, t1 = 0;           // of the present segment: next tile, end
     bool ok = true, more = true;
     // the tile at hand (of a lane: its box), and how to get the one behind
-    int units = 0, boxes = 0, page = 0, in = 0, c4 = 0, h = 0;
-    uint32_t step = 0;  // bytes between boxes
+    int units = 0, boxes = 0, in = 0, c4 = 0, h = 0;
+    int* const page = page_of_box[lane];  // of this tile and the next in turn
+    uint32_t step = 0, ahead = 0;  // bytes between boxes; tiles looked up
     const CUtensorMap* m = nullptr;
     const int i = lane / (D / 64), half = lane % (D / 64);
     auto next_tile = [&]() {
@@ -714,21 +717,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (i < boxes) {
         if (!whole && i == cached) {  // the window is the unit behind the cached ones
           m = &maps.kw;
-          page = seg.idx, in = 0, c4 = 0;
+          in = 0, c4 = 0;
+          page[ahead & 1] = seg.idx;
         } else {
           const int token = t * kTileKeys + i * rows, col = token / d.page_size;
           in = token - col * d.page_size;
-          page = p.table[(long long)seg.slot * d.max_pages + col];
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(page + (ahead & 1))),
+                       "l"(p.table + (long long)seg.slot * d.max_pages + col)
+                       : "memory");
         }
       }
-      ++t;
+      ++t, ++ahead;
     };
     next_tile();
     while (ok && more) {
       const int now_units = units, now_boxes = boxes, now_in = in, now_c4 = c4, now_h = h;
       const uint32_t now_step = step;
       const CUtensorMap* const now_m = m;
-      int now_page = page;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      int now_page = page[n & 1];
       if (i < now_boxes && now_m != &maps.kw && (now_page < 0 || now_page >= d.n_pages)) {  // reads zeros there
         atomicOr(p.err, GDN_DEVERR_KV_PAGE);
         now_page = d.n_pages;
@@ -1293,7 +1300,7 @@ cudaError_t launch_pdl(void (*kernel)(Args...), unsigned grid, int threads, int 
 template <int D, bool F16>
 cudaError_t launch(const AttnParams& p, const AttnWs& w, int box, const TileMaps& maps, cudaStream_t stream) {
   using L = TileLayout<D>;
-  static_assert(L::TOTAL <= 232448 - 64, "shared memory");
+  static_assert(L::TOTAL <= 232448 - 512, "shared memory");
   cudaError_t e = launch_pdl(attn_plan_kernel, 1u, kPlanThreads, 0, stream, p, w);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(attn_tile_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL);
