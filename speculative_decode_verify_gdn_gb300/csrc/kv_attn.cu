@@ -412,11 +412,23 @@ struct TileMaps {
   CUtensorMap qt, qs;
 };
 
-__device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, int c4, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-      "l"(m), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
-      : "memory");
+// A box of tokens of one head, all D elements (two 64-column halves, 16 KB apart in the tile), by an
+// elected lane of the converged warp.
+template <int D>
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* m, int c1, int c2, int c3, int c4, uint32_t bar) {
+  if (D == 128)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%2, {%4, %6, %7, %8, %9}], [%3];\n\t"
+        "@q cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%1], [%2, {%5, %6, %7, %8, %9}], [%3];\n\t}" ::"r"(dst),
+        "r"(dst + kTileKeys * 128), "l"(m), "r"(bar), "r"(0), "r"(64), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];\n\t}" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
 }
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, uint32_t bar) {
   asm volatile(
@@ -570,6 +582,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // A value that all lanes hold, in a form that the compiler knows to be the same in all of them (the
 // tensor core's operands live in uniform registers).
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint32_t uniform_from(uint32_t x, int lane) { return __shfl_sync(0xffffffffu, x, lane); }
 
 // Maximum of a row's 128 scores, in four chains of two values a step (NaN counts for nothing).
 __device__ __forceinline__ float row_max(const float (&x)[128]) {
@@ -680,80 +693,81 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ------------------------------------------------------------ producer
     // Copies go out as slots fall free; the page numbers of the tile behind are on their way to shared
     // memory meanwhile (into a register, the warp would wait for them at its next instruction).
+    // Small pages make many copies (16 tokens each: 32 a tile of keys and values), so all that a copy
+    // needs is in uniform registers when its turn comes; lane i looks up box i.
     uint32_t n = 0, issued = 0;  // tiles and ring uses so far; tile n's keys are use 2n, its values 2n + 1
     uint32_t k = 0;              // segments so far
     int t = 0, t1 = 0;           // of the present segment: next tile, end
     bool ok = true, more = true;
-    // the tile at hand (of a lane: its box), and how to get the one behind
-    int units = 0, boxes = 0, in = 0, c4 = 0, h = 0;
+    uint32_t slot = 0, phase = 1;  // of the next use; the phase that its slot was emptied in
+    const float page_inv = 1.f / float(d.page_size);
+    // the segment at hand
+    int seg_units = 0, seg_cached = 0, seg_h = 0, seg_b = 0;
+    const int32_t* seg_pages = nullptr;
+    // the tile behind the one at hand
+    int units = 0, boxes = 0, in = 0;
+    uint32_t ahead = 0;     // tiles looked up
+    bool whole = false;     // all from the cache, in boxes of `box` tokens
+    int window = -1;        // the unit that is the window (-1: none)
     int* const page = page_of_box[lane];  // of this tile and the next in turn
-    uint32_t step = 0, ahead = 0;  // bytes between boxes; tiles looked up
-    const CUtensorMap* m = nullptr;
-    const int i = lane / (D / 64), half = lane % (D / 64);
     auto next_tile = [&]() {
       while (ok && t == t1) {
-        if (k > 0) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(seg_empty + (k - 1) % kSegRing);
-        }
+        __syncwarp();
+        if (k > 0 && lane == 0) mbar_arrive(seg_empty + (k - 1) % kSegRing);
         ok = wait_warp(seg_full + k % kSegRing, (k / kSegRing) & 1);
-        t = segs[k % kSegRing].t0, t1 = segs[k % kSegRing].t1;
+        const Seg& seg = segs[k % kSegRing];
+        t = int(uniform(uint32_t(seg.t0))), t1 = int(uniform(uint32_t(seg.t1)));
         ++k;
         if (t1 < 0) more = false;
         if (t1 < 0 || !ok) return;
+        seg_units = int(uniform(uint32_t(seg.units))), seg_cached = int(uniform(uint32_t((seg.keys + 15) >> 4)));
+        seg_h = int(uniform(uint32_t(seg.h))), seg_b = int(uniform(uint32_t(seg.idx)));
+        seg_pages = p.table + (long long)seg.slot * d.max_pages;
       }
       if (!ok) return;
-      const Seg& seg = segs[(k - 1) % kSegRing];
-      const int left = seg.units - 8 * t;
-      units = left < 8 ? left : 8;
-      const int cached = ((seg.keys + 15) >> 4) - 8 * t;  // units of this tile from the cache (may exceed 8)
-      const bool whole = cached >= 8;                     // and none from the window: boxes of `box` tokens
-      const int rows = whole ? box : 16;
+      units = seg_units - 8 * t < 8 ? seg_units - 8 * t : 8;
+      const int cached = seg_cached - 8 * t;  // units of this tile from the cache (may exceed 8)
+      whole = cached >= 8;
+      window = !whole && units > cached ? cached : -1;  // (the window is the unit behind the cached ones)
       boxes = whole ? kTileKeys / box : units;
-      step = uint32_t(rows) * 128;
-      m = whole ? &maps.kb : &maps.k16;
-      h = seg.h;
-      c4 = p.layer;
-      if (i < boxes) {
-        if (!whole && i == cached) {  // the window is the unit behind the cached ones
-          m = &maps.kw;
-          in = 0, c4 = 0;
-          page[ahead & 1] = seg.idx;
-        } else {
-          const int token = t * kTileKeys + i * rows, col = token / d.page_size;
-          in = token - col * d.page_size;
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(page + (ahead & 1))),
-                       "l"(p.table + (long long)seg.slot * d.max_pages + col)
-                       : "memory");
-        }
+      if (lane < boxes && lane != window) {
+        const int token = t * kTileKeys + lane * (whole ? box : 16);
+        int col = int(float(token) * page_inv);  // (within one)
+        in = token - col * d.page_size;
+        if (in < 0) --col, in += d.page_size;
+        if (in >= d.page_size) ++col, in -= d.page_size;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(page + (ahead & 1))), "l"(seg_pages + col) : "memory");
       }
       ++t, ++ahead;
     };
     next_tile();
     while (ok && more) {
-      const int now_units = units, now_boxes = boxes, now_in = in, now_c4 = c4, now_h = h;
-      const uint32_t now_step = step;
-      const CUtensorMap* const now_m = m;
+      const int now_units = units, now_boxes = boxes, now_in = in, now_window = window, now_h = seg_h, now_b = seg_b;
+      const bool now_whole = whole;
       asm volatile("cp.async.wait_all;" ::: "memory");
       int now_page = page[n & 1];
-      if (i < now_boxes && now_m != &maps.kw && (now_page < 0 || now_page >= d.n_pages)) {  // reads zeros there
+      if (lane < now_boxes && lane != now_window && (now_page < 0 || now_page >= d.n_pages)) {  // reads zeros there
         atomicOr(p.err, GDN_DEVERR_KV_PAGE);
         now_page = d.n_pages;
       }
 #pragma unroll 1
       for (int v = 0; v < 2; ++v) {
-        const uint32_t use = 2 * n + v, slot = use % NS;
-        if (!wait_warp(empty + slot, ((use / NS) & 1) ^ 1)) {
+        if (!wait_warp(empty + slot, phase)) {
           ok = false;
           break;
         }
         if (lane == 0) mbar_arrive_expect_tx(full + slot, uint32_t(now_units) * 16 * D * 2);
         __syncwarp();
-        if (i < now_boxes)
-          tma_load5(base + L::OFF_RING + slot * L::BYTES + half * L::HALF + i * now_step, now_m + v, half * 64, now_in, now_h,
-                    now_page, now_c4, smem_addr(full + slot));
-        __syncwarp();
-        issued = use + 1;
+        const uint32_t dst = base + L::OFF_RING + slot * L::BYTES, bar = smem_addr(full + slot), step = uint32_t(now_whole ? box : 16) * 128;
+        const CUtensorMap* const m = now_whole ? &maps.kb + v : &maps.k16 + v;
+#pragma unroll 2
+        for (int b = 0; b < now_boxes; ++b) {
+          const bool win = b == now_window;
+          const int c1 = win ? 0 : int(uniform_from(uint32_t(now_in), b)), c3 = win ? now_b : int(uniform_from(uint32_t(now_page), b));
+          tma_box<D>(dst + b * step, win ? &maps.kw + v : m, c1, now_h, c3, win ? 0 : p.layer, bar);
+        }
+        issued = 2 * n + v + 1;
+        if (++slot == NS) slot = 0, phase ^= 1;
         if (v == 0) next_tile();
         if (!ok) break;
       }
