@@ -5,7 +5,9 @@
 // run being consecutive sequences with the same prefix, and (sequence, kv head, block) for what a
 // sequence does not share.  A row is one query head of one window token; its block's rows all
 // meet the same keys, so the prefix is read and multiplied once for every sequence on it.  An
-// item's keys come in tiles of 128.  All tiles of all items, in order, are dealt to the CTAs (one
+// item's keys come in tiles of 128.  Prefix items are in the order run, head, block; the sequences'
+// in the order head, sequence, block, so that CTAs at work at the same time read the same tokens'
+// other heads, which lie beside each other in memory.  All tiles of all items, in order, are dealt to the CTAs (one
 // per SM) in equal contiguous stretches: a CTA's part of an item is a segment, it yields the
 // softmax-weighted sum and the log-sum-exp of its own keys (f32, in the workspace), and a last
 // kernel joins a row's segments.  Which CTA computes what depends on the lengths alone, so
@@ -50,7 +52,7 @@ constexpr uint32_t kMaxTurnLooks = 1u << 14, kMaxIdle = 1u << 25;
 
 // ---------------------------------------------------------------- the plan
 struct SeqRec {       // a sequence: what it does not share, and where its rows are in its prefix run
-  long long off;      // first tile of its items in the order of all tiles
+  long long off;      // its first tile among those of one kv head
   long long pre_off;  // the run's first tile
   long long pre_row;  // the run's first row of partial results
   long long pre_rows; // the run's rows per kv head
@@ -72,6 +74,7 @@ struct RunRec {       // consecutive sequences on one prefix
 struct PlanHead {
   long long tiles, prefix_tiles;  // in all; those of the runs come first
   long long own_row;              // first row of the sequences' partial results
+  long long head_tiles;           // the sequences' tiles of one kv head
   int32_t runs;
   int32_t split;                  // prefixes and sequences are dealt out apart from each other
 };
@@ -247,7 +250,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
   }
   __syncthreads();
   const long long prefix_tiles = tiles;
-  const int own_items = d.Hkv * ((KG + 2 * p.tile_rows - 1) / (2 * p.tile_rows));
+  const int own_blocks = (KG + 2 * p.tile_rows - 1) / (2 * p.tile_rows);
+  long long head_tiles = 0;
   for (int b0 = 0; b0 < d.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
     SeqRec q{};
@@ -266,11 +270,12 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
       }
     }
     long long total;
-    q.off = tiles + block_scan<long long>((long long)own_items * q.tiles, sums, total);
+    q.off = head_tiles + block_scan<long long>((long long)own_blocks * q.tiles, sums, total);
     if (b < d.B) w.seq[b] = q;
     if (once) seq_off[tid] = q.off;
-    tiles += total;
+    head_tiles += total;
   }
+  tiles += head_tiles * d.Hkv;
   const bool split = tiles >= kSplitTiles;
   if (tid == 0) {
     w.head->tiles = tiles;
@@ -278,6 +283,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     w.head->own_row = row + (split ? kBlockRows * kCtas : 0);
     w.head->runs = int(n_runs);
     w.head->split = split;
+    w.head->head_tiles = head_tiles;
   }
   __syncthreads();
   if (tid < 2 * kCtas) {  // where each stretch begins: the last record that starts at or before it
@@ -288,10 +294,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
       s.own = x >= prefix_tiles;
       const bool here = s.own ? once : n_runs <= kPlanThreads;
       const long long* const offs = s.own ? seq_off : run_off;
+      const long long y = s.own ? (x - prefix_tiles) % head_tiles : x;
       int lo = 0, hi = (s.own ? d.B : int(n_runs)) - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if ((here ? offs[mid] : s.own ? w.seq[mid].off : w.run[mid].off) <= x)
+        if ((here ? offs[mid] : s.own ? w.seq[mid].off : w.run[mid].off) <= y)
           lo = mid;
         else
           hi = mid - 1;
@@ -320,25 +327,26 @@ struct SegWalk {
   const AttnParams& p;
   const AttnWs& w;
   long long x, end;
-  int own, idx, cta, deal;
-  long long own_row;
+  int own, idx, h, cta, deal;  // (h: kv head of the sequences' items)
+  long long own_at, own_row, head_tiles;
   int runs;
   __device__ __forceinline__ SegWalk(const AttnParams& p_, const AttnWs& w_, int cta_) : p(p_), w(w_), cta(cta_) {
-    own_row = w.head->own_row, runs = w.head->runs;
+    own_at = w.head->prefix_tiles, own_row = w.head->own_row, head_tiles = w.head->head_tiles, runs = w.head->runs;
     deal = 0;
     begin();
   }
   __device__ __forceinline__ void begin() {  // the CTA's stretch of its first or second deal
-    const PlanHead h = *w.head;
-    if (h.split) {
+    const PlanHead g = *w.head;
+    if (g.split) {
       const int which = deal ^ (cta & 1);
-      const long long o = which ? h.prefix_tiles : 0, n = which ? h.tiles - h.prefix_tiles : h.prefix_tiles;
+      const long long o = which ? g.prefix_tiles : 0, n = which ? g.tiles - g.prefix_tiles : g.prefix_tiles;
       x = o + first_tile(cta, n), end = o + first_tile(cta + 1, n);
       own = w.start[which * kCtas + cta].own, idx = w.start[which * kCtas + cta].idx;
     } else {
-      x = deal ? 0 : first_tile(cta, h.tiles), end = deal ? 0 : first_tile(cta + 1, h.tiles);
+      x = deal ? 0 : first_tile(cta, g.tiles), end = deal ? 0 : first_tile(cta + 1, g.tiles);
       own = w.start[cta].own, idx = w.start[cta].idx;
     }
+    h = own && x < end ? int((x - own_at) / head_tiles) : 0;
   }
   __device__ __forceinline__ bool next(Seg& s) {
     if (x >= end && deal == 0) deal = 1, begin();
@@ -347,13 +355,16 @@ struct SegWalk {
     const int KG = d.K * (d.Hq / d.Hkv);
     while (true) {
       if (!own && idx == runs) own = 1, idx = 0;
-      if (own && idx >= d.B) return false;
+      if (own && idx >= d.B) {  // the next head's
+        if (++h >= d.Hkv) return false;
+        idx = 0;
+      }
       long long off, rows, row;
       int tiles;
       if (own) {
         const SeqRec q = w.seq[idx];
-        off = q.off, tiles = q.tiles, rows = KG;
-        row = own_row + (long long)idx * d.Hkv * rows_width(KG, p.tile_rows);
+        off = own_at + h * head_tiles + q.off, tiles = q.tiles, rows = KG;
+        row = own_row + ((long long)h * d.B + idx) * rows_width(KG, p.tile_rows);
         s.slot = d.slot0 + idx, s.keys = q.keys, s.win = q.win, s.tok0 = idx * d.K;
         s.units = (q.keys + 15) / 16 + 1;
       } else {
@@ -364,15 +375,15 @@ struct SegWalk {
       }
       const int block = 2 * p.tile_rows;
       const int blocks = int((rows + block - 1) / block);
-      const long long items = (long long)blocks * d.Hkv;
+      const long long items = own ? blocks : (long long)blocks * d.Hkv;
       if (tiles == 0 || x >= off + items * tiles) {
         ++idx;
         continue;
       }
       const int item = int((x - off) / tiles);
       s.own = own, s.idx = idx;
-      s.h = item / blocks;
-      const int rb = item - s.h * blocks;
+      const int ph = own ? 0 : item / blocks, rb = item - ph * blocks;
+      s.h = own ? h : ph;
       s.row0 = rb * block;
       s.rows = int(rows - s.row0 < block ? rows - s.row0 : block);
       s.pair = s.rows > p.tile_rows;
@@ -380,7 +391,7 @@ struct SegWalk {
       const long long left = end - x;
       s.t1 = left < tiles - s.t0 ? s.t0 + int(left) : tiles;
       s.parity = int(x & 1);
-      s.part = (long long)kBlockRows * cta + row + s.h * rows_width(rows, p.tile_rows) + s.row0;
+      s.part = (long long)kBlockRows * cta + row + ph * rows_width(rows, p.tile_rows) + s.row0;
       x += s.t1 - s.t0;
       return true;
     }
@@ -1186,9 +1197,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 8)
       const long long blocks = (all + block - 1) / block;
       const int width = int(all - rb * block < block ? all - rb * block : block);
       const bool paired = width > tile;
-      const long long from = (own ? q.off : q.pre_off) + (h * blocks + rb) * n;
+      const long long from = own ? head.prefix_tiles + h * head.head_tiles + q.off + rb * n : q.pre_off + (h * blocks + rb) * n;
       const int c0 = cta_of(from - deal, size), c1 = cta_of(from - deal + n - 1, size);
-      const long long base = (own ? head.own_row + (long long)b * d.Hkv * rows_width(KG, tile) : q.pre_row) + h * rows_width(all, tile) + rb * block;
+      const long long base = (own ? head.own_row + ((long long)h * d.B + b) * rows_width(KG, tile) : q.pre_row + h * rows_width(all, tile)) + rb * block;
       const int parts = (c1 - c0 + 1) * (paired ? 1 : 2);
       for (int i0 = 0; i0 < parts; i0 += 32) {
         const int i = i0 + lane, c = c0 + (paired ? i : i >> 1), s = paired ? 0 : i & 1;
