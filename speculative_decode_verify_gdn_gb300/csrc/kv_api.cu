@@ -57,7 +57,7 @@ gdn_status check_dims(const gdn_kv_dims* d, Use use, bool tree) {
     if (d->n_layers > 1 && (d->win_layer_stride % 8 || d->win_layer_stride < (int64_t)d->Hkv * d->D ||
                             d->win_layer_stride >= (1LL << 40)))
       return fail(GDN_ERR_INVALID_ARG, "win_layer_stride=%lld (a multiple of 8, at least Hkv * D)", (long long)d->win_layer_stride);
-    if ((long long)d->B * (d->K / d->page_size + 2) > (1LL << 30)) return fail(GDN_ERR_UNSUPPORTED, "B * K too large");
+    if ((long long)d->B * (d->K / 16 + 2) * d->n_layers > (1LL << 30)) return fail(GDN_ERR_UNSUPPORTED, "B * K * n_layers too large");
   }
   return GDN_OK;
 }

@@ -8,8 +8,11 @@
 // reference counts from the plan.
 //
 // Bound: the move is a copy, 2 bytes of HBM traffic per byte moved; the plan reads 4 bytes per
-// page of the pool.  Moves go 16 tokens of one layer at a time, 16 bytes a thread, as many loads
-// in flight as a thread has before its first store.
+// page of the pool and is a few dependent trips to L2 long.  A move takes 16 tokens of one layer
+// at a time, keys and values together, 16 bytes a thread and piece, eight loads in flight a
+// thread before its first store.  Pieces are found without a division (by multiplication, or
+// straight on where a page's tokens lie one behind the other): with two divisions a piece the
+// copy was bound by instructions, 5.1 of 6.8 TB/s over 1.65 GB.
 #include "gdn_common.cuh"
 #include "kv_kernels.h"
 
@@ -22,12 +25,12 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveTokens = 16;  // tokens of one layer moved by one CTA at a time
 
 struct CommitRec {  // plan of one sequence of a commit
-  int32_t n;      // tokens kept
-  int32_t len;    // tokens before
-  int32_t first;  // its first new page's rank in the free list
-  int32_t have;   // pages before
-  uint32_t path;  // window nodes of the path (tree)
-  int32_t pad[3];
+  int32_t n;       // tokens kept
+  int32_t len;     // tokens before
+  int32_t first;   // its first new page's rank in the free list
+  int32_t have;    // pages before
+  uint64_t nodes;  // tree: the path's window nodes, 4 bits each, the root's first
+  int32_t pad[2];
 };
 
 struct Move {  // one page's copy (fork, compact)
@@ -126,36 +129,53 @@ __device__ __forceinline__ int checked_len(int len, const gdn_kv_dims& d, uint32
   return len;
 }
 
-// `tokens` rows of Hkv heads x D elements of one layer, by the whole CTA.
-template <typename SrcRow>
-__device__ __forceinline__ void move_rows(uint16_t* dst, long long dst_token, long long dst_head, SrcRow src_row,
-                                          long long src_head, int tokens, int Hkv, int d8_shift) {
-  const int row = Hkv << d8_shift;  // 16-byte pieces of a token
-  const int n = tokens * row;
-  constexpr int U = 8;
+__device__ __forceinline__ uint4 load_piece(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// Keys and values of `n` 16-byte pieces by the whole CTA; from(i) and to(i) are a piece's places (in
+// elements, the same in keys and values).
+template <typename From, typename To>
+__device__ __forceinline__ void move_pieces(uint16_t* k_dst, uint16_t* v_dst, const uint16_t* k_src, const uint16_t* v_src, int n,
+                                            From from, To to) {
+  constexpr int U = 4;
   for (int i0 = threadIdx.x; i0 < n; i0 += U * kMoveThreads) {
-    uint4 v[U];
+    uint4 k[U], v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kMoveThreads;
       if (i < n) {
-        const int t = i / row, c = i - t * row, h = c >> d8_shift, e = c - (h << d8_shift);
-        v[u] = *reinterpret_cast<const uint4*>(src_row(t) + h * src_head + 8 * e);
+        const long long o = from(i);
+        k[u] = load_piece(k_src + o);
+        v[u] = load_piece(v_src + o);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kMoveThreads;
       if (i < n) {
-        const int t = i / row, c = i - t * row, h = c >> d8_shift, e = c - (h << d8_shift);
-        *reinterpret_cast<uint4*>(dst + t * dst_token + h * dst_head + 8 * e) = v[u];
+        const long long o = to(i);
+        *reinterpret_cast<uint4*>(k_dst + o) = k[u];
+        *reinterpret_cast<uint4*>(v_dst + o) = v[u];
       }
     }
   }
 }
 
+// Splits a piece of [token][head][D / 8] into its three indices; by_heads = ceil(2^32 / Hkv), exact
+// for the at most 16 x 4096 (token, head) pairs of a move.
+struct Piece {
+  int t, h, e;
+};
+__device__ __forceinline__ Piece split_piece(int i, int d8_shift, int Hkv, uint32_t by_heads) {
+  const int th = i >> d8_shift, t = Hkv == 1 ? th : int(__umulhi(uint32_t(th), by_heads));
+  return Piece{t, th - t * Hkv, i - (th << d8_shift)};
+}
+
 // ---------------------------------------------------------------- commit
-__global__ void __launch_bounds__(kPlanThreads) kv_commit_plan_kernel(const PagesParams p, PagesWs w) {
+__global__ void __launch_bounds__(kPlanThreads) kv_commit_plan_kernel(const __grid_constant__ PagesParams p, const __grid_constant__ PagesWs w) {
   __shared__ int sums[32];
   grid_launch_dependents();
   grid_wait();
@@ -180,19 +200,24 @@ __global__ void __launch_bounds__(kPlanThreads) kv_commit_plan_kernel(const Page
         atomicOr(p.err, GDN_DEVERR_ACCEPT_RANGE);
         n = 0;
       }
-      uint32_t path = 0;
+      uint64_t nodes = 0;
       if (p.parent && n > 0) {
-        int t = n - 1;
-        while (t >= 0) {
-          path |= 1u << t;
-          int up = p.parent[(long long)b * d.K + t];
-          if (up < -1 || up >= t) {
-            atomicOr(p.err, GDN_DEVERR_TREE_PARENT);
-            up = -1;
+        int up[kKvWinMax];  // (read together: one after the other they would be a trip to memory each)
+#pragma unroll
+        for (int t = 0; t < kKvWinMax; ++t) up[t] = t < n ? p.parent[(long long)b * d.K + t] : -1;
+        uint32_t path = 1u << (n - 1);
+        int count = 0;
+#pragma unroll
+        for (int t = kKvWinMax - 1; t >= 0; --t)
+          if (path >> t & 1) {
+            if (up[t] < -1 || up[t] >= t)
+              atomicOr(p.err, GDN_DEVERR_TREE_PARENT);
+            else if (up[t] >= 0)
+              path |= 1u << up[t];
+            nodes = nodes << 4 | uint64_t(t);  // (leaf first, so that the root ends lowest)
+            ++count;
           }
-          t = up;
-        }
-        n = __popc(path);
+        n = count;
       }
       const int have = pages_of(len, d.page_size);
       if (n > 0 && len % d.page_size != 0) {  // the page that still has room is this slot's own
@@ -213,7 +238,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_commit_plan_kernel(const Page
       r.n = n;
       r.len = len;
       r.have = have;
-      r.path = path;
+      r.nodes = nodes;
     }
     int total;
     r.first = wanted + block_scan(need, sums, total);
@@ -233,58 +258,56 @@ __global__ void __launch_bounds__(kPlanThreads) kv_commit_plan_kernel(const Page
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) kv_commit_move_kernel(const PagesParams p, PagesWs w, int tiles) {
-  __shared__ int node[kMoveTokens];
+// One CTA per (sequence, 16 tokens, layer).
+__global__ void __launch_bounds__(kMoveThreads) kv_commit_move_kernel(const __grid_constant__ PagesParams p, const PagesWs w, int tiles,
+                                                                      uint32_t by_heads) {
   grid_launch_dependents();
   grid_wait();
   const gdn_kv_dims& d = p.d;
   const int d8_shift = d.D == 128 ? 4 : 3;
-  const long long units = (long long)d.B * tiles * d.n_layers;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int layer = int(u % d.n_layers);
-    const long long v = u / d.n_layers;
-    const int tile = int(v % tiles), b = int(v / tiles);
-    const CommitRec r = w.rec[b];
-    const int t0 = tile * kMoveTokens;
-    if (r.n <= 0 || t0 >= r.n) continue;
-    const int tokens = r.n - t0 < kMoveTokens ? r.n - t0 : kMoveTokens;
-    const int slot = d.slot0 + b;
-    const int32_t* row = p.table_in + (long long)slot * d.max_pages;
-    __syncthreads();  // the node list of the unit before has been read
-    if (int(threadIdx.x) < tokens) {
-      int t = t0 + int(threadIdx.x);
-      if (p.parent) t = int(__fns(r.path, 0, t + 1));
-      node[threadIdx.x] = t;
+  const int layer = int(blockIdx.x % unsigned(d.n_layers)), unit = int(blockIdx.x / unsigned(d.n_layers));
+  const int tile = unit % tiles, b = unit / tiles;
+  const CommitRec r = w.rec[b];
+  const int t0 = tile * kMoveTokens;
+  if (r.n <= t0) return;
+  const int tokens = r.n - t0 < kMoveTokens ? r.n - t0 : kMoveTokens;
+  const int slot = d.slot0 + b;
+  const int32_t* row = p.table_in + (long long)slot * d.max_pages;
+  // the tokens lie in the page of the first, from `in` on, and the one behind it
+  const int at = r.len + t0, col = at / d.page_size, in = at - col * d.page_size;
+  auto page_at = [&](int c) { return c < r.have ? row[c] : w.ids[r.first + c - r.have]; };
+  const int page0 = page_at(col), page1 = in + tokens > d.page_size ? page_at(col + 1) : page0;
+  const long long layer_at = layer * d.cache_layer_stride;
+  const long long from = layer * d.win_layer_stride + (long long)b * d.K * d.win_token_stride;
+  const int D = d.D;
+  move_pieces(
+      p.k_cache, p.v_cache, p.k_win + from, p.v_win + from, tokens * d.Hkv << d8_shift,
+      [&](int i) {
+        const Piece q = split_piece(i, d8_shift, d.Hkv, by_heads);
+        const int node = p.parent ? int(r.nodes >> (4 * q.t) & 15) : t0 + q.t;
+        return node * d.win_token_stride + q.h * D + 8 * q.e;
+      },
+      [&](int i) {
+        const Piece q = split_piece(i, d8_shift, d.Hkv, by_heads);
+        const int pos = in + q.t;
+        const bool behind = pos >= d.page_size;
+        return layer_at + (behind ? page1 : page0) * d.cache_page_stride + (behind ? pos - d.page_size : pos) * d.cache_token_stride +
+               q.h * d.cache_head_stride + 8 * q.e;
+      });
+  if (tile == 0 && layer == 0) {
+    const int want = pages_of(r.len + r.n, d.page_size);
+    int32_t* out = p.table_out + (long long)slot * d.max_pages;
+    for (int c = r.have + int(threadIdx.x); c < want; c += kMoveThreads) {
+      const int page = w.ids[r.first + c - r.have];
+      out[c] = page;
+      p.ref_out[page] = 1;
     }
-    __syncthreads();
-    for (int s = 0; s < tokens;) {  // the stretch of tokens that lies in one page
-      const int at = r.len + t0 + s, col = at / d.page_size, in = at - col * d.page_size;
-      const int n = tokens - s < d.page_size - in ? tokens - s : d.page_size - in;
-      const int page = col < r.have ? row[col] : w.ids[r.first + col - r.have];
-      const long long to = layer * d.cache_layer_stride + page * d.cache_page_stride + in * d.cache_token_stride;
-      const long long from = layer * d.win_layer_stride + (long long)b * d.K * d.win_token_stride;
-      const int* nodes = node + s;
-      move_rows(p.k_cache + to, d.cache_token_stride, d.cache_head_stride,
-                [&](int t) { return p.k_win + from + nodes[t] * d.win_token_stride; }, d.D, n, d.Hkv, d8_shift);
-      move_rows(p.v_cache + to, d.cache_token_stride, d.cache_head_stride,
-                [&](int t) { return p.v_win + from + nodes[t] * d.win_token_stride; }, d.D, n, d.Hkv, d8_shift);
-      s += n;
-    }
-    if (tile == 0 && layer == 0) {
-      const int have = r.have, want = pages_of(r.len + r.n, d.page_size);
-      int32_t* out = p.table_out + (long long)slot * d.max_pages;
-      for (int c = have + int(threadIdx.x); c < want; c += kMoveThreads) {
-        const int page = w.ids[r.first + c - have];
-        out[c] = page;
-        p.ref_out[page] = 1;
-      }
-      if (threadIdx.x == 0) p.len_out[slot] = r.len + r.n;
-    }
+    if (threadIdx.x == 0) p.len_out[slot] = r.len + r.n;
   }
 }
 
 // ---------------------------------------------------------------- fork
-__global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const PagesParams p, PagesWs w) {
+__global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const __grid_constant__ PagesParams p, const __grid_constant__ PagesWs w) {
   __shared__ int sums[32];
   grid_launch_dependents();
   grid_wait();
@@ -292,21 +315,27 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const PagesP
   if (blockIdx.x > 0) {
     const int cta = int(blockIdx.x) - 1, ctas = int(gridDim.x) - 1;
     copy_ints(p.ref_out, p.ref_in, d.n_pages, cta, ctas);
-    for (int i = cta; i < d.n_slots; i += ctas) {
+    const long long entries = (long long)d.n_slots * d.max_pages;
+    for (long long e = (long long)cta * kPlanThreads + threadIdx.x; e < entries; e += (long long)ctas * kPlanThreads) {
+      const int i = int(e / d.max_pages), c = int(e - (long long)i * d.max_pages);
       int s = p.src[i];
       if (s < 0 || s >= d.n_slots) s = -1;
-      for (int c = int(threadIdx.x); c < d.max_pages; c += int(blockDim.x))
-        p.table_out[(long long)i * d.max_pages + c] = s < 0 ? -1 : p.table_in[(long long)s * d.max_pages + c];
+      p.table_out[e] = s < 0 ? -1 : p.table_in[(long long)s * d.max_pages + c];
     }
     return;
   }
-  for (int i = int(threadIdx.x); i < d.n_slots; i += kPlanThreads) w.first[i] = d.n_slots;
+  // lowest taker of each slot (in shared memory as far as that goes; the move reads it again)
+  __shared__ int first_here[kPlanThreads];
+  const bool here = d.n_slots <= kPlanThreads;
+  int* const first = here ? first_here : w.first;
+  for (int i = int(threadIdx.x); i < d.n_slots; i += kPlanThreads) first[i] = d.n_slots;
   __syncthreads();
   for (int i = int(threadIdx.x); i < d.n_slots; i += kPlanThreads) {
     const int s = p.src[i];
-    if (s >= 0 && s < d.n_slots) atomicMin(&w.first[s], i);
+    if (s >= 0 && s < d.n_slots) atomicMin(&first[s], i);
   }
   __syncthreads();
+  if (here && int(threadIdx.x) < d.n_slots) w.first[threadIdx.x] = first[threadIdx.x];
   int copies = 0;
   for (int pass = 0; pass < 2; ++pass) {  // count the copies; then hand out pages
     int found = 0;
@@ -326,7 +355,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const PagesP
         }
         if (s >= 0) {
           len = checked_len(p.len_in[s], d, p.err);
-          copy = (len % d.page_size != 0 && w.first[s] != i) ? 1 : 0;
+          copy = (len % d.page_size != 0 && first[s] != i) ? 1 : 0;
         }
       }
       int total;
@@ -362,31 +391,36 @@ __device__ __forceinline__ void add_ref(int32_t* ref, int id, int delta, const g
 }
 
 // Copies the listed pages' filled tokens, all layers, keys and values.
-__device__ void move_pages(const PagesParams& p, const PagesWs& w) {
+__device__ __forceinline__ void move_pages(const PagesParams& p, const PagesWs& w, uint32_t by_heads) {
   const gdn_kv_dims& d = p.d;
   const int d8_shift = d.D == 128 ? 4 : 3;
-  const int tiles = (d.page_size + kMoveTokens - 1) / kMoveTokens;
-  const long long units = (long long)w.head[0] * d.n_layers * tiles;
+  const unsigned tiles = unsigned(d.page_size + kMoveTokens - 1) / kMoveTokens, per_page = tiles * unsigned(d.n_layers);
+  const bool straight = d.cache_head_stride == d.D && d.cache_token_stride == (long long)d.Hkv * d.D;
+  const long long units = (long long)w.head[0] * per_page;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int tile = int(u % tiles);
-    const long long v = u / tiles;
-    const int layer = int(v % d.n_layers);
-    const Move m = w.move[v / d.n_layers];
-    const int t0 = tile * kMoveTokens;
+    const long long page = u / per_page;
+    const unsigned in_page = unsigned(u - page * per_page);
+    const int layer = int(in_page / tiles), t0 = int(in_page % tiles) * kMoveTokens;
+    const Move m = w.move[page];
     const int tokens = m.tokens - t0 < kMoveTokens ? m.tokens - t0 : kMoveTokens;
     if (tokens <= 0) continue;
     const long long base = layer * d.cache_layer_stride + t0 * d.cache_token_stride;
     const long long to = base + m.to * d.cache_page_stride, from = base + m.from * d.cache_page_stride;
-    move_rows(p.k_cache + to, d.cache_token_stride, d.cache_head_stride,
-              [&](int t) { return p.k_cache + from + t * d.cache_token_stride; }, d.cache_head_stride, tokens, d.Hkv,
-              d8_shift);
-    move_rows(p.v_cache + to, d.cache_token_stride, d.cache_head_stride,
-              [&](int t) { return p.v_cache + from + t * d.cache_token_stride; }, d.cache_head_stride, tokens, d.Hkv,
-              d8_shift);
+    const int n = tokens * d.Hkv << d8_shift;
+    if (straight) {
+      auto at = [](int i) { return 8ll * i; };
+      move_pieces(p.k_cache + to, p.v_cache + to, p.k_cache + from, p.v_cache + from, n, at, at);
+    } else {
+      auto at = [&](int i) {
+        const Piece q = split_piece(i, d8_shift, d.Hkv, by_heads);
+        return q.t * d.cache_token_stride + q.h * d.cache_head_stride + 8 * q.e;
+      };
+      move_pieces(p.k_cache + to, p.v_cache + to, p.k_cache + from, p.v_cache + from, n, at, at);
+    }
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) kv_fork_move_kernel(const PagesParams p, PagesWs w) {
+__global__ void __launch_bounds__(kMoveThreads) kv_fork_move_kernel(const __grid_constant__ PagesParams p, const __grid_constant__ PagesWs w, uint32_t by_heads) {
   grid_launch_dependents();
   grid_wait();
   const gdn_kv_dims& d = p.d;
@@ -420,11 +454,11 @@ __global__ void __launch_bounds__(kMoveThreads) kv_fork_move_kernel(const PagesP
     }
     if (threadIdx.x == 0) p.len_out[i] = len;
   }
-  move_pages(p, w);
+  move_pages(p, w, by_heads);
 }
 
 // ---------------------------------------------------------------- compact
-__global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const PagesParams p, PagesWs w) {
+__global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const __grid_constant__ PagesParams p, const __grid_constant__ PagesWs w) {
   __shared__ int sums[32];
   grid_launch_dependents();
   grid_wait();
@@ -434,6 +468,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const Pag
     return;
   }
   int mine = 0;
+#pragma unroll 4
   for (int i = int(threadIdx.x); i < d.n_pages; i += kPlanThreads) mine += p.ref_in[i] > 0;
   int live;
   block_scan(mine, sums, live);
@@ -441,16 +476,26 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const Pag
   for (int side = 0; side < 2; ++side) {
     const int lo = side ? live : 0, hi = side ? d.n_pages : live;
     int count = 0;
-    for (int at = lo; at < hi; at += kPlanThreads) {
-      const int i = at + int(threadIdx.x);
-      const int take = (i < hi && (p.ref_in[i] > 0) == (side == 1)) ? 1 : 0;
+    for (int at = lo; at < hi; at += 4 * kPlanThreads) {
+      const int i0 = at + 4 * int(threadIdx.x);
+      int take = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (i0 + q < hi && (p.ref_in[i0 + q] > 0) == (side == 1)) take |= 1 << q;
       int total;
-      const int r = count + block_scan(take, sums, total);
-      if (side == 0) {
-        if (take) w.ids[r] = i;
-      } else if (i < hi) {
-        w.map[i] = take ? w.ids[r] : -1;
-        if (take) w.move[r] = Move{i, w.ids[r], d.page_size, 0};
+      int r = count + block_scan(__popc(take), sums, total);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + q;
+        if (i >= hi) continue;
+        const bool taken = take >> q & 1;
+        if (side == 0) {
+          if (taken) w.ids[r++] = i;
+        } else {
+          const int to = taken ? w.ids[r++] : -1;
+          w.map[i] = to;
+          if (taken) w.move[r - 1] = Move{i, to, d.page_size, 0};
+        }
       }
       count += total;
     }
@@ -459,7 +504,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const Pag
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) kv_compact_move_kernel(const PagesParams p, PagesWs w) {
+__global__ void __launch_bounds__(kMoveThreads) kv_compact_move_kernel(const __grid_constant__ PagesParams p, const __grid_constant__ PagesWs w, uint32_t by_heads) {
   grid_launch_dependents();
   grid_wait();
   const gdn_kv_dims& d = p.d;
@@ -487,7 +532,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_move_kernel(const Pag
       out[c] = page;
     }
   }
-  move_pages(p, w);
+  move_pages(p, w, by_heads);
 }
 
 template <typename... Args>
@@ -503,6 +548,8 @@ cudaError_t launch_pdl(void (*kernel)(Args...), int grid, int threads, cudaStrea
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
+uint32_t by_heads(const gdn_kv_dims& d) { return uint32_t(((1ull << 32) + d.Hkv - 1) / d.Hkv); }  // (unused for one head)
 
 // CTAs of a move over `units` pieces: what fits on the card at once, no more than there are pieces.
 int move_grid(long long units) { return int(units < 1 ? 1 : (units < 152 * 8 ? units : 152 * 8)); }
@@ -525,8 +572,9 @@ cudaError_t launch_commit(const PagesParams& p, cudaStream_t stream) {
   cudaError_t e = launch_pdl(kv_commit_plan_kernel, plan_grid((long long)d.n_slots * d.max_pages + d.n_pages),
                              kPlanThreads, stream, p, w);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv_commit_move_kernel, move_grid((long long)d.B * tiles * d.n_layers), kMoveThreads, stream, p, w,
-                    tiles);
+  const long long units = (long long)d.B * tiles * d.n_layers;
+  if (units == 0) return cudaSuccess;
+  return launch_pdl(kv_commit_move_kernel, int(units), kMoveThreads, stream, p, w, tiles, by_heads(d));
 }
 
 cudaError_t launch_fork(const PagesParams& p, cudaStream_t stream) {
@@ -536,7 +584,7 @@ cudaError_t launch_fork(const PagesParams& p, cudaStream_t stream) {
                              kPlanThreads, stream, p, w);
   if (e != cudaSuccess) return e;
   const long long units = (long long)d.n_slots * d.n_layers * (d.page_size / kMoveTokens);
-  return launch_pdl(kv_fork_move_kernel, move_grid(units), kMoveThreads, stream, p, w);
+  return launch_pdl(kv_fork_move_kernel, move_grid(units), kMoveThreads, stream, p, w, by_heads(d));
 }
 
 cudaError_t launch_compact(const PagesParams& p, cudaStream_t stream) {
@@ -545,7 +593,7 @@ cudaError_t launch_compact(const PagesParams& p, cudaStream_t stream) {
   cudaError_t e = launch_pdl(kv_compact_plan_kernel, plan_grid(d.n_pages), kPlanThreads, stream, p, w);
   if (e != cudaSuccess) return e;
   const long long units = (long long)d.n_pages * d.n_layers * (d.page_size / kMoveTokens);
-  return launch_pdl(kv_compact_move_kernel, move_grid(units), kMoveThreads, stream, p, w);
+  return launch_pdl(kv_compact_move_kernel, move_grid(units), kMoveThreads, stream, p, w, by_heads(d));
 }
 
 }  // namespace gdn
