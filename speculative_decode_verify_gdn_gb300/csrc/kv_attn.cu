@@ -21,6 +21,7 @@
 // groups of four warps, one per stream, turn S into P, a row per thread.  A block of more than 128 rows uses the two streams for its two halves on the
 // same keys; a smaller one gives them alternate tiles of the same rows.  While one stream's
 // softmax runs, the tensor core works for the other.
+#include <atomic>
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -1328,8 +1329,15 @@ cudaError_t launch(const AttnParams& p, const AttnWs& w, int box, const TileMaps
   static_assert(L::TOTAL <= 232448 - 512, "shared memory");
   cudaError_t e = launch_pdl(attn_plan_kernel, 1u, kPlanThreads, 0, stream, p, w);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(attn_tile_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL);
+  static std::atomic<uint64_t> allowed{0};  // a bit per device: the kernel may use its shared memory there
+  int dev = 0;
+  e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (!(allowed.load() >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(attn_tile_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(1ull << (dev & 63));
+  }
   e = launch_pdl(attn_tile_kernel<D, F16>, unsigned(kCtas), kTileThreads, L::TOTAL, stream, p, w, box, maps);
   if (e != cudaSuccess) return e;
   const int KG = p.d.K * (p.d.Hq / p.d.Hkv);

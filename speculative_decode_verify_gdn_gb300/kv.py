@@ -17,7 +17,7 @@ import ctypes
 import torch
 
 from . import gdn
-from .gdn import _check, _stream
+from .gdn import _check
 
 EXPORTED = ("gdn_attn_verify", "gdn_attn_workspace_size", "gdn_kv_commit", "gdn_kv_fork", "gdn_kv_compact",
             "gdn_kv_workspace_size")
@@ -26,6 +26,7 @@ DEVERR_KV_LEN, DEVERR_KV_PAGE, DEVERR_KV_SLOT, DEVERR_KV_FULL, DEVERR_KV_SHARED,
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 _TORCH = (torch.bfloat16, torch.float16)
+_I32 = torch.int32
 
 
 class KvDims(ctypes.Structure):
@@ -76,7 +77,16 @@ def load_library() -> ctypes.CDLL:
 
 
 def _tensor(t, name, dtype, shape, strides):
-    """Address of a CUDA tensor of this dtype, shape and strides (those of single entries aside)."""
+    """Address of a CUDA tensor of this dtype, shape and strides (those of single entries aside;
+    None: contiguous)."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and \
+            (t.is_contiguous() if strides is None else t.stride() == strides):
+        return t.data_ptr()
+    return _explain(t, name, dtype, shape, strides)
+
+
+def _explain(t, name, dtype, shape, strides):
+    """What _tensor found amiss, if anything is."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -88,17 +98,19 @@ def _tensor(t, name, dtype, shape, strides):
     if strides is None:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-    elif t.stride() != strides:
-        for n, have, want in zip(shape, t.stride(), strides):
-            if n > 1 and have != want:
-                raise ValueError(f"{name} has strides {t.stride()}, dims say {strides}")
+    elif any(n > 1 and have != want for n, have, want in zip(shape, t.stride(), strides)):
+        raise ValueError(f"{name} has strides {t.stride()}, dims say {strides}")
     return t.data_ptr()
 
 
 def _ints(t, name, shape, optional=False):
     if t is None and optional:
         return None
-    return _tensor(t, name, torch.int32, shape, None)
+    return _tensor(t, name, _I32, shape, None)
+
+
+def _stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def _cache(d, k_cache, v_cache):
