@@ -1,0 +1,99 @@
+"""Device-resident paged cache of a hybrid model's softmax-attention layers, and its part of the
+verify round (attend -> commit, fork, compact).
+
+Torch allocates the memory; every step runs through the C ABI (include/gdn_kv.h).  The slots are
+the batch's sequences, 0..B-1, and behind them the shared prefixes.  Tables, lengths and
+reference counts are updated in place except by a fork, which writes the other one of two sets.
+"""
+from __future__ import annotations
+
+import math
+from dataclasses import dataclass
+
+import torch
+
+from . import kv
+
+
+@dataclass
+class PagedCache:
+    B: int
+    K: int
+    Hq: int
+    Hkv: int
+    D: int
+    page_size: int
+    n_pages: int
+    max_pages: int
+    n_prefixes: int
+    n_layers: int
+    dtype: torch.dtype
+    k: torch.Tensor           # [n_layers, n_pages, page_size, Hkv, D]
+    v: torch.Tensor
+    tables: list              # two [n_slots, max_pages] int32
+    lens: list                # two [n_slots] int32
+    ref: torch.Tensor         # [n_pages] int32
+    prefix_of: torch.Tensor   # [B] int32: slot of the sequence's prefix, -1 without
+    n_live: torch.Tensor      # [1] int32, set by compact
+    dims: kv.KvDims
+    attn_workspace: torch.Tensor
+    pool_workspace: torch.Tensor
+    cur: int = 0
+
+    @classmethod
+    def create(cls, B, K, Hq, Hkv, D, page_size, n_pages, max_pages, n_prefixes=0, n_layers=1, dtype=torch.bfloat16,
+               device="cuda") -> "PagedCache":
+        n_slots = B + n_prefixes
+        dims = kv.make_kv_dims(B, K, Hq, Hkv, D, page_size, n_pages, max_pages, n_slots, 0, n_layers, dtype)
+        shape = (n_layers, n_pages, page_size, Hkv, D)
+
+        def ints(*s, fill=0):
+            return torch.full(s, fill, dtype=torch.int32, device=device)
+
+        return cls(B, K, Hq, Hkv, D, page_size, n_pages, max_pages, n_prefixes, n_layers, dtype,
+                   torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device),
+                   [ints(n_slots, max_pages, fill=-1) for _ in range(2)], [ints(n_slots) for _ in range(2)],
+                   ints(n_pages), ints(B, fill=-1), ints(1), dims, kv.alloc_attn_workspace(dims, device),
+                   kv.alloc_kv_workspace(dims, device))
+
+    @property
+    def table(self) -> torch.Tensor:
+        return self.tables[self.cur]
+
+    @property
+    def seq_len(self) -> torch.Tensor:
+        return self.lens[self.cur]
+
+    def append(self, slot, k_new, v_new, stream=None) -> None:
+        """Adds N tokens [n_layers, N, Hkv, D] to one slot: a prompt, or a shared prefix."""
+        n = k_new.shape[1]
+        d = kv.make_kv_dims(1, n, self.Hq, self.Hkv, self.D, self.page_size, self.n_pages, self.max_pages,
+                            self.B + self.n_prefixes, slot, self.n_layers, self.dtype, win=k_new.unsqueeze(1))
+        all_of_it = torch.full((1,), n, dtype=torch.int32, device=k_new.device)
+        kv.gdn_kv_commit(d, all_of_it, None, k_new.unsqueeze(1), v_new.unsqueeze(1), self.k, self.v, self.table,
+                         self.table, self.seq_len, self.seq_len, self.ref, self.ref,
+                         kv.alloc_kv_workspace(d, k_new.device), stream)
+
+    def attend(self, layer, q, k_win, v_win, out, lse=None, parent=None, win_len=None, scale=None, stream=None) -> None:
+        """The window's attention in one layer (a chain, or a token tree given by parent [B, K])."""
+        kv.gdn_attn_verify(self.dims, layer, q, k_win, v_win, self.k, self.v, self.table, self.seq_len,
+                           self.prefix_of if self.n_prefixes else None, win_len, parent,
+                           1.0 / math.sqrt(self.D) if scale is None else scale, out, lse, self.attn_workspace, stream)
+
+    def commit(self, accept_len, k_win, v_win, parent=None, stream=None) -> None:
+        """Keeps each sequence's accepted window tokens, all layers: k_win, v_win [n_layers, B, K, Hkv, D]."""
+        kv.gdn_kv_commit(self.dims, accept_len, parent, k_win, v_win, self.k, self.v, self.table, self.table,
+                         self.seq_len, self.seq_len, self.ref, self.ref, self.pool_workspace, stream)
+
+    def fork(self, src, stream=None) -> None:
+        """Sequence i goes on from sequence src[i] (src [n_slots] int32; prefixes keep their slots by
+        src[s] = s, and the sequences their prefix_of); -1 drops it."""
+        i, o = self.cur, 1 - self.cur
+        kv.gdn_kv_fork(self.dims, src, self.k, self.v, self.tables[i], self.tables[o], self.lens[i], self.lens[o],
+                       self.ref, self.ref, self.pool_workspace, stream)
+        self.cur = o
+
+    def compact(self, stream=None) -> None:
+        """Moves the live pages to the front of the pool; their number goes to n_live."""
+        kv.gdn_kv_compact(self.dims, self.k, self.v, self.table, self.table, self.seq_len, self.ref, self.ref,
+                          self.n_live, self.pool_workspace, stream)
