@@ -39,9 +39,6 @@ constexpr int kBlockRows = 256;  // rows of an item, at most
 constexpr int kPlanThreads = 1024;
 constexpr int kGroupThreads = 128;  // a softmax group: one thread per row of a stream
 constexpr int kTileThreads = 3 * kGroupThreads;  // two softmax groups; producer, two tensor-core warps, scheduler
-// Registers: 168 a thread at launch (64512 in all), then 224 for the softmax threads, which hold a
-// row of 128 scores, and 56 for the rest: 256 x 224 + 128 x 56 = 64512.
-constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 constexpr int kJoinWarps = 4, kJoinRowsMax = 32;  // (four warps: four lists)
 constexpr float kLn2 = 0.693147180559945f, kLog2e = 1.442695040888963f;
 // A running maximum may lag behind by up to 8 powers of two before O is rescaled: probabilities
@@ -596,16 +593,35 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ uint32_t uniform_from(uint32_t x, int lane) { return __shfl_sync(0xffffffffu, x, lane); }
 
-// Maximum of a row's 128 scores, in four chains of two values a step (NaN counts for nothing).
-__device__ __forceinline__ float row_max(const float (&x)[128]) {
+// Maximum of 64 scores, in four chains of two values a step (NaN counts for nothing).
+__device__ __forceinline__ float max64(const float (&x)[64]) {
   float m[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-  for (int j = 4; j < 124; j += 8)
+  for (int j = 4; j < 60; j += 8)
 #pragma unroll
     for (int q = 0; q < 4; ++q) m[q] = fmaxf(fmaxf(m[q], x[j + q]), x[j + 4 + q]);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) m[q] = fmaxf(m[q], x[124 + q]);
+  for (int q = 0; q < 4; ++q) m[q] = fmaxf(m[q], x[60 + q]);
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// 32 probabilities of this thread's row (16 words of tensor memory) times f.
+template <bool F16>
+__device__ __forceinline__ void rescale_pairs(uint32_t taddr, float f) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float2 v = F16 ? __half22float2(*reinterpret_cast<const __half2*>(&r[j])) : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r[j]));
+    r[j] = pack2<F16>(v.x * f, v.y * f);
+  }
+  tmem_st16_words(taddr, r);
 }
 
 // Tensor-memory columns: S of stream s (P over its first half once S has been read), then O.
@@ -700,7 +716,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     return true;
   };
 
-  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 8) {
     // ------------------------------------------------------------ producer
     // Copies go out as slots fall free; the page numbers of the tile behind are on their way to shared
@@ -905,7 +920,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax: stream s, one row per thread
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int s = warp >> 2, r = tid & 127;
     const uint32_t lane_sel = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + tmem_s(s) + lane_sel, to = tmem + tmem_o(s) + lane_sel;
@@ -975,59 +989,63 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int units = seg.units - 8 * t < 8 ? seg.units - 8 * t : 8;
         const int cached = seg.keys - t * kTileKeys;  // keys of this tile from the cache (may exceed 128)
         if (!idle) {
-          float x[128];
-          tmem_ld64(ts, x);
-          tmem_ld64(ts + 64, x + 64);
-          if (cached < kTileKeys) {
-            const int wu = (cached + 15) & ~15;  // the window's unit (own; behind the tile for a prefix)
+          // 64 scores at a time, in a loop (all 128 unrolled hold up the other warps' instruction fetches, 32
+          // at a time wait longer for their loads).  The exponentials take the maximum that is known; only if
+          // a row's next 64 lie more than kLag above it are O, its sum and the tile's P so far rescaled.
+          // P goes over scores that have been read.
+          float2 sum = make_float2(0.f, 0.f);
+          const float2 c2 = make_float2(c, c);
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            float x[64];
+            tmem_ld64(ts + 64 * q, x);
+            if (cached < kTileKeys) {
+              const int wu = (cached + 15) & ~15;  // the window's unit (own; behind the tile for a prefix)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int n_seen = cached - 32 * q;
-              uint32_t see = n_seen >= 32 ? 0xffffffffu : n_seen <= 0 ? 0u : (1u << n_seen) - 1u;
-              if (seg.own && (wu >> 5) == q) see |= seen << (wu & 31);
+              for (int g = 0; g < 2; ++g) {
+                const int n_seen = cached - 64 * q - 32 * g;
+                uint32_t see = n_seen >= 32 ? 0xffffffffu : n_seen <= 0 ? 0u : (1u << n_seen) - 1u;
+                if (seg.own && (wu >> 5) == 2 * q + g) see |= seen << (wu & 31);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[32 * q + j] = (see >> j) & 1u ? x[32 * q + j] : -INFINITY;
+                for (int j = 0; j < 32; ++j) x[32 * g + j] = (see >> j) & 1u ? x[32 * g + j] : -INFINITY;
+              }
             }
-          }
-          // The exponentials take the maximum that is known and the tile's own is found beside them: only
-          // if a row lies more than kLag above is O rescaled and the tile's P done again.  (A pass for the
-          // maximum ahead of them adds a third to the softmax, which the tensor core waits for.)
-          if (first) m = row_max(x);
-          while (true) {
-            const float mc = m == -INFINITY ? 0.f : m * c;
-            const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
-            float2 sum = make_float2(0.f, 0.f);
+            const float mx = max64(x);
+            const bool move = mx > m && !((mx - m) * c <= kLag) && r < rows;  // (m = -inf: infinitely far)
+            if (__any_sync(0xffffffffu, move)) {
+              const float f = move ? exp2_fast((m - mx) * c) : 1.f;
+              if (!first) {
+#pragma unroll 1
+                for (int k2 = 0; k2 < D; k2 += 32) {
+                  float o[32];
+                  tmem_ld32(to + k2, o);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+                  for (int j = 0; j < 32; ++j) o[j] *= f;
+                  tmem_st32(to + k2, o);
+                }
+              }
+              tmem_st_wait();
+#pragma unroll 1
+              for (int k2 = 0; k2 < 2 * q; ++k2) rescale_pairs<F16>(ts + 16 * k2, f);
+              sum.x *= f, sum.y *= f, l *= f;
+              if (move) m = mx;
+            }
+            const float mc = m == -INFINITY ? 0.f : m * c;
+            const float2 mc2 = make_float2(-mc, -mc);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
               uint32_t pk[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const float2 e = fma2(make_float2(x[32 * q + 2 * j], x[32 * q + 2 * j + 1]), c2, mc2);
+                const float2 e = fma2(make_float2(x[32 * g + 2 * j], x[32 * g + 2 * j + 1]), c2, mc2);
                 const float2 w2 = make_float2(exp2_fast(e.x), exp2_fast(e.y));
                 sum = add2(sum, w2);
                 pk[j] = pack2<F16>(w2.x, w2.y);
               }
-              tmem_st16_words(ts + 16 * q, pk);
+              tmem_st16_words(ts + 32 * q + 16 * g, pk);
             }
-            const float mx = row_max(x);
-            const bool move = mx > m && !((mx - m) * c <= kLag) && r < rows;  // (m = -inf: infinitely far)
-            if (!__any_sync(0xffffffffu, move)) {
-              l += sum.x + sum.y;
-              break;
-            }
-            const float f = move ? exp2_fast((m - mx) * c) : 1.f;
-            if (!first) {
-#pragma unroll 1
-              for (int q = 0; q < D; q += 32) {
-                float o[32];
-                tmem_ld32(to + q, o);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] *= f;
-                tmem_st32(to + q, o);
-              }
-            }
-            if (move) l *= f, m = mx;
           }
+          l += sum.x + sum.y;
           tmem_st_wait();
         }
         first = false;
