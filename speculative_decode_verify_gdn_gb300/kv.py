@@ -110,7 +110,13 @@ def _ints(t, name, shape, optional=False):
 
 
 def _stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    """Handle of `stream`, or of the current one (straight from torch's runtime: building a Stream
+    object for it takes 3 us, as long as a launch)."""
+    return _current_stream(_current_device()) if stream is None else stream.cuda_stream
+
+
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _cache(d, k_cache, v_cache):
