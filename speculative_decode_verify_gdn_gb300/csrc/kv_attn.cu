@@ -36,7 +36,7 @@ constexpr int kCtas = 152;       // one per SM; no CTA waits for another, so any
 constexpr int kTileKeys = 128;
 constexpr int kTileRows = 128;   // rows of a stream's tile, whole tokens of G query heads: 128 / G * G are used
 constexpr int kBlockRows = 256;  // rows of an item, at most
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024, kPlanRuns = 512;
 constexpr int kGroupThreads = 128;  // a softmax group: one thread per row of a stream
 constexpr int kTileThreads = 3 * kGroupThreads;  // two softmax groups; producer, two tensor-core warps, scheduler
 constexpr int kJoinWarps = 4, kJoinRowsMax = 32;  // (four warps: four lists)
@@ -178,12 +178,16 @@ __device__ __forceinline__ int prefix_slot(const AttnParams& p, int b) {
 
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWs w) {
   __shared__ long long sums[32];
-  __shared__ long long run_off[kPlanThreads], seq_off[kPlanThreads];  // first tiles, where they fit here
+  // runs and first tiles, where they fit here: what one step of the plan hands to the next would
+  // otherwise be a trip to L2
+  __shared__ RunRec runs[kPlanRuns];
+  __shared__ long long seq_off[kPlanThreads];
   grid_launch_dependents();
   grid_wait();
   const gdn_kv_dims& d = p.d;
   const int tid = int(threadIdx.x), KG = d.K * (d.Hq / d.Hkv);
   long long n_runs = 0;
+  auto run_at = [&](long long r) -> RunRec& { return r < kPlanRuns ? runs[r] : w.run[r]; };
   // (one step of threads, the usual case, keeps what it knows of its sequence for the steps below)
   const bool once = d.B <= kPlanThreads;
   int win = 0, keys = 0, slot = -1;
@@ -217,13 +221,16 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         w.seq[b].pre_off = run;  // (for now)
       }
       if (first) {
-        w.run[run].b0 = b;
-        w.run[run].slot = slot;
-        w.run[run].keys = run_keys;
-        w.run[run].tiles = (run_keys + kTileKeys - 1) / kTileKeys;
+        RunRec x{};
+        x.b0 = b;
+        x.slot = slot;
+        x.keys = run_keys;
+        x.tiles = (run_keys + kTileKeys - 1) / kTileKeys;
+        run_at(run) = x;
       }
-      if (last) w.run[run].n = b + 1;  // (its end; the length follows)
     }
+    __syncthreads();
+    if (last) run_at(run).n = b + 1;  // (its end; the length follows)
     n_runs += total;
   }
   __syncthreads();
@@ -231,18 +238,21 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
   for (int r0 = 0; r0 < n_runs; r0 += kPlanThreads) {
     const int r = r0 + tid;
     long long mine = 0, rows = 0;
+    RunRec x{};
     if (r < n_runs) {
-      const int n = w.run[r].n - w.run[r].b0;
-      w.run[r].n = n;
-      const long long block = (long long)n * KG;
-      mine = (block + 2 * p.tile_rows - 1) / (2 * p.tile_rows) * d.Hkv * w.run[r].tiles;
+      x = run_at(r);
+      x.n -= x.b0;
+      const long long block = (long long)x.n * KG;
+      mine = (block + 2 * p.tile_rows - 1) / (2 * p.tile_rows) * d.Hkv * x.tiles;
       rows = d.Hkv * rows_width(block, p.tile_rows);
     }
     long long total, total_rows;
-    const long long off = tiles + block_scan<long long>(mine, sums, total);
-    const long long at = row + block_scan<long long>(rows, sums, total_rows);
-    if (r < n_runs) w.run[r].off = off, w.run[r].row = at;
-    if (n_runs <= kPlanThreads) run_off[tid] = off;
+    x.off = tiles + block_scan<long long>(mine, sums, total);
+    x.row = row + block_scan<long long>(rows, sums, total_rows);
+    if (r < n_runs) {
+      w.run[r] = x;
+      if (r < kPlanRuns) runs[r] = x;
+    }
     tiles += total;
     row += total_rows;
   }
@@ -259,7 +269,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
       q.win = win;
       q.tiles = win > 0 ? ((keys + 15) / 16 + 1 + 7) / 8 : 0;  // units of 16 keys; the window is one unit
       if (run >= 0) {
-        const RunRec r = w.run[run];
+        const RunRec r = run_at(run);
         q.pre_off = r.off;
         q.pre_row = r.row;
         q.pre_rows = (long long)r.n * KG;
@@ -290,13 +300,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     StartRec s{0, 0};
     if (x < tiles) {
       s.own = x >= prefix_tiles;
-      const bool here = s.own ? once : n_runs <= kPlanThreads;
-      const long long* const offs = s.own ? seq_off : run_off;
       const long long y = s.own ? (x - prefix_tiles) % head_tiles : x;
       int lo = 0, hi = (s.own ? d.B : int(n_runs)) - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if ((here ? offs[mid] : s.own ? w.seq[mid].off : w.run[mid].off) <= y)
+        if ((!s.own ? run_at(mid).off : once ? seq_off[mid] : w.seq[mid].off) <= y)
           lo = mid;
         else
           hi = mid - 1;
@@ -329,20 +337,21 @@ struct SegWalk {
   long long own_at, own_row, head_tiles;
   int runs;
   __device__ __forceinline__ SegWalk(const AttnParams& p_, const AttnWs& w_, int cta_) : p(p_), w(w_), cta(cta_) {
-    own_at = w.head->prefix_tiles, own_row = w.head->own_row, head_tiles = w.head->head_tiles, runs = w.head->runs;
     deal = 0;
     begin();
   }
   __device__ __forceinline__ void begin() {  // the CTA's stretch of its first or second deal
+    const StartRec starts[2] = {w.start[cta], w.start[kCtas + cta]};  // (read beside the head)
     const PlanHead g = *w.head;
+    own_at = g.prefix_tiles, own_row = g.own_row, head_tiles = g.head_tiles, runs = g.runs;
     if (g.split) {
       const int which = deal ^ (cta & 1);
       const long long o = which ? g.prefix_tiles : 0, n = which ? g.tiles - g.prefix_tiles : g.prefix_tiles;
       x = o + first_tile(cta, n), end = o + first_tile(cta + 1, n);
-      own = w.start[which * kCtas + cta].own, idx = w.start[which * kCtas + cta].idx;
+      own = which ? starts[1].own : starts[0].own, idx = which ? starts[1].idx : starts[0].idx;
     } else {
       x = deal ? 0 : first_tile(cta, g.tiles), end = deal ? 0 : first_tile(cta + 1, g.tiles);
-      own = w.start[cta].own, idx = w.start[cta].idx;
+      own = starts[0].own, idx = starts[0].idx;
     }
     h = own && x < end ? int((x - own_at) / head_tiles) : 0;
   }

@@ -252,6 +252,19 @@ def test_many_tiles_of_both_kinds(B, K, Hq, Hkv, D, plen, own):
     assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("runs", [1, 3, 700, 1300])
+def test_more_sequences_than_the_plan_has_threads(runs):
+    """1300 sequences in runs of equal prefixes: fewer and more runs than the plan keeps at hand."""
+    B = 1300
+    pool = Pool(31, [(7 * i) % 40 for i in range(B)] + [50, 200], Hkv=1, D=64)
+    pre = [B + (i * runs // B) % 2 for i in range(B)]
+    q, k, v = window(pool, B, 2, 2)
+    out, lse = attend(pool, B, 2, 2, q, k, v, prefix_of=pre)
+    ref, ref_lse, mag = torch_reference(pool, B, 2, 2, q, k, v, pre)
+    assert ((out.double() - ref).abs() <= ROUND[BF] * (mag + ref.abs()) + 2e-4 * mag).all()
+    assert ((lse.double() - ref_lse).abs() <= 1e-4).all()
+
+
 def test_cache_offsets_beyond_32_bits():
     """Pages whose elements lie past 2^32 elements of the pool."""
     ps, Hkv, D = 64, 8, 128
