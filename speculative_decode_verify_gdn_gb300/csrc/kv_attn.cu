@@ -1,26 +1,46 @@
 // Attention of verify windows over the paged cache (contract in include/gdn_kv.h), on the tensor
 // cores.
 //
+// Mathematics: softmax over a row's keys in one pass with a running maximum m and sum l, and joined
+// over disjoint sets of keys by their log-sum-exps: with (o_i, e_i) of set i,
+// e = log sum exp(e_i), o = sum exp(e_i - e) o_i.  So a row's prefix, its own sequence and any
+// pieces of either can be computed apart.
+//
 // The work is cut into items: (prefix run, kv head, block of up to 256 rows) for the prefixes, a
 // run being consecutive sequences with the same prefix, and (sequence, kv head, block) for what a
-// sequence does not share.  A row is one query head of one window token; its block's rows all
-// meet the same keys, so the prefix is read and multiplied once for every sequence on it.  An
-// item's keys come in tiles of 128.  Prefix items are in the order run, head, block; the sequences'
-// in the order head, sequence, block, so that CTAs at work at the same time read the same tokens'
-// other heads, which lie beside each other in memory.  All tiles of all items, in order, are dealt to the CTAs (one
-// per SM) in equal contiguous stretches: a CTA's part of an item is a segment, it yields the
+// sequence does not share.  A row is one query head of one window token; a block's rows all meet
+// the same keys, so the prefix is read and multiplied once for every sequence on it.  An item's
+// keys come in tiles of 128.  Prefix items are in the order run, head, block; the sequences' in
+// the order head, sequence, block, so that CTAs at work at the same time read the same tokens'
+// other heads, which lie beside each other in memory (B=256 K=1: 163 us, 173 with a sequence's heads
+// one after the other).  All tiles of all items, in order, are dealt to the CTAs (one per SM) in
+// equal contiguous stretches: a CTA's part of an item is a segment, it yields the
 // softmax-weighted sum and the log-sum-exp of its own keys (f32, in the workspace), and a last
-// kernel joins a row's segments.  Which CTA computes what depends on the lengths alone, so
-// results repeat bit for bit.
+// kernel joins a row's segments.  Few rows over a long axis are split over the card by that, and
+// many over a short one are not.  Which CTA computes what depends on the lengths alone, and no
+// sum is formed by atomics, so results repeat bit for bit.
 //
 // Kernels: plan (one CTA: lengths -> items and stretches), tiles (persistent, tcgen05), join.
 //
 // The tile kernel: a producer warp brings keys and values by TMA (128-byte swizzle) into a ring
 // of tiles; a warp per stream issues S = Q K^T and O += P V (tcgen05, M = 128, accumulators in
-// tensor memory, P read from tensor memory); one warp deals out segments and fetches their queries; two
-// groups of four warps, one per stream, turn S into P, a row per thread.  A block of more than 128 rows uses the two streams for its two halves on the
-// same keys; a smaller one gives them alternate tiles of the same rows.  While one stream's
-// softmax runs, the tensor core works for the other.
+// tensor memory, P read from tensor memory); one warp deals out segments and fetches their
+// queries; two groups of four warps, one per stream, turn S into P, a row per thread.  A block of
+// more rows than a tile's uses the two streams for its two halves on the same keys (32 KB of
+// keys or values serve 256 rows, half the L2 traffic of one stream each); a smaller one gives them
+// alternate tiles of the same rows.  While one stream's softmax runs, the tensor core works for
+// the other.
+//
+// Measured on one GB300 (plan + tiles + join; peaks: 6796 GB/s copy, 1957 TFLOP/s cuBLAS bf16, 1733
+// when the power cap sets the clock):
+//   B=64 K=16 Hq=32 Hkv=4 D=128 behind 32768 tokens   410-430 us, 1290-1350 TFLOP/s; the tile kernel
+//     alone 358-370: bound by the tensor core's wait for a stream's chain (S, softmax, P, O), a
+//     tile pair every ~3000 cycles where its products take 2048
+//   B=1 K=16 Hq=32 Hkv=8 over 131072 tokens           102 us, 5250 GB/s: HBM, then the join
+//   B=32 K=16 Hq=32 Hkv=8 behind 8192 + 1..2048       117 us: prefix tiles 45, own tiles 25 (latency
+//     of a 5-tile ring), start, ends and join the rest
+//   B=256 K=1 Hq=32 Hkv=8, 4 prefixes of 3001 + 5..1024  154 us, 3870 GB/s
+//   B=1 K=1 over 700 tokens                           17 us: three dependent launches
 #include <atomic>
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -44,7 +64,7 @@ constexpr float kLn2 = 0.693147180559945f, kLog2e = 1.442695040888963f;
 // A running maximum may lag behind by up to 8 powers of two before O is rescaled: probabilities
 // stay below 2^8, far inside both 16-bit types, and keep their relative precision.
 constexpr float kLag = 8.0f;
-// Longest wait inside the tile kernel: looks of at most about a microsecond each, a few seconds in all.
+// Longest wait inside the tile kernel (kMaxLooks): looks of at most about a microsecond each, a few seconds in all.
 constexpr uint32_t kMaxLooks = 1u << 22;
 constexpr uint32_t kMaxTurnLooks = 1u << 14, kMaxIdle = 1u << 25;
 
@@ -123,7 +143,8 @@ __host__ __device__ inline AttnWs carve_attn(void* base, const gdn_kv_dims& d, s
 // gets its share of both - even CTAs in this order, odd ones in the other: a prefix tile costs
 // tensor-core time and a sequence's tile memory time, so a CTA that had one kind alone would end
 // early or late, and at any time half the CTAs wait for memory while half compute.  With fewer,
-// one deal over all tiles puts them on as many CTAs as there are.
+// one deal over all tiles puts them on as many CTAs as there are.  (B=64 behind 32768 tokens: 543 us in
+// two deals, 849 in one.)
 constexpr long long kSplitTiles = 4 * kCtas;
 __device__ __forceinline__ long long first_tile(long long c, long long tiles) { return c * tiles / kCtas; }
 __device__ __forceinline__ int cta_of(long long x, long long tiles) {
@@ -422,10 +443,9 @@ struct TileLayout {
 };
 
 struct TileMaps {
-  // (D, token, kv head, page or sequence, layer); a keys' map and the values' behind it
-  CUtensorMap k16, v16;  // boxes of 16 tokens of the cache
-  CUtensorMap kb, vb;    // boxes of `box` tokens
-  CUtensorMap kw, vw;    // boxes of 16 tokens of the window
+  // (D, token, kv head, page or sequence, layer), keys and values: boxes of 16 tokens of the cache, of
+  // `box` tokens of it, and of 16 tokens of the window
+  CUtensorMap few[2], many[2], window[2];
   // queries, (D, query head, token): boxes of G heads x the tokens of a row tile, and of a sequence's
   CUtensorMap qt, qs;
 };
@@ -795,12 +815,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(full + slot, uint32_t(now_units) * 16 * D * 2);
         __syncwarp();
         const uint32_t dst = base + L::OFF_RING + slot * L::BYTES, bar = smem_addr(full + slot), step = uint32_t(now_whole ? box : 16) * 128;
-        const CUtensorMap* const m = now_whole ? &maps.kb + v : &maps.k16 + v;
+        const CUtensorMap* const m = now_whole ? &maps.many[v] : &maps.few[v];
 #pragma unroll 2
         for (int b = 0; b < now_boxes; ++b) {
           const bool win = b == now_window;
           const int c1 = win ? 0 : int(uniform_from(uint32_t(now_in), b)), c3 = win ? now_b : int(uniform_from(uint32_t(now_page), b));
-          tma_box<D>(dst + b * step, win ? &maps.kw + v : m, c1, now_h, c3, win ? 0 : p.layer, bar);
+          tma_box<D>(dst + b * step, win ? &maps.window[v] : m, c1, now_h, c3, win ? 0 : p.layer, bar);
         }
         issued = 2 * n + v + 1;
         if (++slot == NS) slot = 0, phase ^= 1;
@@ -816,11 +836,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp == 9 || warp == 10) {
     // ------------------------------------------------------------ tensor core, stream s
-    // A warp per stream, taking turns on the tiles they share: the O += P V of the stream's tile before and the S = Q K^T of its
-    // next go out in one go, 1024 cycles of the tensor core, during which the other stream's softmax
-    // runs and the other warp does its waiting.  (Without turns the two streams' products interleave
-    // and take twice as long each; one warp for both leaves the tensor core idle while it waits.)  The
-    // whole warp walks the schedule, in uniform registers.
+    // A warp per stream, taking turns on the tiles they share: the O += P V of the stream's tile before
+    // and the S = Q K^T of its next go out in one go, 1024 cycles of the tensor core (16 products of
+    // 64), during which the other stream's softmax runs and the other warp does its waiting.  (Without
+    // turns the two streams' products interleave and take twice as long each; one warp for both leaves
+    // the tensor core idle while it waits.)  The whole warp walks the schedule, in uniform registers.
     //
     // Each of the two warps sees every tile land, in order, and releases each of its slots once - the
     // stream that does not use a tile by a plain arrival.  A wait on a phase's parity is sound only
@@ -1405,15 +1425,15 @@ cudaError_t launch_attn(const AttnParams& params, cudaStream_t stream) {
   const cuuint64_t cd[5] = {cuuint64_t(d.D), cuuint64_t(d.page_size), cuuint64_t(d.Hkv), cuuint64_t(d.n_pages), cuuint64_t(d.n_layers)};
   const cuuint64_t cs[4] = {2ull * d.cache_token_stride, 2ull * d.cache_head_stride, 2ull * d.cache_page_stride, 2ull * d.cache_layer_stride};
   const cuuint32_t b16[5] = {64, 16, 1, 1, 1}, bb[5] = {64, cuuint32_t(box), 1, 1, 1};
-  map(&maps.k16, p.k_cache, 5, cd, cs, b16);
-  map(&maps.v16, p.v_cache, 5, cd, cs, b16);
-  map(&maps.kb, p.k_cache, 5, cd, cs, bb);
-  map(&maps.vb, p.v_cache, 5, cd, cs, bb);
+  map(&maps.few[0], p.k_cache, 5, cd, cs, b16);
+  map(&maps.few[1], p.v_cache, 5, cd, cs, b16);
+  map(&maps.many[0], p.k_cache, 5, cd, cs, bb);
+  map(&maps.many[1], p.v_cache, 5, cd, cs, bb);
   // rows behind a window's K-th token read as zeros
   const cuuint64_t wd[5] = {cuuint64_t(d.D), cuuint64_t(d.K), cuuint64_t(d.Hkv), cuuint64_t(d.B), 1};
   const cuuint64_t wst[4] = {2ull * d.win_token_stride, 2ull * d.D, 2ull * d.K * d.win_token_stride, 2ull * d.K * d.win_token_stride};
-  map(&maps.kw, p.k_win, 5, wd, wst, b16);
-  map(&maps.vw, p.v_win, 5, wd, wst, b16);
+  map(&maps.window[0], p.k_win, 5, wd, wst, b16);
+  map(&maps.window[1], p.v_win, 5, wd, wst, b16);
   const cuuint64_t qd[3] = {cuuint64_t(d.D), cuuint64_t(d.Hq), cuuint64_t(d.B) * d.K};
   const cuuint64_t qst[2] = {2ull * d.D, 2ull * d.q_token_stride};
   const cuuint32_t bt[3] = {64, cuuint32_t(G), cuuint32_t(p.tile_toks)}, bs[3] = {64, cuuint32_t(G), cuuint32_t(d.K < p.tile_toks ? d.K : p.tile_toks)};
