@@ -56,7 +56,7 @@ constexpr int kCtas = 152;       // one per SM; no CTA waits for another, so any
 constexpr int kTileKeys = 128;
 constexpr int kTileRows = 128;   // rows of a stream's tile, whole tokens of G query heads: 128 / G * G are used
 constexpr int kBlockRows = 256;  // rows of an item, at most
-constexpr int kPlanThreads = 1024, kPlanRuns = 512;
+constexpr int kPlanThreads = 512, kPlanRuns = 512;
 constexpr int kGroupThreads = 128;  // a softmax group: one thread per row of a stream
 constexpr int kTileThreads = 3 * kGroupThreads;  // two softmax groups; producer, two tensor-core warps, scheduler
 constexpr int kJoinWarps = 4, kJoinRowsMax = 32;  // (four warps: four lists)
@@ -170,7 +170,7 @@ __device__ __forceinline__ T block_scan(T v, T* sums, T& total) {  // exclusive,
   __syncthreads();
   if (lane == 31) sums[warp] = x;
   __syncthreads();
-  T s = sums[lane];
+  T s = lane < kPlanThreads / 32 ? sums[lane] : T(0);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const T y = __shfl_up_sync(0xffffffffu, s, o);
@@ -1209,8 +1209,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // weighted by their log-sum-exps.  Where the segments are follows from the plan and is listed once
 // per CTA; then a warp takes a row at a time.  Bound by the latency of its loads (lengths, then
 // log-sum-exps, then sums): the sums of a row are read together, and a CTA takes as many rows as
-// leave two CTAs to an SM (32 rows at B=64 K=16: 24 us where 4 take 62; 4 rows at B=1 K=16 with 40
-// segments a row: 12 us where 32 take 63).
+// leave eight CTAs to an SM, 4 at least (the whole call at B=32 K=16 behind 8192 tokens: 106 us, 117
+// with two CTAs to an SM, 109 with sixteen; at B=1 K=16 with 40 segments a row a join with 32 rows to
+// a CTA takes 63 us where 4 take 12).
 template <int D, bool F16>
 __global__ void __launch_bounds__(32 * kJoinWarps, 8)
     attn_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWs w, const int join_rows) {
@@ -1390,7 +1391,7 @@ cudaError_t launch(const AttnParams& p, const AttnWs& w, int box, const TileMaps
   const int KG = p.d.K * (p.d.Hq / p.d.Hkv);
   const long long heads = (long long)p.d.B * p.d.Hkv;
   int join_rows = kJoinRowsMax;
-  while (join_rows > kJoinWarps && heads * ((KG + join_rows - 1) / join_rows) < 2 * kCtas) join_rows /= 2;
+  while (join_rows > kJoinWarps && heads * ((KG + join_rows - 1) / join_rows) < 8 * kCtas) join_rows /= 2;
   return launch_pdl(attn_join_kernel<D, F16>, unsigned(heads * ((KG + join_rows - 1) / join_rows)), 32 * kJoinWarps, 0,
                     stream, p, w, join_rows);
 }
