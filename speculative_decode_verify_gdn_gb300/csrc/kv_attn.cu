@@ -20,7 +20,8 @@
 // many over a short one are not.  Which CTA computes what depends on the lengths alone, and no
 // sum is formed by atomics, so results repeat bit for bit.
 //
-// Kernels: plan (one CTA: lengths -> items and stretches), tiles (persistent, tcgen05), join.
+// Kernels: plan (one CTA: lengths -> items and stretches; up to 32 sequences the tile kernel's
+// schedulers do that), tiles (persistent, tcgen05), join.
 //
 // The tile kernel: a producer warp brings keys and values by TMA (128-byte swizzle) into a ring
 // of tiles; a warp per stream issues S = Q K^T and O += P V (tcgen05, M = 128, accumulators in
@@ -349,32 +350,146 @@ struct Seg {
   __device__ __forceinline__ bool paired() const { return pair != 0; }
 };
 
-// Walks a CTA's stretch segment by segment.
+// The plan of a batch of at most 32 sequences, by one converged warp: lane b has sequence b's record
+// and lane r run r's.  The tile kernel's scheduler makes it for itself, which saves the plan kernel's
+// launch (B=1 decode: 17.4 us with it).
+constexpr int kWarpPlan = 32;
+__device__ __forceinline__ long long warp_scan(long long v, int lane, long long& total) {  // exclusive
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  total = __shfl_sync(0xffffffffu, x, 31);
+  return x - v;
+}
+__device__ __forceinline__ void warp_plan(const AttnParams& p, int lane, PlanHead& head, SeqRec& q, RunRec& r) {
+  const gdn_kv_dims& d = p.d;
+  const int KG = d.K * (d.Hq / d.Hkv), block = 2 * p.tile_rows;
+  const bool there = lane < d.B;
+  q = SeqRec{};
+  r = RunRec{};
+  int slot = -1;
+  if (there) {
+    slot = prefix_slot(p, lane);
+    if (slot < 0 && p.prefix_of && p.prefix_of[lane] != -1) atomicOr(p.err, GDN_DEVERR_KV_SLOT);
+    q.keys = slot_len(p, d.slot0 + lane);
+    q.win = p.win_len ? p.win_len[lane] : d.K;
+    if (q.win < 0 || q.win > d.K) {
+      atomicOr(p.err, GDN_DEVERR_KV_WINDOW);
+      q.win = q.win < 0 ? 0 : d.K;
+    }
+    q.tiles = q.win > 0 ? ((q.keys + 15) / 16 + 1 + 7) / 8 : 0;  // units of 16 keys; the window is one unit
+  }
+  const int before = __shfl_up_sync(0xffffffffu, slot, 1), after = __shfl_down_sync(0xffffffffu, slot, 1);
+  const uint32_t firsts = __ballot_sync(0xffffffffu, slot >= 0 && (lane == 0 || before != slot));
+  const uint32_t lasts = __ballot_sync(0xffffffffu, slot >= 0 && (lane == 31 || after != slot));
+  const int runs = __popc(firsts);
+  const int b0 = lane < runs ? int(__fns(firsts, 0, lane + 1)) : 0;
+  r.slot = __shfl_sync(0xffffffffu, slot, b0);
+  long long mine = 0, rows = 0;
+  if (lane < runs) {
+    r.b0 = b0;
+    r.n = int(__fns(lasts, 0, lane + 1)) + 1 - b0;
+    r.keys = slot_len(p, r.slot);
+    r.tiles = (r.keys + kTileKeys - 1) / kTileKeys;
+    const long long all = (long long)r.n * KG;
+    mine = (all + block - 1) / block * d.Hkv * r.tiles;
+    rows = d.Hkv * rows_width(all, p.tile_rows);
+  }
+  long long prefix_tiles, prefix_rows, head_tiles;
+  r.off = warp_scan(mine, lane, prefix_tiles);
+  r.row = warp_scan(rows, lane, prefix_rows);
+  q.off = warp_scan((long long)((KG + block - 1) / block) * q.tiles, lane, head_tiles);
+  const int run = slot >= 0 ? __popc(firsts & ((2u << lane) - 1u)) - 1 : 0;
+  const long long run_off = __shfl_sync(0xffffffffu, r.off, run), run_row = __shfl_sync(0xffffffffu, r.row, run);
+  const int run_n = __shfl_sync(0xffffffffu, r.n, run), run_b0 = __shfl_sync(0xffffffffu, r.b0, run);
+  const int run_tiles = __shfl_sync(0xffffffffu, r.tiles, run);
+  if (slot >= 0) {
+    q.pre_off = run_off;
+    q.pre_row = run_row;
+    q.pre_rows = (long long)run_n * KG;
+    q.pre_at = (long long)(lane - run_b0) * KG;
+    q.pre_tiles = run_tiles;
+  }
+  head.prefix_tiles = prefix_tiles;
+  head.tiles = prefix_tiles + head_tiles * d.Hkv;
+  head.split = head.tiles >= kSplitTiles;
+  head.own_row = prefix_rows + (head.split ? kBlockRows * kCtas : 0);
+  head.head_tiles = head_tiles;
+  head.runs = runs;
+}
+
+// Walks a CTA's stretch segment by segment (a converged warp).
 struct SegWalk {
   const AttnParams& p;
   const AttnWs& w;
+  const bool small;  // the plan is the warp's own
+  PlanHead head;
+  SeqRec my_seq;
+  RunRec my_run;
   long long x, end;
   int own, idx, h, cta, deal;  // (h: kv head of the sequences' items)
-  long long own_at, own_row, head_tiles;
-  int runs;
-  __device__ __forceinline__ SegWalk(const AttnParams& p_, const AttnWs& w_, int cta_) : p(p_), w(w_), cta(cta_) {
+  __device__ __forceinline__ SegWalk(const AttnParams& p_, const AttnWs& w_, int cta_, int lane)
+      : p(p_), w(w_), small(p_.d.B <= kWarpPlan), cta(cta_) {
+    if (small) {
+      warp_plan(p, lane, head, my_seq, my_run);
+      if (cta == 0) {  // for the join
+        if (lane < p.d.B) w.seq[lane] = my_seq;
+        if (lane == 0) *w.head = head;
+      }
+    } else {
+      head = *w.head;
+    }
     deal = 0;
     begin();
   }
-  __device__ __forceinline__ void begin() {  // the CTA's stretch of its first or second deal
-    const StartRec starts[2] = {w.start[cta], w.start[kCtas + cta]};  // (read beside the head)
-    const PlanHead g = *w.head;
-    own_at = g.prefix_tiles, own_row = g.own_row, head_tiles = g.head_tiles, runs = g.runs;
-    if (g.split) {
-      const int which = deal ^ (cta & 1);
-      const long long o = which ? g.prefix_tiles : 0, n = which ? g.tiles - g.prefix_tiles : g.prefix_tiles;
-      x = o + first_tile(cta, n), end = o + first_tile(cta + 1, n);
-      own = which ? starts[1].own : starts[0].own, idx = which ? starts[1].idx : starts[0].idx;
-    } else {
-      x = deal ? 0 : first_tile(cta, g.tiles), end = deal ? 0 : first_tile(cta + 1, g.tiles);
-      own = starts[0].own, idx = starts[0].idx;
+  // The last record that starts at or before a stretch's first tile (the plan kernel has looked for it).
+  __device__ __forceinline__ StartRec start(int which) const {
+    if (!small) return w.start[which * kCtas + cta];
+    StartRec s{0, 0};
+    if (x < head.tiles) {
+      s.own = x >= head.prefix_tiles;
+      const long long y = s.own ? (x - head.prefix_tiles) % head.head_tiles : x;
+      const uint32_t at = s.own ? __ballot_sync(0xffffffffu, (threadIdx.x & 31) < unsigned(p.d.B) && my_seq.off <= y)
+                                : __ballot_sync(0xffffffffu, (threadIdx.x & 31) < unsigned(head.runs) && my_run.off <= y);
+      s.idx = 31 - __clz(int(at));
     }
-    h = own && x < end ? int((x - own_at) / head_tiles) : 0;
+    return s;
+  }
+  __device__ __forceinline__ void begin() {  // the CTA's stretch of its first or second deal
+    const int which = head.split ? deal ^ (cta & 1) : 0;
+    if (head.split) {
+      const long long o = which ? head.prefix_tiles : 0, n = which ? head.tiles - head.prefix_tiles : head.prefix_tiles;
+      x = o + first_tile(cta, n), end = o + first_tile(cta + 1, n);
+    } else {
+      x = deal ? 0 : first_tile(cta, head.tiles), end = deal ? 0 : first_tile(cta + 1, head.tiles);
+    }
+    const StartRec s = start(which);
+    own = s.own, idx = s.idx;
+    h = own && x < end ? int((x - head.prefix_tiles) / head.head_tiles) : 0;
+  }
+  __device__ __forceinline__ SeqRec seq(int i) const {
+    if (!small) return w.seq[i];
+    SeqRec q{};
+    q.off = __shfl_sync(0xffffffffu, my_seq.off, i);
+    q.tiles = __shfl_sync(0xffffffffu, my_seq.tiles, i);
+    q.keys = __shfl_sync(0xffffffffu, my_seq.keys, i);
+    q.win = __shfl_sync(0xffffffffu, my_seq.win, i);
+    return q;
+  }
+  __device__ __forceinline__ RunRec run(int i) const {
+    if (!small) return w.run[i];
+    RunRec r{};
+    r.off = __shfl_sync(0xffffffffu, my_run.off, i);
+    r.row = __shfl_sync(0xffffffffu, my_run.row, i);
+    r.tiles = __shfl_sync(0xffffffffu, my_run.tiles, i);
+    r.keys = __shfl_sync(0xffffffffu, my_run.keys, i);
+    r.slot = __shfl_sync(0xffffffffu, my_run.slot, i);
+    r.b0 = __shfl_sync(0xffffffffu, my_run.b0, i);
+    r.n = __shfl_sync(0xffffffffu, my_run.n, i);
+    return r;
   }
   __device__ __forceinline__ bool next(Seg& s) {
     if (x >= end && deal == 0) deal = 1, begin();
@@ -382,7 +497,7 @@ struct SegWalk {
     const gdn_kv_dims& d = p.d;
     const int KG = d.K * (d.Hq / d.Hkv);
     while (true) {
-      if (!own && idx == runs) own = 1, idx = 0;
+      if (!own && idx == head.runs) own = 1, idx = 0;
       if (own && idx >= d.B) {  // the next head's
         if (++h >= d.Hkv) return false;
         idx = 0;
@@ -390,13 +505,13 @@ struct SegWalk {
       long long off, rows, row;
       int tiles;
       if (own) {
-        const SeqRec q = w.seq[idx];
-        off = own_at + h * head_tiles + q.off, tiles = q.tiles, rows = KG;
-        row = own_row + ((long long)h * d.B + idx) * rows_width(KG, p.tile_rows);
+        const SeqRec q = seq(idx);
+        off = head.prefix_tiles + h * head.head_tiles + q.off, tiles = q.tiles, rows = KG;
+        row = head.own_row + ((long long)h * d.B + idx) * rows_width(KG, p.tile_rows);
         s.slot = d.slot0 + idx, s.keys = q.keys, s.win = q.win, s.tok0 = idx * d.K;
         s.units = (q.keys + 15) / 16 + 1;
       } else {
-        const RunRec r = w.run[idx];
+        const RunRec r = run(idx);
         off = r.off, tiles = r.tiles, rows = (long long)r.n * KG, row = r.row;
         s.slot = r.slot, s.keys = r.keys, s.win = -1, s.tok0 = r.b0 * d.K;
         s.units = (r.keys + 15) / 16;
@@ -1136,7 +1251,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // queries as soon as the products with the ones before are done - whichever comes first.  Queries
     // come by TMA, whole tokens of G heads: rows behind the block's last hold other tokens' queries or
     // what was there, and nothing reads their results.
-    SegWalk walk(p, w, int(blockIdx.x));
+    SegWalk walk(p, w, int(blockIdx.x), lane);
     uint32_t k = 0, kq = 0;      // segments handed on; segment whose queries are next
     uint32_t nq0 = 0, nq1 = 0;   // segments of each stream
     int part = 0;                // of segment kq: its first or second stream
@@ -1375,7 +1490,7 @@ template <int D, bool F16>
 cudaError_t launch(const AttnParams& p, const AttnWs& w, int box, const TileMaps& maps, cudaStream_t stream) {
   using L = TileLayout<D>;
   static_assert(L::TOTAL <= 232448 - 512, "shared memory");
-  cudaError_t e = launch_pdl(attn_plan_kernel, 1u, kPlanThreads, 0, stream, p, w);
+  cudaError_t e = p.d.B <= kWarpPlan ? cudaSuccess : launch_pdl(attn_plan_kernel, 1u, kPlanThreads, 0, stream, p, w);
   if (e != cudaSuccess) return e;
   static std::atomic<uint64_t> allowed{0};  // a bit per device: the kernel may use its shared memory there
   int dev = 0;
