@@ -9,8 +9,8 @@
 //
 // Bound: the move is a copy, 2 bytes of HBM traffic per byte moved; the plan reads 4 bytes per
 // page of the pool and is a few dependent trips to L2 long.  A move takes 16 tokens of one layer
-// at a time, keys and values together, 16 bytes a thread and piece, eight loads in flight a
-// thread before its first store.  Pieces are found without a division (by multiplication, or
+// at a time, keys and values together, 16 bytes a thread and piece, four or eight loads in
+// flight a thread before its first store.  Pieces are found without a division (by multiplication, or
 // straight on where a page's tokens lie one behind the other): with two divisions a piece the
 // copy was bound by instructions, 5.1 of 6.8 TB/s over 1.65 GB.
 #include "gdn_common.cuh"
@@ -20,7 +20,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveTokens = 16;  // tokens of one layer moved by one CTA at a time
 
@@ -82,7 +82,7 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int& total) {
   __syncthreads();  // the sums of the call before have been read
   if (lane == 31) sums[warp] = x;
   __syncthreads();
-  int s = sums[lane];
+  int s = lane < kPlanThreads / 32 ? sums[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, s, o);
@@ -137,10 +137,11 @@ __device__ __forceinline__ uint4 load_piece(const uint16_t* p) {
 
 // Keys and values of `n` 16-byte pieces by the whole CTA; from(i) and to(i) are a piece's places (in
 // elements, the same in keys and values).
-template <typename From, typename To>
+// U pieces of each at a time a thread (4 for pages; 2 for the few rows of a commit, whose CTAs are more
+// than the card holds at once: 26 us, 28 with 4, at 256 sequences and 12 layers).
+template <int U, typename From, typename To>
 __device__ __forceinline__ void move_pieces(uint16_t* k_dst, uint16_t* v_dst, const uint16_t* k_src, const uint16_t* v_src, int n,
                                             From from, To to) {
-  constexpr int U = 4;
   for (int i0 = threadIdx.x; i0 < n; i0 += U * kMoveThreads) {
     uint4 k[U], v[U];
 #pragma unroll
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_commit_move_kernel(const __gr
   const long long layer_at = layer * d.cache_layer_stride;
   const long long from = layer * d.win_layer_stride + (long long)b * d.K * d.win_token_stride;
   const int D = d.D;
-  move_pieces(
+  move_pieces<2>(
       p.k_cache, p.v_cache, p.k_win + from, p.v_win + from, tokens * d.Hkv << d8_shift,
       [&](int i) {
         const Piece q = split_piece(i, d8_shift, d.Hkv, by_heads);
@@ -409,13 +410,13 @@ __device__ __forceinline__ void move_pages(const PagesParams& p, const PagesWs& 
     const int n = tokens * d.Hkv << d8_shift;
     if (straight) {
       auto at = [](int i) { return 8ll * i; };
-      move_pieces(p.k_cache + to, p.v_cache + to, p.k_cache + from, p.v_cache + from, n, at, at);
+      move_pieces<4>(p.k_cache + to, p.v_cache + to, p.k_cache + from, p.v_cache + from, n, at, at);
     } else {
       auto at = [&](int i) {
         const Piece q = split_piece(i, d8_shift, d.Hkv, by_heads);
         return q.t * d.cache_token_stride + q.h * d.cache_head_stride + 8 * q.e;
       };
-      move_pieces(p.k_cache + to, p.v_cache + to, p.k_cache + from, p.v_cache + from, n, at, at);
+      move_pieces<4>(p.k_cache + to, p.v_cache + to, p.k_cache + from, p.v_cache + from, n, at, at);
     }
   }
 }
@@ -424,7 +425,9 @@ __global__ void __launch_bounds__(kMoveThreads) kv_fork_move_kernel(const __grid
   grid_launch_dependents();
   grid_wait();
   const gdn_kv_dims& d = p.d;
-  for (int i = int(blockIdx.x); i < d.n_slots; i += int(gridDim.x)) {
+  move_pages(p, w, by_heads);
+  // (books last, from the other end: the CTAs with the fewest moves first)
+  for (int i = int(gridDim.x - 1 - blockIdx.x); i < d.n_slots; i += int(gridDim.x)) {
     // as an old slot: a sequence that nobody took gives its pages back
     if (w.first[i] == d.n_slots) {
       int len = p.len_in[i];
@@ -454,7 +457,6 @@ __global__ void __launch_bounds__(kMoveThreads) kv_fork_move_kernel(const __grid
     }
     if (threadIdx.x == 0) p.len_out[i] = len;
   }
-  move_pages(p, w, by_heads);
 }
 
 // ---------------------------------------------------------------- compact
@@ -551,8 +553,11 @@ cudaError_t launch_pdl(void (*kernel)(Args...), int grid, int threads, cudaStrea
 
 uint32_t by_heads(const gdn_kv_dims& d) { return uint32_t(((1ull << 32) + d.Hkv - 1) / d.Hkv); }  // (unused for one head)
 
-// CTAs of a move over `units` pieces: what fits on the card at once, no more than there are pieces.
-int move_grid(long long units) { return int(units < 1 ? 1 : (units < 152 * 8 ? units : 152 * 8)); }
+// CTAs of a move over `units` pieces of pages: no more than there are pieces, nor than 40 to an SM,
+// twenty times what runs at once - those that start later fill the gaps of those that end earlier
+// (compaction of 1.66 GB: 268 us with 8 to an SM, 260 with 40, 271 with 160; fork of a population
+// 45.5, 40.6, 43.5).
+int move_grid(long long units) { return int(units < 1 ? 1 : (units < 152 * 40 ? units : 152 * 40)); }
 
 // CTA 0 plans; one more CTA for each 16K ints of tables to copy.
 int plan_grid(long long ints) { return 1 + int(ints < 1 ? 1 : (ints + 16383) / 16384 > 64 ? 64 : (ints + 16383) / 16384); }
