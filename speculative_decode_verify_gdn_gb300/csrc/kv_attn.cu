@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         __syncwarp();
         const uint32_t dst = base + L::OFF_RING + slot * L::BYTES, bar = smem_addr(full + slot), step = uint32_t(now_whole ? box : 16) * 128;
         const CUtensorMap* const m = now_whole ? &maps.many[v] : &maps.few[v];
-#pragma unroll 2
+#pragma unroll 1
         for (int b = 0; b < now_boxes; ++b) {
           const bool win = b == now_window;
           const int c1 = win ? 0 : int(uniform_from(uint32_t(now_in), b)), c3 = win ? now_b : int(uniform_from(uint32_t(now_page), b));
