@@ -1326,11 +1326,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // log-sum-exps, then sums): the sums of a row are read together, and a CTA takes as many rows as
 // leave eight CTAs to an SM, 4 at least (the whole call at B=32 K=16 behind 8192 tokens: 106 us, 117
 // with two CTAs to an SM, 109 with sixteen; at B=1 K=16 with 40 segments a row a join with 32 rows to
-// a CTA takes 63 us where 4 take 12).
-template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kJoinWarps, 8)
+// a CTA takes 63 us where 4 take 12).  A grid that is on the card at once has registers for sixteen
+// rows of sums in flight instead of four (B=1 K=16 over 131072 tokens: 94 us, 99 with four; with
+// sixteen everywhere B=32 K=16 takes 110 us, 100 with four).
+template <int D, bool F16, int U>
+__global__ void __launch_bounds__(32 * kJoinWarps, U == 4 ? 8 : 4)
     attn_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWs w, const int join_rows) {
-  constexpr int N = D / 32, U = 4;
+  constexpr int N = D / 32;
   // the partial results of a block's first row: of the sequence (0, 1) and of the prefix (2, 3), the
   // block that holds the CTA's first row and the one behind it
   __shared__ long long list[4][2 * kCtas];
@@ -1507,8 +1509,9 @@ cudaError_t launch(const AttnParams& p, const AttnWs& w, int box, const TileMaps
   const long long heads = (long long)p.d.B * p.d.Hkv;
   int join_rows = kJoinRowsMax;
   while (join_rows > kJoinWarps && heads * ((KG + join_rows - 1) / join_rows) < 8 * kCtas) join_rows /= 2;
-  return launch_pdl(attn_join_kernel<D, F16>, unsigned(heads * ((KG + join_rows - 1) / join_rows)), 32 * kJoinWarps, 0,
-                    stream, p, w, join_rows);
+  const long long joins = heads * ((KG + join_rows - 1) / join_rows);
+  return launch_pdl(joins <= 4 * kCtas ? attn_join_kernel<D, F16, 16> : attn_join_kernel<D, F16, 4>, unsigned(joins),
+                    32 * kJoinWarps, 0, stream, p, w, join_rows);
 }
 
 }  // namespace
