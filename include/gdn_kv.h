@@ -144,6 +144,8 @@ gdn_status gdn_kv_fork(const gdn_kv_dims* dims, const int32_t* src, void* k_cach
  * Compact: with n pages live (ref > 0), the live pages numbered n and up move, lowest first, to
  * the free pages below n, lowest first, in all layers; the tables and ref follow, and *n_live
  * becomes n.  Pages 0..n-1 are then the live ones.  table_out may be table_in, ref_out ref_in.
+ * A page that is live by a count that only the caller raised, with no table that names it, moves
+ * like the others, and no output says where to.
  * dims: B, K, Hq, slot0 and the q and window strides are not read.
  */
 gdn_status gdn_kv_compact(const gdn_kv_dims* dims, void* k_cache, void* v_cache, const int32_t* table_in,

@@ -34,14 +34,16 @@
 //
 // Measured on one GB300 (plan + tiles + join; peaks: 6796 GB/s copy, 1957 TFLOP/s cuBLAS bf16, 1733
 // when the power cap sets the clock):
-//   B=64 K=16 Hq=32 Hkv=4 D=128 behind 32768 tokens   410-430 us, 1290-1350 TFLOP/s; the tile kernel
-//     alone 358-370: bound by the tensor core's wait for a stream's chain (S, softmax, P, O), a
-//     tile pair every ~3000 cycles where its products take 2048
-//   B=1 K=16 Hq=32 Hkv=8 over 131072 tokens           102 us, 5250 GB/s: HBM, then the join
-//   B=32 K=16 Hq=32 Hkv=8 behind 8192 + 1..2048       117 us: prefix tiles 45, own tiles 25 (latency
+//   B=64 K=16 Hq=32 Hkv=4 D=128 behind 32768 tokens   392 us, 1410 TFLOP/s: bound by the tensor
+//     core's wait for a stream's chain (S, softmax, P, O), a tile pair every ~3000 cycles where its
+//     products take 2048
+//   B=1 K=16 Hq=32 Hkv=8 over 131072 tokens           95 us, 5670 GB/s: HBM, then the join
+//   B=32 K=16 Hq=32 Hkv=8 behind 8192 + 1..2048       100 us: prefix tiles 45, own tiles 25 (latency
 //     of a 5-tile ring), start, ends and join the rest
 //   B=256 K=1 Hq=32 Hkv=8, 4 prefixes of 3001 + 5..1024  154 us, 3870 GB/s
-//   B=1 K=1 over 700 tokens                           17 us: three dependent launches
+//   B=1 K=1 over 700 tokens                           15 us: two dependent launches
+// The loops over boxes and over scores are kept rolled: the kernel's code is more than the
+// instruction cache holds, and unrolling them costs more in misses than it saves.
 #include <atomic>
 #include <cuda.h>
 #include <cuda_fp16.h>
