@@ -34,11 +34,11 @@
 //
 // Measured on one GB300 (plan + tiles + join; peaks: 6796 GB/s copy, 1957 TFLOP/s cuBLAS bf16, 1733
 // when the power cap sets the clock):
-//   B=64 K=16 Hq=32 Hkv=4 D=128 behind 32768 tokens   392 us, 1410 TFLOP/s: bound by the tensor
+//   B=64 K=16 Hq=32 Hkv=4 D=128 behind 32768 tokens   384 us, 1440 TFLOP/s: bound by the tensor
 //     core's wait for a stream's chain (S, softmax, P, O), a tile pair every ~3000 cycles where its
 //     products take 2048
-//   B=1 K=16 Hq=32 Hkv=8 over 131072 tokens           95 us, 5670 GB/s: HBM, then the join
-//   B=32 K=16 Hq=32 Hkv=8 behind 8192 + 1..2048       100 us: prefix tiles 45, own tiles 25 (latency
+//   B=1 K=16 Hq=32 Hkv=8 over 131072 tokens           94 us, 5710 GB/s: HBM, then the join
+//   B=32 K=16 Hq=32 Hkv=8 behind 8192 + 1..2048       99 us: prefix tiles 45, own tiles 25 (latency
 //     of a 5-tile ring), start, ends and join the rest
 //   B=256 K=1 Hq=32 Hkv=8, 4 prefixes of 3001 + 5..1024  154 us, 3870 GB/s
 //   B=1 K=1 over 700 tokens                           15 us: two dependent launches
@@ -118,8 +118,9 @@ __host__ __device__ inline size_t up256(size_t n) { return (n + 255) & ~size_t(2
 // hold its halves, else two (one per stream).
 __host__ __device__ inline int block_width(int rows, int tile) { return rows > tile ? rows : 2 * rows; }
 // Rows of partial results of all blocks of `rows` rows.
-__host__ __device__ inline long long rows_width(long long rows, int tile) {
-  const long long full = (rows - 1) / (2 * tile);
+template <typename T>
+__host__ __device__ inline T rows_width(T rows, int tile) {
+  const T full = (rows - 1) / (2 * tile);
   return full * 2 * tile + block_width(int(rows - full * 2 * tile), tile);
 }
 
@@ -1324,7 +1325,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // ---------------------------------------------------------------- join
 // One CTA per (sequence, kv head, 4 to 32 of its rows): the segments of the sequence and of its prefix,
 // weighted by their log-sum-exps.  Where the segments are follows from the plan and is listed once
-// per CTA; then a warp takes a row at a time.  Bound by the latency of its loads (lengths, then
+// per CTA; then a warp takes a row at a time, without a division (document batch of the file's head:
+// 384 us, 392 with 64-bit divisions by the block's rows for every row).  Bound by the latency of its loads (lengths, then
 // log-sum-exps, then sums): the sums of a row are read together, and a CTA takes as many rows as
 // leave eight CTAs to an SM, 4 at least (the whole call at B=32 K=16 behind 8192 tokens: 106 us, 117
 // with two CTAs to an SM, 109 with sixteen; at B=1 K=16 with 40 segments a row a join with 32 rows to
@@ -1351,23 +1353,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps, U == 4 ? 8 : 4)
   const SeqRec q = w.seq[b];
   const PlanHead head = *w.head;
   const int rows = KG - r0 < join_rows ? KG - r0 : join_rows;
-  const long long pre0 = q.pre_at + r0;  // the CTA's first row in the prefix's
+  const int pre0 = int(q.pre_at) + r0;  // the CTA's first row in the prefix's (rows in all: below 2^29)
   const int tile = p.tile_rows, block = 2 * tile;
+  const int own_block = r0 / block, pre_block = pre0 / block;
   {
     const bool own = warp < 2;
-    const long long all = own ? KG : q.pre_rows, first = own ? r0 : pre0;
+    const int all = own ? KG : int(q.pre_rows), first = own ? r0 : pre0;
     const int n = own ? q.tiles : q.pre_tiles;
-    const long long rb = first / block + (warp & 1);
+    const int rb = (own ? own_block : pre_block) + (warp & 1);
     int count = 0;
     if (n > 0 && ((warp & 1) == 0 || rb * block < first + rows)) {
       const long long deal = head.split && own ? head.prefix_tiles : 0;
       const long long size = !head.split ? head.tiles : own ? head.tiles - head.prefix_tiles : head.prefix_tiles;
-      const long long blocks = (all + block - 1) / block;
-      const int width = int(all - rb * block < block ? all - rb * block : block);
+      const int blocks = (all + block - 1) / block;
+      const int width = all - rb * block < block ? all - rb * block : block;
       const bool paired = width > tile;
-      const long long from = own ? head.prefix_tiles + h * head.head_tiles + q.off + rb * n : q.pre_off + (h * blocks + rb) * n;
+      const long long from = own ? head.prefix_tiles + h * head.head_tiles + q.off + (long long)rb * n : q.pre_off + ((long long)h * blocks + rb) * n;
       const int c0 = cta_of(from - deal, size), c1 = cta_of(from - deal + n - 1, size);
-      const long long base = (own ? head.own_row + ((long long)h * d.B + b) * rows_width(KG, tile) : q.pre_row + h * rows_width(all, tile)) + rb * block;
+      const long long base = (own ? head.own_row + ((long long)h * d.B + b) * rows_width(KG, tile) : q.pre_row + (long long)h * rows_width(all, tile)) + rb * block;
       const int parts = (c1 - c0 + 1) * (paired ? 1 : 2);
       for (int i0 = 0; i0 < parts; i0 += 32) {
         const int i = i0 + lane, c = c0 + (paired ? i : i >> 1), s = paired ? 0 : i & 1;
@@ -1394,9 +1397,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps, U == 4 ? 8 : 4)
     float M = -INFINITY, W = 0.f;
     const bool live = t < q.win;
     if (live) {
-      const int side_own = r / block != r0 / block ? 1 : 0, side = (pre0 + i) / block != pre0 / block ? 3 : 2;
+      // (a CTA's rows are fewer than a block's: in its first row's block or the next)
+      int lr_own = r - own_block * block, lr_pre = pre0 + i - pre_block * block;
+      const int side_own = lr_own >= block ? 1 : 0, side = lr_pre >= block ? 3 : 2;
+      if (side_own == 1) lr_own -= block;
+      if (side == 3) lr_pre -= block;
       const int n_own = counts[side_own], count = n_own + counts[side];
-      const int lr_own = r % block, lr_pre = int((pre0 + i) % block);
       for (int j0 = 0; j0 < count; j0 += 32) {
         const int j = j0 + lane;
         long long at = 0;
