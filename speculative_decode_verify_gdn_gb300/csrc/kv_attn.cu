@@ -34,7 +34,7 @@
 //
 // Measured on one GB300 (plan + tiles + join; peaks: 6796 GB/s copy, 1957 TFLOP/s cuBLAS bf16, 1733
 // when the power cap sets the clock):
-//   B=64 K=16 Hq=32 Hkv=4 D=128 behind 32768 tokens   384 us, 1440 TFLOP/s: bound by the tensor
+//   B=64 K=16 Hq=32 Hkv=4 D=128 behind 32768 tokens   384-408 us, 1360-1440 TFLOP/s: bound by the tensor
 //     core's wait for a stream's chain (S, softmax, P, O), a tile pair every ~3000 cycles where its
 //     products take 2048
 //   B=1 K=16 Hq=32 Hkv=8 over 131072 tokens           94 us, 5710 GB/s: HBM, then the join
