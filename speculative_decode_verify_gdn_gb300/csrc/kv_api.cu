@@ -211,7 +211,7 @@ gdn_status gdn_attn_verify(const gdn_kv_dims* dims, int32_t layer, const void* q
   uint32_t* err = nullptr;
   GDN_RETURN_IF(gdn::device_status_word(&err));
   const gdn::AttnParams p{d, layer, q, k_win, v_win, k_cache, v_cache, page_table, seq_len, prefix_of, win_len, parent,
-                          scale, out, lse, workspace, err, 0, 0};
+                          scale, out, lse, workspace, err, 0, 0, 0};
   const cudaError_t e = gdn::launch_attn(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
   return gdn::report_ok();

@@ -49,6 +49,7 @@
 #include <cuda_fp16.h>
 
 #include "gdn_common.cuh"
+#include "kv_index.h"
 #include "kv_kernels.h"
 
 namespace gdn {
@@ -874,7 +875,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int t = 0, t1 = 0;           // of the present segment: next tile, end
     bool ok = true, more = true;
     uint32_t slot = 0, phase = 1;  // of the next use; the phase that its slot was emptied in
-    const float page_inv = 1.f / float(d.page_size);
     // the segment at hand
     int seg_units = 0, seg_cached = 0, seg_h = 0, seg_b = 0;
     const int32_t* seg_pages = nullptr;
@@ -906,10 +906,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       boxes = whole ? kTileKeys / box : units;
       if (lane < boxes && lane != window) {
         const int token = t * kTileKeys + lane * (whole ? box : 16);
-        int col = int(float(token) * page_inv);  // (within one)
+        const int col = page_column(token, p.page_inv);
         in = token - col * d.page_size;
-        if (in < 0) --col, in += d.page_size;
-        if (in >= d.page_size) ++col, in -= d.page_size;
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(page + (ahead & 1))), "l"(seg_pages + col) : "memory");
       }
       ++t, ++ahead;
@@ -1536,6 +1534,7 @@ cudaError_t launch_attn(const AttnParams& params, cudaStream_t stream) {
   const int G = d.Hq / d.Hkv;
   p.tile_toks = kTileRows / G;
   p.tile_rows = p.tile_toks * G;
+  p.page_inv = page_units_inv(d.page_size);
   const EncodeTiled encode = encoder();
   if (!encode) return cudaErrorNotSupported;
   // Tokens per copy of a full tile: as many as lie together in a page, a divisor of the tile's 128.

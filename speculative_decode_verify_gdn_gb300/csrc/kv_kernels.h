@@ -31,6 +31,7 @@ struct AttnParams {
   void* ws;
   uint32_t* err;
   int tile_toks, tile_rows;  // tokens and rows (tokens x query heads per kv head) of a row tile; set by launch_attn
+  uint32_t page_inv;         // of page_column (kv_index.h); set by launch_attn
 };
 
 size_t attn_workspace_bytes(const gdn_kv_dims& d);

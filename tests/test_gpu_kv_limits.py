@@ -1,0 +1,52 @@
+"""Attention over the paged cache at its limits.  Tolerances are those of test_gpu_kv_attn.py."""
+import numpy as np
+import pytest
+import torch
+
+from kv_util import ROUND, i32
+from speculative_decode_verify_gdn_gb300 import gdn, kv
+from speculative_decode_verify_gdn_gb300.build import build_library
+
+pytestmark = pytest.mark.gpu
+BF, HF = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available(), "GPU tests need CUDA"
+    build_library()
+    kv.load_library()
+    gdn.gdn_device_status(clear=True)
+    yield
+    assert gdn.gdn_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("ps", [16, 48, 112])
+def test_the_longest_slot(ps):
+    """A slot of nearly 2^30 tokens whose columns name one page of negligible weight, but for a few
+    marked ones beyond 2^29 tokens and the last: each of their tokens has its share of the output."""
+    rng = np.random.default_rng(ps)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(ps)
+    D, cols = 64, (1 << 30) // ps
+    n = cols * ps - 7
+    marks = np.unique(np.concatenate([rng.integers((1 << 29) // ps, cols, 60), [(1 << 29) // ps + 2, 939524192 // ps,
+                                                                                 cols - 2, cols - 1]]))
+    pages = 1 + len(marks)
+    k, v = (torch.empty((1, pages, ps, 1, D), dtype=BF, device="cuda").normal_(generator=gen) for _ in range(2))
+    k[0, 0, :, 0, 0] = -64.0          # e^-64 of 2^30 tokens: 2e-19 of the sum
+    table = torch.zeros((1, cols), dtype=torch.int32, device="cuda")
+    table[0, torch.from_numpy(marks).cuda()] = torch.arange(1, pages, dtype=torch.int32, device="cuda")
+    k[0, -1, ps - 7:], v[0, -1, ps - 7:] = float("nan"), float("nan")
+    q = torch.zeros((1, 1, 1, D), dtype=BF, device="cuda")
+    q[..., 0] = 1.0
+    kw, vw = (torch.empty((1, 1, 1, D), dtype=BF, device="cuda").normal_(generator=gen) for _ in range(2))
+    out, lse = torch.empty_like(q), torch.empty((1, 1, 1), dtype=torch.float32, device="cuda")
+    dims = kv.make_kv_dims(1, 1, 1, 1, D, ps, pages, cols)
+    kv.gdn_attn_verify(dims, 0, q, kw, vw, k, v, table, i32([n]), None, None, None, 1.0, out, lse, kv.alloc_attn_workspace(dims))
+    keys = torch.cat([k[0, 1:].reshape(-1, D)[:-7], kw.view(1, D)]).double()
+    values = torch.cat([v[0, 1:].reshape(-1, D)[:-7], vw.view(1, D)]).double()
+    w = torch.softmax(keys[:, 0], 0)
+    ref, mag = w @ values, w @ values.abs()
+    assert ((out.view(D).double() - ref).abs() <= ROUND[BF] * (mag + ref.abs()) + 2e-4 * mag).all()
+    assert abs(lse.item() - torch.logsumexp(keys[:, 0], 0).item()) <= 1e-4
