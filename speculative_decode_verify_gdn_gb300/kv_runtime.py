@@ -4,6 +4,10 @@ verify round (attend -> commit, fork, compact).
 Torch allocates the memory; every step runs through the C ABI (include/gdn_kv.h).  The slots are
 the batch's sequences, 0..B-1, and behind them the shared prefixes.  Tables, lengths and
 reference counts are updated in place except by a fork, which writes the other one of two sets.
+
+Every method takes the stream that it runs on (None: the current one).  What it allocates for
+itself belongs to that stream; the caller's tensors and the cache have to be ready there, as for the
+C calls.
 """
 from __future__ import annotations
 
@@ -69,10 +73,11 @@ class PagedCache:
         n = k_new.shape[1]
         d = kv.make_kv_dims(1, n, self.Hq, self.Hkv, self.D, self.page_size, self.n_pages, self.max_pages,
                             self.B + self.n_prefixes, slot, self.n_layers, self.dtype, win=k_new.unsqueeze(1))
-        all_of_it = torch.full((1,), n, dtype=torch.int32, device=k_new.device)
-        kv.gdn_kv_commit(d, all_of_it, None, k_new.unsqueeze(1), v_new.unsqueeze(1), self.k, self.v, self.table,
-                         self.table, self.seq_len, self.seq_len, self.ref, self.ref,
-                         kv.alloc_kv_workspace(d, k_new.device), stream)
+        with torch.cuda.stream(stream):  # (what the call allocates belongs to the stream it runs on)
+            all_of_it = torch.full((1,), n, dtype=torch.int32, device=k_new.device)
+            kv.gdn_kv_commit(d, all_of_it, None, k_new.unsqueeze(1), v_new.unsqueeze(1), self.k, self.v, self.table,
+                             self.table, self.seq_len, self.seq_len, self.ref, self.ref,
+                             kv.alloc_kv_workspace(d, k_new.device), stream)
 
     def attend(self, layer, q, k_win, v_win, out, lse=None, parent=None, win_len=None, scale=None, stream=None) -> None:
         """The window's attention in one layer (a chain, or a token tree given by parent [B, K])."""
