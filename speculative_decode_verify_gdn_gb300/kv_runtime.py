@@ -91,12 +91,18 @@ class PagedCache:
                          self.seq_len, self.seq_len, self.ref, self.ref, self.pool_workspace, stream)
 
     def fork(self, src, stream=None) -> None:
-        """Sequence i goes on from sequence src[i] (src [n_slots] int32; prefixes keep their slots by
-        src[s] = s, and the sequences their prefix_of); -1 drops it."""
+        """Sequence i goes on from sequence src[i], behind that one's prefix (src [n_slots] int32; prefixes
+        keep their slots by src[s] = s); -1 drops it and leaves its entry of prefix_of.  A sequence that
+        goes on from a prefix's own slot has that as its tokens, and none behind them."""
         i, o = self.cur, 1 - self.cur
         kv.gdn_kv_fork(self.dims, src, self.k, self.v, self.tables[i], self.tables[o], self.lens[i], self.lens[o],
                        self.ref, self.ref, self.pool_workspace, stream)
         self.cur = o
+        if self.n_prefixes:
+            with torch.cuda.stream(stream):
+                s = src[:self.B].long()
+                taken = torch.where(s < self.B, self.prefix_of[s.clamp(0, self.B - 1)], -1)
+                self.prefix_of.copy_(torch.where((s >= 0) & (s < self.B + self.n_prefixes), taken, self.prefix_of))
 
     def compact(self, stream=None) -> None:
         """Moves the live pages to the front of the pool; their number goes to n_live."""

@@ -1,8 +1,11 @@
 """PagedCache on streams of its own and with several prefixes.  Tolerances are those of
 test_gpu_kv_attn.py."""
+import numpy as np
 import pytest
 import torch
 
+from kv_util import ROUND, f64
+from oracle import kv_oracle as O
 from speculative_decode_verify_gdn_gb300 import gdn, kv
 from speculative_decode_verify_gdn_gb300.build import build_library
 from speculative_decode_verify_gdn_gb300.kv_runtime import PagedCache
@@ -75,3 +78,36 @@ def test_attention_in_two_streams_at_once():
     torch.cuda.synchronize()
     for w, outs in zip(want, got):
         assert all(torch.equal(w, o) for o in outs)
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_fork_across_prefixes(side):
+    """Sequences of two prefixes, and one without, forked into each other's slots attend to what the
+    sequences they go on from attended to."""
+    B, K, Hq, Hkv, D, ps = 6, 3, 4, 2, 64, 16
+    cache = PagedCache.create(B, K, Hq, Hkv, D, ps, n_pages=200, max_pages=12, n_prefixes=2)
+    lens = [5, 40, 33, 0, 64, 17, 90, 130]
+    for slot, n in enumerate(lens):
+        if n:
+            cache.append(slot, gauss(1, n, Hkv, D), gauss(1, n, Hkv, D))
+    cache.prefix_of.copy_(torch.tensor([6, 7, -1, 6, 7, 6], dtype=torch.int32))
+    one = [gauss(1, K, h, D) for h in (Hq, Hkv, Hkv)]
+    q, kw, vw = (x.expand(B, K, -1, -1).contiguous() for x in one)   # every sequence drafts the same window
+    before, after = torch.empty_like(q), torch.empty_like(q)
+    cache.attend(0, q, kw, vw, before)
+    src = [1, 2, 0, 4, 3, 3]
+    s = torch.cuda.Stream() if side else None
+    torch.cuda.synchronize()
+    cache.fork(torch.tensor(src + [6, 7], dtype=torch.int32, device="cuda"), stream=s)
+    cache.attend(0, q, kw, vw, after, stream=s)
+    torch.cuda.synchronize()
+    assert cache.prefix_of.tolist() == [7, -1, 6, 7, 6, 6]
+    table, n = cache.table.cpu().numpy(), cache.seq_len.cpu().numpy()
+    args = (f64(kw), np.abs(f64(vw)), np.nan_to_num(f64(cache.k[0])), np.abs(np.nan_to_num(f64(cache.v[0]))), table, n,
+            cache.prefix_of.tolist(), None, None, D ** -0.5)
+    mag, _ = O.attention(f64(q), *args)
+    want, got = f64(before)[src], f64(after)
+    # two roundings of the probabilities and of the output, from different tiles
+    assert (np.abs(got - want) <= 2 * (ROUND[BF] * (mag + np.abs(want)) + 2e-4 * mag)).all()
+    ref, _ = O.attention(f64(q), f64(kw), f64(vw), np.nan_to_num(f64(cache.k[0])), np.nan_to_num(f64(cache.v[0])), *args[4:])
+    assert (np.abs(got - ref) <= ROUND[BF] * (mag + np.abs(ref)) + 2e-4 * mag).all()

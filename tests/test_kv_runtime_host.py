@@ -58,3 +58,23 @@ def test_append_allocates_and_fills_on_the_stream_it_runs_on(on, monkeypatch):
         assert made and all(m is stream for m in made)
         accept, passed = calls[-1]
         assert passed is stream and accept.tolist() == [5]
+
+
+def test_fork_takes_the_prefix_along(on, monkeypatch):
+    """Sequence i goes on behind the prefix of the sequence it takes.  One that goes on from a prefix's own
+    slot has none behind it; a dropped slot, or one whose source is no slot, keeps its entry."""
+    seen = []
+    monkeypatch.setattr(kv, "gdn_kv_fork", lambda *args: seen.append((on[-1], args[-1])))
+    c = cache(B=5)
+    prefix_of = c.prefix_of
+    side = FakeStream()
+    for src, before, after in (([1, 0, 3, 3, -1, 5, 6], [5, 6, -1, 6, 5], [6, 5, 6, 6, 5]),
+                               ([4, 4, 2, 2, 0, 5, 6], [5, 6, -1, 6, 6], [6, 6, -1, -1, 5]),
+                               ([5, 6, -9, 7, 1, 5, 6], [5, 5, 6, 5, 6], [-1, -1, 6, 5, 5])):
+        prefix_of.copy_(torch.tensor(before, dtype=torch.int32))
+        c.fork(torch.tensor(src, dtype=torch.int32), stream=side)
+        assert c.prefix_of is prefix_of and prefix_of.tolist() == after
+    assert seen[-1][1] is side
+    alone = cache(n_prefixes=0)
+    alone.fork(torch.tensor([2, 1, 0], dtype=torch.int32))
+    assert alone.prefix_of.tolist() == [-1, -1, -1] and seen[-1][1] is None
