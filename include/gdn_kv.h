@@ -18,7 +18,8 @@
  *   layer * cache_layer_stride + page * cache_page_stride + token * cache_token_stride
  *   + head * cache_head_stride + i
  * in both, so [page][token][head][D] and [page][head][token][D] orders, and keys and values
- * interleaved in one buffer, are all described by the strides.  A slot is one sequence (or one
+ * interleaved in one buffer, are all described by the strides.  Where a call writes them, the two may
+ * have no element in common (GDN_ERR_ALIAS).  A slot is one sequence (or one
  * shared prefix): row s of page_table [n_slots, max_pages] int32 lists its pages in order, and
  * seq_len[s] int32 counts its tokens; it owns ceil(seq_len / page_size) pages, and the rest of
  * the row is not read.  ref[p] int32 counts the slots that hold page p (plus whatever the

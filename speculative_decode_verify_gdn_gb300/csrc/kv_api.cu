@@ -71,11 +71,40 @@ struct Buf {
   const char* may_be;  // the input that this output may be
 };
 
+// A cache's dimensions, the largest stride first.
+struct CacheDim {
+  int64_t stride, n;
+};
+void sorted_dims(const gdn_kv_dims& d, CacheDim (&m)[4]) {
+  m[0] = {d.cache_layer_stride, d.n_layers}, m[1] = {d.cache_page_stride, d.n_pages};
+  m[2] = {d.cache_token_stride, d.page_size}, m[3] = {d.cache_head_stride, d.Hkv};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 4; ++j)
+      if (m[j].stride > m[i].stride) {
+        const CacheDim t = m[i];
+        m[i] = m[j];
+        m[j] = t;
+      }
+}
+
+// Whether two caches of these dimensions, `delta` elements apart, share an element: whether delta is a
+// sum of differences of indices times strides, and of places in a row.  Where the strides do not fold
+// (check_cache_strides) what the smaller ones can add is less than a stride, so that only the two
+// multiples next to delta come into question.
+bool share_element(const CacheDim* m, int left, int64_t D, int64_t delta) {
+  if (left == 0) return delta > -D && delta < D;
+  if (m->n == 1) return share_element(m + 1, left - 1, D, delta);
+  const int64_t q = delta / m->stride - (delta % m->stride < 0 ? 1 : 0);
+  for (int64_t i = q; i <= q + 1; ++i)
+    if (i > -m->n && i < m->n && share_element(m + 1, left - 1, D, delta - i * m->stride)) return true;
+  return false;
+}
+
 // k_cache and v_cache may lie interleaved in one buffer
 const char* const kInterleaved = "interleaved";
 
 // Null pointers, alignment, and overlaps of outputs with anything else.
-gdn_status check_bufs(const Buf* b, int n) {
+gdn_status check_bufs(const gdn_kv_dims& d, const Buf* b, int n) {
   for (int i = 0; i < n; ++i) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(b[i].p);
     if (!a && !b[i].optional) return fail(GDN_ERR_INVALID_ARG, "%s is NULL", b[i].name);
@@ -89,7 +118,11 @@ gdn_status check_bufs(const Buf* b, int n) {
       const uintptr_t lo2 = reinterpret_cast<uintptr_t>(b[j].p), hi2 = lo2 + b[j].bytes;
       if (lo >= hi2 || lo2 >= hi) continue;
       if (lo == lo2 && b[i].may_be == b[j].name) continue;
-      if (b[i].may_be == kInterleaved && b[j].may_be == kInterleaved && lo != lo2) continue;
+      if (b[i].may_be == kInterleaved && b[j].may_be == kInterleaved) {
+        CacheDim m[4];
+        sorted_dims(d, m);
+        if (!share_element(m, 4, d.D, (int64_t(lo2) - int64_t(lo)) / 2)) continue;
+      }
       return fail(GDN_ERR_ALIAS, "%s overlaps %s", b[i].name, b[j].name);
     }
   }
@@ -116,19 +149,10 @@ unsigned long long cache_bytes(const gdn_kv_dims& d) {
 // has to start at or beyond the extent of those below it.  (Reads would be harmless, but pages are
 // written too.)
 gdn_status check_cache_strides(const gdn_kv_dims& d) {
-  struct Dim {
-    int64_t stride, n;
-  } m[4] = {{d.cache_layer_stride, d.n_layers}, {d.cache_page_stride, d.n_pages}, {d.cache_token_stride, d.page_size},
-            {d.cache_head_stride, d.Hkv}};
-  for (int i = 0; i < 4; ++i)
-    for (int j = i + 1; j < 4; ++j)
-      if (m[j].stride < m[i].stride) {
-        const Dim t = m[i];
-        m[i] = m[j];
-        m[j] = t;
-      }
+  CacheDim m[4];
+  sorted_dims(d, m);
   int64_t extent = d.D;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 3; i >= 0; --i) {
     if (m[i].n == 1) continue;
     if (m[i].stride < extent) return fail(GDN_ERR_INVALID_ARG, "cache strides make elements overlap");
     if (m[i].n > (INT64_MAX / 4) / m[i].stride) return fail(GDN_ERR_INVALID_ARG, "cache too large");
@@ -163,7 +187,7 @@ gdn_status check_pool(gdn::PagesParams& p, const Buf* bufs, int n, uint64_t work
   const unsigned long long need = gdn::pages_workspace_bytes(p.d);
   if (workspace_bytes < need)
     return fail(GDN_ERR_INVALID_ARG, "workspace has %llu bytes, %llu needed", (unsigned long long)workspace_bytes, need);
-  GDN_RETURN_IF(check_bufs(bufs, n));
+  GDN_RETURN_IF(check_bufs(p.d, bufs, n));
   return gdn::device_status_word(&p.err);
 }
 
@@ -207,7 +231,7 @@ gdn_status gdn_attn_verify(const gdn_kv_dims* dims, int32_t layer, const void* q
       {"lse", lse, 4ull * rows * d.Hq, 4, true, true, nullptr},
       {"workspace", workspace, need, 256, true, false, nullptr},
   };
-  GDN_RETURN_IF(check_bufs(bufs, int(sizeof bufs / sizeof bufs[0])));
+  GDN_RETURN_IF(check_bufs(d, bufs, int(sizeof bufs / sizeof bufs[0])));
   uint32_t* err = nullptr;
   GDN_RETURN_IF(gdn::device_status_word(&err));
   const gdn::AttnParams p{d, layer, q, k_win, v_win, k_cache, v_cache, page_table, seq_len, prefix_of, win_len, parent,
