@@ -18,6 +18,7 @@ gdn_status fail(gdn_status s, const char* fmt, ...) {
   return gdn::report_error(s, buf);
 }
 
+constexpr int kMaxBatch = 65535;
 enum Use { kAttn, kCommit, kPool };
 
 gdn_status check_dims(const gdn_kv_dims* d, Use use, bool tree) {
@@ -39,7 +40,7 @@ gdn_status check_dims(const gdn_kv_dims* d, Use use, bool tree) {
     if (cn_n[i] > 1 && (cs[i] < d->D || cs[i] % 8 || cs[i] >= (1LL << 36)))
       return fail(GDN_ERR_INVALID_ARG, "cache_%s_stride=%lld (a multiple of 8, at least D)", cn[i], (long long)cs[i]);
   if (use == kPool) return GDN_OK;
-  if (d->B < 0 || d->B > 65535) return fail(GDN_ERR_INVALID_ARG, "B=%d outside 0..65535", d->B);
+  if (d->B < 0 || d->B > kMaxBatch) return fail(GDN_ERR_INVALID_ARG, "B=%d outside 0..%d", d->B, kMaxBatch);
   if (d->slot0 < 0 || (long long)d->slot0 + d->B > d->n_slots)
     return fail(GDN_ERR_INVALID_ARG, "slots %d..%d outside the table's %d", d->slot0, d->slot0 + d->B - 1, d->n_slots);
   const int kmax = use == kAttn || tree ? gdn::kKvWinMax : 1 << 20;
@@ -184,7 +185,7 @@ gdn::PagesParams pool_params(const gdn_kv_dims& d, void* k_cache, void* v_cache,
 // The checks that the three pool calls share; fills in the status word.
 gdn_status check_pool(gdn::PagesParams& p, const Buf* bufs, int n, uint64_t workspace_bytes) {
   GDN_RETURN_IF(check_cache_strides(p.d));
-  const unsigned long long need = gdn::pages_workspace_bytes(p.d);
+  const unsigned long long need = bufs[n - 1].bytes;  // (the last buffer is the workspace)
   if (workspace_bytes < need)
     return fail(GDN_ERR_INVALID_ARG, "workspace has %llu bytes, %llu needed", (unsigned long long)workspace_bytes, need);
   GDN_RETURN_IF(check_bufs(p.d, bufs, n));
@@ -244,7 +245,8 @@ gdn_status gdn_attn_verify(const gdn_kv_dims* dims, int32_t layer, const void* q
 gdn_status gdn_kv_workspace_size(const gdn_kv_dims* dims, uint64_t* bytes) {
   GDN_RETURN_IF(check_dims(dims, kPool, false));
   if (!bytes) return fail(GDN_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = gdn::pages_workspace_bytes(*dims);
+  // (a batch that commit refuses takes no room)
+  *bytes = gdn::pages_workspace_bytes(*dims, dims->B < 0 || dims->B > kMaxBatch ? 0 : dims->B);
   return gdn::report_ok();
 }
 
@@ -273,7 +275,7 @@ gdn_status gdn_kv_commit(const gdn_kv_dims* dims, const int32_t* accept_len, con
       {"table_out", table_out, 4ull * d.n_slots * d.max_pages, 4, true, false, bufs[4].name},
       {"len_out", len_out, 4ull * d.n_slots, 4, true, false, bufs[5].name},
       {"ref_out", ref_out, 4ull * d.n_pages, 4, true, false, bufs[6].name},
-      {"workspace", workspace, gdn::pages_workspace_bytes(d), 256, true, false, nullptr},
+      {"workspace", workspace, gdn::pages_workspace_bytes(d, d.B), 256, true, false, nullptr},
   };
   gdn::PagesParams p = pool_params(d, k_cache, v_cache, table_in, table_out, ref_in, ref_out, workspace);
   GDN_RETURN_IF(check_pool(p, bufs, int(sizeof bufs / sizeof bufs[0]), workspace_bytes));
@@ -304,7 +306,7 @@ gdn_status gdn_kv_fork(const gdn_kv_dims* dims, const int32_t* src, void* k_cach
       {"table_out", table_out, 4ull * d.n_slots * d.max_pages, 4, true, false, nullptr},
       {"len_out", len_out, 4ull * d.n_slots, 4, true, false, nullptr},
       {"ref_out", ref_out, 4ull * d.n_pages, 4, true, false, bufs[3].name},
-      {"workspace", workspace, gdn::pages_workspace_bytes(d), 256, true, false, nullptr},
+      {"workspace", workspace, gdn::pages_workspace_bytes(d, 0), 256, true, false, nullptr},
   };
   gdn::PagesParams p = pool_params(d, k_cache, v_cache, table_in, table_out, ref_in, ref_out, workspace);
   GDN_RETURN_IF(check_pool(p, bufs, int(sizeof bufs / sizeof bufs[0]), workspace_bytes));
@@ -330,7 +332,7 @@ gdn_status gdn_kv_compact(const gdn_kv_dims* dims, void* k_cache, void* v_cache,
       {"table_out", table_out, 4ull * d.n_slots * d.max_pages, 4, true, false, bufs[0].name},
       {"ref_out", ref_out, 4ull * d.n_pages, 4, true, false, bufs[2].name},
       {"n_live", n_live, 4, 4, true, false, nullptr},
-      {"workspace", workspace, gdn::pages_workspace_bytes(d), 256, true, false, nullptr},
+      {"workspace", workspace, gdn::pages_workspace_bytes(d, 0), 256, true, false, nullptr},
   };
   gdn::PagesParams p = pool_params(d, k_cache, v_cache, table_in, table_out, ref_in, ref_out, workspace);
   GDN_RETURN_IF(check_pool(p, bufs, int(sizeof bufs / sizeof bufs[0]), workspace_bytes));

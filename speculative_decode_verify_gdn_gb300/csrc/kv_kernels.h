@@ -58,7 +58,7 @@ struct PagesParams {
   uint32_t* err;
 };
 
-size_t pages_workspace_bytes(const gdn_kv_dims& d);
+size_t pages_workspace_bytes(const gdn_kv_dims& d, int sequences);  // (those of a commit; else 0)
 cudaError_t launch_commit(const PagesParams& p, cudaStream_t stream);
 cudaError_t launch_fork(const PagesParams& p, cudaStream_t stream);
 cudaError_t launch_compact(const PagesParams& p, cudaStream_t stream);

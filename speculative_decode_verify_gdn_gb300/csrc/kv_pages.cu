@@ -1,7 +1,7 @@
 // Upkeep of the paged key/value cache: commit of accepted window tokens, fork / drop / reorder of
 // sequences, compaction of the pool (contracts in include/gdn_kv.h).
 //
-// Each call is two launches.  The first plans: its CTA 0 (1024 threads) walks lengths and
+// Each call is two launches.  The first plans: its CTA 0 (512 threads) walks lengths and
 // reference counts and writes, into the workspace, which pages go where; its other CTAs copy the
 // tables that are not updated in place.  It changes no input, so a call may work in place.  The
 // second moves the data (all layers, keys and values) and then edits tables, lengths and
@@ -37,16 +37,16 @@ struct Move {  // one page's copy (fork, compact)
   int32_t from, to, tokens, pad;
 };
 
-// Workspace: header, then records (commit: B, fork: n_slots), the free or move lists, and one
-// int per page.
+// Workspace: header, the move list, the free pages, one int per page and two per slot, and last the
+// records of a commit's sequences: fork and compact neither need them nor read B.
 struct PagesWs {
-  int32_t* head;      // [0] moves in the list, [1] free pages found, [2] live pages
-  CommitRec* rec;     // [max(B, 1)]
-  Move* move;         // [max(n_slots, n_pages)]
+  int32_t* head;      // [0] moves in the list, [1] live pages
+  Move* move;         // [max(n_slots, n_pages)] fork, compact
   int32_t* ids;       // [n_pages] free pages in order
   int32_t* map;       // [n_pages] compact: new number of each page from n_live on (-1: it is free)
   int32_t* first;     // [n_slots] fork: lowest taker
   int32_t* made;      // [n_slots] fork: the slot's copied page (-1 none, -2 failed)
+  CommitRec* rec;     // [B] commit
 };
 
 __host__ __device__ inline size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -57,12 +57,12 @@ __host__ __device__ inline PagesWs carve_pages(void* base, const gdn_kv_dims& d,
   const size_t pages = size_t(d.n_pages), slots = size_t(d.n_slots), moves = pages > slots ? pages : slots;
   PagesWs w;
   w.head = reinterpret_cast<int32_t*>(p + o), o += 256;
-  w.rec = reinterpret_cast<CommitRec*>(p + o), o += up256(sizeof(CommitRec) * size_t(d.B > 0 ? d.B : 1));
   w.move = reinterpret_cast<Move*>(p + o), o += up256(sizeof(Move) * moves);
   w.ids = reinterpret_cast<int32_t*>(p + o), o += up256(4 * pages);
   w.map = reinterpret_cast<int32_t*>(p + o), o += up256(4 * pages);
   w.first = reinterpret_cast<int32_t*>(p + o), o += up256(4 * slots);
   w.made = reinterpret_cast<int32_t*>(p + o), o += up256(4 * slots);
+  w.rec = reinterpret_cast<CommitRec*>(p + o);
   if (total) *total = o;
   return w;
 }
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const __g
       count += total;
     }
     __syncthreads();
-    if (threadIdx.x == 0) w.head[0] = count, w.head[2] = live;
+    if (threadIdx.x == 0) w.head[0] = count, w.head[1] = live;
   }
 }
 
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_move_kernel(const __g
   grid_launch_dependents();
   grid_wait();
   const gdn_kv_dims& d = p.d;
-  const int live = w.head[2], moves = w.head[0];
+  const int live = w.head[1], moves = w.head[0];
   const long long at = (long long)blockIdx.x * kMoveThreads + threadIdx.x, step = (long long)gridDim.x * kMoveThreads;
   if (at == 0) p.n_live[0] = live;
   for (long long r = at; r < moves; r += step) {  // (one thread per pair: reads, then writes, in place too)
@@ -564,10 +564,10 @@ int plan_grid(long long ints) { return 1 + int(ints < 1 ? 1 : (ints + 16383) / 1
 
 }  // namespace
 
-size_t pages_workspace_bytes(const gdn_kv_dims& d) {
+size_t pages_workspace_bytes(const gdn_kv_dims& d, int sequences) {
   size_t n = 0;
   carve_pages(nullptr, d, &n);
-  return n;
+  return n + up256(sizeof(CommitRec) * size_t(sequences));
 }
 
 cudaError_t launch_commit(const PagesParams& p, cudaStream_t stream) {
