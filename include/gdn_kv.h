@@ -84,7 +84,8 @@ typedef struct {
  *   win_len    [B] int32 or NULL (= K): tokens t >= win_len[b] are padding; their out is 0 and
  *              their lse -inf, and what q, k_win and v_win hold there (NaN included) reaches no
  *              other row
- *   parent     [B, K] int32 or NULL: parent[b][t] in -1..t-1, as in gdn_verify_tree
+ *   parent     [B, K] int32 or NULL: parent[b][t] in -1..t-1, as in gdn_verify_tree; not read at padding
+ *              tokens
  *   scale      finite
  *   out        [B, K, Hq, D] contiguous, dtype; lse [B, K, Hq] f32 or NULL
  *   workspace  at least gdn_attn_workspace_size() bytes, no initialisation needed, dead after

@@ -1102,7 +1102,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t anc = 0;
         if (p.parent) {
           int up = -1;
-          if (lane < d.K) {
+          if (lane < seg.win) {  // (a padding token has no parent)
             up = p.parent[(long long)seg.idx * d.K + lane];
             if (up < -1 || up >= lane) {
               atomicOr(p.err, kDevErrTreeParent);

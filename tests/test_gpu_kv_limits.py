@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from kv_util import ROUND, i32
+from kv_util import ROUND, Pool, i32, random_trees
 from speculative_decode_verify_gdn_gb300 import gdn, kv
 from speculative_decode_verify_gdn_gb300.build import build_library
 
@@ -50,3 +50,24 @@ def test_the_longest_slot(ps):
     ref, mag = w @ values, w @ values.abs()
     assert ((out.view(D).double() - ref).abs() <= ROUND[BF] * (mag + ref.abs()) + 2e-4 * mag).all()
     assert abs(lse.item() - torch.logsumexp(keys[:, 0], 0).item()) <= 1e-4
+
+
+def test_parents_of_padding_tokens_are_not_read():
+    """Whatever a tree holds behind a window's tokens, no status bit is set and no row changes."""
+    B, K, Hq = 5, 9, 4
+    pool = Pool(40, [20, 0, 130, 7, 64])
+    win = np.array([0, 1, 4, 8, 9])
+    par = random_trees(pool.rng, B, K)
+    q, k, v = (pool.gauss((B, K, h, pool.D)) for h in (Hq, pool.Hkv, pool.Hkv))
+    dims = pool.dims(B, K, Hq)
+    ws, results = kv.alloc_attn_workspace(dims), []
+    for fill in (None, 99, -7, K - 1, -(1 << 31), (1 << 31) - 1):
+        p = par.copy()
+        if fill is not None:
+            p[np.arange(K)[None, :] >= win[:, None]] = fill
+        out, lse = torch.empty_like(q), torch.empty((B, K, Hq), dtype=torch.float32, device="cuda")
+        kv.gdn_attn_verify(dims, 0, q, k, v, pool.k, pool.v, i32(pool.table), i32(pool.lens), None, i32(win), i32(p),
+                           pool.D ** -0.5, out, lse, ws)
+        assert gdn.gdn_device_status(clear=True) == 0, fill
+        results.append((out, lse))
+    assert all(torch.equal(a, b) for r in results[1:] for a, b in zip(r, results[0]))
