@@ -46,11 +46,11 @@ def make_kv_dims(B, K, Hq, Hkv, D, page_size, n_pages, max_pages, n_slots=None, 
         raise ValueError(f"dtype must be bfloat16 or float16, got {dtype}")
     row = Hkv * D
     cs = (n_pages * page_size * row, page_size * row, row, D) if cache is None else cache.stride()[:4]
-    qs = Hq * D if q is None else q.stride(1) if K > 1 else q.stride(0)
-    ws, ls = row, B * K * row
-    if win is not None:
-        ws = win.stride(-3) if K > 1 else win.stride(-4)
-        ls = win.stride(0) if win.dim() == 5 else 0
+    step = -3 if K > 1 else -4  # from token to token; a single one has none, whatever its stride says
+    one = B * K == 1
+    qs = Hq * D if q is None or one else q.stride(step)
+    ws = row if win is None or one else win.stride(step)
+    ls = B * K * row if win is None else win.stride(0) if win.dim() == 5 else 0
     return KvDims(B, K, Hq, Hkv, D, page_size, n_pages, max_pages, B if n_slots is None else n_slots, slot0, n_layers,
                   _DTYPES[dtype], *cs, qs, ws, ls)
 
