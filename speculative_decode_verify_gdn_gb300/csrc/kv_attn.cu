@@ -70,7 +70,10 @@ constexpr float kLn2 = 0.693147180559945f, kLog2e = 1.442695040888963f;
 constexpr float kLag = 8.0f;
 // Longest wait inside the tile kernel (kMaxLooks): looks of at most about a microsecond each, a few seconds in all.
 constexpr uint32_t kMaxLooks = 1u << 22;
-constexpr uint32_t kMaxTurnLooks = 1u << 14, kMaxIdle = 1u << 25;
+// The scheduler looks on for as long as a segment takes, every 220 ns: up to a slot of 2^30 tokens on one
+// CTA, 7 s and for a pair of row tiles about twice that.  A CTA that is stuck is found by the other
+// warps' waits, and the scheduler ends with them.
+constexpr uint32_t kMaxTurnLooks = 1u << 14, kMaxIdle = 1u << 28;
 
 // ---------------------------------------------------------------- the plan
 struct SeqRec {       // a sequence: what it does not share, and where its rows are in its prefix run

@@ -71,3 +71,35 @@ def test_parents_of_padding_tokens_are_not_read():
         assert gdn.gdn_device_status(clear=True) == 0, fill
         results.append((out, lse))
     assert all(torch.equal(a, b) for r in results[1:] for a, b in zip(r, results[0]))
+
+
+def test_segments_of_many_seconds():
+    """More sequences of 3 x 2^28 tokens, a pair of row tiles each, than there are CTAs: each works on a
+    segment for ten seconds with another behind it, and no bounded wait takes that for a fault.  The
+    columns name pages of negligible weight but for one."""
+    D, ps, B, K, G = 64, 1024, 153, 16, 16
+    cols = 3 * (1 << 28) // ps
+    n = cols * ps - 5
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    k, v = (torch.empty((1, 65, ps, 1, D), dtype=BF, device="cuda").normal_(generator=gen) for _ in range(2))
+    k[0, :64, :, 0, 0] = -64.0
+    table = (torch.arange(cols, dtype=torch.int32, device="cuda") % 64).repeat(B, 1)
+    table[:, cols - 2] = 64
+    q = torch.zeros((B, K, G, D), dtype=BF, device="cuda")
+    q[..., 0] = 1.0
+    kw, vw = (torch.empty((B, K, 1, D), dtype=BF, device="cuda").normal_(generator=gen) for _ in range(2))
+    out, lse = torch.empty_like(q), torch.empty((B, K, G), dtype=torch.float32, device="cuda")
+    dims = kv.make_kv_dims(B, K, G, 1, D, ps, 65, cols)
+    kv.gdn_attn_verify(dims, 0, q, kw, vw, k, v, table, i32([n] * B), None, None, None, 1.0, out, lse,
+                       kv.alloc_attn_workspace(dims))
+    torch.cuda.synchronize()
+    assert gdn.gdn_device_status(clear=True) == 0
+    keys = torch.cat([k[0, 64, :, 0].expand(B, ps, D), kw[:, :, 0]], 1).double()
+    values = torch.cat([v[0, 64, :, 0].expand(B, ps, D), vw[:, :, 0]], 1).double()
+    seen = torch.cat([torch.ones(K, ps, device="cuda"), torch.ones(K, K, device="cuda").tril()], 1) > 0
+    scores = keys[:, None, :, 0].expand(B, K, -1).masked_fill(~seen, float("-inf"))
+    w = torch.softmax(scores, 2)
+    ref, mag = (w @ values)[:, :, None], (w @ values.abs())[:, :, None]
+    assert ((out.double() - ref).abs() <= ROUND[BF] * (mag + ref.abs()) + 2e-4 * mag).all()
+    assert ((lse.double() - torch.logsumexp(scores, 2)[:, :, None]).abs() <= 1e-4).all()
