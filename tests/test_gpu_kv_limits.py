@@ -103,3 +103,27 @@ def test_segments_of_many_seconds():
     ref, mag = (w @ values)[:, :, None], (w @ values.abs())[:, :, None]
     assert ((out.double() - ref).abs() <= ROUND[BF] * (mag + ref.abs()) + 2e-4 * mag).all()
     assert ((lse.double() - torch.logsumexp(scores, 2)[:, :, None]).abs() <= 1e-4).all()
+
+
+@pytest.mark.parametrize("page", [-1, 1 << 27])
+@pytest.mark.parametrize("shared", [False, True])
+def test_a_bad_page_leaves_the_other_sequences_alone(page, shared):
+    """A page number outside the pool in one sequence's row (or in the prefix of two): the sequences that
+    do not read it get the results that they get without it."""
+    B, K, Hq = 5, 3, 4
+    pre = [5, 5, 6, 6, -1]
+    pool = Pool(41, [40, 300, 17, 0, 130, 90, 200], D=64)
+    q, k, v = (pool.gauss((B, K, h, pool.D)) for h in (Hq, pool.Hkv, pool.Hkv))
+    dims = pool.dims(B, K, Hq)
+    ws, results = kv.alloc_attn_workspace(dims), []
+    for bad in (False, True):
+        table = pool.table.copy()
+        if bad:
+            table[5 if shared else 1, 0] = page
+        out, lse = torch.empty_like(q), torch.empty((B, K, Hq), dtype=torch.float32, device="cuda")
+        kv.gdn_attn_verify(dims, 0, q, k, v, pool.k, pool.v, i32(table), i32(pool.lens), i32(pre), None, None,
+                           pool.D ** -0.5, out, lse, ws)
+        assert gdn.gdn_device_status(clear=True) == (kv.DEVERR_KV_PAGE if bad else 0)
+        results.append((out, lse))
+    for b in [2, 3, 4] + ([] if shared else [0]):
+        assert all(torch.equal(x[b], y[b]) for x, y in zip(*results)), b
