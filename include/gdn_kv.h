@@ -91,7 +91,8 @@ typedef struct {
  *   workspace  at least gdn_attn_workspace_size() bytes, no initialisation needed, dead after
  *              the call
  * Scores, softmax statistics and sums are f32; the probabilities are rounded to dtype for the
- * product with the values.  What the cache holds beyond a slot's tokens reaches no output; a
+ * product with the values (some of them twice, where a row's running maximum rises by more than
+ * 2^8 within a tile of 128 keys: they then hold less than that row's new largest).  What the cache holds beyond a slot's tokens reaches no output; a
  * value that is not finite at a token that any row of the same window sees may reach every row
  * of that window.  Results do not depend on the order in which CTAs run.
  */

@@ -34,14 +34,14 @@
 //
 // Measured on one GB300 (plan + tiles + join; peaks: 6796 GB/s copy, 1957 TFLOP/s cuBLAS bf16, 1733
 // when the power cap sets the clock):
-//   B=64 K=16 Hq=32 Hkv=4 D=128 behind 32768 tokens   384-408 us, 1360-1440 TFLOP/s: bound by the tensor
+//   B=64 K=16 Hq=32 Hkv=4 D=128 behind 32768 tokens   383-409 us, 1350-1450 TFLOP/s: bound by the tensor
 //     core's wait for a stream's chain (S, softmax, P, O), a tile pair every ~3000 cycles where its
 //     products take 2048
 //   B=1 K=16 Hq=32 Hkv=8 over 131072 tokens           94 us, 5710 GB/s: HBM, then the join
-//   B=32 K=16 Hq=32 Hkv=8 behind 8192 + 1..2048       99 us: prefix tiles 45, own tiles 25 (latency
+//   B=32 K=16 Hq=32 Hkv=8 behind 8192 + 1..2048       99-100 us: prefix tiles 45, own tiles 25 (latency
 //     of a 5-tile ring), start, ends and join the rest
-//   B=256 K=1 Hq=32 Hkv=8, 4 prefixes of 3001 + 5..1024  154 us, 3870 GB/s
-//   B=1 K=1 over 700 tokens                           15 us: two dependent launches
+//   B=256 K=1 Hq=32 Hkv=8, 4 prefixes of 3001 + 5..1024  151 us, 3930 GB/s
+//   B=1 K=1 over 700 tokens                           14-15 us: two dependent launches
 // The loops over boxes and over scores are kept rolled: the kernel's code is more than the
 // instruction cache holds, and unrolling them costs more in misses than it saves.
 #include <atomic>
@@ -359,7 +359,7 @@ struct Seg {
 
 // The plan of a batch of at most 32 sequences, by one converged warp: lane b has sequence b's record
 // and lane r run r's.  The tile kernel's scheduler makes it for itself, which saves the plan kernel's
-// launch (B=1 decode: 17.4 us with it).
+// launch (B=1 decode: 17.1 us with it, 14.8 without).
 constexpr int kWarpPlan = 32;
 __device__ __forceinline__ long long warp_scan(long long v, int lane, long long& total) {  // exclusive
   long long x = v;
@@ -756,7 +756,9 @@ __device__ __forceinline__ float max64(const float (&x)[64]) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// 32 probabilities of this thread's row (16 words of tensor memory) times f.
+// 32 probabilities of this thread's row (16 words of tensor memory) times f, rounded to the type a second
+// time: they belong to a tile's first half, whose second half holds a score whose weight is more than 2^kLag
+// times the largest that the row knew of.
 template <bool F16>
 __device__ __forceinline__ void rescale_pairs(uint32_t taddr, float f) {
   uint32_t r[16];
@@ -1332,8 +1334,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // leave eight CTAs to an SM, 4 at least (the whole call at B=32 K=16 behind 8192 tokens: 106 us, 117
 // with two CTAs to an SM, 109 with sixteen; at B=1 K=16 with 40 segments a row a join with 32 rows to
 // a CTA takes 63 us where 4 take 12).  A grid that is on the card at once has registers for sixteen
-// rows of sums in flight instead of four (B=1 K=16 over 131072 tokens: 94 us, 99 with four; with
-// sixteen everywhere B=32 K=16 takes 110 us, 100 with four).
+// rows of sums in flight instead of four (K=16 Hq=32 Hkv=8: one sequence of 131072 tokens 94.2 us, 99.2
+// with four; four of 32768, 512 CTAs, 92.6 and 94.3; five of 26000, 640 CTAs and more than four to an SM,
+// 94.2 and 93.9; sixteen of 8192 103.6 and 97.8).
 template <int D, bool F16, int U>
 __global__ void __launch_bounds__(32 * kJoinWarps, U == 4 ? 8 : 4)
     attn_join_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnWs w, const int join_rows) {
