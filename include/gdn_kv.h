@@ -10,6 +10,13 @@
  *   gdn_kv_commit    moves the accepted tokens' keys and values of all layers into pages;
  *   gdn_kv_fork      forks, drops and reorders sequences, sharing pages by reference count;
  *   gdn_kv_compact   moves the live pages to the lowest page numbers.
+ * Around that, what comes before a window's attention, and prompts:
+ *   gdn_attn_rope    norms and rotates the window's queries and keys as they come from the projection;
+ *   gdn_kv_reserve   takes the pages for new tokens of each sequence, once for all layers;
+ *   gdn_kv_append    brings one layer's packed tokens into place: queries and keys normed and rotated,
+ *                    keys and values written to the reserved pages;
+ *   gdn_attn_prefill attends packed queries to the pages, causally (prompts, chunks of prompts, single
+ *                    tokens) or to all of a slot (cross attention to states of another length).
  * The window's keys and values stay outside the pages until they are accepted, so a rejected
  * draft needs no rollback here.
  *
@@ -43,7 +50,7 @@ extern "C" {
 #endif
 
 /* Further bits of the per-device status word (gdn_device_status). */
-#define GDN_DEVERR_KV_LEN 32u      /* a seq_len was negative or beyond the table's columns; the slot was read as empty */
+#define GDN_DEVERR_KV_LEN 32u      /* a seq_len was negative or beyond the table's columns; the slot was read as empty (also as said at a call) */
 #define GDN_DEVERR_KV_PAGE 64u     /* a page number was outside 0..n_pages-1; results that read it are invalid */
 #define GDN_DEVERR_KV_SLOT 128u    /* a slot index (prefix_of, src) was outside -1..n_slots-1; it was read as -1 */
 #define GDN_DEVERR_KV_FULL 256u    /* no free page, or no column, was left; that sequence was not changed */
@@ -160,6 +167,112 @@ gdn_status gdn_kv_compact(const gdn_kv_dims* dims, void* k_cache, void* v_cache,
  * last two do not read B: what B = 0 gives is enough for them.
  */
 gdn_status gdn_kv_workspace_size(const gdn_kv_dims* dims, uint64_t* bytes);
+
+/*
+ * Norm and rotation of the heads of queries and keys, and the strides of the rows they come from.
+ * With a weight w [D] the head is first divided by its root mean square,
+ *   x_i <- x_i (weight_offset + w_i) / sqrt(mean_j x_j^2 + eps),
+ * then the pairs (a, b) of its first rot_dim elements are turned: with the angle phi of the pair at
+ * the token's position,
+ *   (a, b) <- magnitude * (a cos phi - b sin phi, b cos phi + a sin phi).
+ * All of it is computed in f32 and rounded to dtype once.  The rest of the head is normed only.
+ * Angles are exact for far positions: turns[i] is the i-th pair's angle of one token as a 64-bit
+ * fraction of a turn (gdn_rope_turns), so that position x turns mod 2^64 is the angle.  Frequencies
+ * scaled for long contexts are a matter of that table.
+ */
+typedef struct {
+  int32_t rot_dim;       /* a multiple of 8, 0..D */
+  int32_t interleaved;   /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1); i = 0 .. rot_dim / 2 - 1 */
+  float magnitude;       /* of the rotated elements (1 unless long contexts rescale it); finite */
+  float eps;             /* of the norms; finite, >= 0 */
+  float weight_offset;   /* added to the norms' weights (0, or 1 where they are kept as differences from 1); finite */
+  int32_t reserved;      /* 0 */
+  int64_t q_token_stride, q_head_stride;   /* elements between tokens and heads of the q that is read, multiples of 8 */
+  int64_t kv_token_stride, kv_head_stride; /* the same for k and v */
+} gdn_rope;
+
+/*
+ * turns[i] (host, [n]) of radians[i] (host, [n]): the angle of a pair from one token to the next, such as
+ * base^(-2 i / rot_dim), as a fraction of a turn times 2^64, rounded.  radians: finite, |radians| < 2^32.
+ */
+gdn_status gdn_rope_turns(const double* radians, int32_t n, uint64_t* turns);
+
+/*
+ * Norms and rotation of verify windows: queries and keys of B windows of K tokens from the projection to
+ * where gdn_attn_verify and gdn_kv_commit read them.  Window token t of sequence b is at position
+ *   seq_len[prefix_of[b]] (with a prefix) + seq_len[slot0 + b] + the number of its ancestors in the window
+ * (a chain: t), or at positions[b][t].
+ *   turns      [rot_dim / 2] uint64, 8-byte aligned (NULL if rot_dim is 0)
+ *   q_weight, k_weight  [D] f32, 16-byte aligned, or NULL (no norm)
+ *   q, k, v    [B, K, heads, D] with the strides in rope; any of them may be NULL together with its output
+ *   seq_len    [n_slots] (NULL with positions); prefix_of, win_len [B], parent [B, K] or NULL as in
+ *              gdn_attn_verify; positions [B, K] int32 or NULL (then prefix_of and parent are not read)
+ *   q_out      [B, K, Hq, D], tokens q_token_stride apart; k_win, v_win [B, K, Hkv, D], tokens win_token_stride
+ *              apart (strides in dims).  v_win is v.  Each may be its input where that has the same token
+ *              stride and heads D apart (in place), and parts of rows of one buffer may be rewritten
+ *              beside one another.
+ * Padding tokens (t >= win_len[b]) become 0.  The cache's fields of dims are checked and, but for the number of
+ * slots and the longest slot, not used.
+ */
+gdn_status gdn_attn_rope(const gdn_kv_dims* dims, const gdn_rope* rope, const uint64_t* turns, const float* q_weight,
+                         const float* k_weight, const void* q, const void* k, const void* v, const int32_t* seq_len,
+                         const int32_t* prefix_of, const int32_t* win_len, const int32_t* parent,
+                         const int32_t* positions, void* q_out, void* k_win, void* v_win, gdn_stream_t stream);
+
+/*
+ * Reserve: slot slot0 + b grows by n_new[b] tokens (0..2^30), whose pages are taken and whose elements
+ * are left as they are: a layer's gdn_kv_append fills them.  Pages, order, in-place use and failures are those of
+ * gdn_kv_commit: a sequence that gets no pages (GDN_DEVERR_KV_FULL), whose last page is shared
+ * (GDN_DEVERR_KV_SHARED) or whose n_new is out of range (GDN_DEVERR_KV_LEN) is left unchanged.
+ * dims: K, Hq and the strides are checked as by gdn_kv_fork; the workspace is gdn_kv_workspace_size's.
+ */
+gdn_status gdn_kv_reserve(const gdn_kv_dims* dims, const int32_t* n_new, const int32_t* table_in, int32_t* table_out,
+                          const int32_t* len_in, int32_t* len_out, const int32_t* ref_in, int32_t* ref_out,
+                          void* workspace, uint64_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * Append: one layer's packed new tokens.  Tokens cu_seqlens[b] .. cu_seqlens[b+1] - 1 are the last ones of
+ * slot slot0 + b, whose seq_len counts them already (gdn_kv_reserve); token j of n is at its position
+ * seq_len - n + j, and at that plus the prefix's tokens for the rotation (or at positions[token]).
+ *   n_tokens   0 <= n_tokens < 2^31: rows of q, k, v
+ *   cu_seqlens [B + 1] int32: 0 = c_0 <= ... <= c_B <= n_tokens, else GDN_DEVERR_SEQLENS is set and what the
+ *              slots' last tokens hold is undefined.  Rows behind c_B are neither read nor written.
+ *   q, q_out   [n_tokens, Hq, D] (strides in rope; q_token_stride in dims), or both NULL
+ *   k, v       [n_tokens, Hkv, D] (strides in rope)
+ *   k_cache, v_cache  written, as described above; q_out may be q as in gdn_attn_rope
+ * A sequence with more tokens than its slot holds is not written (GDN_DEVERR_KV_LEN), nor are keys and values of
+ * a token on a page outside the pool (GDN_DEVERR_KV_PAGE).  dims: K and win_token_stride are not read.
+ */
+gdn_status gdn_kv_append(const gdn_kv_dims* dims, int32_t layer, const gdn_rope* rope, const uint64_t* turns,
+                         const float* q_weight, const float* k_weight, int64_t n_tokens, const int32_t* cu_seqlens,
+                         const void* q, const void* k, const void* v, const int32_t* positions, void* k_cache,
+                         void* v_cache, const int32_t* page_table, const int32_t* seq_len, const int32_t* prefix_of,
+                         void* q_out, gdn_stream_t stream);
+
+/*
+ * Attention of packed queries over the cache, one layer.  Row (token j of the n of sequence b, h) attends to
+ *   - all seq_len[p] tokens of slot p = prefix_of[b], if prefix_of is not NULL and p >= 0;
+ *   - causal != 0: the first seq_len[slot0 + b] - n + j + 1 tokens of its own slot (the row's own token is the
+ *     last of them; fewer than one: none);
+ *   - causal == 0: all seq_len[slot0 + b] tokens of its own slot (cross attention: the slot holds an encoder's
+ *     states, and the queries of sequences that share a slot may be packed as one sequence's);
+ * out and lse as in gdn_attn_verify; a row without keys gets out 0 and lse -inf.
+ *   n_tokens, cu_seqlens  as in gdn_kv_append; where cu_seqlens is wrong nothing is written.  Rows of out and lse
+ *              behind c_B are left as they are.
+ *   q          [n_tokens, Hq, D], tokens q_token_stride apart
+ *   out        [n_tokens, Hq, D] contiguous, dtype; lse [n_tokens, Hq] f32 or NULL
+ *   workspace  at least gdn_attn_prefill_workspace_size() bytes, no initialisation needed, dead after the call
+ * Rounding as in gdn_attn_verify.  What the cache holds beyond a slot's tokens reaches no output; a value
+ * that is not finite at a token of a slot may reach every row of the sequences that read the slot.
+ * Results do not depend on the order in which CTAs run.  dims: K and win_token_stride are not read.
+ */
+gdn_status gdn_attn_prefill(const gdn_kv_dims* dims, int32_t layer, int64_t n_tokens, const int32_t* cu_seqlens,
+                            const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                            const int32_t* seq_len, const int32_t* prefix_of, int32_t causal, float scale, void* out,
+                            float* lse, void* workspace, uint64_t workspace_bytes, gdn_stream_t stream);
+
+/* Bytes of workspace gdn_attn_prefill needs for `dims` and n_tokens rows (any lengths). */
+gdn_status gdn_attn_prefill_workspace_size(const gdn_kv_dims* dims, int64_t n_tokens, uint64_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -1,7 +1,8 @@
 // Upkeep of the paged key/value cache: commit of accepted window tokens, fork / drop / reorder of
-// sequences, compaction of the pool (contracts in include/gdn_kv.h).
+// sequences, compaction of the pool (contracts in include/gdn_kv.h); and pages for new tokens (reserve,
+// one launch of one cluster, described there).
 //
-// Each call is two launches.  The first plans: its CTA 0 (512 threads) walks lengths and
+// Each of these calls is two launches.  The first plans: its CTA 0 (512 threads) walks lengths and
 // reference counts and writes, into the workspace, which pages go where; its other CTAs copy the
 // tables that are not updated in place.  It changes no input, so a call may work in place.  The
 // second moves the data (all layers, keys and values) and then edits tables, lengths and
@@ -307,6 +308,149 @@ __global__ void __launch_bounds__(kMoveThreads) kv_commit_move_kernel(const __gr
   }
 }
 
+// ---------------------------------------------------------------- reserve
+// One cluster.  Every CTA plans all sequences (their needs and the running sum of them), and counts the
+// free pages of its own part of the pool; after the cluster's one barrier it knows the rank of its first
+// free page among all, and writes each free page of a rank below the sum to the table entry that wants
+// it: the sequence whose first rank is the last one not above it.  So no list of free pages is kept.
+// Tables that are not updated in place are copied before the barrier; what the plan reads of the counts
+// (pages that are held) is never what is written behind it (pages that were free).
+constexpr int kReserveCtas = 8;
+struct ReserveRec {
+  long long first;  // rank of the sequence's first new page
+  int32_t need;     // new pages
+  int32_t have;     // pages before
+  int32_t len;      // tokens after
+  int32_t pad;
+};
+
+__device__ __forceinline__ long long block_scan64(long long v, long long* sums, long long& total) {  // exclusive, kPlanThreads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  long long s = lane < kPlanThreads / 32 ? sums[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  total = __shfl_sync(0xffffffffu, s, 31);
+  const long long before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+  return x - v + (warp > 0 ? before : 0);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const __grid_constant__ PagesParams p, const __grid_constant__ PagesWs w) {
+  __shared__ long long sums[32];
+  __shared__ ReserveRec here[kPlanThreads];
+  const int tid = int(threadIdx.x), rank = int(blockIdx.x), ranks = int(gridDim.x);
+  grid_launch_dependents();
+  grid_wait();
+  const gdn_kv_dims& d = p.d;
+  // free pages of this CTA's part, its counts copied on the way
+  const int part = ((d.n_pages + ranks - 1) / ranks + 3) & ~3;
+  const int lo = rank * part < d.n_pages ? rank * part : d.n_pages, hi = lo + part < d.n_pages ? lo + part : d.n_pages;
+  long long free_here = 0;
+  for (int i = lo + tid; i < hi; i += kPlanThreads) {
+    const int held = p.ref_in[i];
+    free_here += held == 0;
+    if (p.ref_out != p.ref_in) p.ref_out[i] = held;
+  }
+  copy_ints(p.table_out, p.table_in, (long long)d.n_slots * d.max_pages, rank, ranks);
+  copy_ints(p.len_out, p.len_in, d.n_slots, rank, ranks);
+  // the plan
+  ReserveRec* const rec = d.B <= kPlanThreads ? here : static_cast<ReserveRec*>(static_cast<void*>(w.rec));
+  const bool writes = rec == here || rank == 0;
+  long long wanted = 0;
+  for (int b0 = 0; b0 < d.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    ReserveRec r{};
+    if (b < d.B) {
+      const int slot = d.slot0 + b;
+      int n = p.accept[b], len = p.len_in[slot];
+      uint32_t bad = 0;
+      if (len < 0 || (long long)len > (long long)d.max_pages * d.page_size) bad |= GDN_DEVERR_KV_LEN;
+      if (n < 0 || n > (1 << 30)) bad |= GDN_DEVERR_KV_LEN;
+      if (bad) n = 0;
+      r.have = pages_of(bad ? 0 : len, d.page_size);
+      if (n > 0 && len % d.page_size != 0) {  // the page that still has room is this slot's own
+        const int last = p.table_in[(long long)slot * d.max_pages + r.have - 1];
+        if (last < 0 || last >= d.n_pages)
+          bad |= GDN_DEVERR_KV_PAGE;
+        else if (p.ref_in[last] != 1)
+          bad |= GDN_DEVERR_KV_SHARED;
+      }
+      if (!bad && (long long)len + n > (long long)d.max_pages * d.page_size) bad |= GDN_DEVERR_KV_FULL;
+      if (bad) n = 0;
+      if (bad && rank == 0) atomicOr(p.err, bad);
+      r.len = n > 0 ? len + n : -1;  // (-1: as before)
+      r.need = n > 0 ? pages_of(len + n, d.page_size) - r.have : 0;
+    }
+    long long total;
+    r.first = wanted + block_scan64(r.need, sums, total);
+    if (b < d.B && writes) rec[b] = r;
+    wanted += total;
+  }
+  long long mine;
+  block_scan64(free_here, sums, mine);
+  if (tid == 0) w.head[rank] = int(mine);
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  long long at = 0, found = 0;  // free pages before this part, and in all
+  for (int i = 0; i < ranks; ++i) {
+    const int n = w.head[i];
+    at += i < rank ? n : 0;
+    found += n;
+  }
+  if (rank == 0) {
+    for (int b = tid; b < d.B; b += kPlanThreads) {
+      const ReserveRec r = rec[b];
+      if (r.len < 0) continue;
+      if (r.need > 0 && r.first + r.need > found)
+        atomicOr(p.err, GDN_DEVERR_KV_FULL);
+      else
+        p.len_out[d.slot0 + b] = r.len;
+    }
+  }
+  for (int i0 = lo; i0 < hi && at < wanted; i0 += 4 * kPlanThreads) {
+    int mask = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + 4 * tid + q;
+      if (i < hi && p.ref_in[i] == 0) mask |= 1 << q;
+    }
+    long long total;
+    long long r = at + block_scan64(__popc(mask), sums, total);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (!(mask >> q & 1)) continue;
+      if (r < wanted) {
+        int b = 0, end = d.B;  // the last sequence whose first rank is not above r (those without needs come before it)
+        while (end - b > 1) {
+          const int mid = (b + end) / 2;
+          if (rec[mid].first <= r)
+            b = mid;
+          else
+            end = mid;
+        }
+        const ReserveRec x = rec[b];
+        if (x.first + x.need <= found) {
+          p.table_out[(long long)(d.slot0 + b) * d.max_pages + x.have + int(r - x.first)] = i0 + 4 * tid + q;
+          p.ref_out[i0 + 4 * tid + q] = 1;
+        }
+      }
+      ++r;
+    }
+    at += total;
+  }
+}
+
 // ---------------------------------------------------------------- fork
 __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const __grid_constant__ PagesParams p, const __grid_constant__ PagesWs w) {
   __shared__ int sums[32];
@@ -580,6 +724,26 @@ cudaError_t launch_commit(const PagesParams& p, cudaStream_t stream) {
   const long long units = (long long)d.B * tiles * d.n_layers;
   if (units == 0) return cudaSuccess;
   return launch_pdl(kv_commit_move_kernel, int(units), kMoveThreads, stream, p, w, tiles, by_heads(d));
+}
+
+cudaError_t launch_reserve(const PagesParams& p, cudaStream_t stream) {
+  static_assert(sizeof(ReserveRec) <= sizeof(CommitRec), "the workspace has room for a commit's records");
+  const gdn_kv_dims& d = p.d;
+  const PagesWs w = carve_pages(p.ws, d, nullptr);
+  const int ctas = d.n_pages + (long long)d.n_slots * d.max_pages <= 8192 ? 1 : kReserveCtas;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(ctas), 1, 1);
+  cfg.blockDim = dim3(kPlanThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(ctas);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kv_reserve_kernel, p, w);
 }
 
 cudaError_t launch_fork(const PagesParams& p, cudaStream_t stream) {
