@@ -1,86 +1,780 @@
-// Attention of packed queries over the paged cache (gdn_attn_prefill; contract in include/gdn_kv.h).
+// Attention of packed queries over the paged cache (gdn_attn_prefill; contract in include/gdn_kv.h), on the
+// tensor cores.
 //
-// Mathematics: softmax over a row's keys in one pass with a running maximum m and sum l.  A warp per
-// (token, query head); a lane holds D / 32 elements of the head.
+// Mathematics: softmax over a row's keys in one pass with a running maximum and sum, and joined over disjoint
+// sets of keys by their log-sum-exps, as in kv_attn.cu, whose tiles (kv_tile.cuh) this uses.
+//
+// The work is cut into items (kv head, block): a block is up to 2 x 128 rows of consecutive tokens of one
+// sequence - a row is one query head of one token, the head's whole group of tokens go together - and its
+// keys are the prefix's, then those of its own slot that its last row sees, in tiles of 128.  All tiles of all
+// items, head by head, are dealt to the CTAs (one per SM) in equal contiguous stretches, so every CTA has the
+// same number of tiles whatever the lengths are.  An item that lies within a stretch is finished by its CTA; of
+// one that is cut, each CTA writes the softmax-weighted sum and log-sum-exp of its own keys (f32, in the
+// workspace: at most two such pieces a CTA), and a last kernel joins them.  Which CTA computes what depends on
+// the lengths alone, and no sum is formed by atomics, so results repeat bit for bit.
+//
+// Kernels: plan (one CTA: lengths -> blocks and their tiles), tiles (persistent, tcgen05), join.
+//
+// A block of more than 128 rows gives each stream half of them, on the same keys; a smaller one gives the
+// streams alternate tiles of the same rows, and at its end the two sums are joined in tensor memory, each
+// softmax group taking half of the columns.
+#include <atomic>
+
 #include "kv_device.cuh"
+#include "kv_index.h"
+#include "kv_tile.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kRowWarps = 8;
+constexpr int kPlanThreads = 512;
+constexpr int kJoinWarps = 4;
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kRowWarps) prefill_rows_kernel(const __grid_constant__ PackedAttnParams p) {
-  constexpr int N = D / 32;
+// ---------------------------------------------------------------- the plan
+struct BlockRec {
+  long long off;       // its first tile among those of one kv head
+  int32_t tok0, toks;  // its packed tokens
+  int32_t slot, keys;  // own slot, and the keys in it that the last row sees
+  int32_t lim;         // the keys in it that the first row sees (causal: a token more each token; may be below 1)
+  int32_t pre_slot, pre_keys;
+  int32_t tiles;
+};
+struct PlanHead {
+  long long head_tiles, tiles;  // of one kv head, and of all
+  int32_t blocks;
+  int32_t ctas;                 // that the tiles are dealt to: each has one at least
+  // The deal gives CTA c tiles [begin(c), begin(c + 1)); the CTA of tile x.
+  __device__ __forceinline__ long long begin(long long c) const { return c * tiles / ctas; }
+  __device__ __forceinline__ int cta_of(long long x) const {
+    int c = int(float(x) * (float(ctas) / float(tiles)));  // (within one of it)
+    c = c < 0 ? 0 : c > ctas - 1 ? ctas - 1 : c;
+    while (c > 0 && begin(c) > x) --c;
+    while (c < ctas - 1 && begin(c + 1) <= x) ++c;
+    return c;
+  }
+};
+struct JoinRec {       // an item that begins in CTA c0 and ends in CTA c1, c1 > c0
+  int32_t tok0, rows;  // rows 0: there is none
+  int32_t h, c0, c1, part0;
+};
+
+struct PackedWs {
+  PlanHead* head;
+  JoinRec* join;     // [kCtas]
+  int32_t* first;    // [B] each sequence's first block
+  BlockRec* block;   // [N / block tokens + B]
+  float* lse;        // [kCtas][2][kBlockRows] log2 units
+  float* o;          // [kCtas][2][kBlockRows][D]
+};
+
+__host__ __device__ inline size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+
+__host__ __device__ inline int block_toks(const gdn_kv_dims& d) { return 2 * (kTileRows / (d.Hq / d.Hkv)); }
+
+__host__ __device__ inline PackedWs carve_packed(void* base, const gdn_kv_dims& d, long long n_tokens, size_t* total) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  size_t o = 0;
+  const size_t parts = 2 * size_t(kBlockRows) * kCtas, blocks = size_t(n_tokens / block_toks(d)) + size_t(d.B);
+  PackedWs w;
+  w.head = reinterpret_cast<PlanHead*>(p + o), o += 256;
+  w.join = reinterpret_cast<JoinRec*>(p + o), o += round256(sizeof(JoinRec) * kCtas);
+  w.first = reinterpret_cast<int32_t*>(p + o), o += round256(4 * size_t(d.B));
+  w.block = reinterpret_cast<BlockRec*>(p + o), o += round256(sizeof(BlockRec) * blocks);
+  w.lse = reinterpret_cast<float*>(p + o), o += round256(4 * parts);
+  w.o = reinterpret_cast<float*>(p + o), o += 4 * parts * size_t(d.D);
+  if (total) *total = o;
+  return w;
+}
+
+template <typename T>
+__device__ __forceinline__ T scan_block(T v, T* sums, T& total) {  // exclusive, kPlanThreads threads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  T s = lane < kPlanThreads / 32 ? sums[lane] : T(0);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  total = __shfl_sync(0xffffffffu, s, 31);
+  const T before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+  return x - v + (warp > 0 ? before : 0);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w) {
+  __shared__ long long sums[32];
+  __shared__ int first_here[kPlanThreads];
   pdl_launch_dependents();
   pdl_wait();
   const gdn_kv_dims& d = p.d;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  if (row >= (long long)p.n_tokens * d.Hq) return;
-  bool bad = p.cu[0] != 0 || p.cu[d.B] > p.n_tokens;
-  for (int i = lane; i < d.B; i += 32) bad |= p.cu[i] > p.cu[i + 1];
-  if (__any_sync(0xffffffffu, bad)) {
-    atomicOr(p.err, kDevErrSeqlens);
+  const int tid = int(threadIdx.x), per = block_toks(d);
+  bool bad = tid == 0 && (p.cu[0] != 0 || p.cu[d.B] > p.n_tokens);
+  for (int i = tid; i < d.B; i += kPlanThreads) bad |= p.cu[i] > p.cu[i + 1];
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) {
+      atomicOr(p.err, kDevErrSeqlens);
+      *w.head = PlanHead{0, 0, 0, 0};
+    }
     return;
   }
-  const int token = int(row / d.Hq), h = int(row - (long long)token * d.Hq), kvh = h / (d.Hq / d.Hkv);
-  const int b = find_sequence(p.cu, d.B, token, lane);
-  const int lo = p.cu[b], hi = p.cu[b + 1];
-  if (token >= hi) return;
-  const int own = checked_slot_len(p.seq_len[d.slot0 + b], d, p.err);
-  const int prefix = checked_prefix(p.prefix_of, b, d, p.err);
-  float q[N], o[N], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int j = 0; j < N; j += 2) {
-    const float2 x = unpack16<F16>(*reinterpret_cast<const uint32_t*>(p.q + token * d.q_token_stride + h * D + lane * N + j));
-    q[j] = x.x * p.scale, q[j + 1] = x.y * p.scale, o[j] = o[j + 1] = 0.f;
+  int* const first = d.B <= kPlanThreads ? first_here : w.first;
+  long long blocks = 0;
+  for (int b0 = 0; b0 < d.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    const int n = b < d.B ? p.cu[b + 1] - p.cu[b] : 0;
+    long long total;
+    const long long at = blocks + scan_block<long long>((n + per - 1) / per, sums, total);
+    if (b < d.B) first[b] = int(at);
+    blocks += total;
   }
-  for (int part = 0; part < 2; ++part) {
-    const int slot = part ? d.slot0 + b : prefix;
-    if (slot < 0) continue;
-    long long n = part ? own : checked_slot_len(p.seq_len[slot], d, p.err);
-    if (part && p.causal) n = (long long)own - (hi - lo) + (token - lo) + 1;
-    for (int i = 0; i < n; ++i) {
-      const int col = i / d.page_size, page = p.table[(long long)slot * d.max_pages + col];
-      if (page < 0 || page >= d.n_pages) {
-        atomicOr(p.err, GDN_DEVERR_KV_PAGE);
-        continue;
+  __syncthreads();
+  long long tiles = 0;
+  for (int i0 = 0; i0 < blocks; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    BlockRec r{};
+    if (i < blocks) {
+      int b = 0, end = d.B;  // the last sequence whose first block is not behind i (those without tokens come before it)
+      while (end - b > 1) {
+        const int mid = (b + end) / 2;
+        if (first[mid] <= i)
+          b = mid;
+        else
+          end = mid;
       }
-      const long long at = page * d.cache_page_stride + (i - col * d.page_size) * d.cache_token_stride + kvh * d.cache_head_stride + lane * N;
-      float s = 0.f, v[N];
-#pragma unroll
-      for (int j = 0; j < N; j += 2) {
-        const float2 k = unpack16<F16>(*reinterpret_cast<const uint32_t*>(p.k_cache + at + j));
-        const float2 x = unpack16<F16>(*reinterpret_cast<const uint32_t*>(p.v_cache + at + j));
-        s += q[j] * k.x + q[j + 1] * k.y;
-        v[j] = x.x, v[j + 1] = x.y;
-      }
-      s = warp_sum(s);
-      const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.f : expf(m - mn), w = mn == -INFINITY ? 0.f : expf(s - mn);
-      m = mn;
-      l = l * f + w;
-#pragma unroll
-      for (int j = 0; j < N; ++j) o[j] = o[j] * f + w * v[j];
+      const int lo = p.cu[b], n = p.cu[b + 1] - lo, j0 = (i - first[b]) * per;
+      const int len = checked_slot_len(p.seq_len[d.slot0 + b], d, p.err);
+      r.tok0 = lo + j0;
+      r.toks = n - j0 < per ? n - j0 : per;
+      r.slot = d.slot0 + b;
+      r.pre_slot = checked_prefix(p.prefix_of, b, d, p.err);
+      r.pre_keys = r.pre_slot < 0 ? 0 : checked_slot_len(p.seq_len[r.pre_slot], d, p.err);
+      r.lim = p.causal ? len - n + j0 + 1 : len;
+      r.keys = p.causal ? r.lim + r.toks - 1 : len;
+      if (r.keys < 0) r.keys = 0;
+      r.tiles = (r.pre_keys + kTileKeys - 1) / kTileKeys + (r.keys + kTileKeys - 1) / kTileKeys;
+    }
+    long long total;
+    r.off = tiles + scan_block<long long>(r.tiles, sums, total);
+    if (i < blocks) w.block[i] = r;
+    tiles += total;
+    // rows of blocks without keys
+    uint32_t empty = __ballot_sync(0xffffffffu, i < blocks && r.tiles == 0);
+    while (empty) {
+      const int from = __ffs(int(empty)) - 1, lane = tid & 31;
+      empty &= empty - 1;
+      const int tok0 = __shfl_sync(0xffffffffu, r.tok0, from), toks = __shfl_sync(0xffffffffu, r.toks, from);
+      uint4* const out = reinterpret_cast<uint4*>(p.out + (long long)tok0 * d.Hq * d.D);
+      for (long long k = lane; k < (long long)toks * d.Hq * (d.D / 8); k += 32) out[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse)
+        for (long long k = lane; k < (long long)toks * d.Hq; k += 32) p.lse[(long long)tok0 * d.Hq + k] = -INFINITY;
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t* const out = reinterpret_cast<uint32_t*>(p.out + ((long long)token * d.Hq + h) * D + lane * N);
+  if (tid == 0) *w.head = PlanHead{tiles, tiles * d.Hkv, int(blocks), int(tiles * d.Hkv < kCtas ? tiles * d.Hkv : kCtas)};
+}
+
+// ---------------------------------------------------------------- segments
+struct Seg {
+  int tok0, rows;               // packed tokens, rows of the block
+  int h;                        // kv head
+  int pair;                     // they fill more than one row tile: both streams take every tile of keys
+  int slot, keys, lim;          // as in BlockRec
+  int pre_slot, pre_keys, pre_tiles;
+  int t0, t1;                   // tiles of the item
+  int parity;                   // of tile t0 in the order of all tiles
+  int part;                     // first row of its partial results (-1: the whole item, which goes to the outputs)
+  __device__ __forceinline__ bool paired() const { return pair != 0; }
+  struct Tiles {
+    int pre_tiles, pre_units, own_units;  // units of 16 keys
+    __device__ __forceinline__ int units(int t) const {
+      const int left = t < pre_tiles ? pre_units - 8 * t : own_units - 8 * (t - pre_tiles);
+      return left < 8 ? left : 8;
+    }
+  };
+  __device__ __forceinline__ Tiles tiles() const {  // (a converged warp)
+    return Tiles{int(uniform(uint32_t(pre_tiles))), int(uniform(uint32_t((pre_keys + 15) >> 4))), int(uniform(uint32_t((keys + 15) >> 4)))};
+  }
+};
+
+// Walks a CTA's stretch segment by segment (a converged warp).
+struct SegWalk {
+  const PackedAttnParams& p;
+  const PackedWs& w;
+  const int cta, tile_rows, G;
+  PlanHead head;
+  long long begin, x, end;
+  int h, k;
+  __device__ __forceinline__ SegWalk(const PackedAttnParams& p_, const PackedWs& w_, int cta_, int lane)
+      : p(p_), w(w_), cta(cta_), tile_rows(kTileRows / (p_.d.Hq / p_.d.Hkv) * (p_.d.Hq / p_.d.Hkv)), G(p_.d.Hq / p_.d.Hkv) {
+    head = *w.head;
+    begin = x = end = 0;
+    h = k = 0;
+    if (lane == 0) w.join[cta].rows = 0;
+    if (cta >= head.ctas) return;
+    begin = x = head.begin(cta), end = head.begin(cta + 1);
+    h = int(x / head.head_tiles);
+    const long long y = x - h * head.head_tiles;
+    int n = head.blocks;  // the last block that starts at or before y, 32 at a time
+    while (n > 1) {
+      const int step = (n + 31) / 32, i = lane * step;
+      const uint32_t at_or_before = __ballot_sync(0xffffffffu, i < n && w.block[k + i].off <= y);
+      const int j = 31 - __clz(int(at_or_before));
+      k += j * step;
+      n = n - j * step < step ? n - j * step : step;
+    }
+  }
+  __device__ __forceinline__ bool next(Seg& s, int lane) {
+    if (x >= end) return false;
+    while (true) {
+      const BlockRec r = w.block[k];
+      const long long from = h * head.head_tiles + r.off;
+      if (x >= from + r.tiles) {
+        if (++k == head.blocks) k = 0, ++h;
+        continue;
+      }
+      s.tok0 = r.tok0, s.rows = r.toks * G, s.h = h;
+      s.pair = s.rows > tile_rows;
+      s.slot = r.slot, s.keys = r.keys, s.lim = r.lim, s.pre_slot = r.pre_slot, s.pre_keys = r.pre_keys;
+      s.pre_tiles = (r.pre_keys + kTileKeys - 1) / kTileKeys;
+      s.t0 = int(x - from);
+      s.t1 = end - x < r.tiles - s.t0 ? s.t0 + int(end - x) : r.tiles;
+      s.parity = int(x & 1);
+      const int second = x == begin ? 0 : 1;  // (of the CTA's pieces: one that its stretch begins with, one that it ends with)
+      s.part = s.t0 == 0 && s.t1 == r.tiles ? -1 : (2 * cta + second) * kBlockRows;
+      if (s.t0 == 0 && s.t1 < r.tiles && lane == 0)
+        w.join[cta] = JoinRec{s.tok0, s.rows, h, cta, head.cta_of(from + r.tiles - 1), s.part};
+      x += s.t1 - s.t0;
+      return true;
+    }
+  }
+};
+
+// ---------------------------------------------------------------- the tile kernel
+struct PackedMaps {
+  // (D, token, kv head, page, 1), keys and values: boxes of 16 tokens, and of `box` tokens
+  CUtensorMap few[2], many[2];
+  // queries, (D, query head, token): boxes of G heads x the tokens of a row tile, and x a few tokens
+  CUtensorMap qt, qs;
+};
+constexpr int kFewToks = 4;
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    packed_tile_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w, const int box, const uint32_t page_inv,
+                       const __grid_constant__ PackedMaps maps) {
+  using L = TileLayout<D, Seg>;
+  constexpr int NS = L::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int page_of_box[32][2];
+  __shared__ volatile uint32_t gave_up, turns[2];  // (turns: taken so far by each tensor-core warp)
+  __shared__ uint64_t merge_bar;                   // the two softmax groups, at the end of a segment that they share
+  __shared__ float2 merge_ml[kTileRows];           // maximum (log2 units) and sum of a row, one stream's and then the other's
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
+  const TileBars bars = tile_bars<NS>(reinterpret_cast<uint64_t*>(smem + L::OFF_BAR));
+  Seg* const segs = reinterpret_cast<Seg*>(smem + L::OFF_SEG);
+  const int tid = int(threadIdx.x), warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const gdn_kv_dims& d = p.d;
+  const int G = d.Hq / d.Hkv, tile_toks = kTileRows / G, tile_rows = tile_toks * G;
+
+  if (tid == 0) {
+    init_tile_bars<NS>(bars);
+    mbar_init(&merge_bar, 2 * kGroupThreads);
+    turns[0] = turns[1] = 0;
+    gave_up = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) tmem_alloc(&tmem_slot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // Bounded wait of a whole warp, which goes on or gives up together; once one warp has given up, all of the
+  // CTA's do.
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
+    for (uint32_t i = 0; !__all_sync(0xffffffffu, mbar_sleep(bar, parity)); ++i) {
+      if (__any_sync(0xffffffffu, gave_up || i > kMaxLooks)) {
+        if (i > kMaxLooks) {
+          gave_up = 1;
+          atomicOr(p.err, kDevErrTimeout);
+        }
+        return false;
+      }
+    }
+    return true;
+  };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    // As in kv_attn.cu: copies go out as slots fall free, the page numbers of the tile behind are on their way to
+    // shared memory meanwhile, and lane i looks up box i.
+    uint32_t n = 0, issued = 0;  // tiles and ring uses so far; tile n's keys are use 2n, its values 2n + 1
+    uint32_t k = 0;              // segments so far
+    int t = 0, t1 = 0;           // of the present segment: next tile, end
+    bool ok = true, more = true;
+    uint32_t slot = 0, phase = 1;  // of the next use; the phase that its slot was emptied in
+    // the segment at hand
+    Seg::Tiles tiles{};
+    int seg_h = 0;
+    const int32_t *own_pages = nullptr, *pre_pages = nullptr;
+    // the tile behind the one at hand
+    int units = 0, boxes = 0, in = 0;
+    uint32_t ahead = 0;     // tiles looked up
+    bool whole = false;     // in boxes of `box` tokens
+    int* const page = page_of_box[lane];  // of this tile and the next in turn
+    auto next_tile = [&]() {
+      while (ok && t == t1) {
+        __syncwarp();
+        if (k > 0 && lane == 0) mbar_arrive(bars.seg_empty + (k - 1) % kSegRing);
+        ok = wait_warp(bars.seg_full + k % kSegRing, (k / kSegRing) & 1);
+        const Seg& seg = segs[k % kSegRing];
+        t = int(uniform(uint32_t(seg.t0))), t1 = int(uniform(uint32_t(seg.t1)));
+        ++k;
+        if (t1 < 0) more = false;
+        if (t1 < 0 || !ok) return;
+        tiles = seg.tiles();
+        seg_h = int(uniform(uint32_t(seg.h)));
+        own_pages = p.table + (long long)seg.slot * d.max_pages;
+        pre_pages = p.table + (long long)(seg.pre_slot < 0 ? 0 : seg.pre_slot) * d.max_pages;
+      }
+      if (!ok) return;
+      units = tiles.units(t);
+      whole = units == 8;
+      boxes = whole ? kTileKeys / box : units;
+      if (lane < boxes) {
+        const bool own = t >= tiles.pre_tiles;
+        const int token = (own ? t - tiles.pre_tiles : t) * kTileKeys + lane * (whole ? box : 16);
+        const int col = page_column(token, page_inv);
+        in = token - col * d.page_size;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(page + (ahead & 1))), "l"((own ? own_pages : pre_pages) + col) : "memory");
+      }
+      ++t, ++ahead;
+    };
+    next_tile();
+    while (ok && more) {
+      const int now_units = units, now_boxes = boxes, now_in = in, now_h = seg_h;
+      const bool now_whole = whole;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      int now_page = page[n & 1];
+      if (lane < now_boxes && (now_page < 0 || now_page >= d.n_pages)) {  // reads zeros there
+        atomicOr(p.err, GDN_DEVERR_KV_PAGE);
+        now_page = d.n_pages;
+      }
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {
+        if (!wait_warp(bars.empty + slot, phase)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(bars.full + slot, uint32_t(now_units) * 16 * D * 2);
+        __syncwarp();
+        const uint32_t dst = base + L::OFF_RING + slot * L::BYTES, bar = smem_addr(bars.full + slot), step = uint32_t(now_whole ? box : 16) * 128;
+        const CUtensorMap* const m = now_whole ? &maps.many[v] : &maps.few[v];
+#pragma unroll 1
+        for (int b = 0; b < now_boxes; ++b)
+          tma_box<D>(dst + b * step, m, int(uniform_from(uint32_t(now_in), b)), now_h, int(uniform_from(uint32_t(now_page), b)), 0, bar);
+        issued = 2 * n + v + 1;
+        if (++slot == NS) slot = 0, phase ^= 1;
+        if (v == 0) next_tile();
+        if (!ok) break;
+      }
+      ++n;
+    }
+    // the last uses of the ring: the copies have landed and the tensor core has read them
+    for (uint32_t use = issued > NS ? issued - NS : 0; use < issued; ++use) {
+      if (ok) ok = wait_warp(bars.empty + use % NS, (use / NS) & 1);
+      if (!ok) mbar_drain(bars.full + use % NS, (use / NS) & 1);
+    }
+  } else if (warp == 9 || warp == 10) {
+    tensor_warp<D, F16>(warp - 9, lane, tmem, base, p.scale < 0.f, segs, bars, turns, wait_warp);
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax: stream s, one row per thread
+    const int s = warp >> 2, r = tid & 127;
+    const uint32_t lane_sel = uint32_t(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + tmem_s(s) + lane_sel, to = tmem + tmem_o(s) + lane_sel;
+    const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);  // (0 is as good as 1e-30)
+    uint32_t n = 0, ns = 0;          // tiles of the CTA, tiles of this stream
+    uint32_t no = 0, no_other = 0;   // segments of this stream and of the other
+    uint32_t meets = 0;              // phases of the groups' barrier so far
+    auto meet = [&] {
+      mbar_arrive(&merge_bar);
+      return wait_warp(&merge_bar, meets++ & 1);
+    };
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+      const Seg& seg = segs[k % kSegRing];
+      if (!wait_warp(bars.seg_full + k % kSegRing, (k / kSegRing) & 1)) {
+        ok = false;
+        break;
+      }
+      auto done = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.seg_empty + k % kSegRing);
+      };
+      if (seg.t1 < 0) break;
+      const bool paired = seg.paired();
+      const uint32_t n0 = n;
+      n += uint32_t(seg.t1 - seg.t0);
+      int t = seg.t0;
+      if (!paired && ((seg.parity ^ s) & 1)) ++t;
+      const bool shared = !paired && seg.t1 - seg.t0 > 1;  // both streams have tiles of the same rows
+      if (t >= seg.t1) {
+        ++no_other;
+        done();
+        continue;
+      }
+      const int step = paired ? 1 : 2;
+      const int srow0 = paired ? s * tile_rows : 0;
+      const int rows = seg.rows - srow0 < tile_rows ? seg.rows - srow0 : tile_rows;
+      const bool idle = 32 * (warp & 3) >= rows;  // a warp without rows only keeps the barriers going
+      // own keys that this row sees, and that the stream's first row sees
+      const int tok = (srow0 + r) / G, tok_first = srow0 / G;
+      const int lim = seg.lim + (p.causal ? tok : 0), lim_first = seg.lim + (p.causal ? tok_first : 0);
+
+      float m = -INFINITY, l = 0.f;  // running maximum (unscaled) and sum
+      bool first = true;
+      for (; ok && t < seg.t1; t += step, ++ns) {
+        if (!wait_warp(bars.s_ready + s, ns & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const bool own = t >= seg.pre_tiles;
+        const int key0 = (own ? t - seg.pre_tiles : t) * kTileKeys;
+        const int left = (own ? seg.keys : seg.pre_keys) - key0;  // keys of this tile that some row sees (may exceed 128)
+        if (!idle) {
+          const int mine = (own ? lim : seg.pre_keys) - key0, fewest = (own ? lim_first : seg.pre_keys) - key0;
+          softmax_tile<D, F16>(ts, to, c, r < rows, first, fewest < kTileKeys, [&](int q, int g) {
+            const int n_seen = mine - 64 * q - 32 * g;
+            return n_seen >= 32 ? 0xffffffffu : n_seen <= 0 ? 0u : (1u << n_seen) - 1u;
+          }, m, l);
+        }
+        first = false;
+        if (left < kTileKeys && (left & 15)) {
+          // values behind the last token of its unit may be anything: zero them, for 0 x NaN is NaN
+          const uint32_t use = 2 * (n0 + uint32_t(t - seg.t0)) + 1, slot = use % NS;
+          if (!wait_warp(bars.full + slot, (use / NS) & 1)) {
+            ok = false;
+            break;
+          }
+          const int end = (left + 15) & ~15;
+          uint8_t* const v_tile = smem + L::OFF_RING + slot * L::BYTES;
+          constexpr int C = D / 8;
+          for (int i = r; i < (end - left) * C; i += kGroupThreads) {
+            const int row = left + i / C, ch = i % C;
+            *reinterpret_cast<uint4*>(v_tile + (ch >> 3) * L::HALF + row * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        mbar_arrive(bars.p_ready + s);
+      }
+      if (!ok) break;
+
+      // the segment's result
+      if (!wait_warp(bars.o_done + s, no & 1)) {
+        ok = false;
+        break;
+      }
+      ++no;
+      float w_own = 1.f, w_other = 0.f, M = m == -INFINITY ? -INFINITY : m * c, sum = l;  // (log2 units)
+      if (shared) {  // each group takes the sums of both streams, in half of the columns
+        float2 other;
+        if (s) merge_ml[r] = make_float2(M, l);
+        ok = meet();
+        if (!s && ok) other = merge_ml[r], merge_ml[r] = make_float2(M, l);
+        ok = ok && meet() && wait_warp(bars.o_done + (s ^ 1), no_other & 1);
+        if (!ok) break;
+        if (s) other = merge_ml[r];
+        ++no_other;
+        const float top = fmaxf(M, other.x);
+        w_own = M == -INFINITY ? 0.f : exp2f(M - top);
+        w_other = other.x == -INFINITY ? 0.f : exp2f(other.x - top);
+        M = top;
+        sum = l * w_own + other.y * w_other;
+      }
+      if (paired) ++no_other;
+      tc_fence_after();
+      if (!idle) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float f_own = w_own * inv, f_other = w_other * inv;
+        const uint32_t to_other = tmem + tmem_o(s ^ 1) + lane_sel;
+        const int token = seg.tok0 + tok;
+        const long long out_row = (long long)token * d.Hq + seg.h * G + (srow0 + r - tok * G);
+        const int q0 = shared ? s * (D / 2) : 0, q1 = shared ? q0 + D / 2 : D;
+#pragma unroll 1
+        for (int q = q0; q < q1; q += 32) {
+          float o[32];
+          tmem_ld32(to + q, o);
+          if (shared) {
+            float x[32];
+            tmem_ld32(to_other + q, x);
 #pragma unroll
-  for (int j = 0; j < N; j += 2) out[j / 2] = pack16<F16>(o[j] * inv, o[j + 1] * inv);
-  if (p.lse && lane == 0) p.lse[(long long)token * d.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
+            for (int j = 0; j < 32; ++j) o[j] = (w_own == 0.f ? 0.f : o[j] * f_own) + (w_other == 0.f ? 0.f : x[j] * f_other);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] *= inv;
+          }
+          if (r < rows) {
+            if (seg.part < 0) {
+              uint4* const out = reinterpret_cast<uint4*>(p.out + out_row * D + q);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                out[j] = make_uint4(pack2<F16>(o[8 * j], o[8 * j + 1]), pack2<F16>(o[8 * j + 2], o[8 * j + 3]),
+                                    pack2<F16>(o[8 * j + 4], o[8 * j + 5]), pack2<F16>(o[8 * j + 6], o[8 * j + 7]));
+            } else {
+              float* const out = w.o + (long long)(seg.part + srow0 + r) * D + q;
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) store8(out + j, o + j);
+            }
+          }
+        }
+        if (r < rows && q0 == 0) {
+          const float e = sum == 0.f ? -INFINITY : M + log2f(sum);
+          if (seg.part >= 0)
+            w.lse[seg.part + srow0 + r] = e;
+          else if (p.lse)
+            p.lse[out_row] = e * kLn2;
+        }
+      }
+      tc_fence_before();
+      // neither stream's next products overwrite sums that the other group still reads
+      if (shared && !meet()) {
+        ok = false;
+        break;
+      }
+      done();
+    }
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ segments and queries, ahead of the rest
+    // As in kv_attn.cu: segments go out as the ring has room, and a segment's queries as soon as the products with
+    // the ones before are done.  Queries come by TMA, whole tokens of G heads: rows behind the block's last hold
+    // other tokens' queries or what was there, and nothing reads their results.
+    SegWalk walk(p, w, int(blockIdx.x), lane);
+    uint32_t k = 0, kq = 0;      // segments handed on; segment whose queries are next
+    uint32_t nq0 = 0, nq1 = 0;   // segments of each stream
+    int part = 0;                // of segment kq: its first or second stream
+    uint32_t idle = 0;
+    bool more = true, ok = true;
+    while (ok && (more || kq < k)) {
+      bool did = false;
+      if (more && __all_sync(0xffffffffu, mbar_look(bars.seg_empty + k % kSegRing, ((k / kSegRing) & 1) ^ 1))) {
+        Seg seg;
+        more = walk.next(seg, lane);
+        if (lane == 0) {
+          if (!more) seg.t1 = -1;
+          segs[k % kSegRing] = seg;
+          mbar_arrive(bars.seg_full + k % kSegRing);
+        }
+        __syncwarp();
+        if (more) ++k;
+        did = true;
+      }
+      if (kq < k) {
+        const Seg& seg = segs[kq % kSegRing];
+        const bool paired = seg.paired();
+        const int s = paired ? part : (seg.parity + part) & 1;  // in the order of their first tiles
+        const uint32_t nq = s ? nq1 : nq0;
+        if (nq == 0 || __all_sync(0xffffffffu, mbar_look(bars.q_free + s, (nq - 1) & 1))) {
+          const bool few = seg.rows <= kFewToks * G && kFewToks < tile_toks;
+          if (lane == 0) mbar_arrive_expect_tx(bars.q_ready + s, uint32_t((few ? kFewToks : tile_toks) * G) * D * 2);
+          __syncwarp();
+          if (lane < D / 64)
+            tma_load3(base + L::OFF_Q + s * L::BYTES + lane * L::HALF, few ? &maps.qs : &maps.qt, lane * 64, seg.h * G,
+                      seg.tok0 + (paired ? s * tile_toks : 0), smem_addr(bars.q_ready + s));
+          if (s)
+            ++nq1;
+          else
+            ++nq0;
+          if (++part == 2 || (!paired && seg.t1 - seg.t0 == 1)) {
+            part = 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.seg_empty + kq % kSegRing);
+            ++kq;
+          }
+          did = true;
+        }
+      }
+      idle = did ? 0 : idle + 1;
+      if (__any_sync(0xffffffffu, gave_up || idle > kMaxIdle)) {
+        if (idle > kMaxIdle) {
+          gave_up = 1;
+          atomicOr(p.err, kDevErrTimeout);
+        }
+        ok = false;
+      }
+    }
+    // (the tensor core waits for every tile of queries; after a wait that gave up, they land first)
+    if (!ok) {
+      if (nq0 > 0) mbar_drain(bars.q_ready, (nq0 - 1) & 1);
+      if (nq1 > 0) mbar_drain(bars.q_ready + 1, (nq1 - 1) & 1);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- join
+// kCtas x chunks CTAs: a few rows of the cut item that begins in a CTA's stretch, if one does.  A warp takes a row
+// at a time: its pieces' log-sum-exps, then their sums, four in flight.
+template <int D, bool F16>
+__global__ void __launch_bounds__(32 * kJoinWarps) packed_join_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w, const int chunk_rows) {
+  constexpr int N = D / 32, U = 4;
+  pdl_launch_dependents();
+  pdl_wait();
+  const gdn_kv_dims& d = p.d;
+  const JoinRec rec = w.join[blockIdx.x % kCtas];
+  const int r0 = int(blockIdx.x / kCtas) * chunk_rows;
+  const int G = d.Hq / d.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r1 = r0 + chunk_rows < rec.rows ? r0 + chunk_rows : rec.rows, parts = rec.rows > 0 ? rec.c1 - rec.c0 + 1 : 0;
+  for (int r = r0 + warp; r < r1; r += kJoinWarps) {
+    // piece j's row: the first CTA's piece, then the one that each stretch begins with
+    auto at = [&](int j) { return (j == 0 ? rec.part0 : 2 * (rec.c0 + j) * kBlockRows) + r; };
+    float acc[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) acc[k] = 0.f;
+    float M = -INFINITY, W = 0.f;
+    for (int j0 = 0; j0 < parts; j0 += 32) {
+      const int n = parts - j0 < 32 ? parts - j0 : 32;
+      const float e = lane < n ? w.lse[at(j0 + lane)] : -INFINITY;
+      float mx = e;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float Mn = fmaxf(M, mx), f = M == -INFINITY ? 0.f : exp2f(M - Mn);
+      const float wt = e == -INFINITY ? 0.f : exp2f(e - (Mn == -INFINITY ? 0.f : Mn));  // (NaN stays NaN)
+      M = Mn;
+      W = W * f + warp_sum(wt);
+#pragma unroll
+      for (int k = 0; k < N; ++k) acc[k] *= f;
+      for (int i0 = 0; i0 < n; i0 += U) {
+        float v[U][N];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i0 + u < n) {
+            const float* o = w.o + (long long)at(j0 + i0 + u) * D + lane * N;
+            if (N == 4)
+              *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(o);
+            else
+              *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(o);
+          }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float wj = __shfl_sync(0xffffffffu, wt, (i0 + u) & 31);
+          if (i0 + u < n && wj != 0.f)
+#pragma unroll
+            for (int k = 0; k < N; ++k) acc[k] += wj * v[u][k];
+        }
+      }
+    }
+    const float inv = W == 0.f ? 0.f : 1.f / W;
+#pragma unroll
+    for (int k = 0; k < N; ++k) acc[k] *= inv;
+    const int tok = r / G;
+    const long long row = (long long)(rec.tok0 + tok) * d.Hq + rec.h * G + (r - tok * G);
+    uint32_t* const o = reinterpret_cast<uint32_t*>(p.out + row * D) + lane * (N / 2);
+    if (N == 4)
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack2<F16>(acc[0], acc[1]), pack2<F16>(acc[N - 2], acc[N - 1]));
+    else
+      *o = pack2<F16>(acc[0], acc[1]);
+    if (p.lse && lane == 0) p.lse[row] = W == 0.f ? -INFINITY : (M + log2f(W)) * kLn2;
+  }
+}
+
+// ---------------------------------------------------------------- launches
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder (the library does not link against libcuda).
+EncodeTiled encoder() {
+  static const EncodeTiled f = [] {
+    void* sym = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      sym = nullptr;
+    return reinterpret_cast<EncodeTiled>(sym);
+  }();
+  return f;
+}
+
+template <int D, bool F16>
+cudaError_t launch(const PackedAttnParams& p, const PackedWs& w, int box, const PackedMaps& maps, cudaStream_t stream) {
+  using L = TileLayout<D, Seg>;
+  static_assert(L::TOTAL + 1536 <= 232448, "shared memory");
+  cudaError_t e = launch_dependent(packed_plan_kernel, 1u, kPlanThreads, 0, stream, p, w);
+  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> allowed{0};  // a bit per device: the kernel may use its shared memory there
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(allowed.load() >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(packed_tile_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(1ull << (dev & 63));
+  }
+  e = launch_dependent(packed_tile_kernel<D, F16>, unsigned(kCtas), kTileThreads, L::TOTAL, stream, p, w, box, page_units_inv(p.d.page_size), maps);
+  if (e != cudaSuccess) return e;
+  constexpr int chunk_rows = 8;
+  return launch_dependent(packed_join_kernel<D, F16>, unsigned(kCtas * (kBlockRows / chunk_rows)), 32 * kJoinWarps, 0, stream, p, w, chunk_rows);
 }
 
 }  // namespace
 
-size_t packed_attn_workspace_bytes(const gdn_kv_dims&, int64_t) { return 256; }
+size_t packed_attn_workspace_bytes(const gdn_kv_dims& d, int64_t n_tokens) {
+  size_t n = 0;
+  carve_packed(nullptr, d, n_tokens, &n);
+  return n;
+}
 
 cudaError_t launch_packed_attn(const PackedAttnParams& p, cudaStream_t stream) {
-  const unsigned grid = unsigned(((long long)p.n_tokens * p.d.Hq + kRowWarps - 1) / kRowWarps);
-  auto kernel = p.d.D == 128 ? (p.d.dtype ? prefill_rows_kernel<128, true> : prefill_rows_kernel<128, false>)
-                             : (p.d.dtype ? prefill_rows_kernel<64, true> : prefill_rows_kernel<64, false>);
-  return launch_dependent(kernel, grid, 32 * kRowWarps, 0, stream, p);
+  const gdn_kv_dims& d = p.d;
+  const int G = d.Hq / d.Hkv, toks = kTileRows / G;
+  const EncodeTiled encode = encoder();
+  if (!encode) return cudaErrorNotSupported;
+  // Tokens per copy of a full tile: as many as lie together in a page, a divisor of the tile's 128.
+  int box = 16;
+  while (box < kTileKeys && d.page_size % (2 * box) == 0) box *= 2;
+  const auto type = d.dtype ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  bool ok = true;
+  auto map = [&](CUtensorMap* m, const void* at, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* boxes) {
+    ok = ok && encode(m, type, cuuint32_t(rank), const_cast<void*>(at), dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  PackedMaps maps;
+  const cuuint64_t cd[5] = {cuuint64_t(d.D), cuuint64_t(d.page_size), cuuint64_t(d.Hkv), cuuint64_t(d.n_pages), 1};
+  const cuuint64_t cs[4] = {2ull * d.cache_token_stride, 2ull * d.cache_head_stride, 2ull * d.cache_page_stride, 2ull * d.cache_layer_stride};
+  const cuuint32_t b16[5] = {64, 16, 1, 1, 1}, bb[5] = {64, cuuint32_t(box), 1, 1, 1};
+  map(&maps.few[0], p.k_cache, 5, cd, cs, b16);
+  map(&maps.few[1], p.v_cache, 5, cd, cs, b16);
+  map(&maps.many[0], p.k_cache, 5, cd, cs, bb);
+  map(&maps.many[1], p.v_cache, 5, cd, cs, bb);
+  const cuuint64_t qd[3] = {cuuint64_t(d.D), cuuint64_t(d.Hq), cuuint64_t(p.n_tokens)};
+  const cuuint64_t qst[2] = {2ull * d.D, 2ull * d.q_token_stride};
+  const cuuint32_t bt[3] = {64, cuuint32_t(G), cuuint32_t(toks)}, bs[3] = {64, cuuint32_t(G), cuuint32_t(toks < kFewToks ? toks : kFewToks)};
+  map(&maps.qt, p.q, 3, qd, qst, bt);
+  map(&maps.qs, p.q, 3, qd, qst, bs);
+  if (!ok) return cudaErrorInvalidValue;
+  const PackedWs w = carve_packed(p.ws, d, p.n_tokens, nullptr);
+  if (d.D == 128) return d.dtype ? launch<128, true>(p, w, box, maps, stream) : launch<128, false>(p, w, box, maps, stream);
+  return d.dtype ? launch<64, true>(p, w, box, maps, stream) : launch<64, false>(p, w, box, maps, stream);
 }
 
 }  // namespace gdn
