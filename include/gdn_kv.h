@@ -181,7 +181,7 @@ gdn_status gdn_kv_workspace_size(const gdn_kv_dims* dims, uint64_t* bytes);
  * scaled for long contexts are a matter of that table.
  */
 typedef struct {
-  int32_t rot_dim;       /* a multiple of 8, 0..D */
+  int32_t rot_dim;       /* a multiple of 16, 0..D */
   int32_t interleaved;   /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1); i = 0 .. rot_dim / 2 - 1 */
   float magnitude;       /* of the rotated elements (1 unless long contexts rescale it); finite */
   float eps;             /* of the norms; finite, >= 0 */

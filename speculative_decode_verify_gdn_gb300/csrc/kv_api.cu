@@ -173,7 +173,7 @@ gdn_status check_rows(const Rows* t, int n, int D) {
 gdn_status check_rope(const gdn_rope* r, const gdn_kv_dims& d, const uint64_t* turns, const float* q_weight, const float* k_weight) {
   if (!r) return fail(GDN_ERR_INVALID_ARG, "rope is NULL");
   if (r->rot_dim < 0 || r->rot_dim > d.D) return fail(GDN_ERR_INVALID_ARG, "rot_dim=%d outside 0..%d", r->rot_dim, d.D);
-  if (r->rot_dim % 8) return fail(GDN_ERR_UNSUPPORTED, "rot_dim=%d (a multiple of 8)", r->rot_dim);
+  if (r->rot_dim % 16) return fail(GDN_ERR_UNSUPPORTED, "rot_dim=%d (a multiple of 16)", r->rot_dim);
   if (r->interleaved != 0 && r->interleaved != 1) return fail(GDN_ERR_INVALID_ARG, "interleaved=%d (0 or 1)", r->interleaved);
   if (r->reserved != 0) return fail(GDN_ERR_INVALID_ARG, "reserved=%d (0)", r->reserved);
   if (!std::isfinite(r->magnitude)) return fail(GDN_ERR_INVALID_ARG, "magnitude not finite");

@@ -136,9 +136,6 @@ __host__ __device__ inline AttnWs carve_attn(void* base, const gdn_kv_dims& d, s
 // one deal over all tiles puts them on as many CTAs as there are.  (B=64 behind 32768 tokens: 543 us in
 // two deals, 849 in one.)
 constexpr long long kSplitTiles = 4 * kCtas;
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 template <typename T>
 __device__ __forceinline__ T block_scan(T v, T* sums, T& total) {  // exclusive, kPlanThreads threads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -184,8 +181,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
   // otherwise be a trip to L2
   __shared__ RunRec runs[kPlanRuns];
   __shared__ long long seq_off[kPlanThreads];
-  grid_launch_dependents();
-  grid_wait();
+  pdl_launch_dependents();
+  pdl_wait();
   const gdn_kv_dims& d = p.d;
   const int tid = int(threadIdx.x), KG = d.K * (d.Hq / d.Hkv);
   long long n_runs = 0;
@@ -566,8 +563,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  grid_launch_dependents();
-  grid_wait();
+  pdl_launch_dependents();
+  pdl_wait();
 
   // Bounded wait of a whole warp, which goes on or gives up together; once one warp has given up,
   // all of the CTA's do.  (Every branch is on a vote: the tensor-core warp's operands stay in
@@ -901,8 +898,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps, U == 4 ? 8 : 4)
   __shared__ int counts[4];
   __shared__ int row_at[kJoinWarps][32];
   __shared__ float row_w[kJoinWarps][32];
-  grid_launch_dependents();
-  grid_wait();
+  pdl_launch_dependents();
+  pdl_wait();
   const gdn_kv_dims& d = p.d;
   const int G = d.Hq / d.Hkv, KG = d.K * G, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunks = (KG + join_rows - 1) / join_rows;
@@ -1022,43 +1019,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps, U == 4 ? 8 : 4)
 }
 
 // ---------------------------------------------------------------- launches
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder (the library does not link against libcuda).
-EncodeTiled encoder() {
-  static const EncodeTiled f = [] {
-    void* sym = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      sym = nullptr;
-    return reinterpret_cast<EncodeTiled>(sym);
-  }();
-  return f;
-}
-
-template <typename... Args>
-cudaError_t launch_pdl(void (*kernel)(Args...), unsigned grid, int threads, int smem, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(unsigned(threads), 1, 1);
-  cfg.dynamicSmemBytes = size_t(smem);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int D, bool F16>
 cudaError_t launch(const AttnParams& p, const AttnWs& w, int box, const TileMaps& maps, cudaStream_t stream) {
   using L = TileLayout<D, Seg>;
   static_assert(L::TOTAL <= 232448 - 512, "shared memory");
-  cudaError_t e = p.d.B <= kWarpPlan ? cudaSuccess : launch_pdl(attn_plan_kernel, 1u, kPlanThreads, 0, stream, p, w);
+  cudaError_t e = p.d.B <= kWarpPlan ? cudaSuccess : launch_dependent(attn_plan_kernel, 1u, kPlanThreads, 0, stream, p, w);
   if (e != cudaSuccess) return e;
   static std::atomic<uint64_t> allowed{0};  // a bit per device: the kernel may use its shared memory there
   int dev = 0;
@@ -1069,14 +1034,14 @@ cudaError_t launch(const AttnParams& p, const AttnWs& w, int box, const TileMaps
     if (e != cudaSuccess) return e;
     allowed.fetch_or(1ull << (dev & 63));
   }
-  e = launch_pdl(attn_tile_kernel<D, F16>, unsigned(kCtas), kTileThreads, L::TOTAL, stream, p, w, box, maps);
+  e = launch_dependent(attn_tile_kernel<D, F16>, unsigned(kCtas), kTileThreads, L::TOTAL, stream, p, w, box, maps);
   if (e != cudaSuccess) return e;
   const int KG = p.d.K * (p.d.Hq / p.d.Hkv);
   const long long heads = (long long)p.d.B * p.d.Hkv;
   int join_rows = kJoinRowsMax;
   while (join_rows > kJoinWarps && heads * ((KG + join_rows - 1) / join_rows) < 8 * kCtas) join_rows /= 2;
   const long long joins = heads * ((KG + join_rows - 1) / join_rows);
-  return launch_pdl(joins <= 4 * kCtas ? attn_join_kernel<D, F16, 16> : attn_join_kernel<D, F16, 4>, unsigned(joins),
+  return launch_dependent(joins <= 4 * kCtas ? attn_join_kernel<D, F16, 16> : attn_join_kernel<D, F16, 4>, unsigned(joins),
                     32 * kJoinWarps, 0, stream, p, w, join_rows);
 }
 

@@ -697,23 +697,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) packed_join_kernel(const __gr
 }
 
 // ---------------------------------------------------------------- launches
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder (the library does not link against libcuda).
-EncodeTiled encoder() {
-  static const EncodeTiled f = [] {
-    void* sym = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      sym = nullptr;
-    return reinterpret_cast<EncodeTiled>(sym);
-  }();
-  return f;
-}
-
 template <int D, bool F16>
 cudaError_t launch(const PackedAttnParams& p, const PackedWs& w, int box, const PackedMaps& maps, cudaStream_t stream) {
   using L = TileLayout<D, Seg>;

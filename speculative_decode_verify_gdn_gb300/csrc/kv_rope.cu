@@ -20,7 +20,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128, kRopeCtas = 8;  // CTAs to an SM
 constexpr int kRopeToks = 4;   // tokens of a CTA, at most (a warp each looks them up)
 constexpr int kRopeAhead = 4;  // heads that a group of lanes has in flight
 
@@ -100,153 +100,198 @@ __device__ __forceinline__ Tok packed_token(const RopeParams& p, int token, int 
   return x;
 }
 
+// Eight elements of a head: a lane's four and the four that they pair with (INTER: pairs side by side).
+struct Part {
+  uint2 lo, hi;
+};
 __device__ __forceinline__ uint2 load4(const uint16_t* p) {
   uint2 v;
   asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
 
-template <int D, bool F16, bool PACKED>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p, const int toks, const uint32_t by_heads) {
+// A token's transform of queries (0) and keys (1), as coefficients of the pairs (a, b) of a head:
+// a <- a ca + b sb, b <- b cb + a sa, with the norm's weights and the magnitude in them.
+template <int D>
+struct Turn {
+  float ca[D / 2], sb[D / 2], cb[D / 2], sa[D / 2];
+};
+// A lane's four pairs of them, two pairs to a float2.
+struct Coefs {
+  float2 ca[2], sb[2], cb[2], sa[2];
+  template <int D>
+  __device__ __forceinline__ Coefs(const Turn<D>& f, int first) {
+    read(f.ca + first, ca), read(f.sb + first, sb), read(f.cb + first, cb), read(f.sa + first, sa);
+  }
+  static __device__ __forceinline__ void read(const float* p, float2 (&v)[2]) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    v[0] = make_float2(x.x, x.y), v[1] = make_float2(x.z, x.w);
+  }
+};
+__device__ __forceinline__ float rsqrt_fast(float x) {  // (to 2 units; a mean square below 2^-126 counts as 0)
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int D, bool F16, bool INTER>
+__device__ __forceinline__ Part transform(const Part& x, const Coefs& f, bool turned, bool normed, float eps) {
+  const float2 w0 = unpack2<F16>(x.lo.x), w1 = unpack2<F16>(x.lo.y), w2 = unpack2<F16>(x.hi.x), w3 = unpack2<F16>(x.hi.y);
+  const float2 a[2] = {INTER ? make_float2(w0.x, w1.x) : w0, INTER ? make_float2(w2.x, w3.x) : w1};
+  const float2 b[2] = {INTER ? make_float2(w0.y, w1.y) : w2, INTER ? make_float2(w2.y, w3.y) : w3};
+  float2 y[2], z[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    y[j] = mul2(a[j], f.ca[j]), z[j] = mul2(b[j], f.cb[j]);
+    if (turned) y[j] = fma2(b[j], f.sb[j], y[j]), z[j] = fma2(a[j], f.sa[j], z[j]);
+  }
+  if (normed) {
+    float2 q = mul2(a[0], a[0]);
+    q = fma2(a[1], a[1], q), q = fma2(b[0], b[0], q), q = fma2(b[1], b[1], q);
+    float sq = q.x + q.y;
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    const float inv = rsqrt_fast(sq * (1.f / D) + eps);
+    const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) y[j] = mul2(y[j], inv2), z[j] = mul2(z[j], inv2);
+  }
+  if (INTER)
+    return Part{make_uint2(pack2<F16>(y[0].x, z[0].x), pack2<F16>(y[0].y, z[0].y)), make_uint2(pack2<F16>(y[1].x, z[1].x), pack2<F16>(y[1].y, z[1].y))};
+  return Part{make_uint2(pack2<F16>(y[0].x, y[0].y), pack2<F16>(y[1].x, y[1].y)), make_uint2(pack2<F16>(z[0].x, z[0].y), pack2<F16>(z[1].x, z[1].y))};
+}
+
+template <int D, bool F16, bool PACKED, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __grid_constant__ RopeParams p, const int toks) {
   constexpr int LANES = D / 8, GROUPS = kRopeThreads / LANES, U = kRopeAhead;
   __shared__ Tok tok[kRopeToks];
-  __shared__ __align__(16) float cs[kRopeToks][2][D / 2];
-  __shared__ __align__(16) float weight[2][D];
+  __shared__ __align__(16) Turn<D> turn[kRopeToks][2];
   pdl_launch_dependents();
   pdl_wait();
   const gdn_kv_dims& d = p.d;
   const gdn_rope& r = p.r;
-  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, l = tid % LANES, group = tid / LANES;
+  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, l = tid % LANES;
   const int tok0 = int(blockIdx.x) * toks, n = p.n_tokens - tok0 < toks ? p.n_tokens - tok0 : toks;
-  const int H = p.hq + p.hk + p.hv, rows = n * H;
+  // `per` groups of lanes share a token: heads g, g + per, ...
+  const int per = GROUPS / toks, t = tid / LANES / per, g = tid / LANES % per;
+  const bool there = t < n;
   const int half = r.rot_dim / 2;
   const bool turned = 8 * l < r.rot_dim;
-  const int o0 = turned && !r.interleaved ? 4 * l : 8 * l, o1 = turned && !r.interleaved ? half + 4 * l : 8 * l + 4;
+  const int o0 = turned && !INTER ? 4 * l : 8 * l, o1 = turned && !INTER ? half + 4 * l : 8 * l + 4;
+  const long long token = tok0 + (there ? t : 0);
+  // what nobody reads is not fetched: windows' padding, and packed rows behind the last sequence (in a large call:
+  // it costs the loads a trip to L2)
+  bool fetch = there;
+  if (!PACKED && p.win_len && there) fetch = int(token % d.K) < p.win_len[token / d.K];
+  if (PACKED && toks > 1 && tok0 >= p.cu[d.B] && blockIdx.x > 0) return;
 
-  struct Row {
-    int t, h, kind;  // token of the CTA, head of its kind: 0 q, 1 k, 2 v
-  };
-  auto row_of = [&](int i) {
-    Row x;
-    x.t = by_heads ? int(__umulhi(uint32_t(i), by_heads)) : i / H;
-    x.h = i - x.t * H;
-    x.kind = x.h < p.hq ? 0 : x.h < p.hq + p.hk ? 1 : 2;
-    x.h -= x.kind == 0 ? 0 : x.kind == 1 ? p.hq : p.hq + p.hk;
-    return x;
-  };
-  uint2 a[U], b[U];
-  auto load = [&](int base) {
+  auto load = [&](const uint16_t* src) { return Part{load4(src + o0), load4(src + o1)}; };
+  const Part zero{make_uint2(0u, 0u), make_uint2(0u, 0u)};
+  const uint16_t* q_src = p.q + token * r.q_token_stride + g * r.q_head_stride;
+  const long long kv_at = token * r.kv_token_stride + g * r.kv_head_stride;
+  const uint16_t *k_src = p.k + kv_at, *v_src = p.v + kv_at;
+  const long long q_step = per * r.q_head_stride, kv_step = per * r.kv_head_stride;
+  const int hq = there ? p.hq : 0, hk = there ? p.hk : 0, hv = there ? p.hv : 0;
+  const int fq = fetch ? hq : 0, fk = fetch ? hk : 0, fv = fetch ? hv : 0;  // heads to fetch
+  Part q[U], k = zero, v = zero;
+  auto load_q = [&](int h) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = base + u * GROUPS;
-      a[u] = b[u] = make_uint2(0u, 0u);
-      if (i < rows) {
-        const Row x = row_of(i);
-        const long long token = tok0 + x.t;
-        const uint16_t* src = x.kind == 0 ? p.q + token * r.q_token_stride + x.h * r.q_head_stride
-                                          : (x.kind == 1 ? p.k : p.v) + token * r.kv_token_stride + x.h * r.kv_head_stride;
-        a[u] = load4(src + o0);
-        b[u] = load4(src + o1);
-      }
-    }
+    for (int u = 0; u < U; ++u, q_src += q_step) q[u] = h + u * per < fq ? load(q_src) : zero;
   };
-  load(group);
+  load_q(g);
+  if (g < fk) k = load(k_src);
+  if (g < fv) v = load(v_src);
 
+  // a thread's pair is the same in every token: its turns and weights are on their way, too
+  static_assert(kRopeThreads % (D / 2) == 0 && kRopeThreads >= D / 2, "a thread's pair is the same in every token");
+  const int pair = tid % (D / 2), pair_lane = pair / 4;
+  const bool pair_turned = 8 * pair_lane < r.rot_dim;
+  const int e0 = INTER ? 2 * pair : pair_turned ? pair : 4 * pair_lane + pair, e1 = INTER ? e0 + 1 : pair_turned ? half + pair : e0 + 4;
+  const uint64_t step = pair_turned ? p.turns[pair] : 0;
+  float w[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
+  if (p.q_weight) w[0][0] = p.q_weight[e0] + r.weight_offset, w[0][1] = p.q_weight[e1] + r.weight_offset;
+  if (p.k_weight) w[1][0] = p.k_weight[e0] + r.weight_offset, w[1][1] = p.k_weight[e1] + r.weight_offset;
   if (warp < n) {
     const Tok x = PACKED ? packed_token(p, tok0 + warp, lane) : window_token(p, tok0 + warp, lane);
     if (lane == 0) tok[warp] = x;
   }
-  if (p.q_weight)
-    for (int i = tid; i < D; i += kRopeThreads) weight[0][i] = r.weight_offset + p.q_weight[i];
-  if (p.k_weight)
-    for (int i = tid; i < D; i += kRopeThreads) weight[1][i] = r.weight_offset + p.k_weight[i];
   if (PACKED && blockIdx.x == 0) {  // (a token's own bounds are checked where it is looked up)
     bool bad = tid == 0 && (p.cu[0] != 0 || p.cu[d.B] > p.n_tokens);
     for (int i = tid; i < d.B; i += kRopeThreads) bad |= p.cu[i] > p.cu[i + 1];
     if (bad) atomicOr(p.err, kDevErrSeqlens);
   }
   __syncthreads();
-  for (int i = tid; i < n * (D / 2); i += kRopeThreads) {
-    const int t = i / (D / 2), j = i % (D / 2);
-    if (j < half) {
-      const uint64_t turn = uint64_t(tok[t].pos) * p.turns[j];
-      float s, c;
-      sincospif(float(int32_t(uint32_t((turn + (1ull << 31)) >> 32))) * 0x1p-31f, &s, &c);
-      cs[t][0][j] = c * r.magnitude;
-      cs[t][1][j] = s * r.magnitude;
+  for (int i = tid / (D / 2); i < n; i += kRopeThreads / (D / 2)) {
+    float s = 0.f, c = 1.f;
+    if (pair_turned) {
+      const uint64_t angle = uint64_t(tok[i].pos) * step;
+      sincospif(float(int32_t(uint32_t((angle + (1ull << 31)) >> 32))) * 0x1p-31f, &s, &c);
+      c *= r.magnitude, s *= r.magnitude;
+    }
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      Turn<D>& f = turn[i][kind];
+      f.ca[pair] = w[kind][0] * c, f.sb[pair] = -w[kind][1] * s, f.cb[pair] = w[kind][1] * c, f.sa[pair] = w[kind][0] * s;
     }
   }
   __syncthreads();
 
-  for (int base = group; base - group < rows; base += U * GROUPS) {
-    if (base != group) load(base);
+  const Tok here = tok[there ? t : 0];
+  const Turn<D>* const mine = turn[there ? t : 0];
+  const bool keep_q = PACKED ? here.live != 0 : true, keep_kv = PACKED ? here.live == 1 : true;
+  const bool blank = !PACKED && !here.live;  // (padding)
+  auto store = [&](uint16_t* dst, const Part& x) {
+    __stcs(reinterpret_cast<uint2*>(dst + o0), blank ? zero.lo : x.lo);
+    __stcs(reinterpret_cast<uint2*>(dst + o1), blank ? zero.lo : x.hi);
+  };
+  {  // (every lane of a warp runs the same number of rounds: heads are summed over lanes)
+    const Coefs f(mine[0], 4 * l);
+    uint16_t* q_dst = p.q_out + token * d.q_token_stride + g * D;
+    for (int h0 = 0; h0 < p.hq; h0 += U * per) {
+      if (h0 > 0) load_q(g + h0);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = base + u * GROUPS;
-      const Row x = row_of(i < rows ? i : 0);
-      const bool normed = x.kind == 0 ? p.q_weight != nullptr : x.kind == 1 && p.k_weight != nullptr;
-      float v[8];
-      {
-        const float2 v0 = unpack16<F16>(a[u].x), v1 = unpack16<F16>(a[u].y), v2 = unpack16<F16>(b[u].x), v3 = unpack16<F16>(b[u].y);
-        v[0] = v0.x, v[1] = v0.y, v[2] = v1.x, v[3] = v1.y, v[4] = v2.x, v[5] = v2.y, v[6] = v3.x, v[7] = v3.y;
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * per;
+        if (h >= p.hq) break;
+        const Part y = transform<D, F16, INTER>(q[u], f, turned, p.q_weight != nullptr, r.eps);
+        if (g + h < hq && keep_q) store(q_dst, y);
+        q_dst += per * D;
       }
-      if (p.q_weight || p.k_weight) {  // (the lanes of a warp may hold heads of different kinds: all sum)
-        float sq = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sq += v[j] * v[j];
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-        if (normed) {
-          const float inv = rsqrtf(sq * (1.f / D) + r.eps);
-          const float4 w0 = *reinterpret_cast<const float4*>(&weight[x.kind][o0]), w1 = *reinterpret_cast<const float4*>(&weight[x.kind][o1]);
-          v[0] *= inv * w0.x, v[1] *= inv * w0.y, v[2] *= inv * w0.z, v[3] *= inv * w0.w;
-          v[4] *= inv * w1.x, v[5] *= inv * w1.y, v[6] *= inv * w1.z, v[7] *= inv * w1.w;
-        }
-      }
-      if (i >= rows) continue;
-      if (turned && x.kind < 2) {
-        const float4 c = *reinterpret_cast<const float4*>(&cs[x.t][0][4 * l]), s = *reinterpret_cast<const float4*>(&cs[x.t][1][4 * l]);
-        const float cj[4] = {c.x, c.y, c.z, c.w}, sj[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float &e0 = r.interleaved ? v[2 * j] : v[j], &e1 = r.interleaved ? v[2 * j + 1] : v[4 + j];
-          const float y0 = e0 * cj[j] - e1 * sj[j], y1 = e1 * cj[j] + e0 * sj[j];
-          e0 = y0, e1 = y1;
-        }
-      }
-      uint2 out0 = a[u], out1 = b[u];  // (values are copied as they are)
-      if (x.kind < 2 && (normed || turned)) {
-        out0 = make_uint2(pack16<F16>(v[0], v[1]), pack16<F16>(v[2], v[3]));
-        out1 = make_uint2(pack16<F16>(v[4], v[5]), pack16<F16>(v[6], v[7]));
-      }
-      const int live = tok[x.t].live;
-      const long long token = tok0 + x.t;
-      uint16_t* dst;
-      if (PACKED) {
-        if (live == 0 || (live == 2 && x.kind != 0)) continue;
-        dst = x.kind == 0 ? p.q_out + token * d.q_token_stride + x.h * D
-                          : (x.kind == 1 ? p.k_out : p.v_out) + tok[x.t].at + x.h * d.cache_head_stride;
-      } else {
-        if (!live) out0 = out1 = make_uint2(0u, 0u);
-        dst = x.kind == 0 ? p.q_out + token * d.q_token_stride + x.h * D
-                          : (x.kind == 1 ? p.k_out : p.v_out) + token * d.win_token_stride + x.h * D;
-      }
-      *reinterpret_cast<uint2*>(dst + o0) = out0;
-      *reinterpret_cast<uint2*>(dst + o1) = out1;
+    }
+  }
+  {
+    const Coefs f(mine[1], 4 * l);
+    const long long to = PACKED ? here.at + g * d.cache_head_stride : token * d.win_token_stride + g * D;
+    const long long to_step = PACKED ? per * d.cache_head_stride : per * D;
+    uint16_t *k_dst = p.k_out + to, *v_dst = p.v_out + to;
+    const int all = p.hk > p.hv ? p.hk : p.hv;
+    for (int h0 = 0; h0 < all; h0 += per) {
+      const int h = g + h0;
+      const Part k_now = k, v_now = v;
+      k_src += kv_step, v_src += kv_step;
+      if (h + per < fk) k = load(k_src);
+      if (h + per < fv) v = load(v_src);
+      const Part y = transform<D, F16, INTER>(k_now, f, turned, p.k_weight != nullptr, r.eps);
+      if (h < hk && keep_kv) store(k_dst, y);
+      if (h < hv && keep_kv) store(v_dst, v_now);
+      k_dst += to_step, v_dst += to_step;
     }
   }
 }
 
 template <bool PACKED>
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
-  const int toks = p.n_tokens <= 8 * 152 ? 1 : kRopeToks;
-  const unsigned long long H = (unsigned long long)(p.hq + p.hk + p.hv);
-  // ceil(2^32 / H): the quotient by H is exact while row x H < 2^32
-  const uint32_t by_heads = H > 1 && H * H * toks < (1ull << 32) ? uint32_t(((1ull << 32) + H - 1) / H) : 0u;
+  const int toks = p.n_tokens <= kRopeCtas * 152 ? 1 : kRopeToks;
   const unsigned grid = unsigned((p.n_tokens + toks - 1) / toks);
-  auto kernel = p.d.D == 128 ? (p.d.dtype ? rope_kernel<128, true, PACKED> : rope_kernel<128, false, PACKED>)
-                             : (p.d.dtype ? rope_kernel<64, true, PACKED> : rope_kernel<64, false, PACKED>);
-  return launch_dependent(kernel, grid, kRopeThreads, 0, stream, p, toks, by_heads);
+  const bool f16 = p.d.dtype != 0;
+  auto kernel = [&]() -> void (*)(RopeParams, int) {
+    if (p.d.D == 128)
+      return p.r.interleaved ? (f16 ? rope_kernel<128, true, PACKED, true> : rope_kernel<128, false, PACKED, true>)
+                             : (f16 ? rope_kernel<128, true, PACKED, false> : rope_kernel<128, false, PACKED, false>);
+    return p.r.interleaved ? (f16 ? rope_kernel<64, true, PACKED, true> : rope_kernel<64, false, PACKED, true>)
+                           : (f16 ? rope_kernel<64, true, PACKED, false> : rope_kernel<64, false, PACKED, false>);
+  }();
+  return launch_dependent(kernel, grid, kRopeThreads, 0, stream, p, toks);
 }
 
 }  // namespace

@@ -96,7 +96,7 @@ def test_dims_of_single_calls(lib, call, name, value, status):
 
 
 @pytest.mark.parametrize("name,value,status", [
-    ("rot_dim", -8, INV), ("rot_dim", 72, INV), ("rot_dim", 20, UNS), ("interleaved", 2, INV), ("reserved", 1, INV),
+    ("rot_dim", -8, INV), ("rot_dim", 72, INV), ("rot_dim", 20, UNS), ("rot_dim", 40, UNS), ("interleaved", 2, INV), ("reserved", 1, INV),
     ("magnitude", float("nan"), INV), ("magnitude", float("inf"), INV), ("eps", -1e-6, INV), ("eps", float("nan"), INV),
     ("weight_offset", float("inf"), INV), ("q_token_stride", 100, INV), ("q_head_stride", -64, INV),
     ("kv_token_stride", 12, INV), ("kv_head_stride", 1 << 36, INV)])
