@@ -13,7 +13,7 @@
 // workspace: at most two such pieces a CTA), and a last kernel joins them.  Which CTA computes what depends on
 // the lengths alone, and no sum is formed by atomics, so results repeat bit for bit.
 //
-// Kernels: plan (one CTA: lengths -> blocks and their tiles), tiles (persistent, tcgen05), join.
+// Kernels: tiles (persistent, tcgen05; every CTA plans for itself), join.
 //
 // A block of more than 128 rows gives each stream half of them, on the same keys; a smaller one gives the
 // streams alternate tiles of the same rows, and at its end the two sums are joined in tensor memory, each
@@ -28,22 +28,115 @@ namespace gdn {
 
 namespace {
 
-constexpr int kPlanThreads = 512;
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8, kJoinChunks = 8;  // CTAs to a cut item
+
+struct JoinRec {       // a cut item, by the CTA c0 that it begins in; it ends in CTA c1
+  int32_t tok0, rows;  // rows 0: there is none
+  int32_t h, c0, c1, part0;
+};
+
+struct PackedWs {
+  JoinRec* join;     // [kCtas]
+  float* lse;        // [kCtas][2][kBlockRows] log2 units
+  float* o;          // [kCtas][2][kBlockRows][D]
+};
+
+__host__ __device__ inline size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+
+__host__ __device__ inline PackedWs carve_packed(void* base, const gdn_kv_dims& d, size_t* total) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  size_t o = 0;
+  const size_t parts = 2 * size_t(kBlockRows) * kCtas;
+  PackedWs w;
+  w.join = reinterpret_cast<JoinRec*>(p + o), o += round256(sizeof(JoinRec) * kCtas);
+  w.lse = reinterpret_cast<float*>(p + o), o += round256(4 * parts);
+  w.o = reinterpret_cast<float*>(p + o), o += 4 * parts * size_t(d.D);
+  if (total) *total = o;
+  return w;
+}
 
 // ---------------------------------------------------------------- the plan
-struct BlockRec {
-  long long off;       // its first tile among those of one kv head
-  int32_t tok0, toks;  // its packed tokens
-  int32_t slot, keys;  // own slot, and the keys in it that the last row sees
-  int32_t lim;         // the keys in it that the first row sees (causal: a token more each token; may be below 1)
-  int32_t pre_slot, pre_keys;
-  int32_t tiles;
+// How the calls' rows are cut into blocks: all that depends on the heads alone.
+struct Cut {
+  int tile_toks, toks;  // tokens of a row tile, of a block
+  int period_log;       // after so many (2^period_log) blocks, their keys are a whole number of tiles more
+  int causal;
 };
-struct PlanHead {
+
+struct SeqRows {
+  int lo, n;       // its packed tokens
+  int len;         // tokens in its slot
+  int pre_slot, pre_keys;
+  __device__ __forceinline__ int pre_tiles() const { return (pre_keys + kTileKeys - 1) / kTileKeys; }
+  __device__ __forceinline__ int blocks(const Cut& c) const { return int((unsigned(n) + unsigned(c.toks) - 1u) / unsigned(c.toks)); }
+  // own keys that the last row of block k sees
+  __device__ __forceinline__ int keys(const Cut& c, int k) const {
+    if (!c.causal) return len;
+    const long long e = (long long)len - n + (long long)c.toks * (k + 1);
+    return e < 0 ? 0 : e < len ? int(e) : len;
+  }
+  // Tiles of the first k blocks: sums of ceil(keys / 128), period by period.
+  __device__ __forceinline__ long long tiles(const Cut& c, int k) const {
+    const long long pre = (long long)pre_tiles() * k;
+    if (!c.causal) return pre + (long long)((len + kTileKeys - 1) / kTileKeys) * k;
+    const long long off = (long long)len - n;
+    const int i0 = off >= 0 ? 1 : int((unsigned long long)(-off) / unsigned(c.toks)) + 1;  // the first block with keys, counted from 1
+    long long sum = 0;
+    if (k >= i0) {
+      const long long m = (long long)k - i0 + 1, first = off + (long long)c.toks * i0 + kTileKeys - 1;
+      const int period = 1 << c.period_log, rest = int(m & (period - 1));
+      const long long whole = m >> c.period_log, more = (long long)c.toks << c.period_log >> 7;  // (tiles that a period adds)
+      long long one = 0, part = 0;
+      for (int i = 0; i < period && i < m; ++i) {
+        const long long t = (first + (long long)c.toks * i) >> 7;
+        one += t;
+        if (i < rest) part += t;
+      }
+      sum = (whole > 0 ? whole * one : 0) + (more * whole * (whole - 1) / 2 << c.period_log) + part + rest * more * whole;
+    }
+    if (k == blocks(c) && k > 0) {  // the last block is as long as it is
+      const long long e = off + (long long)c.toks * k;
+      sum += (len + kTileKeys - 1) / kTileKeys - (e > 0 ? (e + kTileKeys - 1) >> 7 : 0);
+    }
+    return pre + sum;
+  }
+  // Tokens in blocks without keys, the first ones.
+  __device__ __forceinline__ int without_keys(const Cut& c) const {
+    if (pre_keys > 0 || n == 0) return 0;
+    if (len == 0) return n;
+    if (!c.causal || len >= n) return 0;
+    const int k = (n - len) / c.toks;
+    return k * c.toks;
+  }
+};
+
+__device__ __forceinline__ SeqRows load_sequence(const PackedAttnParams& p, int b, bool report) {
+  const gdn_kv_dims& d = p.d;
+  SeqRows s;
+  const int lo = p.cu[b], hi = p.cu[b + 1], len = p.seq_len[d.slot0 + b], slot = p.prefix_of ? p.prefix_of[b] : -1;
+  uint32_t bad = 0;
+  s.lo = lo, s.n = hi > lo ? hi - lo : 0;
+  s.len = len;
+  if (len < 0 || (long long)len > (long long)d.max_pages * d.page_size) s.len = 0, bad |= GDN_DEVERR_KV_LEN;
+  if (slot < -1 || slot >= d.n_slots) bad |= GDN_DEVERR_KV_SLOT;
+  s.pre_slot = slot < 0 || slot >= d.n_slots ? -1 : slot;
+  s.pre_keys = 0;
+  if (s.pre_slot >= 0) {
+    s.pre_keys = p.seq_len[s.pre_slot];
+    if (s.pre_keys < 0 || (long long)s.pre_keys > (long long)d.max_pages * d.page_size) s.pre_keys = 0, bad |= GDN_DEVERR_KV_LEN;
+  }
+  if (bad && report) atomicOr(p.err, bad);
+  return s;
+}
+
+// Every CTA plans for itself: each thread sums the tiles of a few consecutive sequences, the CTA the sums of its
+// threads, and the thread that has the first tile of the CTA's stretch among its own says in which sequence.
+struct Plan {
   long long head_tiles, tiles;  // of one kv head, and of all
-  int32_t blocks;
+  long long into;               // the stretch begins so many tiles into
+  int32_t b, h;                 // sequence b, kv head h
   int32_t ctas;                 // that the tiles are dealt to: each has one at least
+  int32_t empty;                // some rows have no keys
   // The deal gives CTA c tiles [begin(c), begin(c + 1)); the CTA of tile x.
   __device__ __forceinline__ long long begin(long long c) const { return c * tiles / ctas; }
   __device__ __forceinline__ int cta_of(long long x) const {
@@ -54,131 +147,78 @@ struct PlanHead {
     return c;
   }
 };
-struct JoinRec {       // an item that begins in CTA c0 and ends in CTA c1, c1 > c0
-  int32_t tok0, rows;  // rows 0: there is none
-  int32_t h, c0, c1, part0;
-};
 
-struct PackedWs {
-  PlanHead* head;
-  JoinRec* join;     // [kCtas]
-  int32_t* first;    // [B] each sequence's first block
-  BlockRec* block;   // [N / block tokens + B]
-  float* lse;        // [kCtas][2][kBlockRows] log2 units
-  float* o;          // [kCtas][2][kBlockRows][D]
-};
-
-__host__ __device__ inline size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
-
-__host__ __device__ inline int block_toks(const gdn_kv_dims& d) { return 2 * (kTileRows / (d.Hq / d.Hkv)); }
-
-__host__ __device__ inline PackedWs carve_packed(void* base, const gdn_kv_dims& d, long long n_tokens, size_t* total) {
-  uint8_t* p = static_cast<uint8_t*>(base);
-  size_t o = 0;
-  const size_t parts = 2 * size_t(kBlockRows) * kCtas, blocks = size_t(n_tokens / block_toks(d)) + size_t(d.B);
-  PackedWs w;
-  w.head = reinterpret_cast<PlanHead*>(p + o), o += 256;
-  w.join = reinterpret_cast<JoinRec*>(p + o), o += round256(sizeof(JoinRec) * kCtas);
-  w.first = reinterpret_cast<int32_t*>(p + o), o += round256(4 * size_t(d.B));
-  w.block = reinterpret_cast<BlockRec*>(p + o), o += round256(sizeof(BlockRec) * blocks);
-  w.lse = reinterpret_cast<float*>(p + o), o += round256(4 * parts);
-  w.o = reinterpret_cast<float*>(p + o), o += 4 * parts * size_t(d.D);
-  if (total) *total = o;
-  return w;
-}
-
-template <typename T>
-__device__ __forceinline__ T scan_block(T v, T* sums, T& total) {  // exclusive, kPlanThreads threads
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  T x = v;
+__device__ __forceinline__ void make_plan(const PackedAttnParams& p, const Cut& cut, Plan& plan, long long* sums) {
+  const gdn_kv_dims& d = p.d;
+  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, cta = int(blockIdx.x);
+  const int each = (d.B + kTileThreads - 1) / kTileThreads;
+  const int b0 = tid * each < d.B ? tid * each : d.B, b1 = b0 + each < d.B ? b0 + each : d.B;
+  bool bad = tid == 0 && (p.cu[0] != 0 || p.cu[d.B] > p.n_tokens), empty = false;
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    bad |= p.cu[b] > p.cu[b + 1];
+    const SeqRows s = load_sequence(p, b, cta == 0);
+    mine += s.tiles(cut, s.blocks(cut));
+    empty |= s.without_keys(cut) > 0;
+  }
+  bad = __syncthreads_or(bad) != 0;
+  empty = __syncthreads_or(empty) != 0;
+  long long x = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();
   if (lane == 31) sums[warp] = x;
   __syncthreads();
-  T s = lane < kPlanThreads / 32 ? sums[lane] : T(0);
+  long long before = 0, all = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += y;
+  for (int i = 0; i < kTileThreads / 32; ++i) {
+    before += i < warp ? sums[i] : 0;
+    all += sums[i];
   }
-  total = __shfl_sync(0xffffffffu, s, 31);
-  const T before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
-  return x - v + (warp > 0 ? before : 0);
-}
-
-__global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w) {
-  __shared__ long long sums[32];
-  __shared__ int first_here[kPlanThreads];
-  pdl_launch_dependents();
-  pdl_wait();
-  const gdn_kv_dims& d = p.d;
-  const int tid = int(threadIdx.x), per = block_toks(d);
-  bool bad = tid == 0 && (p.cu[0] != 0 || p.cu[d.B] > p.n_tokens);
-  for (int i = tid; i < d.B; i += kPlanThreads) bad |= p.cu[i] > p.cu[i + 1];
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) {
-      atomicOr(p.err, kDevErrSeqlens);
-      *w.head = PlanHead{0, 0, 0, 0};
+  before += x - mine;
+  if (bad) all = 0;
+  Plan q;
+  q.head_tiles = all, q.tiles = all * d.Hkv;
+  q.ctas = int(q.tiles < kCtas ? q.tiles : kCtas);
+  q.empty = empty && !bad;
+  q.b = q.h = 0, q.into = 0;
+  if (tid == 0 && bad && cta == 0) atomicOr(p.err, kDevErrSeqlens);
+  if (cta >= q.ctas) {
+    if (tid == 0) plan = q;
+  } else {
+    const long long first = q.begin(cta);
+    q.h = int(first / q.head_tiles);
+    long long y = first - q.h * q.head_tiles;
+    if (y >= before && y < before + mine) {  // (one thread)
+      y -= before;
+      for (int b = b0; b < b1; ++b) {
+        const SeqRows s = load_sequence(p, b, false);
+        const long long t = s.tiles(cut, s.blocks(cut));
+        if (y < t) {
+          q.b = b, q.into = y;
+          break;
+        }
+        y -= t;
+      }
+      plan = q;
     }
-    return;
-  }
-  int* const first = d.B <= kPlanThreads ? first_here : w.first;
-  long long blocks = 0;
-  for (int b0 = 0; b0 < d.B; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    const int n = b < d.B ? p.cu[b + 1] - p.cu[b] : 0;
-    long long total;
-    const long long at = blocks + scan_block<long long>((n + per - 1) / per, sums, total);
-    if (b < d.B) first[b] = int(at);
-    blocks += total;
   }
   __syncthreads();
-  long long tiles = 0;
-  for (int i0 = 0; i0 < blocks; i0 += kPlanThreads) {
-    const int i = i0 + tid;
-    BlockRec r{};
-    if (i < blocks) {
-      int b = 0, end = d.B;  // the last sequence whose first block is not behind i (those without tokens come before it)
-      while (end - b > 1) {
-        const int mid = (b + end) / 2;
-        if (first[mid] <= i)
-          b = mid;
-        else
-          end = mid;
-      }
-      const int lo = p.cu[b], n = p.cu[b + 1] - lo, j0 = (i - first[b]) * per;
-      const int len = checked_slot_len(p.seq_len[d.slot0 + b], d, p.err);
-      r.tok0 = lo + j0;
-      r.toks = n - j0 < per ? n - j0 : per;
-      r.slot = d.slot0 + b;
-      r.pre_slot = checked_prefix(p.prefix_of, b, d, p.err);
-      r.pre_keys = r.pre_slot < 0 ? 0 : checked_slot_len(p.seq_len[r.pre_slot], d, p.err);
-      r.lim = p.causal ? len - n + j0 + 1 : len;
-      r.keys = p.causal ? r.lim + r.toks - 1 : len;
-      if (r.keys < 0) r.keys = 0;
-      r.tiles = (r.pre_keys + kTileKeys - 1) / kTileKeys + (r.keys + kTileKeys - 1) / kTileKeys;
-    }
-    long long total;
-    r.off = tiles + scan_block<long long>(r.tiles, sums, total);
-    if (i < blocks) w.block[i] = r;
-    tiles += total;
-    // rows of blocks without keys
-    uint32_t empty = __ballot_sync(0xffffffffu, i < blocks && r.tiles == 0);
-    while (empty) {
-      const int from = __ffs(int(empty)) - 1, lane = tid & 31;
-      empty &= empty - 1;
-      const int tok0 = __shfl_sync(0xffffffffu, r.tok0, from), toks = __shfl_sync(0xffffffffu, r.toks, from);
-      uint4* const out = reinterpret_cast<uint4*>(p.out + (long long)tok0 * d.Hq * d.D);
-      for (long long k = lane; k < (long long)toks * d.Hq * (d.D / 8); k += 32) out[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (p.lse)
-        for (long long k = lane; k < (long long)toks * d.Hq; k += 32) p.lse[(long long)tok0 * d.Hq + k] = -INFINITY;
-    }
+}
+
+// Outputs of rows without keys, whole blocks of them: 0 and -inf.
+__device__ __noinline__ void write_empty(const PackedAttnParams& p, const Cut& cut) {
+  const gdn_kv_dims& d = p.d;
+  for (int b = int(blockIdx.x); b < d.B; b += kCtas) {
+    const SeqRows s = load_sequence(p, b, false);
+    const long long rows = (long long)s.without_keys(cut) * d.Hq, first = (long long)s.lo * d.Hq;
+    uint4* const out = reinterpret_cast<uint4*>(p.out + first * d.D);
+    for (long long k = threadIdx.x; k < rows * (d.D / 8); k += kTileThreads) out[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse)
+      for (long long k = threadIdx.x; k < rows; k += kTileThreads) p.lse[first + k] = -INFINITY;
   }
-  if (tid == 0) *w.head = PlanHead{tiles, tiles * d.Hkv, int(blocks), int(tiles * d.Hkv < kCtas ? tiles * d.Hkv : kCtas)};
 }
 
 // ---------------------------------------------------------------- segments
@@ -204,54 +244,78 @@ struct Seg {
   }
 };
 
-// Walks a CTA's stretch segment by segment (a converged warp).
+// Walks a CTA's stretch segment by segment (a converged warp).  Lane i knows sequence from + i.
 struct SegWalk {
   const PackedAttnParams& p;
   const PackedWs& w;
-  const int cta, tile_rows, G;
-  PlanHead head;
+  const Cut& cut;
+  const Plan& plan;
+  const int cta, lane, G;
   long long begin, x, end;
-  int h, k;
-  __device__ __forceinline__ SegWalk(const PackedAttnParams& p_, const PackedWs& w_, int cta_, int lane)
-      : p(p_), w(w_), cta(cta_), tile_rows(kTileRows / (p_.d.Hq / p_.d.Hkv) * (p_.d.Hq / p_.d.Hkv)), G(p_.d.Hq / p_.d.Hkv) {
-    head = *w.head;
+  int h, b, k, t_in;  // the item at hand: kv head, sequence, block; its tiles before x
+  int from;
+  SeqRows mine;
+  __device__ __forceinline__ SeqRows sequence(int i) {
+    if (i < from || i >= from + 32) {
+      from = i;
+      const int at = i + lane < p.d.B ? i + lane : p.d.B - 1;
+      mine = load_sequence(p, at, false);
+    }
+    const int l = i - from;
+    SeqRows s;
+    s.lo = __shfl_sync(0xffffffffu, mine.lo, l), s.n = __shfl_sync(0xffffffffu, mine.n, l);
+    s.len = __shfl_sync(0xffffffffu, mine.len, l), s.pre_slot = __shfl_sync(0xffffffffu, mine.pre_slot, l);
+    s.pre_keys = __shfl_sync(0xffffffffu, mine.pre_keys, l);
+    return s;
+  }
+  __device__ __forceinline__ SegWalk(const PackedAttnParams& p_, const PackedWs& w_, const Cut& cut_, const Plan& plan_, int lane_)
+      : p(p_), w(w_), cut(cut_), plan(plan_), cta(int(blockIdx.x)), lane(lane_), G(p_.d.Hq / p_.d.Hkv) {
     begin = x = end = 0;
-    h = k = 0;
+    h = b = k = t_in = 0;
+    from = -64;
     if (lane == 0) w.join[cta].rows = 0;
-    if (cta >= head.ctas) return;
-    begin = x = head.begin(cta), end = head.begin(cta + 1);
-    h = int(x / head.head_tiles);
-    const long long y = x - h * head.head_tiles;
-    int n = head.blocks;  // the last block that starts at or before y, 32 at a time
+    if (cta >= plan.ctas) return;
+    begin = x = plan.begin(cta), end = plan.begin(cta + 1);
+    h = plan.h, b = plan.b;
+    const SeqRows s = sequence(b);
+    int n = s.blocks(cut);  // the last block with at most `into` tiles before it, 32 at a time
     while (n > 1) {
       const int step = (n + 31) / 32, i = lane * step;
-      const uint32_t at_or_before = __ballot_sync(0xffffffffu, i < n && w.block[k + i].off <= y);
+      const uint32_t at_or_before = __ballot_sync(0xffffffffu, i < n && s.tiles(cut, k + i) <= plan.into);
       const int j = 31 - __clz(int(at_or_before));
       k += j * step;
       n = n - j * step < step ? n - j * step : step;
     }
+    t_in = int(plan.into - s.tiles(cut, k));
   }
-  __device__ __forceinline__ bool next(Seg& s, int lane) {
+  __device__ __forceinline__ bool next(Seg& g) {
     if (x >= end) return false;
     while (true) {
-      const BlockRec r = w.block[k];
-      const long long from = h * head.head_tiles + r.off;
-      if (x >= from + r.tiles) {
-        if (++k == head.blocks) k = 0, ++h;
+      if (b == p.d.B) b = 0, ++h;
+      const SeqRows s = sequence(b);
+      if (k >= s.blocks(cut)) {
+        ++b, k = 0;
         continue;
       }
-      s.tok0 = r.tok0, s.rows = r.toks * G, s.h = h;
-      s.pair = s.rows > tile_rows;
-      s.slot = r.slot, s.keys = r.keys, s.lim = r.lim, s.pre_slot = r.pre_slot, s.pre_keys = r.pre_keys;
-      s.pre_tiles = (r.pre_keys + kTileKeys - 1) / kTileKeys;
-      s.t0 = int(x - from);
-      s.t1 = end - x < r.tiles - s.t0 ? s.t0 + int(end - x) : r.tiles;
-      s.parity = int(x & 1);
+      const int pre = s.pre_tiles(), keys = s.keys(cut, k), tiles = pre + (keys + kTileKeys - 1) / kTileKeys;
+      if (tiles == 0) {
+        ++k;
+        continue;
+      }
+      const int j0 = k * cut.toks, toks = s.n - j0 < cut.toks ? s.n - j0 : cut.toks;
+      g.tok0 = s.lo + j0, g.rows = toks * G, g.h = h;
+      g.pair = toks > cut.tile_toks;
+      g.slot = p.d.slot0 + b, g.keys = keys, g.lim = cut.causal ? s.len - s.n + j0 + 1 : s.len;
+      g.pre_slot = s.pre_slot, g.pre_keys = s.pre_keys, g.pre_tiles = pre;
+      g.t0 = t_in;
+      g.t1 = end - x < tiles - t_in ? t_in + int(end - x) : tiles;
+      g.parity = int(x & 1);
       const int second = x == begin ? 0 : 1;  // (of the CTA's pieces: one that its stretch begins with, one that it ends with)
-      s.part = s.t0 == 0 && s.t1 == r.tiles ? -1 : (2 * cta + second) * kBlockRows;
-      if (s.t0 == 0 && s.t1 < r.tiles && lane == 0)
-        w.join[cta] = JoinRec{s.tok0, s.rows, h, cta, head.cta_of(from + r.tiles - 1), s.part};
-      x += s.t1 - s.t0;
+      g.part = g.t0 == 0 && g.t1 == tiles ? -1 : (2 * cta + second) * kBlockRows;
+      if (g.t0 == 0 && g.t1 < tiles && lane == 0)
+        w.join[cta] = JoinRec{g.tok0, g.rows, h, cta, plan.cta_of(x + tiles - 1), g.part};
+      x += g.t1 - g.t0;
+      t_in = 0, ++k;  // (an item that goes on ends the stretch)
       return true;
     }
   }
@@ -268,8 +332,8 @@ constexpr int kFewToks = 4;
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    packed_tile_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w, const int box, const uint32_t page_inv,
-                       const __grid_constant__ PackedMaps maps) {
+    packed_tile_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w, const __grid_constant__ Cut cut, const int box,
+                       const uint32_t page_inv, const __grid_constant__ PackedMaps maps) {
   using L = TileLayout<D, Seg>;
   constexpr int NS = L::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -277,6 +341,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ int page_of_box[32][2];
   __shared__ volatile uint32_t gave_up, turns[2];  // (turns: taken so far by each tensor-core warp)
   __shared__ uint64_t merge_bar;                   // the two softmax groups, at the end of a segment that they share
+  __shared__ Plan plan;
   __shared__ float2 merge_ml[kTileRows];           // maximum (log2 units) and sum of a row, one stream's and then the other's
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
@@ -284,7 +349,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   Seg* const segs = reinterpret_cast<Seg*>(smem + L::OFF_SEG);
   const int tid = int(threadIdx.x), warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const gdn_kv_dims& d = p.d;
-  const int G = d.Hq / d.Hkv, tile_toks = kTileRows / G, tile_rows = tile_toks * G;
+  const int G = d.Hq / d.Hkv, tile_toks = cut.tile_toks, tile_rows = tile_toks * G;
 
   if (tid == 0) {
     init_tile_bars<NS>(bars);
@@ -300,6 +365,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t tmem = tmem_slot;
   pdl_launch_dependents();
   pdl_wait();
+  make_plan(p, cut, plan, reinterpret_cast<long long*>(merge_ml));
+  if (plan.empty) write_empty(p, cut);
 
   // Bounded wait of a whole warp, which goes on or gives up together; once one warp has given up, all of the
   // CTA's do.
@@ -562,7 +629,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // As in kv_attn.cu: segments go out as the ring has room, and a segment's queries as soon as the products with
     // the ones before are done.  Queries come by TMA, whole tokens of G heads: rows behind the block's last hold
     // other tokens' queries or what was there, and nothing reads their results.
-    SegWalk walk(p, w, int(blockIdx.x), lane);
+    SegWalk walk(p, w, cut, plan, lane);
     uint32_t k = 0, kq = 0;      // segments handed on; segment whose queries are next
     uint32_t nq0 = 0, nq1 = 0;   // segments of each stream
     int part = 0;                // of segment kq: its first or second stream
@@ -572,7 +639,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bool did = false;
       if (more && __all_sync(0xffffffffu, mbar_look(bars.seg_empty + k % kSegRing, ((k / kSegRing) & 1) ^ 1))) {
         Seg seg;
-        more = walk.next(seg, lane);
+        more = walk.next(seg);
         if (lane == 0) {
           if (!more) seg.t1 = -1;
           segs[k % kSegRing] = seg;
@@ -631,28 +698,39 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 }
 
 // ---------------------------------------------------------------- join
-// kCtas x chunks CTAs: a few rows of the cut item that begins in a CTA's stretch, if one does.  A warp takes a row
-// at a time: its pieces' log-sum-exps, then their sums, four in flight.
+// kJoinChunks CTAs for each CTA of the tile kernel, if a cut item begins in its stretch: a warp takes a row at a time,
+// its pieces' log-sum-exps and, on their way with them, the first pieces' sums.
 template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kJoinWarps) packed_join_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w, const int chunk_rows) {
+__global__ void __launch_bounds__(32 * kJoinWarps) packed_join_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w) {
   constexpr int N = D / 32, U = 4;
   pdl_launch_dependents();
   pdl_wait();
   const gdn_kv_dims& d = p.d;
   const JoinRec rec = w.join[blockIdx.x % kCtas];
-  const int r0 = int(blockIdx.x / kCtas) * chunk_rows;
-  const int G = d.Hq / d.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r1 = r0 + chunk_rows < rec.rows ? r0 + chunk_rows : rec.rows, parts = rec.rows > 0 ? rec.c1 - rec.c0 + 1 : 0;
-  for (int r = r0 + warp; r < r1; r += kJoinWarps) {
+  const int G = d.Hq / d.Hkv, lane = threadIdx.x & 31;
+  const int parts = rec.rows > 0 ? rec.c1 - rec.c0 + 1 : 0;
+  for (int r = int(blockIdx.x / kCtas) * kJoinWarps + int(threadIdx.x >> 5); r < rec.rows; r += kJoinWarps * kJoinChunks) {
     // piece j's row: the first CTA's piece, then the one that each stretch begins with
     auto at = [&](int j) { return (j == 0 ? rec.part0 : 2 * (rec.c0 + j) * kBlockRows) + r; };
-    float acc[N];
+    float acc[N], v[U][N];
+    auto load = [&](int j0, int end) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j0 + u < end) {
+          const float* o = w.o + (long long)at(j0 + u) * D + lane * N;
+          if (N == 4)
+            *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(o);
+          else
+            *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(o);
+        }
+    };
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[k] = 0.f;
     float M = -INFINITY, W = 0.f;
     for (int j0 = 0; j0 < parts; j0 += 32) {
       const int n = parts - j0 < 32 ? parts - j0 : 32;
       const float e = lane < n ? w.lse[at(j0 + lane)] : -INFINITY;
+      load(j0, j0 + n);
       float mx = e;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -663,16 +741,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) packed_join_kernel(const __gr
 #pragma unroll
       for (int k = 0; k < N; ++k) acc[k] *= f;
       for (int i0 = 0; i0 < n; i0 += U) {
-        float v[U][N];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (i0 + u < n) {
-            const float* o = w.o + (long long)at(j0 + i0 + u) * D + lane * N;
-            if (N == 4)
-              *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(o);
-            else
-              *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(o);
-          }
+        if (i0 > 0) load(j0 + i0, j0 + n);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const float wj = __shfl_sync(0xffffffffu, wt, (i0 + u) & 31);
@@ -698,31 +767,28 @@ __global__ void __launch_bounds__(32 * kJoinWarps) packed_join_kernel(const __gr
 
 // ---------------------------------------------------------------- launches
 template <int D, bool F16>
-cudaError_t launch(const PackedAttnParams& p, const PackedWs& w, int box, const PackedMaps& maps, cudaStream_t stream) {
+cudaError_t launch(const PackedAttnParams& p, const PackedWs& w, const Cut& cut, int box, const PackedMaps& maps, cudaStream_t stream) {
   using L = TileLayout<D, Seg>;
   static_assert(L::TOTAL + 1536 <= 232448, "shared memory");
-  cudaError_t e = launch_dependent(packed_plan_kernel, 1u, kPlanThreads, 0, stream, p, w);
-  if (e != cudaSuccess) return e;
   static std::atomic<uint64_t> allowed{0};  // a bit per device: the kernel may use its shared memory there
   int dev = 0;
-  e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!(allowed.load() >> (dev & 63) & 1)) {
     e = cudaFuncSetAttribute(packed_tile_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL);
     if (e != cudaSuccess) return e;
     allowed.fetch_or(1ull << (dev & 63));
   }
-  e = launch_dependent(packed_tile_kernel<D, F16>, unsigned(kCtas), kTileThreads, L::TOTAL, stream, p, w, box, page_units_inv(p.d.page_size), maps);
+  e = launch_dependent(packed_tile_kernel<D, F16>, unsigned(kCtas), kTileThreads, L::TOTAL, stream, p, w, cut, box, page_units_inv(p.d.page_size), maps);
   if (e != cudaSuccess) return e;
-  constexpr int chunk_rows = 8;
-  return launch_dependent(packed_join_kernel<D, F16>, unsigned(kCtas * (kBlockRows / chunk_rows)), 32 * kJoinWarps, 0, stream, p, w, chunk_rows);
+  return launch_dependent(packed_join_kernel<D, F16>, unsigned(kCtas * kJoinChunks), 32 * kJoinWarps, 0, stream, p, w);
 }
 
 }  // namespace
 
-size_t packed_attn_workspace_bytes(const gdn_kv_dims& d, int64_t n_tokens) {
+size_t packed_attn_workspace_bytes(const gdn_kv_dims& d, int64_t) {
   size_t n = 0;
-  carve_packed(nullptr, d, n_tokens, &n);
+  carve_packed(nullptr, d, &n);
   return n;
 }
 
@@ -755,9 +821,11 @@ cudaError_t launch_packed_attn(const PackedAttnParams& p, cudaStream_t stream) {
   map(&maps.qt, p.q, 3, qd, qst, bt);
   map(&maps.qs, p.q, 3, qd, qst, bs);
   if (!ok) return cudaErrorInvalidValue;
-  const PackedWs w = carve_packed(p.ws, d, p.n_tokens, nullptr);
-  if (d.D == 128) return d.dtype ? launch<128, true>(p, w, box, maps, stream) : launch<128, false>(p, w, box, maps, stream);
-  return d.dtype ? launch<64, true>(p, w, box, maps, stream) : launch<64, false>(p, w, box, maps, stream);
+  const PackedWs w = carve_packed(p.ws, d, nullptr);
+  Cut cut{toks, 2 * toks, 0, p.causal};
+  while ((cut.toks << cut.period_log) % kTileKeys) ++cut.period_log;
+  if (d.D == 128) return d.dtype ? launch<128, true>(p, w, cut, box, maps, stream) : launch<128, false>(p, w, cut, box, maps, stream);
+  return d.dtype ? launch<64, true>(p, w, cut, box, maps, stream) : launch<64, false>(p, w, cut, box, maps, stream);
 }
 
 }  // namespace gdn
