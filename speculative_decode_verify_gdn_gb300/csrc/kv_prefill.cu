@@ -28,17 +28,21 @@ namespace gdn {
 
 namespace {
 
-constexpr int kJoinWarps = 8, kJoinChunks = 8;  // CTAs to a cut item
+constexpr int kJoinWarps = 8, kJoinChunks = 8;  // CTAs to a cut item of the tile kernel
+constexpr int kFewRows = 8;     // rows of a block of the kernel for few rows
+constexpr int kFewThreads = 128;
+constexpr int few_ctas(int D) { return D == 128 ? 3 : 4; }  // CTAs to an SM
+constexpr int few_workers(int D) { return kCtas * few_ctas(D) * (kFewThreads / 32); }
 
-struct JoinRec {       // a cut item, by the CTA c0 that it begins in; it ends in CTA c1
+struct JoinRec {       // a cut item, by the worker c0 that it begins with; it ends with worker c1
   int32_t tok0, rows;  // rows 0: there is none
   int32_t h, c0, c1, part0;
 };
 
 struct PackedWs {
-  JoinRec* join;     // [kCtas]
-  float* lse;        // [kCtas][2][kBlockRows] log2 units
-  float* o;          // [kCtas][2][kBlockRows][D]
+  JoinRec* join;     // [workers]
+  float* lse;        // [workers][2][rows] log2 units (kCtas workers with kBlockRows, or few_workers with kFewRows)
+  float* o;          // [workers][2][rows][D]
 };
 
 __host__ __device__ inline size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -47,8 +51,9 @@ __host__ __device__ inline PackedWs carve_packed(void* base, const gdn_kv_dims& 
   uint8_t* p = static_cast<uint8_t*>(base);
   size_t o = 0;
   const size_t parts = 2 * size_t(kBlockRows) * kCtas;
+  static_assert(few_workers(64) * kFewRows <= kBlockRows * kCtas && few_workers(64) >= few_workers(128), "room for either kernel's pieces");
   PackedWs w;
-  w.join = reinterpret_cast<JoinRec*>(p + o), o += round256(sizeof(JoinRec) * kCtas);
+  w.join = reinterpret_cast<JoinRec*>(p + o), o += round256(sizeof(JoinRec) * few_workers(64));
   w.lse = reinterpret_cast<float*>(p + o), o += round256(4 * parts);
   w.o = reinterpret_cast<float*>(p + o), o += 4 * parts * size_t(d.D);
   if (total) *total = o;
@@ -59,15 +64,18 @@ __host__ __device__ inline PackedWs carve_packed(void* base, const gdn_kv_dims& 
 // How the calls' rows are cut into blocks: all that depends on the heads alone.
 struct Cut {
   int tile_toks, toks;  // tokens of a row tile, of a block
+  int key_log;          // a tile has 2^key_log keys
   int period_log;       // after so many (2^period_log) blocks, their keys are a whole number of tiles more
   int causal;
+  int workers;          // that the tiles are dealt to
+  __host__ __device__ __forceinline__ long long tiles_of(long long keys) const { return (keys + (1 << key_log) - 1) >> key_log; }
 };
 
 struct SeqRows {
   int lo, n;       // its packed tokens
   int len;         // tokens in its slot
   int pre_slot, pre_keys;
-  __device__ __forceinline__ int pre_tiles() const { return (pre_keys + kTileKeys - 1) / kTileKeys; }
+  __device__ __forceinline__ int pre_tiles(const Cut& c) const { return int(c.tiles_of(pre_keys)); }
   __device__ __forceinline__ int blocks(const Cut& c) const { return int((unsigned(n) + unsigned(c.toks) - 1u) / unsigned(c.toks)); }
   // own keys that the last row of block k sees
   __device__ __forceinline__ int keys(const Cut& c, int k) const {
@@ -75,20 +83,20 @@ struct SeqRows {
     const long long e = (long long)len - n + (long long)c.toks * (k + 1);
     return e < 0 ? 0 : e < len ? int(e) : len;
   }
-  // Tiles of the first k blocks: sums of ceil(keys / 128), period by period.
+  // Tiles of the first k blocks: sums of their keys' tiles, period by period.
   __device__ __forceinline__ long long tiles(const Cut& c, int k) const {
-    const long long pre = (long long)pre_tiles() * k;
-    if (!c.causal) return pre + (long long)((len + kTileKeys - 1) / kTileKeys) * k;
+    const long long pre = c.tiles_of(pre_keys) * k;
+    if (!c.causal) return pre + c.tiles_of(len) * k;
     const long long off = (long long)len - n;
     const int i0 = off >= 0 ? 1 : int((unsigned long long)(-off) / unsigned(c.toks)) + 1;  // the first block with keys, counted from 1
     long long sum = 0;
     if (k >= i0) {
-      const long long m = (long long)k - i0 + 1, first = off + (long long)c.toks * i0 + kTileKeys - 1;
+      const long long m = (long long)k - i0 + 1, first = off + (long long)c.toks * i0 + (1 << c.key_log) - 1;
       const int period = 1 << c.period_log, rest = int(m & (period - 1));
-      const long long whole = m >> c.period_log, more = (long long)c.toks << c.period_log >> 7;  // (tiles that a period adds)
+      const long long whole = m >> c.period_log, more = (long long)c.toks << c.period_log >> c.key_log;  // (tiles that a period adds)
       long long one = 0, part = 0;
       for (int i = 0; i < period && i < m; ++i) {
-        const long long t = (first + (long long)c.toks * i) >> 7;
+        const long long t = (first + (long long)c.toks * i) >> c.key_log;
         one += t;
         if (i < rest) part += t;
       }
@@ -96,7 +104,7 @@ struct SeqRows {
     }
     if (k == blocks(c) && k > 0) {  // the last block is as long as it is
       const long long e = off + (long long)c.toks * k;
-      sum += (len + kTileKeys - 1) / kTileKeys - (e > 0 ? (e + kTileKeys - 1) >> 7 : 0);
+      sum += c.tiles_of(len) - (e > 0 ? c.tiles_of(e) : 0);
     }
     return pre + sum;
   }
@@ -129,29 +137,29 @@ __device__ __forceinline__ SeqRows load_sequence(const PackedAttnParams& p, int 
   return s;
 }
 
-// Every CTA plans for itself: each thread sums the tiles of a few consecutive sequences, the CTA the sums of its
-// threads, and the thread that has the first tile of the CTA's stretch among its own says in which sequence.
+// Every CTA plans for itself: each thread sums the tiles of a few consecutive sequences, and the CTA the sums of its
+// threads.  A worker then looks for the thread, and that thread's sequence, with the first tile of its stretch.
 struct Plan {
   long long head_tiles, tiles;  // of one kv head, and of all
-  long long into;               // the stretch begins so many tiles into
-  int32_t b, h;                 // sequence b, kv head h
-  int32_t ctas;                 // that the tiles are dealt to: each has one at least
+  int32_t workers;              // that the tiles are dealt to: each has one at least
   int32_t empty;                // some rows have no keys
-  // The deal gives CTA c tiles [begin(c), begin(c + 1)); the CTA of tile x.
-  __device__ __forceinline__ long long begin(long long c) const { return c * tiles / ctas; }
-  __device__ __forceinline__ int cta_of(long long x) const {
-    int c = int(float(x) * (float(ctas) / float(tiles)));  // (within one of it)
-    c = c < 0 ? 0 : c > ctas - 1 ? ctas - 1 : c;
-    while (c > 0 && begin(c) > x) --c;
-    while (c < ctas - 1 && begin(c + 1) <= x) ++c;
-    return c;
+  // The deal gives worker i tiles [begin(i), begin(i + 1)); the worker of tile x.
+  __device__ __forceinline__ long long begin(long long i) const { return i * tiles / workers; }
+  __device__ __forceinline__ int worker_of(long long x) const {
+    int i = int(float(x) * (float(workers) / float(tiles)));  // (within one of it)
+    i = i < 0 ? 0 : i > workers - 1 ? workers - 1 : i;
+    while (i > 0 && begin(i) > x) --i;
+    while (i < workers - 1 && begin(i + 1) <= x) ++i;
+    return i;
   }
 };
 
-__device__ __forceinline__ void make_plan(const PackedAttnParams& p, const Cut& cut, Plan& plan, long long* sums) {
+// before[i]: tiles of the sequences of the threads before thread i (T + 32 of them: sums of the warps behind).
+template <int T>
+__device__ __forceinline__ void make_plan(const PackedAttnParams& p, const Cut& cut, Plan& plan, long long* before) {
   const gdn_kv_dims& d = p.d;
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, cta = int(blockIdx.x);
-  const int each = (d.B + kTileThreads - 1) / kTileThreads;
+  const int each = (d.B + T - 1) / T;
   const int b0 = tid * each < d.B ? tid * each : d.B, b1 = b0 + each < d.B ? b0 + each : d.B;
   bool bad = tid == 0 && (p.cu[0] != 0 || p.cu[d.B] > p.n_tokens), empty = false;
   long long mine = 0;
@@ -169,41 +177,22 @@ __device__ __forceinline__ void make_plan(const PackedAttnParams& p, const Cut& 
     const long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
+  long long* const sums = before + T;
   if (lane == 31) sums[warp] = x;
   __syncthreads();
-  long long before = 0, all = 0;
+  long long sum = 0, all = 0;
 #pragma unroll
-  for (int i = 0; i < kTileThreads / 32; ++i) {
-    before += i < warp ? sums[i] : 0;
+  for (int i = 0; i < T / 32; ++i) {
+    sum += i < warp ? sums[i] : 0;
     all += sums[i];
   }
-  before += x - mine;
-  if (bad) all = 0;
-  Plan q;
-  q.head_tiles = all, q.tiles = all * d.Hkv;
-  q.ctas = int(q.tiles < kCtas ? q.tiles : kCtas);
-  q.empty = empty && !bad;
-  q.b = q.h = 0, q.into = 0;
-  if (tid == 0 && bad && cta == 0) atomicOr(p.err, kDevErrSeqlens);
-  if (cta >= q.ctas) {
-    if (tid == 0) plan = q;
-  } else {
-    const long long first = q.begin(cta);
-    q.h = int(first / q.head_tiles);
-    long long y = first - q.h * q.head_tiles;
-    if (y >= before && y < before + mine) {  // (one thread)
-      y -= before;
-      for (int b = b0; b < b1; ++b) {
-        const SeqRows s = load_sequence(p, b, false);
-        const long long t = s.tiles(cut, s.blocks(cut));
-        if (y < t) {
-          q.b = b, q.into = y;
-          break;
-        }
-        y -= t;
-      }
-      plan = q;
-    }
+  before[tid] = sum + x - mine;
+  if (tid == 0) {
+    if (bad) all = 0;
+    if (bad && cta == 0) atomicOr(p.err, kDevErrSeqlens);
+    plan.head_tiles = all, plan.tiles = all * d.Hkv;
+    plan.workers = int(plan.tiles < cut.workers ? plan.tiles : cut.workers);
+    plan.empty = empty && !bad;
   }
   __syncthreads();
 }
@@ -211,13 +200,13 @@ __device__ __forceinline__ void make_plan(const PackedAttnParams& p, const Cut& 
 // Outputs of rows without keys, whole blocks of them: 0 and -inf.
 __device__ __noinline__ void write_empty(const PackedAttnParams& p, const Cut& cut) {
   const gdn_kv_dims& d = p.d;
-  for (int b = int(blockIdx.x); b < d.B; b += kCtas) {
+  for (int b = int(blockIdx.x); b < d.B; b += int(gridDim.x)) {
     const SeqRows s = load_sequence(p, b, false);
     const long long rows = (long long)s.without_keys(cut) * d.Hq, first = (long long)s.lo * d.Hq;
     uint4* const out = reinterpret_cast<uint4*>(p.out + first * d.D);
-    for (long long k = threadIdx.x; k < rows * (d.D / 8); k += kTileThreads) out[k] = make_uint4(0u, 0u, 0u, 0u);
+    for (long long k = threadIdx.x; k < rows * (d.D / 8); k += blockDim.x) out[k] = make_uint4(0u, 0u, 0u, 0u);
     if (p.lse)
-      for (long long k = threadIdx.x; k < rows; k += kTileThreads) p.lse[first + k] = -INFINITY;
+      for (long long k = threadIdx.x; k < rows; k += blockDim.x) p.lse[first + k] = -INFINITY;
   }
 }
 
@@ -244,13 +233,14 @@ struct Seg {
   }
 };
 
-// Walks a CTA's stretch segment by segment (a converged warp).  Lane i knows sequence from + i.
+// Walks a worker's stretch segment by segment (a converged warp).  Lane i knows sequence from + i.
+template <int T, int ROWS>  // threads that planned, rows of a piece's partial results
 struct SegWalk {
   const PackedAttnParams& p;
   const PackedWs& w;
   const Cut& cut;
   const Plan& plan;
-  const int cta, lane, G;
+  const int id, lane, G;
   long long begin, x, end;
   int h, b, k, t_in;  // the item at hand: kv head, sequence, block; its tiles before x
   int from;
@@ -268,25 +258,41 @@ struct SegWalk {
     s.pre_keys = __shfl_sync(0xffffffffu, mine.pre_keys, l);
     return s;
   }
-  __device__ __forceinline__ SegWalk(const PackedAttnParams& p_, const PackedWs& w_, const Cut& cut_, const Plan& plan_, int lane_)
-      : p(p_), w(w_), cut(cut_), plan(plan_), cta(int(blockIdx.x)), lane(lane_), G(p_.d.Hq / p_.d.Hkv) {
+  __device__ __forceinline__ SegWalk(const PackedAttnParams& p_, const PackedWs& w_, const Cut& cut_, const Plan& plan_,
+                                     const long long* before, int id_, int lane_)
+      : p(p_), w(w_), cut(cut_), plan(plan_), id(id_), lane(lane_), G(p_.d.Hq / p_.d.Hkv) {
     begin = x = end = 0;
     h = b = k = t_in = 0;
     from = -64;
-    if (lane == 0) w.join[cta].rows = 0;
-    if (cta >= plan.ctas) return;
-    begin = x = plan.begin(cta), end = plan.begin(cta + 1);
-    h = plan.h, b = plan.b;
+    if (lane == 0) w.join[id].rows = 0;
+    if (id >= plan.workers) return;
+    begin = x = plan.begin(id), end = plan.begin(id + 1);
+    h = int(begin / plan.head_tiles);
+    long long y = begin - h * plan.head_tiles;
+    // the last thread, and then its last sequence, with at most y tiles before it
+    int at = 0;
+    for (int n = T, step = T / 32; step > 0; n = step, step = step / 32 > 0 ? step / 32 : step > 1 ? 1 : 0) {
+      const uint32_t some = __ballot_sync(0xffffffffu, lane * step < n && before[at + lane * step] <= y);
+      at += (31 - __clz(int(some))) * step;
+    }
+    y -= before[at];
+    const int each = (p.d.B + T - 1) / T;
+    for (b = at * each; b < p.d.B - 1; ++b) {
+      const SeqRows s = sequence(b);
+      const long long t = s.tiles(cut, s.blocks(cut));
+      if (y < t) break;
+      y -= t;
+    }
     const SeqRows s = sequence(b);
-    int n = s.blocks(cut);  // the last block with at most `into` tiles before it, 32 at a time
+    int n = s.blocks(cut);  // its last block with at most y tiles before it, 32 at a time
     while (n > 1) {
       const int step = (n + 31) / 32, i = lane * step;
-      const uint32_t at_or_before = __ballot_sync(0xffffffffu, i < n && s.tiles(cut, k + i) <= plan.into);
-      const int j = 31 - __clz(int(at_or_before));
+      const uint32_t some = __ballot_sync(0xffffffffu, i < n && s.tiles(cut, k + i) <= y);
+      const int j = 31 - __clz(int(some));
       k += j * step;
       n = n - j * step < step ? n - j * step : step;
     }
-    t_in = int(plan.into - s.tiles(cut, k));
+    t_in = int(y - s.tiles(cut, k));
   }
   __device__ __forceinline__ bool next(Seg& g) {
     if (x >= end) return false;
@@ -297,7 +303,7 @@ struct SegWalk {
         ++b, k = 0;
         continue;
       }
-      const int pre = s.pre_tiles(), keys = s.keys(cut, k), tiles = pre + (keys + kTileKeys - 1) / kTileKeys;
+      const int pre = s.pre_tiles(cut), keys = s.keys(cut, k), tiles = pre + int(cut.tiles_of(keys));
       if (tiles == 0) {
         ++k;
         continue;
@@ -310,10 +316,10 @@ struct SegWalk {
       g.t0 = t_in;
       g.t1 = end - x < tiles - t_in ? t_in + int(end - x) : tiles;
       g.parity = int(x & 1);
-      const int second = x == begin ? 0 : 1;  // (of the CTA's pieces: one that its stretch begins with, one that it ends with)
-      g.part = g.t0 == 0 && g.t1 == tiles ? -1 : (2 * cta + second) * kBlockRows;
+      const int second = x == begin ? 0 : 1;  // (of the worker's pieces: one that its stretch begins with, one that it ends with)
+      g.part = g.t0 == 0 && g.t1 == tiles ? -1 : (2 * id + second) * ROWS;
       if (g.t0 == 0 && g.t1 < tiles && lane == 0)
-        w.join[cta] = JoinRec{g.tok0, g.rows, h, cta, plan.cta_of(x + tiles - 1), g.part};
+        w.join[id] = JoinRec{g.tok0, g.rows, h, id, plan.worker_of(x + tiles - 1), g.part};
       x += g.t1 - g.t0;
       t_in = 0, ++k;  // (an item that goes on ends the stretch)
       return true;
@@ -365,7 +371,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t tmem = tmem_slot;
   pdl_launch_dependents();
   pdl_wait();
-  make_plan(p, cut, plan, reinterpret_cast<long long*>(merge_ml));
+  long long* const before = reinterpret_cast<long long*>(smem + L::OFF_SEG - 8 * 1024);  // (in the ring's last slot, which fills after the plan)
+  make_plan<kTileThreads>(p, cut, plan, before);
+  fence_proxy_async_smem();
   if (plan.empty) write_empty(p, cut);
 
   // Bounded wait of a whole warp, which goes on or gives up together; once one warp has given up, all of the
@@ -629,7 +637,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // As in kv_attn.cu: segments go out as the ring has room, and a segment's queries as soon as the products with
     // the ones before are done.  Queries come by TMA, whole tokens of G heads: rows behind the block's last hold
     // other tokens' queries or what was there, and nothing reads their results.
-    SegWalk walk(p, w, cut, plan, lane);
+    SegWalk<kTileThreads, kBlockRows> walk(p, w, cut, plan, before, int(blockIdx.x), lane);
     uint32_t k = 0, kq = 0;      // segments handed on; segment whose queries are next
     uint32_t nq0 = 0, nq1 = 0;   // segments of each stream
     int part = 0;                // of segment kq: its first or second stream
@@ -697,21 +705,239 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
 }
 
-// ---------------------------------------------------------------- join
-// kJoinChunks CTAs for each CTA of the tile kernel, if a cut item begins in its stretch: a warp takes a row at a time,
-// its pieces' log-sum-exps and, on their way with them, the first pieces' sums.
+// ---------------------------------------------------------------- few rows
+// Where sequences have about eight rows to a kv head or fewer (single tokens, with their heads), a tile of 128 rows is all
+// padding and its chain of products, not the memory, sets the pace (64 single tokens over 1..1500 keys: 74 us with it).
+// Here a block is up to 8 rows, and a warp is a worker by itself: it takes 16 keys at a time (D = 64: 32), straight from
+// memory into the registers that the warp-wide products (m16n8k16) read, and no shared memory or barrier is in the way.
+// The elements of a head and the keys are summed in an order of the lanes' own, so that each lane's operands are
+// 16 bytes that lie together:
+//   S = Q K^T: lane (n, j) = (lane / 4, lane % 4) holds elements 32 c + 8 j .. + 7 of query n and of key n (and n + 8);
+//   O^T = V^T P^T: it holds elements 64 c + 8 n .. + 7 of keys 2 j, 2 j + 1, 2 j + 8, 2 j + 9 - the keys whose scores of
+//   row n it has from S - and gets elements 64 c + 8 n .. + 7 of rows 2 j and 2 j + 1.
+// Keys of the round to come are fetched as soon as the products have read the ones before, and values likewise, so that
+// one or the other is always on its way.  Bound: HBM.
+template <bool F16>
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 load16(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
 template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kJoinWarps) packed_join_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w) {
+__global__ void __launch_bounds__(kFewThreads, few_ctas(D))
+    packed_few_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w, const __grid_constant__ Cut cut, const uint32_t page_inv) {
+  constexpr int CK = D / 32, CV = D / 64, H16 = D == 64 ? 2 : 1;  // parts of a key and of a value, 16s of keys in a round
+  constexpr int ROUNDS = 2 / H16;                                 // to a tile of 32 keys
+  __shared__ Plan plan;
+  __shared__ long long before[kFewThreads + 32];
+  pdl_launch_dependents();
+  pdl_wait();
+  make_plan<kFewThreads>(p, cut, plan, before);
+  if (plan.empty) write_empty(p, cut);
+  const gdn_kv_dims& d = p.d;
+  const int lane = threadIdx.x & 31, n = lane >> 2, j = lane & 3, G = d.Hq / d.Hkv;
+  // (neighbours of a stretch on different SMs: the last stretches of a short list are not all on a few)
+  SegWalk<kFewThreads, kFewRows> walk(p, w, cut, plan, before, int(threadIdx.x >> 5) * int(gridDim.x) + int(blockIdx.x), lane);
+  const float c = p.scale * kLog2e;
+  Seg seg;
+  while (walk.next(seg)) {
+    const int rows = seg.rows, tiles = seg.t1 - seg.t0;
+    // queries: zeros in rows that the block has not
+    uint32_t q[CK][4];
+#pragma unroll
+    for (int i = 0; i < CK; ++i) {
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (n < rows) x = load16(p.q + (long long)(seg.tok0 + n / G) * d.q_token_stride + (seg.h * G + n % G) * D + 32 * i + 8 * j);
+      q[i][0] = x.x, q[i][1] = x.y, q[i][2] = x.z, q[i][3] = x.w;
+    }
+    const int lim = seg.lim + (cut.causal ? n / G : 0);  // own keys that row n sees
+    // Places of 16 tiles' keys: lane 2 i + e has those of keys 16 e .. 16 e + 15 of tile i
+    long long place = 0;
+    auto look_up = [&](int t) {
+      const int mine = t + (lane >> 1);
+      if (mine < seg.t1) {
+        const bool own = mine >= seg.pre_tiles;
+        const int token = (own ? mine - seg.pre_tiles : mine) * 32 + 16 * (lane & 1);
+        if (token < (own ? seg.keys : seg.pre_keys)) {
+          const int col = page_column(token, page_inv);
+          int page = p.table[(long long)(own ? seg.slot : seg.pre_slot) * d.max_pages + col];
+          if (page < 0 || page >= d.n_pages) {
+            atomicOr(p.err, GDN_DEVERR_KV_PAGE);
+            page = 0;
+          }
+          place = page * d.cache_page_stride + (token - col * d.page_size) * d.cache_token_stride + seg.h * d.cache_head_stride;
+        }
+      }
+    };
+    // keys of round r that some row sees (may exceed the round's)
+    auto left_of = [&](int r) {
+      const int t = seg.t0 + r / ROUNDS, in = r % ROUNDS * 16;
+      return t >= seg.pre_tiles ? seg.keys - 32 * (t - seg.pre_tiles) - in : seg.pre_keys - 32 * t - in;
+    };
+    auto place_of = [&](int r, int half) {
+      return __shfl_sync(0xffffffffu, place, (r / ROUNDS & 15) * 2 + (ROUNDS == 2 ? r & 1 : half));
+    };
+    uint4 kx[H16][2][CK], vx[H16][4][CV];
+    auto fetch_keys = [&](int r) {
+      const int left = left_of(r);
+#pragma unroll
+      for (int e = 0; e < H16; ++e) {
+        const long long at = place_of(r, e);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < CK; ++i)
+            kx[e][u][i] = 16 * e < left ? load16(p.k_cache + at + (8 * u + n) * d.cache_token_stride + 32 * i + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    auto fetch_values = [&](int r) {
+      const int left = left_of(r);
+#pragma unroll
+      for (int e = 0; e < H16; ++e) {
+        const long long at = place_of(r, e);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int key = 2 * j + (u & 1) + 8 * (u >> 1);
+#pragma unroll
+          for (int i = 0; i < CV; ++i)  // (values behind the last key may be anything, and 0 x NaN is NaN)
+            vx[e][u][i] = 16 * e + key < left ? load16(p.v_cache + at + key * d.cache_token_stride + 64 * i + 8 * n) : make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    };
+    float o[CV][4][4];
+#pragma unroll
+    for (int i = 0; i < CV; ++i)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[i][t][x] = 0.f;
+    float m = -INFINITY, l = 0.f;  // of row n: running maximum (log2 units), this lane's part of the sum
+    const int rounds = tiles * ROUNDS;
+    look_up(seg.t0);
+    fetch_keys(0);
+    fetch_values(0);
+#pragma unroll 1
+    for (int r = 0; r < rounds; ++r) {
+      const int t = seg.t0 + r / ROUNDS;
+      float sc[2 * H16][4];
+#pragma unroll
+      for (int e = 0; e < H16; ++e)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float (&x)[4] = sc[2 * e + u];
+          x[0] = x[1] = x[2] = x[3] = 0.f;
+#pragma unroll
+          for (int i = 0; i < CK; ++i) {
+            mma_16x8x16<F16>(x, q[i][0], 0u, q[i][1], 0u, kx[e][u][i].x, kx[e][u][i].y);
+            mma_16x8x16<F16>(x, q[i][2], 0u, q[i][3], 0u, kx[e][u][i].z, kx[e][u][i].w);
+          }
+        }
+      const bool more = r + 1 < rounds;
+      const bool own = t >= seg.pre_tiles;
+      const int sees = (own ? lim - 32 * (t - seg.pre_tiles) : seg.pre_keys - 32 * t) - r % ROUNDS * 16;  // keys of this round that row n sees
+      if (more) {
+        // (a round's places: the values of the last round of 16 tiles are on their way already)
+        if ((r + 1) % (16 * ROUNDS) == 0) look_up(seg.t0 + (r + 1) / ROUNDS);
+        fetch_keys(r + 1);
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 2 * H16; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sc[i][e] = 8 * i + 2 * j + e < sees ? sc[i][e] * c : -INFINITY;
+          top = fmaxf(top, sc[i][e]);
+        }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const bool move = top > m && !(top - m <= kLag);  // (m = -inf: infinitely far)
+      if (__any_sync(0xffffffffu, move)) {
+        const float f = move ? exp2_fast(m - top) : 1.f;
+        if (move) m = top;
+        l *= f;
+        const float f0 = __shfl_sync(0xffffffffu, f, 8 * j), f1 = __shfl_sync(0xffffffffu, f, 8 * j + 4);  // of rows 2 j, 2 j + 1
+#pragma unroll
+        for (int i = 0; i < CV; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[i][x][0] *= f0, o[i][x][1] *= f1, o[i][x][2] *= f0, o[i][x][3] *= f1;
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int e = 0; e < H16; ++e) {
+        uint32_t pr[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float w0 = exp2_fast(sc[2 * e + u][0] - base), w1 = exp2_fast(sc[2 * e + u][1] - base);
+          l += w0 + w1;
+          pr[u] = pack2<F16>(w0, w1);
+        }
+#pragma unroll
+        for (int i = 0; i < CV; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {  // elements 64 i + 8 n + 2 x and the one behind
+            const uint32_t w0 = word(vx[e][0][i], x), w1 = word(vx[e][1][i], x), w2 = word(vx[e][2][i], x), w3 = word(vx[e][3][i], x);
+            mma_16x8x16<F16>(o[i][x], __byte_perm(w0, w1, 0x5410), __byte_perm(w0, w1, 0x7632), __byte_perm(w2, w3, 0x5410),
+                             __byte_perm(w2, w3, 0x7632), pr[0], pr[1]);
+          }
+      }
+      if (more) fetch_values(r + 1);
+    }
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    const float inv = l == 0.f ? 0.f : 1.f / l, e = l == 0.f ? -INFINITY : m + log2f(l);
+    const int tok = n / G;
+    if (j == 0 && n < rows) {
+      if (seg.part >= 0)
+        w.lse[seg.part + n] = e;
+      else if (p.lse)
+        p.lse[(long long)(seg.tok0 + tok) * d.Hq + seg.h * G + (n - tok * G)] = e * kLn2;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {  // rows 2 j and 2 j + 1
+      const int r = 2 * j + u, rt = r / G;
+      const float f = __shfl_sync(0xffffffffu, inv, 4 * r);
+      if (r < rows) {
+#pragma unroll
+        for (int i = 0; i < CV; ++i) {
+          float y[8];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) y[2 * x] = o[i][x][u] * f, y[2 * x + 1] = o[i][x][2 + u] * f;
+          if (seg.part >= 0)
+            store8(w.o + (long long)(seg.part + r) * D + 64 * i + 8 * n, y);
+          else
+            *reinterpret_cast<uint4*>(p.out + ((long long)(seg.tok0 + rt) * d.Hq + seg.h * G + (r - rt * G)) * D + 64 * i + 8 * n) =
+                make_uint4(pack2<F16>(y[0], y[1]), pack2<F16>(y[2], y[3]), pack2<F16>(y[4], y[5]), pack2<F16>(y[6], y[7]));
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- join
+// `chunks` CTAs for each worker, if a cut item begins in its stretch: a warp takes a row at a time, its pieces'
+// log-sum-exps and, on their way with them, the first pieces' sums.
+template <int D, bool F16, int ROWS>
+__global__ void __launch_bounds__(32 * kJoinWarps) packed_join_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w, const int chunks) {
   constexpr int N = D / 32, U = 4;
   pdl_launch_dependents();
   pdl_wait();
   const gdn_kv_dims& d = p.d;
-  const JoinRec rec = w.join[blockIdx.x % kCtas];
+  const JoinRec rec = w.join[blockIdx.x / unsigned(chunks)];
   const int G = d.Hq / d.Hkv, lane = threadIdx.x & 31;
   const int parts = rec.rows > 0 ? rec.c1 - rec.c0 + 1 : 0;
-  for (int r = int(blockIdx.x / kCtas) * kJoinWarps + int(threadIdx.x >> 5); r < rec.rows; r += kJoinWarps * kJoinChunks) {
-    // piece j's row: the first CTA's piece, then the one that each stretch begins with
-    auto at = [&](int j) { return (j == 0 ? rec.part0 : 2 * (rec.c0 + j) * kBlockRows) + r; };
+  for (int r = int(blockIdx.x % unsigned(chunks)) * kJoinWarps + int(threadIdx.x >> 5); r < rec.rows; r += kJoinWarps * chunks) {
+    // piece j's row: the first worker's piece, then the one that each stretch begins with
+    auto at = [&](int j) { return (j == 0 ? rec.part0 : 2 * (rec.c0 + j) * ROWS) + r; };
     float acc[N], v[U][N];
     auto load = [&](int j0, int end) {
 #pragma unroll
@@ -781,7 +1007,21 @@ cudaError_t launch(const PackedAttnParams& p, const PackedWs& w, const Cut& cut,
   }
   e = launch_dependent(packed_tile_kernel<D, F16>, unsigned(kCtas), kTileThreads, L::TOTAL, stream, p, w, cut, box, page_units_inv(p.d.page_size), maps);
   if (e != cudaSuccess) return e;
-  return launch_dependent(packed_join_kernel<D, F16>, unsigned(kCtas * kJoinChunks), 32 * kJoinWarps, 0, stream, p, w);
+  return launch_dependent(packed_join_kernel<D, F16, kBlockRows>, unsigned(kCtas * kJoinChunks), 32 * kJoinWarps, 0, stream, p, w, kJoinChunks);
+}
+
+template <int D, bool F16>
+cudaError_t launch_few(const PackedAttnParams& p, const PackedWs& w, const Cut& cut, cudaStream_t stream) {
+  const cudaError_t e = launch_dependent(packed_few_kernel<D, F16>, unsigned(kCtas * few_ctas(D)), kFewThreads, 0, stream, p, w, cut, page_units_inv(p.d.page_size));
+  if (e != cudaSuccess) return e;
+  return launch_dependent(packed_join_kernel<D, F16, kFewRows>, unsigned(cut.workers), 32 * kJoinWarps, 0, stream, p, w, 1);
+}
+
+// How rows are cut into blocks of `toks` tokens, and keys into tiles of 2^key_log, dealt to so many workers.
+Cut make_cut(int tile_toks, int toks, int key_log, int causal, int workers) {
+  Cut c{tile_toks, toks, key_log, 0, causal, workers};
+  while ((c.toks << c.period_log) % (1 << key_log)) ++c.period_log;
+  return c;
 }
 
 }  // namespace
@@ -795,6 +1035,13 @@ size_t packed_attn_workspace_bytes(const gdn_kv_dims& d, int64_t) {
 cudaError_t launch_packed_attn(const PackedAttnParams& p, cudaStream_t stream) {
   const gdn_kv_dims& d = p.d;
   const int G = d.Hq / d.Hkv, toks = kTileRows / G;
+  const PackedWs w = carve_packed(p.ws, d, nullptr);
+  if (G <= kFewRows && (long long)p.n_tokens * G <= (long long)kFewRows * d.B) {
+    const int few = kFewRows / G;
+    const Cut cut = make_cut(few, few, 5, p.causal, few_workers(d.D));
+    if (d.D == 128) return d.dtype ? launch_few<128, true>(p, w, cut, stream) : launch_few<128, false>(p, w, cut, stream);
+    return d.dtype ? launch_few<64, true>(p, w, cut, stream) : launch_few<64, false>(p, w, cut, stream);
+  }
   const EncodeTiled encode = encoder();
   if (!encode) return cudaErrorNotSupported;
   // Tokens per copy of a full tile: as many as lie together in a page, a divisor of the tile's 128.
@@ -813,17 +1060,19 @@ cudaError_t launch_packed_attn(const PackedAttnParams& p, cudaStream_t stream) {
   const cuuint32_t b16[5] = {64, 16, 1, 1, 1}, bb[5] = {64, cuuint32_t(box), 1, 1, 1};
   map(&maps.few[0], p.k_cache, 5, cd, cs, b16);
   map(&maps.few[1], p.v_cache, 5, cd, cs, b16);
-  map(&maps.many[0], p.k_cache, 5, cd, cs, bb);
-  map(&maps.many[1], p.v_cache, 5, cd, cs, bb);
+  if (box > 16) {
+    map(&maps.many[0], p.k_cache, 5, cd, cs, bb);
+    map(&maps.many[1], p.v_cache, 5, cd, cs, bb);
+  } else {
+    maps.many[0] = maps.few[0], maps.many[1] = maps.few[1];
+  }
   const cuuint64_t qd[3] = {cuuint64_t(d.D), cuuint64_t(d.Hq), cuuint64_t(p.n_tokens)};
   const cuuint64_t qst[2] = {2ull * d.D, 2ull * d.q_token_stride};
   const cuuint32_t bt[3] = {64, cuuint32_t(G), cuuint32_t(toks)}, bs[3] = {64, cuuint32_t(G), cuuint32_t(toks < kFewToks ? toks : kFewToks)};
   map(&maps.qt, p.q, 3, qd, qst, bt);
   map(&maps.qs, p.q, 3, qd, qst, bs);
   if (!ok) return cudaErrorInvalidValue;
-  const PackedWs w = carve_packed(p.ws, d, nullptr);
-  Cut cut{toks, 2 * toks, 0, p.causal};
-  while ((cut.toks << cut.period_log) % kTileKeys) ++cut.period_log;
+  const Cut cut = make_cut(toks, 2 * toks, 7, p.causal, kCtas);
   if (d.D == 128) return d.dtype ? launch<128, true>(p, w, cut, box, maps, stream) : launch<128, false>(p, w, cut, box, maps, stream);
   return d.dtype ? launch<64, true>(p, w, cut, box, maps, stream) : launch<64, false>(p, w, cut, box, maps, stream);
 }

@@ -262,3 +262,48 @@ def test_many_sequences(B):
     new = np.where(rng.random(B) < 0.3, 0, rng.integers(0, 4, B))
     run_case(19, new, lens, 2, True, prefixes=[30], pre=np.where(rng.random(B) < 0.5, B, -1), Hkv=1, D=64)
     run_case(20, np.minimum(new, 1), lens, 2, False, Hkv=1, D=64)
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 7, 8])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("D,dtype,ps", [(64, HF, 16), (64, BF, 48), (128, BF, 64), (128, HF, 80)])
+def test_few_rows(G, causal, D, dtype, ps):
+    """At most about eight rows a sequence and kv head: single tokens and a few more, beside sequences without any,
+    over lengths around the units of keys, behind prefixes and without, with more tokens than keys."""
+    lens = [1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 100, 129, 0, 2, 517, 40]
+    new = [1] * len(lens)
+    new[3], new[5], new[12], new[13], new[8] = 0, 2, 1, 2, 0
+    if G <= 2:
+        new[10] = 3
+    pre = [16, -1, 17, 16, -1] * 3 + [18]
+    run_case(30 + G, new, lens, 2 * G, causal, prefixes=[33, 0, 300], pre=pre, D=D, dtype=dtype, ps=ps, spare_rows=2)
+    run_case(50 + G, [1, 2, 0, 5] if G == 1 else [1, 0, 1, 1], [1, 1, 0, 3], G, causal, Hkv=1, D=D, dtype=dtype, ps=ps)
+    pool, cu, q, out, lse = run_case(70 + G, [1, 1], [3000, 7], 3 * G, causal, Hkv=3, D=D, dtype=dtype, ps=ps, order="hnd")
+    again = attend(pool, cu, q, causal)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("ps", [16, 64])
+def test_few_rows_of_many_sequences(ps):
+    """More pieces than workers, and stretches of whole items."""
+    rng = np.random.default_rng(ps)
+    lens = rng.integers(0, 200, 400)
+    run_case(80, np.ones(400, dtype=int), lens, 8, False, Hkv=8, D=64, ps=ps, dtype=HF)
+    run_case(81, np.ones(400, dtype=int), lens, 8, True, Hkv=2, D=128, ps=ps, prefixes=[70], pre=[400] * 400)
+
+
+def test_what_few_rows_do_not_see_may_hold_anything():
+    pool = Pool(82, [70, 33, 200], D=128, ps=32)
+    q = pool.gauss((4, 4, 128), 2.0)
+    cu = [0, 2, 3, 4]
+    want = attend(pool, cu, q, True)
+    page, row = pool.table[0, 69 // 32], 69 % 32       # the last token's key: seen by the last row alone
+    for bad in (NAN, float("inf"), -float("inf")):
+        pool.k[0, page, row] = bad
+        got = attend(pool, cu, q, True)
+        assert all(torch.equal(a[:1], b[:1]) and torch.equal(a[2:], b[2:]) for a, b in zip(want, got)), bad
+    table = pool.table.copy()
+    table[1, 1] = 1 << 27
+    got = attend(pool, cu, q, True, table=table)
+    assert gdn.gdn_device_status(clear=True) == kv.DEVERR_KV_PAGE
+    assert all(torch.equal(a[:1], b[:1]) and torch.equal(a[3:], b[3:]) for a, b in zip(want, got))
