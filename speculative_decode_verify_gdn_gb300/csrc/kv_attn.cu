@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int G = d.Hq / d.Hkv;
 
   if (tid == 0) {
-    init_tile_bars<NS>(bars);
+    init_tile_bars<NS>(bars, 2);
     turns[0] = turns[1] = 0;
     gave_up = 0;
     fence_mbar_init();
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             uint32_t see = n_seen >= 32 ? 0xffffffffu : n_seen <= 0 ? 0u : (1u << n_seen) - 1u;
             if (seg.own && (wu >> 5) == 2 * q + g) see |= seen << (wu & 31);
             return see;
-          }, m, l);
+          }, [] {}, m, l);  // (a tile's scores come behind the products of the tile before)
         }
         first = false;
         if (cached < kTileKeys && (seg.own || (cached & 15))) {

@@ -336,6 +336,115 @@ struct PackedMaps {
 };
 constexpr int kFewToks = 4;
 
+// At D = 64 tensor memory has room for a third tile of scores, and the products of a stream's next scores need not wait
+// until its probabilities have been multiplied: that wait, and not the tensor core or the softmax, sets the pace otherwise
+// (a pair of tiles in 1.55 us without it).  All uses of the tensor core are in one order, n = 0, 1, 2, ..: a tile's scores
+// of stream 0 and of stream 1, or a stream's alone; use n has buffer n % 3.  One warp issues
+//   S(0) S(1) S(2) O(0) S(3) O(1) S(4) ..
+// Barriers: s_ready, a stream's i-th use on its barrier i % 4 (three uses may be under way that the stream's softmax
+// has not looked at yet; a fourth one comes behind products that need its probabilities); p_ready by buffer, and the
+// issuing warp sees every phase of it; o_step, a stream's sums after each tile, for a softmax that has to rescale them; a
+// tile's slots are released once.
+template <int D>
+struct Ahead {
+  static constexpr bool ON = D == 64;
+  static constexpr int BUFFERS = 3;
+  static __device__ __forceinline__ uint32_t o_col(int s) { return ON ? 384u + 64u * uint32_t(s) : tmem_o(s); }
+};
+struct AheadBars {
+  uint64_t s_ready[2][4], p_ready[3], o_step[2];
+};
+template <int D, bool F16, typename Wait>
+__device__ __forceinline__ void tensor_warp_ahead(const int lane, const uint32_t tmem, const uint32_t base, const bool negative,
+                                                  const Seg* const segs, const TileBars& bars, AheadBars& ahead, Wait wait_warp) {
+  using L = TileLayout<D, Seg>;
+  constexpr int NS = L::STAGES, NB = Ahead<D>::BUFFERS;
+  const uint32_t tm = uniform(tmem);
+  const uint32_t values_idesc = idesc_f16<F16>(kTileKeys, D) | (1u << 16);  // B (values) MN-major
+  const uint32_t scores_idesc = negative ? 1u << 13 : 0u;                   // a negative scale negates the queries
+  struct Use {
+    uint32_t units, slot, phase, flags;  // its values' slot; flags: 1 stream, 2 first of the stream's sums, 4 last, 8 the slot's last
+  };
+  Use u0{}, u1{}, u2{};  // whose O += P V is still to be issued, the eldest first
+  uint32_t pending = 0;
+  uint32_t n_buf = 0, p_buf = 0, p_phase = 0;  // buffer of the next scores; of the eldest pending use, and its phase
+  uint32_t slot = 0, phase = 0;                // of a tile's keys; its values are in the slot behind
+  uint32_t uses0 = 0, uses1 = 0, nq0 = 0, nq1 = 0;  // scores and segments of each stream
+  bool ok = true;
+  auto values = [&]() {  // O += P V of the eldest
+    ok = wait_warp(bars.full + u0.slot, u0.phase) && wait_warp(ahead.p_ready + p_buf, p_phase);
+    if (!ok) return;
+    tc_fence_after();
+    const uint32_t s = u0.flags & 1u, to = tm + Ahead<D>::o_col(int(s)), ts = tm + 128u * p_buf;
+    const uint32_t db = swizzled_desc_lo(base + L::OFF_RING + u0.slot * L::BYTES, L::HALF);
+    umma_values_first(to, ts, db, values_idesc, u0.flags & 2u ? 0u : 1u);
+    if (u0.units == 8) {
+      umma_values_rest(to, ts, db, values_idesc);
+    } else {
+#pragma unroll 1
+      for (uint32_t u = 1; u < u0.units; ++u) umma_values_first(to, ts + 8 * u, db + 128 * u, values_idesc, 1);
+    }
+    umma_commit_one(ahead.o_step + s);
+    if (u0.flags & 8u) umma_commit_one(bars.empty + u0.slot);
+    if (u0.flags & 4u) umma_commit_one(bars.o_done + s);
+    u0 = u1, u1 = u2, --pending;
+    if (++p_buf == NB) p_buf = 0, p_phase ^= 1;
+  };
+  for (uint32_t k = 0; ok; ++k) {
+    const Seg& seg = segs[k % kSegRing];
+    if (!wait_warp(bars.seg_full + k % kSegRing, (k / kSegRing) & 1)) {
+      ok = false;
+      break;
+    }
+    const int t0 = int(uniform(uint32_t(seg.t0))), t1 = int(uniform(uint32_t(seg.t1)));
+    const auto tiles = seg.tiles();
+    const uint32_t parity = uniform(uint32_t(seg.parity));
+    const bool paired = uniform(seg.paired() ? 1u : 0u) != 0;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars.seg_empty + k % kSegRing);
+    if (t1 < 0) break;
+#pragma unroll 1
+    for (int t = t0; ok && t < t1; ++t) {
+      const uint32_t vslot = slot + 1 < NS ? slot + 1 : 0, vphase = slot + 1 < NS ? phase : phase ^ 1;
+      const uint32_t units = uint32_t(tiles.units(t));
+      const bool first = paired ? t == t0 : t - t0 < 2, last = paired ? t == t1 - 1 : t1 - t <= 2;
+#pragma unroll 1
+      for (uint32_t i = 0; i < (paired ? 2u : 1u); ++i) {
+        const uint32_t s = paired ? i : (parity + uint32_t(t - t0)) & 1u;
+        const bool slot_last = !paired || i == 1;
+        if (pending == NB) values();
+        if (ok && first) ok = wait_warp(bars.q_ready + s, (s ? nq1 : nq0) & 1);
+        ok = ok && wait_warp(bars.full + slot, phase);
+        if (!ok) break;
+        tc_fence_after();
+        umma_scores<D>(tm + 128u * n_buf, swizzled_desc_lo(base + L::OFF_Q + s * L::BYTES, 16),
+                       swizzled_desc_lo(base + L::OFF_RING + slot * L::BYTES, 16), idesc_f16<F16>(kTileKeys, int(16 * units)) | scores_idesc);
+        umma_commit_one(&ahead.s_ready[s][(s ? uses1 : uses0) & 3]);
+        if (slot_last) umma_commit_one(bars.empty + slot);
+        if (last) umma_commit_one(bars.q_free + s);
+        if (first) nq0 += s ^ 1, nq1 += s;
+        uses0 += s ^ 1, uses1 += s;
+        const Use u{units, vslot, vphase, s | (first ? 2u : 0u) | (last ? 4u : 0u) | (slot_last ? 8u : 0u)};
+        if (pending == 0)
+          u0 = u;
+        else if (pending == 1)
+          u1 = u;
+        else
+          u2 = u;
+        ++pending;
+        if (++n_buf == NB) n_buf = 0;
+      }
+      slot += 2, phase ^= slot >= NS ? 1u : 0u, slot -= slot >= NS ? NS : 0;
+    }
+  }
+  while (ok && pending > 0) values();
+  if (!ok) {  // what is under way finishes before tensor memory is freed
+    umma_commit_one(bars.o_done);
+    mbar_drain(bars.o_done, 0);
+    mbar_drain(bars.o_done, 1);
+  }
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(kTileThreads, 1)
     packed_tile_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w, const __grid_constant__ Cut cut, const int box,
@@ -348,6 +457,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __shared__ volatile uint32_t gave_up, turns[2];  // (turns: taken so far by each tensor-core warp)
   __shared__ uint64_t merge_bar;                   // the two softmax groups, at the end of a segment that they share
   __shared__ Plan plan;
+  __shared__ AheadBars ahead;
   __shared__ float2 merge_ml[kTileRows];           // maximum (log2 units) and sum of a row, one stream's and then the other's
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
@@ -358,8 +468,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int G = d.Hq / d.Hkv, tile_toks = cut.tile_toks, tile_rows = tile_toks * G;
 
   if (tid == 0) {
-    init_tile_bars<NS>(bars);
+    init_tile_bars<NS>(bars, Ahead<D>::ON ? 1 : 2);
     mbar_init(&merge_bar, 2 * kGroupThreads);
+    if (Ahead<D>::ON) {
+      for (int i = 0; i < 8; ++i) mbar_init(&ahead.s_ready[i / 4][i % 4], 1);
+      for (int i = 0; i < 3; ++i) mbar_init(ahead.p_ready + i, kGroupThreads);
+      for (int i = 0; i < 2; ++i) mbar_init(ahead.o_step + i, 1);
+    }
     turns[0] = turns[1] = 0;
     gave_up = 0;
     fence_mbar_init();
@@ -473,14 +588,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!ok) mbar_drain(bars.full + use % NS, (use / NS) & 1);
     }
   } else if (warp == 9 || warp == 10) {
-    tensor_warp<D, F16>(warp - 9, lane, tmem, base, p.scale < 0.f, segs, bars, turns, wait_warp);
+    if (!Ahead<D>::ON)
+      tensor_warp<D, F16>(warp - 9, lane, tmem, base, p.scale < 0.f, segs, bars, turns, wait_warp);
+    else if (warp == 9)
+      tensor_warp_ahead<D, F16>(lane, tmem, base, p.scale < 0.f, segs, bars, ahead, wait_warp);
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax: stream s, one row per thread
     const int s = warp >> 2, r = tid & 127;
     const uint32_t lane_sel = uint32_t(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + tmem_s(s) + lane_sel, to = tmem + tmem_o(s) + lane_sel;
+    const uint32_t to = tmem + Ahead<D>::o_col(s) + lane_sel;
     const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);  // (0 is as good as 1e-30)
     uint32_t n = 0, ns = 0;          // tiles of the CTA, tiles of this stream
+    uint32_t uses = 0;               // of the tensor core before this segment (Ahead)
     uint32_t no = 0, no_other = 0;   // segments of this stream and of the other
     uint32_t meets = 0;              // phases of the groups' barrier so far
     auto meet = [&] {
@@ -500,8 +619,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       };
       if (seg.t1 < 0) break;
       const bool paired = seg.paired();
-      const uint32_t n0 = n;
+      const uint32_t n0 = n, uses0 = uses;
       n += uint32_t(seg.t1 - seg.t0);
+      uses += uint32_t(seg.t1 - seg.t0) << (paired ? 1 : 0);
       int t = seg.t0;
       if (!paired && ((seg.parity ^ s) & 1)) ++t;
       const bool shared = !paired && seg.t1 - seg.t0 > 1;  // both streams have tiles of the same rows
@@ -521,7 +641,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       float m = -INFINITY, l = 0.f;  // running maximum (unscaled) and sum
       bool first = true;
       for (; ok && t < seg.t1; t += step, ++ns) {
-        if (!wait_warp(bars.s_ready + s, ns & 1)) {
+        const uint32_t use = uses0 + (paired ? 2 * uint32_t(t - seg.t0) + uint32_t(s) : uint32_t(t - seg.t0)), buffer = use % 3;
+        const uint32_t ts = tmem + lane_sel + (Ahead<D>::ON ? 128u * buffer : tmem_s(s));
+        if (!(Ahead<D>::ON ? wait_warp(&ahead.s_ready[s][ns & 3], (ns >> 2) & 1) : wait_warp(bars.s_ready + s, ns & 1))) {
           ok = false;
           break;
         }
@@ -534,13 +656,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           softmax_tile<D, F16>(ts, to, c, r < rows, first, fewest < kTileKeys, [&](int q, int g) {
             const int n_seen = mine - 64 * q - 32 * g;
             return n_seen >= 32 ? 0xffffffffu : n_seen <= 0 ? 0u : (1u << n_seen) - 1u;
+          }, [&] {
+            // Scores come before the products of the stream's tile before, which has to be done now.  (Those of the tile
+            // before that are: use n's scores are behind the products of use n - 3, and a stream's uses are two apart.
+            // So the phase's parity tells.)
+            if (Ahead<D>::ON) {
+              wait_warp(ahead.o_step + s, (ns - 1) & 1);
+              tc_fence_after();
+            }
           }, m, l);
         }
         first = false;
         if (left < kTileKeys && (left & 15)) {
           // values behind the last token of its unit may be anything: zero them, for 0 x NaN is NaN
-          const uint32_t use = 2 * (n0 + uint32_t(t - seg.t0)) + 1, slot = use % NS;
-          if (!wait_warp(bars.full + slot, (use / NS) & 1)) {
+          const uint32_t fill = 2 * (n0 + uint32_t(t - seg.t0)) + 1, slot = fill % NS;
+          if (!wait_warp(bars.full + slot, (fill / NS) & 1)) {
             ok = false;
             break;
           }
@@ -554,7 +684,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           fence_proxy_async_smem();
         }
         tc_fence_before();
-        mbar_arrive(bars.p_ready + s);
+        mbar_arrive(Ahead<D>::ON ? ahead.p_ready + buffer : bars.p_ready + s);
       }
       if (!ok) break;
 
@@ -585,7 +715,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!idle) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const float f_own = w_own * inv, f_other = w_other * inv;
-        const uint32_t to_other = tmem + tmem_o(s ^ 1) + lane_sel;
+        const uint32_t to_other = tmem + Ahead<D>::o_col(s ^ 1) + lane_sel;
         const int token = seg.tok0 + tok;
         const long long out_row = (long long)token * d.Hq + seg.h * G + (srow0 + r - tok * G);
         const int q0 = shared ? s * (D / 2) : 0, q1 = shared ? q0 + D / 2 : D;
@@ -708,7 +838,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // ---------------------------------------------------------------- few rows
 // Where sequences have about eight rows to a kv head or fewer (single tokens, with their heads), a tile of 128 rows is all
 // padding and its chain of products, not the memory, sets the pace (64 single tokens over 1..1500 keys: 74 us with it).
-// Here a block is up to 8 rows, and a warp is a worker by itself: it takes 16 keys at a time (D = 64: 32), straight from
+// Here a block is up to 8 rows, and a warp is a worker by itself: it takes 16 keys at a time, straight from
 // memory into the registers that the warp-wide products (m16n8k16) read, and no shared memory or barrier is in the way.
 // The elements of a head and the keys are summed in an order of the lanes' own, so that each lane's operands are
 // 16 bytes that lie together:
@@ -736,8 +866,7 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kFewThreads, few_ctas(D))
     packed_few_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w, const __grid_constant__ Cut cut, const uint32_t page_inv) {
-  constexpr int CK = D / 32, CV = D / 64, H16 = D == 64 ? 2 : 1;  // parts of a key and of a value, 16s of keys in a round
-  constexpr int ROUNDS = 2 / H16;                                 // to a tile of 32 keys
+  constexpr int CK = D / 32, CV = D / 64;  // parts of a key and of a value in a lane
   __shared__ Plan plan;
   __shared__ long long before[kFewThreads + 32];
   pdl_launch_dependents();
@@ -781,37 +910,29 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(D))
     };
     // keys of round r that some row sees (may exceed the round's)
     auto left_of = [&](int r) {
-      const int t = seg.t0 + r / ROUNDS, in = r % ROUNDS * 16;
+      const int t = seg.t0 + r / 2, in = r % 2 * 16;
       return t >= seg.pre_tiles ? seg.keys - 32 * (t - seg.pre_tiles) - in : seg.pre_keys - 32 * t - in;
     };
-    auto place_of = [&](int r, int half) {
-      return __shfl_sync(0xffffffffu, place, (r / ROUNDS & 15) * 2 + (ROUNDS == 2 ? r & 1 : half));
-    };
-    uint4 kx[H16][2][CK], vx[H16][4][CV];
+    auto place_of = [&](int r) { return __shfl_sync(0xffffffffu, place, r & 31); };
+    uint4 kx[2][CK], vx[4][CV];
     auto fetch_keys = [&](int r) {
       const int left = left_of(r);
+      const long long at = place_of(r);
 #pragma unroll
-      for (int e = 0; e < H16; ++e) {
-        const long long at = place_of(r, e);
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < CK; ++i)
-            kx[e][u][i] = 16 * e < left ? load16(p.k_cache + at + (8 * u + n) * d.cache_token_stride + 32 * i + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
-      }
+        for (int i = 0; i < CK; ++i)
+          kx[u][i] = left > 0 ? load16(p.k_cache + at + (8 * u + n) * d.cache_token_stride + 32 * i + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
     };
     auto fetch_values = [&](int r) {
       const int left = left_of(r);
+      const long long at = place_of(r);
 #pragma unroll
-      for (int e = 0; e < H16; ++e) {
-        const long long at = place_of(r, e);
+      for (int u = 0; u < 4; ++u) {
+        const int key = 2 * j + (u & 1) + 8 * (u >> 1);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int key = 2 * j + (u & 1) + 8 * (u >> 1);
-#pragma unroll
-          for (int i = 0; i < CV; ++i)  // (values behind the last key may be anything, and 0 x NaN is NaN)
-            vx[e][u][i] = 16 * e + key < left ? load16(p.v_cache + at + key * d.cache_token_stride + 64 * i + 8 * n) : make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int i = 0; i < CV; ++i)  // (values behind the last key may be anything, and 0 x NaN is NaN)
+          vx[u][i] = key < left ? load16(p.v_cache + at + key * d.cache_token_stride + 64 * i + 8 * n) : make_uint4(0u, 0u, 0u, 0u);
       }
     };
     float o[CV][4][4];
@@ -822,37 +943,33 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(D))
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[i][t][x] = 0.f;
     float m = -INFINITY, l = 0.f;  // of row n: running maximum (log2 units), this lane's part of the sum
-    const int rounds = tiles * ROUNDS;
+    const int rounds = 2 * tiles;
     look_up(seg.t0);
     fetch_keys(0);
     fetch_values(0);
 #pragma unroll 1
     for (int r = 0; r < rounds; ++r) {
-      const int t = seg.t0 + r / ROUNDS;
-      float sc[2 * H16][4];
+      const int t = seg.t0 + r / 2;
+      float sc[2][4];
 #pragma unroll
-      for (int e = 0; e < H16; ++e)
+      for (int u = 0; u < 2; ++u) {
+        sc[u][0] = sc[u][1] = sc[u][2] = sc[u][3] = 0.f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float (&x)[4] = sc[2 * e + u];
-          x[0] = x[1] = x[2] = x[3] = 0.f;
-#pragma unroll
-          for (int i = 0; i < CK; ++i) {
-            mma_16x8x16<F16>(x, q[i][0], 0u, q[i][1], 0u, kx[e][u][i].x, kx[e][u][i].y);
-            mma_16x8x16<F16>(x, q[i][2], 0u, q[i][3], 0u, kx[e][u][i].z, kx[e][u][i].w);
-          }
+        for (int i = 0; i < CK; ++i) {
+          mma_16x8x16<F16>(sc[u], q[i][0], 0u, q[i][1], 0u, kx[u][i].x, kx[u][i].y);
+          mma_16x8x16<F16>(sc[u], q[i][2], 0u, q[i][3], 0u, kx[u][i].z, kx[u][i].w);
         }
+      }
       const bool more = r + 1 < rounds;
       const bool own = t >= seg.pre_tiles;
-      const int sees = (own ? lim - 32 * (t - seg.pre_tiles) : seg.pre_keys - 32 * t) - r % ROUNDS * 16;  // keys of this round that row n sees
+      const int sees = (own ? lim - 32 * (t - seg.pre_tiles) : seg.pre_keys - 32 * t) - r % 2 * 16;  // keys of this round that row n sees
       if (more) {
-        // (a round's places: the values of the last round of 16 tiles are on their way already)
-        if ((r + 1) % (16 * ROUNDS) == 0) look_up(seg.t0 + (r + 1) / ROUNDS);
+        if ((r + 1) % 32 == 0) look_up(seg.t0 + (r + 1) / 2);  // (the values of the round before are on their way already)
         fetch_keys(r + 1);
       }
       float top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 2 * H16; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           sc[i][e] = 8 * i + 2 * j + e < sees ? sc[i][e] * c : -INFINITY;
@@ -872,24 +989,21 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(D))
           for (int x = 0; x < 4; ++x) o[i][x][0] *= f0, o[i][x][1] *= f1, o[i][x][2] *= f0, o[i][x][3] *= f1;
       }
       const float base = m == -INFINITY ? 0.f : m;
+      uint32_t pr[2];
 #pragma unroll
-      for (int e = 0; e < H16; ++e) {
-        uint32_t pr[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float w0 = exp2_fast(sc[2 * e + u][0] - base), w1 = exp2_fast(sc[2 * e + u][1] - base);
-          l += w0 + w1;
-          pr[u] = pack2<F16>(w0, w1);
-        }
-#pragma unroll
-        for (int i = 0; i < CV; ++i)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {  // elements 64 i + 8 n + 2 x and the one behind
-            const uint32_t w0 = word(vx[e][0][i], x), w1 = word(vx[e][1][i], x), w2 = word(vx[e][2][i], x), w3 = word(vx[e][3][i], x);
-            mma_16x8x16<F16>(o[i][x], __byte_perm(w0, w1, 0x5410), __byte_perm(w0, w1, 0x7632), __byte_perm(w2, w3, 0x5410),
-                             __byte_perm(w2, w3, 0x7632), pr[0], pr[1]);
-          }
+      for (int u = 0; u < 2; ++u) {
+        const float w0 = exp2_fast(sc[u][0] - base), w1 = exp2_fast(sc[u][1] - base);
+        l += w0 + w1;
+        pr[u] = pack2<F16>(w0, w1);
       }
+#pragma unroll
+      for (int i = 0; i < CV; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {  // elements 64 i + 8 n + 2 x and the one behind
+          const uint32_t w0 = word(vx[0][i], x), w1 = word(vx[1][i], x), w2 = word(vx[2][i], x), w3 = word(vx[3][i], x);
+          mma_16x8x16<F16>(o[i][x], __byte_perm(w0, w1, 0x5410), __byte_perm(w0, w1, 0x7632), __byte_perm(w2, w3, 0x5410),
+                           __byte_perm(w2, w3, 0x7632), pr[0], pr[1]);
+        }
       if (more) fetch_values(r + 1);
     }
     l += __shfl_xor_sync(0xffffffffu, l, 1);

@@ -266,10 +266,10 @@ __device__ __forceinline__ TileBars tile_bars(uint64_t* bars) {
   return TileBars{bars, bars + NS, q, q + 2, q + 4, q + 6, q + 8, q + 10, q + 10 + kSegRing};
 }
 template <int NS>
-__device__ __forceinline__ void init_tile_bars(const TileBars& b) {  // one thread
+__device__ __forceinline__ void init_tile_bars(const TileBars& b, int tensor_warps) {  // one thread
   for (int i = 0; i < NS; ++i) {
     mbar_init(b.full + i, 1);
-    mbar_init(b.empty + i, 2);  // one arrival per stream
+    mbar_init(b.empty + i, uint32_t(tensor_warps));  // an arrival each
   }
   for (int s = 0; s < 2; ++s) {
     mbar_init(b.q_ready + s, 1);
@@ -280,7 +280,7 @@ __device__ __forceinline__ void init_tile_bars(const TileBars& b) {  // one thre
   }
   for (int i = 0; i < kSegRing; ++i) {
     mbar_init(b.seg_full + i, 1);
-    mbar_init(b.seg_empty + i, 4 + 2 * kGroupThreads / 32);  // every warp, the one that hands them on included
+    mbar_init(b.seg_empty + i, uint32_t(2 + tensor_warps + 2 * kGroupThreads / 32));  // every warp, the one that hands them on included
   }
 }
 
@@ -409,9 +409,10 @@ __device__ __forceinline__ void tensor_warp(const int s, const int lane, const u
 // A row's softmax over a tile: scores in tensor memory to probabilities there, with its running maximum m (unscaled)
 // and sum l.  seen(q, g) is the mask of the keys from 64 q + 32 g on that the row sees, 32 of them, asked for where
 // the tile is `masked`; a row that is not `live` never moves its maximum.
-template <int D, bool F16, typename Seen>
+// settle() returns once O holds the tiles before.
+template <int D, bool F16, typename Seen, typename Settle>
 __device__ __forceinline__ void softmax_tile(const uint32_t ts, const uint32_t to, const float c, const bool live, const bool first,
-                                             const bool masked, Seen seen, float& m, float& l) {
+                                             const bool masked, Seen seen, Settle settle, float& m, float& l) {
   // 64 scores at a time, in a loop (all 128 unrolled hold up the other warps' instruction fetches, 32
   // at a time wait longer for their loads).  The exponentials take the maximum that is known; only if
   // a row's next 64 lie more than kLag above it are O, its sum and the tile's P so far rescaled.
@@ -435,6 +436,7 @@ __device__ __forceinline__ void softmax_tile(const uint32_t ts, const uint32_t t
     if (__any_sync(0xffffffffu, move)) {
       const float f = move ? exp2_fast((m - mx) * c) : 1.f;
       if (!first) {
+        settle();
 #pragma unroll 1
         for (int k2 = 0; k2 < D; k2 += 32) {
           float o[32];
