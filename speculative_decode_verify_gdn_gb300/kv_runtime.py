@@ -1,5 +1,6 @@
 """Device-resident paged cache of a hybrid model's softmax-attention layers, and its part of the
-verify round (attend -> commit, fork, compact).
+verify round (rope -> attend -> commit, fork, compact) and of prompts (reserve, then layer by layer
+append_layer -> attend_prefill).
 
 Torch allocates the memory; every step runs through the C ABI (include/gdn_kv.h).  The slots are
 the batch's sequences, 0..B-1, and behind them the shared prefixes.  Tables, lengths and
@@ -43,6 +44,7 @@ class PagedCache:
     attn_workspace: torch.Tensor
     pool_workspace: torch.Tensor
     fork_scratch: tuple
+    prefill_workspace: torch.Tensor
     cur: int = 0
 
     @classmethod
@@ -61,7 +63,8 @@ class PagedCache:
                    ints(n_pages), ints(B, fill=-1), ints(1), dims, kv.alloc_attn_workspace(dims, device),
                    kv.alloc_kv_workspace(dims, device),
                    (ints(B), torch.empty(B, dtype=torch.bool, device=device), ints(B),
-                    torch.arange(B, dtype=torch.int32, device=device), ints(n_slots, fill=-1)))
+                    torch.arange(B, dtype=torch.int32, device=device), ints(n_slots, fill=-1)),
+                   kv.alloc_attn_prefill_workspace(dims, 0, device))
 
     @property
     def table(self) -> torch.Tensor:
@@ -81,6 +84,44 @@ class PagedCache:
             kv.gdn_kv_commit(d, all_of_it, None, k_new.unsqueeze(1), v_new.unsqueeze(1), self.k, self.v, self.table,
                              self.table, self.seq_len, self.seq_len, self.ref, self.ref,
                              kv.alloc_kv_workspace(d, k_new.device), stream)
+
+    def rope(self, rope, q, k, v, q_out, k_win, v_win, parent=None, win_len=None, positions=None, stream=None) -> None:
+        """One layer's window [B, K, heads, D] ready for attend and commit: queries and keys normed and rotated
+        (kv.make_rope) at their positions behind prefix and slot, values copied.  q, k, v may be parts of a
+        projection's rows, and each output its input."""
+        kv.gdn_attn_rope(self._dims(self.B, q=q_out, win=k_win if k_win is not None else v_win), rope, q, k, v, self.seq_len,
+                         self._prefixes(0, self.B), win_len, parent, positions, q_out, k_win, v_win, stream)
+
+    def reserve(self, n_new, slot0=0, stream=None) -> None:
+        """Pages for n_new (int32) more tokens of the sequences from slot0 on, in all layers, which grow by them;
+        append_layer fills them."""
+        kv.gdn_kv_reserve(self._dims(n_new.shape[0], slot0), n_new, self.table, self.table, self.seq_len, self.seq_len, self.ref,
+                          self.ref, self.pool_workspace, stream)
+
+    def append_layer(self, layer, rope, cu_seqlens, q, k, v, q_out, slot0=0, positions=None, stream=None) -> None:
+        """One layer's packed tokens of the sequences from slot0 on, with bounds cu_seqlens (int32), to the places
+        that reserve made for them: q [N, Hq, D] normed and rotated to q_out (both may be None), k normed and
+        rotated, and v, [N, Hkv, D], to the pages."""
+        n = cu_seqlens.shape[0] - 1
+        kv.gdn_kv_append(self._dims(n, slot0, q=q_out), layer, rope, cu_seqlens, q, k, v, positions, self.k, self.v, self.table,
+                         self.seq_len, self._prefixes(slot0, n), q_out, stream)
+
+    def attend_prefill(self, layer, cu_seqlens, q, out, lse=None, slot0=0, causal=True, scale=None, stream=None) -> None:
+        """Packed queries [N, Hq, D] of the sequences from slot0 on attend to prefix and slot: causally, a
+        sequence's queries being those of its last tokens, or to all of the slot (cross attention)."""
+        n = cu_seqlens.shape[0] - 1
+        kv.gdn_attn_prefill(self._dims(n, slot0, q=q), layer, cu_seqlens, q, self.k, self.v, self.table, self.seq_len,
+                            self._prefixes(slot0, n), causal, 1.0 / math.sqrt(self.D) if scale is None else scale, out, lse,
+                            self.prefill_workspace, stream)
+
+    def _dims(self, n, slot0=0, q=None, win=None) -> kv.KvDims:
+        """The dims of a call on n sequences from slot0 on, with these queries' and windows' strides."""
+        return kv.make_kv_dims(n, self.K, self.Hq, self.Hkv, self.D, self.page_size, self.n_pages, self.max_pages,
+                               self.B + self.n_prefixes, slot0, self.n_layers, self.dtype, q=q, win=win)
+
+    def _prefixes(self, slot0, n):
+        """Prefixes of the sequences from slot0 on (the prefixes' own slots have none)."""
+        return self.prefix_of[slot0:slot0 + n] if self.n_prefixes and slot0 + n <= self.B else None
 
     def attend(self, layer, q, k_win, v_win, out, lse=None, parent=None, win_len=None, scale=None, stream=None) -> None:
         """The window's attention in one layer (a chain, or a token tree given by parent [B, K])."""
