@@ -356,13 +356,47 @@ __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const __grid_c
   // free pages of this CTA's part, its counts copied on the way
   const int part = ((d.n_pages + ranks - 1) / ranks + 3) & ~3;
   const int lo = rank * part < d.n_pages ? rank * part : d.n_pages, hi = lo + part < d.n_pages ? lo + part : d.n_pages;
+  // (a thread keeps 32 pages that lie together, as a mask, so that one scan over the CTA ranks up to 16384 of them; a
+  // warp reads up to 32 times 32 pages, eight of them in flight: one after the other they would be most of the call)
+  const int lane = tid & 31, words = part >= 32 * kPlanThreads ? 32 : (part + kPlanThreads - 1) / kPlanThreads, step = words * kPlanThreads;
+  auto free_pages = [&](int i0, bool copy) {  // lane k has the mask of words of 32 pages
+    const int first = i0 + (tid >> 5) * words * 32;
+    uint32_t mine = 0;
+    for (int k0 = 0; k0 < words; k0 += 8) {
+      int held[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = first + 32 * (k0 + u) + lane;
+        held[u] = k0 + u < words && i < hi ? p.ref_in[i] : 1;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = first + 32 * (k0 + u) + lane;
+        const uint32_t word = __ballot_sync(0xffffffffu, held[u] == 0);
+        if (lane == k0 + u) mine = word;
+        if (copy && k0 + u < words && i < hi) p.ref_out[i] = held[u];
+      }
+    }
+    return mine;
+  };
   long long free_here = 0;
-  for (int i = lo + tid; i < hi; i += kPlanThreads) {
-    const int held = p.ref_in[i];
-    free_here += held == 0;
-    if (p.ref_out != p.ref_in) p.ref_out[i] = held;
+  uint32_t first_mask = 0;
+  for (int i0 = lo; i0 < hi; i0 += step) {
+    const uint32_t mask = free_pages(i0, p.ref_out != p.ref_in);
+    if (i0 == lo) first_mask = mask;
+    free_here += __popc(mask);
   }
-  copy_ints(p.table_out, p.table_in, (long long)d.n_slots * d.max_pages, rank, ranks);
+  if (p.table_out != p.table_in) {
+    const long long n = (long long)d.n_slots * d.max_pages, stride = (long long)ranks * kPlanThreads;
+    for (long long i0 = (long long)rank * kPlanThreads + tid; i0 < n; i0 += 8 * stride) {
+      int32_t v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = i0 + u * stride < n ? p.table_in[i0 + u * stride] : 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i0 + u * stride < n) p.table_out[i0 + u * stride] = v[u];
+    }
+  }
   copy_ints(p.len_out, p.len_in, d.n_slots, rank, ranks);
   // the plan
   ReserveRec* const rec = d.B <= kPlanThreads ? here : static_cast<ReserveRec*>(static_cast<void*>(w.rec));
@@ -418,34 +452,28 @@ __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const __grid_c
         p.len_out[d.slot0 + b] = r.len;
     }
   }
-  for (int i0 = lo; i0 < hi && at < wanted; i0 += 4 * kPlanThreads) {
-    int mask = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int i = i0 + 4 * tid + q;
-      if (i < hi && p.ref_in[i] == 0) mask |= 1 << q;
-    }
+  for (int i0 = lo; i0 < hi && at < wanted; i0 += step) {
+    const uint32_t mask = i0 == lo ? first_mask : free_pages(i0, false);
     long long total;
-    long long r = at + block_scan64(__popc(mask), sums, total);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (!(mask >> q & 1)) continue;
-      if (r < wanted) {
-        int b = 0, end = d.B;  // the last sequence whose first rank is not above r (those without needs come before it)
-        while (end - b > 1) {
-          const int mid = (b + end) / 2;
-          if (rec[mid].first <= r)
-            b = mid;
-          else
-            end = mid;
-        }
-        const ReserveRec x = rec[b];
-        if (x.first + x.need <= found) {
-          p.table_out[(long long)(d.slot0 + b) * d.max_pages + x.have + int(r - x.first)] = i0 + 4 * tid + q;
-          p.ref_out[i0 + 4 * tid + q] = 1;
-        }
+    const long long r0 = at + block_scan64(__popc(mask), sums, total);
+    for (int k = 0; k < words; ++k) {  // a word's free pages, a lane each
+      const uint32_t word = __shfl_sync(0xffffffffu, mask, k);
+      const long long r = __shfl_sync(0xffffffffu, r0, k) + __popc(word & ((1u << lane) - 1u));
+      if (!(word >> lane & 1u) || r >= wanted) continue;
+      int b = 0;  // the last sequence whose first rank is not above r (those without needs come before it)
+      for (int end = d.B; end - b > 1;) {
+        const int mid = (b + end) / 2;
+        if (rec[mid].first <= r)
+          b = mid;
+        else
+          end = mid;
       }
-      ++r;
+      const ReserveRec x = rec[b];
+      if (x.first + x.need <= found) {
+        const int page = i0 + ((tid >> 5) * words + k) * 32 + lane;
+        p.table_out[(long long)(d.slot0 + b) * d.max_pages + x.have + int(r - x.first)] = page;
+        p.ref_out[page] = 1;
+      }
     }
     at += total;
   }

@@ -31,8 +31,8 @@ namespace {
 constexpr int kJoinWarps = 8, kJoinChunks = 8;  // CTAs to a cut item of the tile kernel
 constexpr int kFewRows = 8;     // rows of a block of the kernel for few rows
 constexpr int kFewThreads = 128;
-constexpr int few_ctas(int D) { return D == 128 ? 3 : 4; }  // CTAs to an SM
-constexpr int few_workers(int D) { return kCtas * few_ctas(D) * (kFewThreads / 32); }
+__host__ __device__ constexpr int few_ctas(int D) { return D == 128 ? 3 : 4; }  // CTAs to an SM
+__host__ __device__ constexpr int few_workers(int D) { return kCtas * few_ctas(D) * (kFewThreads / 32); }
 
 struct JoinRec {       // a cut item, by the worker c0 that it begins with; it ends with worker c1
   int32_t tok0, rows;  // rows 0: there is none
@@ -363,7 +363,7 @@ __device__ __forceinline__ void tensor_warp_ahead(const int lane, const uint32_t
   const uint32_t values_idesc = idesc_f16<F16>(kTileKeys, D) | (1u << 16);  // B (values) MN-major
   const uint32_t scores_idesc = negative ? 1u << 13 : 0u;                   // a negative scale negates the queries
   struct Use {
-    uint32_t units, slot, phase, flags;  // its values' slot; flags: 1 stream, 2 first of the stream's sums, 4 last, 8 the slot's last
+    uint32_t units, slot, phase, flags;  // its values' slot; flags: 1 stream, 2 first of the stream's sums, 4 last, 8 the slot's last, 16 not its first
   };
   Use u0{}, u1{}, u2{};  // whose O += P V is still to be issued, the eldest first
   uint32_t pending = 0;
@@ -372,7 +372,7 @@ __device__ __forceinline__ void tensor_warp_ahead(const int lane, const uint32_t
   uint32_t uses0 = 0, uses1 = 0, nq0 = 0, nq1 = 0;  // scores and segments of each stream
   bool ok = true;
   auto values = [&]() {  // O += P V of the eldest
-    ok = wait_warp(bars.full + u0.slot, u0.phase) && wait_warp(ahead.p_ready + p_buf, p_phase);
+    ok = ((u0.flags & 16u) || wait_warp(bars.full + u0.slot, u0.phase)) && wait_warp(ahead.p_ready + p_buf, p_phase);
     if (!ok) return;
     tc_fence_after();
     const uint32_t s = u0.flags & 1u, to = tm + Ahead<D>::o_col(int(s)), ts = tm + 128u * p_buf;
@@ -414,7 +414,7 @@ __device__ __forceinline__ void tensor_warp_ahead(const int lane, const uint32_t
         const bool slot_last = !paired || i == 1;
         if (pending == NB) values();
         if (ok && first) ok = wait_warp(bars.q_ready + s, (s ? nq1 : nq0) & 1);
-        ok = ok && wait_warp(bars.full + slot, phase);
+        ok = ok && (i == 1 || wait_warp(bars.full + slot, phase));
         if (!ok) break;
         tc_fence_after();
         umma_scores<D>(tm + 128u * n_buf, swizzled_desc_lo(base + L::OFF_Q + s * L::BYTES, 16),
@@ -424,7 +424,7 @@ __device__ __forceinline__ void tensor_warp_ahead(const int lane, const uint32_t
         if (last) umma_commit_one(bars.q_free + s);
         if (first) nq0 += s ^ 1, nq1 += s;
         uses0 += s ^ 1, uses1 += s;
-        const Use u{units, vslot, vphase, s | (first ? 2u : 0u) | (last ? 4u : 0u) | (slot_last ? 8u : 0u)};
+        const Use u{units, vslot, vphase, s | (first ? 2u : 0u) | (last ? 4u : 0u) | (slot_last ? 8u : 0u) | (i == 1 ? 16u : 0u)};
         if (pending == 0)
           u0 = u;
         else if (pending == 1)
