@@ -331,10 +331,9 @@ struct SegWalk {
 struct PackedMaps {
   // (D, token, kv head, page, 1), keys and values: boxes of 16 tokens, and of `box` tokens
   CUtensorMap few[2], many[2];
-  // queries, (D, query head, token): boxes of G heads x the tokens of a row tile, and x a few tokens
-  CUtensorMap qt, qs;
+  // queries, (D, query head, token): boxes of G heads x the tokens of a row tile
+  CUtensorMap queries;
 };
-constexpr int kFewToks = 4;
 
 // At D = 64 tensor memory has room for a third tile of scores, and the products of a stream's next scores need not wait
 // until its probabilities have been multiplied: that wait, and not the tensor core or the softmax, sets the pace otherwise
@@ -793,11 +792,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int s = paired ? part : (seg.parity + part) & 1;  // in the order of their first tiles
         const uint32_t nq = s ? nq1 : nq0;
         if (nq == 0 || __all_sync(0xffffffffu, mbar_look(bars.q_free + s, (nq - 1) & 1))) {
-          const bool few = seg.rows <= kFewToks * G && kFewToks < tile_toks;
-          if (lane == 0) mbar_arrive_expect_tx(bars.q_ready + s, uint32_t((few ? kFewToks : tile_toks) * G) * D * 2);
+          if (lane == 0) mbar_arrive_expect_tx(bars.q_ready + s, uint32_t(tile_rows) * D * 2);
           __syncwarp();
           if (lane < D / 64)
-            tma_load3(base + L::OFF_Q + s * L::BYTES + lane * L::HALF, few ? &maps.qs : &maps.qt, lane * 64, seg.h * G,
+            tma_load3(base + L::OFF_Q + s * L::BYTES + lane * L::HALF, &maps.queries, lane * 64, seg.h * G,
                       seg.tok0 + (paired ? s * tile_toks : 0), smem_addr(bars.q_ready + s));
           if (s)
             ++nq1;
@@ -1182,9 +1180,8 @@ cudaError_t launch_packed_attn(const PackedAttnParams& p, cudaStream_t stream) {
   }
   const cuuint64_t qd[3] = {cuuint64_t(d.D), cuuint64_t(d.Hq), cuuint64_t(p.n_tokens)};
   const cuuint64_t qst[2] = {2ull * d.D, 2ull * d.q_token_stride};
-  const cuuint32_t bt[3] = {64, cuuint32_t(G), cuuint32_t(toks)}, bs[3] = {64, cuuint32_t(G), cuuint32_t(toks < kFewToks ? toks : kFewToks)};
-  map(&maps.qt, p.q, 3, qd, qst, bt);
-  map(&maps.qs, p.q, 3, qd, qst, bs);
+  const cuuint32_t bt[3] = {64, cuuint32_t(G), cuuint32_t(toks)};
+  map(&maps.queries, p.q, 3, qd, qst, bt);
   if (!ok) return cudaErrorInvalidValue;
   const Cut cut = make_cut(toks, 2 * toks, 7, p.causal, kCtas);
   if (d.D == 128) return d.dtype ? launch<128, true>(p, w, cut, box, maps, stream) : launch<128, false>(p, w, cut, box, maps, stream);
