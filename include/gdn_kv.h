@@ -236,7 +236,7 @@ gdn_status gdn_kv_reserve(const gdn_kv_dims* dims, const int32_t* n_new, const i
  * seq_len - n + j, and at that plus the prefix's tokens for the rotation (or at positions[token]).
  *   n_tokens   0 <= n_tokens < 2^31: rows of q, k, v
  *   cu_seqlens [B + 1] int32: 0 = c_0 <= ... <= c_B <= n_tokens, else GDN_DEVERR_SEQLENS is set and what the
- *              slots' last tokens hold is undefined.  Rows behind c_B are neither read nor written.
+ *              slots' last tokens hold is undefined.  Rows behind c_B reach no output, and none is written for them.
  *   q, q_out   [n_tokens, Hq, D] (strides in rope; q_token_stride in dims), or both NULL
  *   k, v       [n_tokens, Hkv, D] (strides in rope)
  *   k_cache, v_cache  written, as described above; q_out may be q as in gdn_attn_rope

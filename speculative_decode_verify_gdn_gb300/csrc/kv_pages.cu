@@ -315,6 +315,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv_commit_move_kernel(const __gr
 // it: the sequence whose first rank is the last one not above it.  So no list of free pages is kept.
 // Tables that are not updated in place are copied before the barrier; what the plan reads of the counts
 // (pages that are held) is never what is written behind it (pages that were free).
+// Bound: its trips to L2, one behind the other (counts, lengths, last pages, the barrier, ranks): 256 prompts in a pool of
+// 40000 pages 12.5 us (16.5 with four pages a thread and step, and loads one at a time); one sequence 8.5, the host's.
 constexpr int kReserveCtas = 8;
 struct ReserveRec {
   long long first;  // rank of the sequence's first new page

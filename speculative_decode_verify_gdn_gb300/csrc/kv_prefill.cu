@@ -13,11 +13,24 @@
 // workspace: at most two such pieces a CTA), and a last kernel joins them.  Which CTA computes what depends on
 // the lengths alone, and no sum is formed by atomics, so results repeat bit for bit.
 //
-// Kernels: tiles (persistent, tcgen05; every CTA plans for itself), join.
+// Kernels: tiles (persistent, tcgen05; every CTA plans for itself) or, for few rows to a sequence, a kernel of warps that
+// work by themselves (below); join.
 //
 // A block of more than 128 rows gives each stream half of them, on the same keys; a smaller one gives the
 // streams alternate tiles of the same rows, and at its end the two sums are joined in tensor memory, each
 // softmax group taking half of the columns.
+//
+// Measured on one GB300, calls in a row (peaks: 6702 GB/s copy, 1903 TFLOP/s cuBLAS bf16, 1728 when the power cap sets
+// the clock):
+//   prompts of 4096..16384 tokens, Hq=32 Hkv=8 D=128     3.18 ms, 1300 TFLOP/s: the chain scores, softmax, products of a
+//     stream (a pair of tiles in 1.9 us) at the power cap
+//   512 tokens behind 65536, Hq=32 Hkv=8 D=128           413 us, 1340 TFLOP/s; its 64 items read the same keys at
+//     different times, so 2.2 GB come from HBM where 0.28 would do
+//   13 prompts of 1..901 tokens behind 1531 shared and 0..333 own, f16 Hq=24 Hkv=4 D=64   118 us, 610 TFLOP/s: the warp
+//     that issues the products, a pair of tiles in 1.4 us; start, ends of segments and join 25 us
+//   24 prompts of 3..448 tokens over 400..1500 states, Hq=Hkv=16 D=64   61 us: start, ends of 4.6 segments a CTA, join
+//   64 single tokens over 1..1500 states, f16 Hq=Hkv=16 D=64   45 us, 4.4 TB/s (few rows)
+//   one prompt of 37 tokens   14 us: the host's two launches and its four tensor maps
 #include <atomic>
 
 #include "kv_device.cuh"
@@ -28,7 +41,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int kJoinWarps = 8, kJoinChunks = 8;  // CTAs to a cut item of the tile kernel
+constexpr int kJoinWarps = 8, kJoinChunks = 16;  // CTAs to a cut item of the tile kernel (cross attention of prompts 61 us, 63 with 8, 71 with 4, 62 with 32)
 constexpr int kFewRows = 8;     // rows of a block of the kernel for few rows
 constexpr int kFewThreads = 128;
 __host__ __device__ constexpr int few_ctas(int D) { return D == 128 ? 3 : 4; }  // CTAs to an SM
@@ -215,7 +228,8 @@ struct Seg {
   int tok0, rows;               // packed tokens, rows of the block
   int h;                        // kv head
   int pair;                     // they fill more than one row tile: both streams take every tile of keys
-  int slot, keys, lim;          // as in BlockRec
+  int slot, keys;               // own slot, and the keys in it that the last row sees
+  int lim;                      // the keys in it that the first row sees (causal: a token more each token; may be below 1)
   int pre_slot, pre_keys, pre_tiles;
   int t0, t1;                   // tiles of the item
   int parity;                   // of tile t0 in the order of all tiles
@@ -336,8 +350,10 @@ struct PackedMaps {
 };
 
 // At D = 64 tensor memory has room for a third tile of scores, and the products of a stream's next scores need not wait
-// until its probabilities have been multiplied: that wait, and not the tensor core or the softmax, sets the pace otherwise
-// (a pair of tiles in 1.55 us without it).  All uses of the tensor core are in one order, n = 0, 1, 2, ..: a tile's scores
+// until its probabilities have been multiplied (256 rows of 32 heads over 92160 keys: 219 us, 242 with two tiles and a warp
+// per stream).  What then sets the pace is this warp: 1470 cycles a use, 256 + 256 of them the tensor core's, before a
+// tile's second stream stopped waiting for keys and values that the first had seen (235 us).  A warp each for scores and
+// products takes 204 us there, but 71 where this takes 65 on the cross attention of prompts.  All uses of the tensor core are in one order, n = 0, 1, 2, ..: a tile's scores
 // of stream 0 and of stream 1, or a stream's alone; use n has buffer n % 3.  One warp issues
 //   S(0) S(1) S(2) O(0) S(3) O(1) S(4) ..
 // Barriers: s_ready, a stream's i-th use on its barrier i % 4 (three uses may be under way that the stream's softmax
@@ -835,7 +851,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // ---------------------------------------------------------------- few rows
 // Where sequences have about eight rows to a kv head or fewer (single tokens, with their heads), a tile of 128 rows is all
-// padding and its chain of products, not the memory, sets the pace (64 single tokens over 1..1500 keys: 74 us with it).
+// padding and its chain of products, not the memory, sets the pace (64 single tokens over 1..1500 keys: 71 us with it, 45
+// here).
 // Here a block is up to 8 rows, and a warp is a worker by itself: it takes 16 keys at a time, straight from
 // memory into the registers that the warp-wide products (m16n8k16) read, and no shared memory or barrier is in the way.
 // The elements of a head and the keys are summed in an order of the lanes' own, so that each lane's operands are
@@ -844,7 +861,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 //   O^T = V^T P^T: it holds elements 64 c + 8 n .. + 7 of keys 2 j, 2 j + 1, 2 j + 8, 2 j + 9 - the keys whose scores of
 //   row n it has from S - and gets elements 64 c + 8 n .. + 7 of rows 2 j and 2 j + 1.
 // Keys of the round to come are fetched as soon as the products have read the ones before, and values likewise, so that
-// one or the other is always on its way.  Bound: HBM.
+// one or the other is always on its way.  Bound: HBM (4000 keys at Hkv=8 D=128 5.9 TB/s), at short lengths the trips to
+// memory that a segment begins with, one behind the other: bounds, page numbers, keys.  Four CTAs to an SM at D = 64 (120
+// registers; 5 spill and are as fast, 3 take 53 us for 45), three at D = 128 (89 us at 4000 keys, 98 with two or four).
 template <bool F16>
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   if (F16)
@@ -1148,7 +1167,12 @@ cudaError_t launch_packed_attn(const PackedAttnParams& p, cudaStream_t stream) {
   const gdn_kv_dims& d = p.d;
   const int G = d.Hq / d.Hkv, toks = kTileRows / G;
   const PackedWs w = carve_packed(p.ws, d, nullptr);
-  if (G <= kFewRows && (long long)p.n_tokens * G <= (long long)kFewRows * d.B) {
+  // Few rows or tiles, by the rows that a sequence has for a kv head on average; their distribution is known on the
+  // device alone.  Us with one and the other, 64 sequences of 1..1500 keys: f16 Hkv=16 D=64, 1 row 45 and 71, 8 rows 47 and
+  // 72; bf16 Hkv=8 D=128 causal, 4 rows 45 and 52, 8 rows 45 and 52, 12 rows 67 and 52; Hkv=4, 8 rows 31 and 33, 16 rows 40
+  // and 33.  Should all tokens be one sequence's, few rows cost 24 us for 512 tokens where tiles cost 17, and 138 for
+  // 2048 where they cost 35 (Hkv=16 D=64): more than 512 have to be one a sequence on average.
+  if (G <= kFewRows && (long long)p.n_tokens * G <= (long long)kFewRows * d.B && (p.n_tokens <= 512 || p.n_tokens <= d.B)) {
     const int few = kFewRows / G;
     const Cut cut = make_cut(few, few, 5, p.causal, few_workers(d.D));
     if (d.D == 128) return d.dtype ? launch_few<128, true>(p, w, cut, stream) : launch_few<128, false>(p, w, cut, stream);
