@@ -313,17 +313,42 @@ def _on_device(t, name, dev):
 
 
 def _heads(t, name, dtype, shape, dev):
-    """Address, and strides of tokens and heads, of rows [.., heads, D] whose tokens are evenly apart."""
+    """Address, and strides of tokens and heads, of rows [.., heads, D] whose tokens are evenly apart (0: a single one)."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _explain(t, name, dtype, shape, t.stride() if isinstance(t, torch.Tensor) else None)
         _on_device(t, name, dev)
     s = t.stride()
-    step = s[-3]
-    if s[-1] != 1 or (len(s) == 4 and shape[0] > 1 and (s[0] != step * shape[1] if shape[1] > 1 else False)):
+    if len(s) == 3:
+        step = s[0] if shape[0] > 1 else 0
+        even = s[2] == 1
+    else:
+        n, k = shape[0], shape[1]
+        step = s[1] if k > 1 else s[0] if n > 1 else 0
+        even = s[3] == 1 and (n == 1 or k == 1 or s[0] == k * s[1])
+    if not even:
         raise ValueError(f"{name} has strides {s}: elements of a head one after the other, tokens evenly apart")
-    if len(s) == 4 and shape[1] == 1:
-        step = s[0]
-    return t.data_ptr(), step if t.shape[0] > 1 or (len(s) == 4 and shape[1] > 1) else 0, s[-2] if shape[-2] > 1 else shape[-1]
+    return t.data_ptr(), step, s[-2] if shape[-2] > 1 else shape[-1]
+
+
+def _like(t, dtype, shape, other, dev):
+    """Address of a tensor with the shape and strides of another that has been looked at, None of any other."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.stride() == other.stride() and t.get_device() == dev:
+        return t.data_ptr()
+    return None
+
+
+def _beside(k, kt, kh, v, dtype, shape, dev):
+    """Address of the values, and the strides that keys (kt and kh, if there are any) and values have alike."""
+    if v is None:
+        return None, kt, kh
+    if k is not None:
+        at = _like(v, dtype, shape, k, dev)
+        if at is not None:
+            return at, kt, kh
+    vp, vt, vh = _heads(v, "v", dtype, shape, dev)
+    if k is not None and (vt != kt or vh != kh):
+        raise ValueError(f"k and v have different strides: {k.stride()} and {v.stride()}")
+    return vp, vt, vh
 
 
 def _out_rows(t, name, dtype, shape, stride, dev):
@@ -331,7 +356,7 @@ def _out_rows(t, name, dtype, shape, stride, dev):
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _explain(t, name, dtype, shape, t.stride() if isinstance(t, torch.Tensor) else None)
         _on_device(t, name, dev)
-    heads, D = shape[-2:]
+    D = shape[-1]
     want = (stride, D, 1) if len(shape) == 3 else (shape[1] * stride, stride, D, 1)
     if t.stride() != want:
         _explain(t, name, dtype, shape, want)
@@ -372,14 +397,12 @@ def gdn_attn_rope(dims: KvDims, rope: Rope, q, k, v, seq_len, prefix_of, win_len
     dt, qs, ks = _TORCH[d.dtype], (B, K, Hq, D), (B, K, Hkv, D)
     qp, qt, qh = (None, 0, 0) if q is None else _heads(q, "q", dt, qs, dev)
     kp, kt, kh = (None, 0, 0) if k is None else _heads(k, "k", dt, ks, dev)
-    vp, vt, vh = (None, kt, kh) if v is None else _heads(v, "v", dt, ks, dev)
-    if k is None:
-        kt, kh = vt, vh
-    elif vt != kt or vh != kh:
-        raise ValueError(f"k and v have different strides: {k.stride()} and {v.stride()}")
+    vp, kt, kh = _beside(k, kt, kh, v, dt, ks, dev)
     q_to = None if q_out is None else _out_rows(q_out, "q_out", dt, qs, d.q_token_stride, dev)
     k_to = None if k_win is None else _out_rows(k_win, "k_win", dt, ks, d.win_token_stride, dev)
-    v_to = None if v_win is None else _out_rows(v_win, "v_win", dt, ks, d.win_token_stride, dev)
+    v_to = None if v_win is None or k_win is None else _like(v_win, dt, ks, k_win, dev)
+    if v_to is None and v_win is not None:
+        v_to = _out_rows(v_win, "v_win", dt, ks, d.win_token_stride, dev)
     _check(lib.gdn_attn_rope(
         ctypes.byref(d), rope._args((qt, qh, kt, kh)), *rope._at, qp, kp, vp,
         _arg(seq_len, "seq_len", _I32, (d.n_slots,), dev, True), _arg(prefix_of, "prefix_of", _I32, (B,), dev, True),
@@ -419,9 +442,7 @@ def gdn_kv_append(dims: KvDims, layer, rope: Rope, cu_seqlens, q, k, v, position
     _on_device(v_cache, "v_cache", dev)
     qp, qt, qh = (None, 0, 0) if q is None else _heads(q, "q", dt, (N, Hq, D), dev)
     kp, kt, kh = _heads(k, "k", dt, (N, Hkv, D), dev)
-    vp, vt, vh = _heads(v, "v", dt, (N, Hkv, D), dev)
-    if vt != kt or vh != kh:
-        raise ValueError(f"k and v have different strides: {k.stride()} and {v.stride()}")
+    vp, kt, kh = _beside(k, kt, kh, v, dt, (N, Hkv, D), dev)
     q_to = None if q_out is None else _out_rows(q_out, "q_out", dt, (N, Hq, D), d.q_token_stride, dev)
     _check(lib.gdn_kv_append(
         ctypes.byref(d), layer, rope._args((qt, qh, kt, kh)), *rope._at, N, _arg(cu_seqlens, "cu_seqlens", _I32, (d.B + 1,), dev),
