@@ -307,3 +307,49 @@ def test_what_few_rows_do_not_see_may_hold_anything():
     got = attend(pool, cu, q, True, table=table)
     assert gdn.gdn_device_status(clear=True) == kv.DEVERR_KV_PAGE
     assert all(torch.equal(a[:1], b[:1]) and torch.equal(a[3:], b[3:]) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,lens,new,plen,causal", [
+    (128, 16, 4, [40000], [300], 0, True), (128, 16, 4, [21000, 20500], [290, 512], 0, True),
+    (64, 16, 8, [33000], [513], 0, False), (64, 12, 4, [17000, 16801, 17300], [200, 333, 257], 65000, True),
+    (128, 6, 2, [70001], [170], 0, True)])
+def test_late_chunks(D, Hq, Hkv, lens, new, plen, causal):
+    """Few items over many keys, each cut over several CTAs, against float64 row by row."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(D + len(lens))
+    ps, G = 64, Hq // Hkv
+    slots = lens + ([plen] if plen else [])
+    pages = [-(-n // ps) for n in slots]
+    ids = torch.randperm(sum(pages), generator=gen, device="cuda").int()
+    table = torch.full((len(slots), max(pages)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for s, n in enumerate(pages):
+        table[s, :n] = ids[at:at + n]
+        at += n
+    k, v = (torch.empty((1, sum(pages), ps, Hkv, D), dtype=BF, device="cuda").normal_(generator=gen) for _ in range(2))
+    cu = np.concatenate([[0], np.cumsum(new)])
+    q = torch.empty((int(cu[-1]), Hq, D), dtype=BF, device="cuda").normal_(0.0, 2.0, generator=gen)
+    d = kv.make_kv_dims(len(lens), 1, Hq, Hkv, D, ps, sum(pages), max(pages), len(slots))
+    ws = kv.alloc_attn_prefill_workspace(d, q.shape[0])
+    pre = i32([len(lens)] * len(lens)) if plen else None
+    runs = []
+    for fill in (255, 0):
+        ws.fill_(fill)
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], dtype=torch.float32, device="cuda")
+        kv.gdn_attn_prefill(d, 0, i32(cu), q, k, v, table, i32(slots), pre, causal, D ** -0.5, out, lse, ws)
+        runs.append((out, lse))
+    assert gdn.gdn_device_status(clear=True) == 0
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+    for b, n in enumerate(lens):
+        order = ([len(lens)] if plen else []) + [b]
+        kb, vb = (torch.cat([x[0, table[s, :pages[s]].long()].flatten(0, 1)[:slots[s]] for s in order]).double() for x in (k, v))
+        lo, hi = int(cu[b]), int(cu[b + 1])
+        mask = torch.ones((hi - lo, kb.shape[0]), dtype=torch.bool, device="cuda")
+        if causal:
+            mask = mask.tril(kb.shape[0] - (hi - lo))
+        for h in range(Hq):
+            x = (q[lo:hi, h].double() @ kb[:, h // G].T * D ** -0.5).masked_fill(~mask, float("-inf"))
+            w = torch.softmax(x, 1)
+            ref, mag = w @ vb[:, h // G], w @ vb[:, h // G].abs()
+            assert ((out[lo:hi, h].double() - ref).abs() <= ROUND[BF] * (mag + ref.abs()) + 2e-4 * mag).all(), (b, h)
+            assert (lse[lo:hi, h].double() - torch.logsumexp(x, 1)).abs().max() <= 1e-4
