@@ -24,8 +24,9 @@
 // the clock):
 //   prompts of 4096..16384 tokens, Hq=32 Hkv=8 D=128     3.18 ms, 1300 TFLOP/s: the chain scores, softmax, products of a
 //     stream (a pair of tiles in 1.9 us) at the power cap
-//   512 tokens behind 65536, Hq=32 Hkv=8 D=128           413 us, 1340 TFLOP/s; its 64 items read the same keys at
-//     different times, so 2.2 GB come from HBM where 0.28 would do
+//   512 tokens behind 65536, Hq=32 Hkv=8 D=128           413 us, 1340 TFLOP/s: the same chain (359 with half of the
+//     softmax left out).  Its 64 items read the same keys at different times, 2.2 GB from HBM where 0.28 would do; reading
+//     them together (stretches dealt in rounds) gave 408, and 130 for 119 behind 16384
 //   13 prompts of 1..901 tokens behind 1531 shared and 0..333 own, f16 Hq=24 Hkv=4 D=64   118 us, 610 TFLOP/s: the warp
 //     that issues the products, a pair of tiles in 1.4 us; start, ends of segments and join 25 us
 //   24 prompts of 3..448 tokens over 400..1500 states, Hq=Hkv=16 D=64   61 us: start, ends of 4.6 segments a CTA, join
