@@ -163,8 +163,8 @@ gdn_status gdn_kv_compact(const gdn_kv_dims* dims, void* k_cache, void* v_cache,
                           int32_t* n_live, void* workspace, uint64_t workspace_bytes, gdn_stream_t stream);
 
 /*
- * Bytes of workspace for `dims` that serve gdn_kv_commit, gdn_kv_fork and gdn_kv_compact alike.  The
- * last two do not read B: what B = 0 gives is enough for them.
+ * Bytes of workspace for `dims` that serve gdn_kv_commit, gdn_kv_reserve, gdn_kv_fork and gdn_kv_compact
+ * alike.  The last two do not read B: what B = 0 gives is enough for them.
  */
 gdn_status gdn_kv_workspace_size(const gdn_kv_dims* dims, uint64_t* bytes);
 

@@ -162,7 +162,7 @@ def gdn_attn_workspace_size(dims: KvDims) -> int:
 
 
 def gdn_kv_workspace_size(dims: KvDims) -> int:
-    """Bytes of device scratch gdn_kv_commit, gdn_kv_fork and gdn_kv_compact need for these dims."""
+    """Bytes of device scratch gdn_kv_commit, gdn_kv_reserve, gdn_kv_fork and gdn_kv_compact need for these dims."""
     return _size(load_library().gdn_kv_workspace_size, dims)
 
 

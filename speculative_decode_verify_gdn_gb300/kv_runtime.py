@@ -61,7 +61,8 @@ class PagedCache:
                    torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device),
                    [ints(n_slots, max_pages, fill=-1) for _ in range(2)], [ints(n_slots) for _ in range(2)],
                    ints(n_pages), ints(B, fill=-1), ints(1), dims, kv.alloc_attn_workspace(dims, device),
-                   kv.alloc_kv_workspace(dims, device),
+                   kv.alloc_kv_workspace(kv.make_kv_dims(n_slots, K, Hq, Hkv, D, page_size, n_pages, max_pages, n_slots, 0, n_layers,
+                                                         dtype), device),  # (reserve takes any of the slots)
                    (ints(B), torch.empty(B, dtype=torch.bool, device=device), ints(B),
                     torch.arange(B, dtype=torch.int32, device=device), ints(n_slots, fill=-1)),
                    kv.alloc_attn_prefill_workspace(dims, 0, device))
@@ -121,7 +122,11 @@ class PagedCache:
 
     def _prefixes(self, slot0, n):
         """Prefixes of the sequences from slot0 on (the prefixes' own slots have none)."""
-        return self.prefix_of[slot0:slot0 + n] if self.n_prefixes and slot0 + n <= self.B else None
+        if not self.n_prefixes or slot0 >= self.B:
+            return None
+        if slot0 + n > self.B:
+            raise ValueError(f"slots {slot0}..{slot0 + n - 1} are sequences and prefixes (from {self.B} on): one call for each")
+        return self.prefix_of[slot0:slot0 + n]
 
     def attend(self, layer, q, k_win, v_win, out, lse=None, parent=None, win_len=None, scale=None, stream=None) -> None:
         """The window's attention in one layer (a chain, or a token tree given by parent [B, K])."""

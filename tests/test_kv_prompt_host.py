@@ -11,6 +11,7 @@ import pytest
 
 from oracle import prompt_oracle as O
 from speculative_decode_verify_gdn_gb300 import build, gdn, kv, rope
+from speculative_decode_verify_gdn_gb300.kv_runtime import PagedCache
 
 torch = pytest.importorskip("torch")
 INV, UNS, ALIAS = gdn.GDN_ERR_INVALID_ARG, gdn.GDN_ERR_UNSUPPORTED, gdn.GDN_ERR_ALIAS
@@ -376,3 +377,29 @@ def test_prefill_oracle_against_a_masked_softmax():
             assert np.allclose(out[:3, h], w @ v[:, h // 2]) and np.allclose(lse[:3, h], np.log(np.exp(x).sum(1)))
     out, lse = O.attention([0, 3], q[:3], ck, cv, table, np.array([1, 0]), None, True, 1.0)
     assert (out[:2] == 0).all() and np.isneginf(lse[:2]).all() and np.allclose(out[2, 0], cv[3, 0, 0])
+
+
+def test_cache_calls_on_sequences_and_prefixes(monkeypatch):
+    """Prompts of sequences take their prefixes along, and those of prefixes have none.  One call on both kinds, whose
+    prefixes are no slice, is refused; pages for all slots at once fit the cache's workspace."""
+    build.build_library()
+    seen = []
+    monkeypatch.setattr(kv, "gdn_kv_append", lambda *args: seen.append(args[-3]))
+    monkeypatch.setattr(kv, "gdn_attn_prefill", lambda *args: seen.append(args[8]))
+    c = PagedCache.create(40, 1, 2, 1, 64, 16, n_pages=20, max_pages=4, n_prefixes=60, device="cpu")
+    c.prefix_of.copy_(torch.arange(40, dtype=torch.int32) + 40)
+    rows = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+
+    def both(n, slot0):
+        cu = torch.zeros(n + 1, dtype=torch.int32)
+        c.append_layer(0, None, cu, rows, rows[:, :1], rows[:, :1], rows, slot0=slot0)
+        c.attend_prefill(0, cu, rows, torch.empty_like(rows), slot0=slot0)
+        return seen[-2:]
+
+    for n, slot0 in ((40, 0), (3, 37), (1, 0)):
+        assert all(p.tolist() == list(range(40 + slot0, 40 + slot0 + n)) for p in both(n, slot0))
+    assert both(60, 40) == [None, None] and both(1, 99) == [None, None]
+    for n, slot0 in ((41, 0), (2, 39), (100, 0)):
+        with pytest.raises(ValueError, match="prefixes"):
+            both(n, slot0)
+    assert c.pool_workspace.numel() >= kv.gdn_kv_workspace_size(c._dims(100))
