@@ -263,7 +263,7 @@ gdn_status gdn_kv_append(const gdn_kv_dims* dims, int32_t layer, const gdn_rope*
  *   out        [n_tokens, Hq, D] contiguous, dtype; lse [n_tokens, Hq] f32 or NULL
  *   workspace  at least gdn_attn_prefill_workspace_size() bytes, no initialisation needed, dead after the call
  * Rounding as in gdn_attn_verify.  What the cache holds beyond a slot's tokens reaches no output; a value
- * that is not finite at a token of a slot may reach every row of the sequences that read the slot.
+ * that is not finite at a token of a slot may reach every row with keys of the sequences that read the slot.
  * Results do not depend on the order in which CTAs run.  dims: K and win_token_stride are not read.
  */
 gdn_status gdn_attn_prefill(const gdn_kv_dims* dims, int32_t layer, int64_t n_tokens, const int32_t* cu_seqlens,

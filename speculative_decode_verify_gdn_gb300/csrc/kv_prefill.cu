@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int j = 0; j < 32; ++j) o[j] = (w_own == 0.f ? 0.f : o[j] * f_own) + (w_other == 0.f ? 0.f : x[j] * f_other);
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] *= inv;
+            for (int j = 0; j < 32; ++j) o[j] = sum == 0.f ? 0.f : o[j] * inv;  // (a row without keys is 0, whatever values others see)
           }
           if (r < rows) {
             if (seg.part < 0) {
@@ -1043,7 +1043,7 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(D))
         for (int i = 0; i < CV; ++i) {
           float y[8];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) y[2 * x] = o[i][x][u] * f, y[2 * x + 1] = o[i][x][2 + u] * f;
+          for (int x = 0; x < 4; ++x) y[2 * x] = f == 0.f ? 0.f : o[i][x][u] * f, y[2 * x + 1] = f == 0.f ? 0.f : o[i][x][2 + u] * f;
           if (seg.part >= 0)
             store8(w.o + (long long)(seg.part + r) * D + 64 * i + 8 * n, y);
           else

@@ -353,3 +353,21 @@ def test_late_chunks(D, Hq, Hkv, lens, new, plen, causal):
             ref, mag = w @ vb[:, h // G], w @ vb[:, h // G].abs()
             assert ((out[lo:hi, h].double() - ref).abs() <= ROUND[BF] * (mag + ref.abs()) + 2e-4 * mag).all(), (b, h)
             assert (lse[lo:hi, h].double() - torch.logsumexp(x, 1)).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("new,lens,G", [([5], [2], 1), ([200], [60], 4), ([300, 2], [290, 1], 2), ([3, 4], [1, 300], 2), ([200], [199], 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_without_keys_do_not_meet_values_of_others(D, new, lens, G):
+    """Rows before the slot's first token get 0 and -inf, also where the value of a token that others see is not finite."""
+    pool = Pool(83, lens, D=D, ps=32, Hkv=1)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    q = pool.gauss((int(cu[-1]), G, D), 2.0)
+    for bad in (NAN, float("inf")):
+        for s, n in enumerate(lens):
+            pool.v[0, pool.table[s, (n - 1) // 32], (n - 1) % 32] = bad
+        out, lse = attend(pool, cu, q, True)
+        for s, n in enumerate(lens):
+            none = slice(int(cu[s]), int(cu[s]) + max(0, new[s] - n))
+            assert (out[none] == 0).all() and torch.isneginf(lse[none]).all()
+            own = int(cu[s + 1]) - 1
+            assert not torch.isfinite(out[own]).any() and torch.isfinite(lse[own]).all()
