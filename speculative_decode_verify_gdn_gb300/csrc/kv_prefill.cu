@@ -27,9 +27,9 @@
 //   512 tokens behind 65536, Hq=32 Hkv=8 D=128           413 us, 1340 TFLOP/s: the same chain (359 with half of the
 //     softmax left out).  Its 64 items read the same keys at different times, 2.2 GB from HBM where 0.28 would do; reading
 //     them together (stretches dealt in rounds) gave 408, and 130 for 119 behind 16384
-//   13 prompts of 1..901 tokens behind 1531 shared and 0..333 own, f16 Hq=24 Hkv=4 D=64   118 us, 610 TFLOP/s: the warp
-//     that issues the products, a pair of tiles in 1.4 us; start, ends of segments and join 25 us
-//   24 prompts of 3..448 tokens over 400..1500 states, Hq=Hkv=16 D=64   61 us: start, ends of 4.6 segments a CTA, join
+//   13 prompts of 1..901 tokens behind 1531 shared and 0..333 own, f16 Hq=24 Hkv=4 D=64   113 us, 640 TFLOP/s: the warp
+//     that issues the products, a pair of tiles in 1.4 us; start, ends of segments and join 20 us
+//   24 prompts of 3..448 tokens over 400..1500 states, Hq=Hkv=16 D=64   59 us: start, ends of 4.6 segments a CTA, join
 //   64 single tokens over 1..1500 states, f16 Hq=Hkv=16 D=64   45 us, 4.4 TB/s (few rows)
 //   one prompt of 37 tokens   14 us: the host's two launches and its four tensor maps
 #include <atomic>
@@ -42,15 +42,18 @@ namespace gdn {
 
 namespace {
 
-constexpr int kJoinWarps = 8, kJoinChunks = 16;  // CTAs to a cut item of the tile kernel (cross attention of prompts 61 us, 63 with 8, 71 with 4, 62 with 32)
+constexpr int kJoinAlone = 4;   // pieces that the CTAs of one worker join by themselves
+constexpr int kJoinChunks = 8;  // CTAs of the join to a CTA of the tile kernel (cross attention of prompts 59 us, 61 with 4, 60 with 16)
 constexpr int kFewRows = 8;     // rows of a block of the kernel for few rows
 constexpr int kFewThreads = 128;
 __host__ __device__ constexpr int few_ctas(int D) { return D == 128 ? 3 : 4; }  // CTAs to an SM
 __host__ __device__ constexpr int few_workers(int D) { return kCtas * few_ctas(D) * (kFewThreads / 32); }
 
-struct JoinRec {       // a cut item, by the worker c0 that it begins with; it ends with worker c1
+struct alignas(16) JoinRec {  // of worker c: a cut item that begins in its stretch and ends in that of worker `end`
   int32_t tok0, rows;  // rows 0: there is none
-  int32_t h, c0, c1, part0;
+  int32_t h, end, part0;
+  int32_t before;      // the worker in whose stretch the item began that its own begins within; -1: it does not
+  int32_t spare[2];
 };
 
 struct PackedWs {
@@ -258,7 +261,7 @@ struct SegWalk {
   const int id, lane, G;
   long long begin, x, end;
   int h, b, k, t_in;  // the item at hand: kv head, sequence, block; its tiles before x
-  int from;
+  int from, before_me;
   SeqRows mine;
   __device__ __forceinline__ SeqRows sequence(int i) {
     if (i < from || i >= from + 32) {
@@ -278,9 +281,11 @@ struct SegWalk {
       : p(p_), w(w_), cut(cut_), plan(plan_), id(id_), lane(lane_), G(p_.d.Hq / p_.d.Hkv) {
     begin = x = end = 0;
     h = b = k = t_in = 0;
-    from = -64;
-    if (lane == 0) w.join[id].rows = 0;
-    if (id >= plan.workers) return;
+    from = -64, before_me = -1;
+    if (id >= plan.workers) {
+      if (lane == 0) w.join[id].rows = 0, w.join[id].before = -1;
+      return;
+    }
     begin = x = plan.begin(id), end = plan.begin(id + 1);
     h = int(begin / plan.head_tiles);
     long long y = begin - h * plan.head_tiles;
@@ -308,6 +313,8 @@ struct SegWalk {
       n = n - j * step < step ? n - j * step : step;
     }
     t_in = int(y - s.tiles(cut, k));
+    if (t_in > 0) before_me = plan.worker_of(begin - t_in);
+    if (lane == 0) w.join[id].rows = 0, w.join[id].before = before_me;
   }
   __device__ __forceinline__ bool next(Seg& g) {
     if (x >= end) return false;
@@ -334,7 +341,7 @@ struct SegWalk {
       const int second = x == begin ? 0 : 1;  // (of the worker's pieces: one that its stretch begins with, one that it ends with)
       g.part = g.t0 == 0 && g.t1 == tiles ? -1 : (2 * id + second) * ROWS;
       if (g.t0 == 0 && g.t1 < tiles && lane == 0)
-        w.join[id] = JoinRec{g.tok0, g.rows, h, id, plan.worker_of(x + tiles - 1), g.part};
+        w.join[id] = JoinRec{g.tok0, g.rows, h, plan.worker_of(x + tiles - 1), g.part, before_me, {0, 0}};
       x += g.t1 - g.t0;
       t_in = 0, ++k;  // (an item that goes on ends the stretch)
       return true;
@@ -1056,70 +1063,119 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas(D))
 }
 
 // ---------------------------------------------------------------- join
-// `chunks` CTAs for each worker, if a cut item begins in its stretch: a warp takes a row at a time, its pieces'
-// log-sum-exps and, on their way with them, the first pieces' sums.
-template <int D, bool F16, int ROWS>
-__global__ void __launch_bounds__(32 * kJoinWarps) packed_join_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w, const int chunks) {
-  constexpr int N = D / 32, U = 4;
+// `chunks` CTAs for every PER workers.  An item of a few pieces is joined by those of the worker that it begins with, one of many
+// by those of all its workers together.  D / 8 lanes sum a row's pieces; 2, 4, .. such groups of a CTA share a row where pieces
+// are many and the rows do not keep all groups busy, and their sums are joined in shared memory.  Bound: the trips to L2 (the
+// item, its pieces) and the start of its CTAs.  A warp to each row, all by the CTAs of the item's first worker, took 119 us where
+// this takes 113 (prompts of 1..901 tokens behind 1531 shared and 0..333 own), 71 where this takes 54 (a token behind 65536, Hq=32
+// Hkv=8 D=128) and 195 where this takes 35 (Hq=8 Hkv=1).
+template <int D, bool F16, int ROWS, int THREADS, int PER>
+__global__ void __launch_bounds__(THREADS) packed_join_kernel(const __grid_constant__ PackedAttnParams p, const __grid_constant__ PackedWs w, const int chunks) {
+  constexpr int LANES = D / 8, GROUPS = THREADS / LANES, U = ROWS == kFewRows ? 4 : 2;  // (pieces in flight: more are more registers)
+  __shared__ float4 sums[GROUPS][2][LANES];
+  __shared__ float2 weights[GROUPS];
   pdl_launch_dependents();
   pdl_wait();
   const gdn_kv_dims& d = p.d;
-  const JoinRec rec = w.join[blockIdx.x / unsigned(chunks)];
-  const int G = d.Hq / d.Hkv, lane = threadIdx.x & 31;
-  const int parts = rec.rows > 0 ? rec.c1 - rec.c0 + 1 : 0;
-  for (int r = int(blockIdx.x % unsigned(chunks)) * kJoinWarps + int(threadIdx.x >> 5); r < rec.rows; r += kJoinWarps * chunks) {
+  __shared__ JoinRec recs[PER + 1];
+  __shared__ int begins[PER + 1];  // the workers that the items begin with
+  const int me = int(blockIdx.x) / chunks, chunk = int(blockIdx.x) - me * chunks;  // of the CTAs of workers PER me .. PER me + PER - 1
+  const int G = d.Hq / d.Hkv, lane = int(threadIdx.x) % LANES, group = int(threadIdx.x) / LANES;
+  if (int(threadIdx.x) < PER) {
+    const int c = PER * me + int(threadIdx.x);
+    const JoinRec rec = w.join[c];
+    recs[threadIdx.x] = rec, begins[threadIdx.x] = c;
+    if (threadIdx.x == 0) {
+      JoinRec other{};
+      if (rec.before >= 0) other = w.join[rec.before];
+      recs[PER] = other, begins[PER] = rec.before;
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i <= PER; ++i) {
+    const JoinRec rec = recs[i];
+    if (rec.rows == 0) continue;
+    const int c0 = begins[i], parts = rec.end - c0 + 1, first = c0 / PER;
+    const int ctas = (parts > kJoinAlone ? rec.end / PER - first + 1 : 1) * chunks, cta = (me - first) * chunks + chunk;
+    if (cta >= ctas) continue;
+    int log = 0;
+    while ((1 << log) < GROUPS && (rec.rows << (log + 1)) <= ctas * GROUPS && (8 << log) <= parts) ++log;
+    const int split = 1 << log, s = group & (split - 1), each = (parts + split - 1) >> log, rows = GROUPS >> log;
     // piece j's row: the first worker's piece, then the one that each stretch begins with
-    auto at = [&](int j) { return (j == 0 ? rec.part0 : 2 * (rec.c0 + j) * ROWS) + r; };
-    float acc[N], v[U][N];
-    auto load = [&](int j0, int end) {
+    for (int r0 = cta * rows; r0 < rec.rows; r0 += ctas * rows) {
+      const int r = r0 + (group >> log);
+      auto at = [&](int j) { return (j == 0 ? rec.part0 : 2 * (c0 + j) * ROWS) + r; };
+      const int mine = r < rec.rows ? parts : 0;
+      float4 v[U][2];
+      auto load = [&](int i0) {  // this group's pieces i0, i0 + 1, ..
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (j0 + u < end) {
-          const float* o = w.o + (long long)at(j0 + u) * D + lane * N;
-          if (N == 4)
-            *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(o);
-          else
-            *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(o);
-        }
-    };
+        for (int u = 0; u < U; ++u)
+          if (s + split * (i0 + u) < mine) {
+            const float4* o = reinterpret_cast<const float4*>(w.o + (long long)at(s + split * (i0 + u)) * D) + 2 * lane;
+            v[u][0] = o[0], v[u][1] = o[1];
+          }
+      };
+      float acc[8];
 #pragma unroll
-    for (int k = 0; k < N; ++k) acc[k] = 0.f;
-    float M = -INFINITY, W = 0.f;
-    for (int j0 = 0; j0 < parts; j0 += 32) {
-      const int n = parts - j0 < 32 ? parts - j0 : 32;
-      const float e = lane < n ? w.lse[at(j0 + lane)] : -INFINITY;
-      load(j0, j0 + n);
-      float mx = e;
+      for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+      float M = -INFINITY, W = 0.f;
+      for (int b0 = 0; b0 < each; b0 += LANES) {
+        const int j = s + split * (b0 + lane), n = each - b0 < LANES ? each - b0 : LANES;
+        const float e = j < mine ? w.lse[at(j)] : -INFINITY;
+        load(b0);
+        float mx = e;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float Mn = fmaxf(M, mx), f = M == -INFINITY ? 0.f : exp2f(M - Mn);
-      const float wt = e == -INFINITY ? 0.f : exp2f(e - (Mn == -INFINITY ? 0.f : Mn));  // (NaN stays NaN)
-      M = Mn;
-      W = W * f + warp_sum(wt);
+        for (int o = LANES / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float Mn = fmaxf(M, mx), f = M == -INFINITY ? 0.f : exp2_fast(M - Mn);
+        const float wt = e == -INFINITY ? 0.f : exp2_fast(e - (Mn == -INFINITY ? 0.f : Mn));  // (NaN stays NaN)
+        float all = wt;
 #pragma unroll
-      for (int k = 0; k < N; ++k) acc[k] *= f;
-      for (int i0 = 0; i0 < n; i0 += U) {
-        if (i0 > 0) load(j0 + i0, j0 + n);
+        for (int o = LANES / 2; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        M = Mn, W = W * f + all;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float wj = __shfl_sync(0xffffffffu, wt, (i0 + u) & 31);
-          if (i0 + u < n && wj != 0.f)
+        for (int k = 0; k < 8; ++k) acc[k] *= f;
+        for (int i0 = 0; i0 < n; i0 += U) {
+          if (i0 > 0) load(b0 + i0);
 #pragma unroll
-            for (int k = 0; k < N; ++k) acc[k] += wj * v[u][k];
+          for (int u = 0; u < U; ++u) {
+            const float wj = i0 + u < n ? __shfl_sync(0xffffffffu, wt, i0 + u, LANES) : 0.f;
+            if (wj != 0.f) {
+              acc[0] += wj * v[u][0].x, acc[1] += wj * v[u][0].y, acc[2] += wj * v[u][0].z, acc[3] += wj * v[u][0].w;
+              acc[4] += wj * v[u][1].x, acc[5] += wj * v[u][1].y, acc[6] += wj * v[u][1].z, acc[7] += wj * v[u][1].w;
+            }
+          }
         }
       }
-    }
-    const float inv = W == 0.f ? 0.f : 1.f / W;
+      if (split > 1) {
+        __syncthreads();
+        sums[group][0][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]), sums[group][1][lane] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (lane == 0) weights[group] = make_float2(M, W);
+        __syncthreads();
+        if (s == 0) {
+          for (int x = 1; x < split; ++x) M = fmaxf(M, weights[group + x].x);
+          W = 0.f;
 #pragma unroll
-    for (int k = 0; k < N; ++k) acc[k] *= inv;
-    const int tok = r / G;
-    const long long row = (long long)(rec.tok0 + tok) * d.Hq + rec.h * G + (r - tok * G);
-    uint32_t* const o = reinterpret_cast<uint32_t*>(p.out + row * D) + lane * (N / 2);
-    if (N == 4)
-      *reinterpret_cast<uint2*>(o) = make_uint2(pack2<F16>(acc[0], acc[1]), pack2<F16>(acc[N - 2], acc[N - 1]));
-    else
-      *o = pack2<F16>(acc[0], acc[1]);
-    if (p.lse && lane == 0) p.lse[row] = W == 0.f ? -INFINITY : (M + log2f(W)) * kLn2;
+          for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+          for (int x = 0; x < split; ++x) {
+            const float2 mw = weights[group + x];
+            const float f = mw.x == -INFINITY ? 0.f : exp2_fast(mw.x - M);
+            const float4 a = sums[group + x][0][lane], b = sums[group + x][1][lane];
+            W += f * mw.y;
+            acc[0] += f * a.x, acc[1] += f * a.y, acc[2] += f * a.z, acc[3] += f * a.w;
+            acc[4] += f * b.x, acc[5] += f * b.y, acc[6] += f * b.z, acc[7] += f * b.w;
+          }
+        }
+      }
+      if (s != 0 || r >= rec.rows) continue;
+      const float inv = W == 0.f ? 0.f : __fdividef(1.f, W);
+      const int tok = r / G;
+      const long long row = (long long)(rec.tok0 + tok) * d.Hq + rec.h * G + (r - tok * G);
+      *reinterpret_cast<uint4*>(p.out + row * D + 8 * lane) =
+          make_uint4(pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv), pack2<F16>(acc[4] * inv, acc[5] * inv),
+                     pack2<F16>(acc[6] * inv, acc[7] * inv));
+      if (p.lse && lane == 0) p.lse[row] = W == 0.f ? -INFINITY : (M + log2f(W)) * kLn2;
+    }
   }
 }
 
@@ -1139,14 +1195,18 @@ cudaError_t launch(const PackedAttnParams& p, const PackedWs& w, const Cut& cut,
   }
   e = launch_dependent(packed_tile_kernel<D, F16>, unsigned(kCtas), kTileThreads, L::TOTAL, stream, p, w, cut, box, page_units_inv(p.d.page_size), maps);
   if (e != cudaSuccess) return e;
-  return launch_dependent(packed_join_kernel<D, F16, kBlockRows>, unsigned(kCtas * kJoinChunks), 32 * kJoinWarps, 0, stream, p, w, kJoinChunks);
+  return launch_dependent(packed_join_kernel<D, F16, kBlockRows, 256, 1>, unsigned(kCtas * kJoinChunks), 256, 0, stream, p, w, kJoinChunks);
 }
 
 template <int D, bool F16>
 cudaError_t launch_few(const PackedAttnParams& p, const PackedWs& w, const Cut& cut, cudaStream_t stream) {
   const cudaError_t e = launch_dependent(packed_few_kernel<D, F16>, unsigned(kCtas * few_ctas(D)), kFewThreads, 0, stream, p, w, cut, page_units_inv(p.d.page_size));
   if (e != cudaSuccess) return e;
-  return launch_dependent(packed_join_kernel<D, F16, kFewRows>, unsigned(cut.workers), 32 * kJoinWarps, 0, stream, p, w, 1);
+  // A token's items by wide CTAs for four workers, where they are few and in hundreds of pieces each, or by a small one for each
+  // worker: 8 items behind 65536 keys 54 and 59 us, one 35 and 79, but 16 (D = 64) 57 and 54, and 1024 of 1..1500 keys 49 and 45.
+  const long long blocks = p.n_tokens / cut.toks + p.d.B, items = (blocks < p.n_tokens ? blocks : p.n_tokens) * p.d.Hkv;  // at most
+  if (items <= 8) return launch_dependent(packed_join_kernel<D, F16, kFewRows, 256, 4>, unsigned(cut.workers / 4), 256, 0, stream, p, w, 1);
+  return launch_dependent(packed_join_kernel<D, F16, kFewRows, 64, 1>, unsigned(cut.workers), 64, 0, stream, p, w, 1);
 }
 
 // How rows are cut into blocks of `toks` tokens, and keys into tiles of 2^key_log, dealt to so many workers.

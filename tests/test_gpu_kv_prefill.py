@@ -371,3 +371,13 @@ def test_rows_without_keys_do_not_meet_values_of_others(D, new, lens, G):
             assert (out[none] == 0).all() and torch.isneginf(lse[none]).all()
             own = int(cu[s + 1]) - 1
             assert not torch.isfinite(out[own]).any() and torch.isfinite(lse[own]).all()
+
+
+@pytest.mark.parametrize("length", [40, 128, 129, 161, 300, 1000, 2049, 20000, 60001])
+@pytest.mark.parametrize("D,Hq,Hkv,B", [(128, 8, 1, 1), (64, 3, 3, 1), (128, 32, 8, 1), (64, 32, 4, 2), (128, 18, 9, 1), (64, 16, 16, 2)])
+def test_a_token_in_many_pieces(D, Hq, Hkv, B, length):
+    """Single tokens, whose keys are dealt to so many warps that a few or all of the join's CTAs share their pieces."""
+    lens = [length, 77][:B]
+    pool, cu, q, out, lse = run_case(84, [1] * B, lens, Hq, D=D, Hkv=Hkv, ps=64)
+    again, lse2 = attend(pool, cu, q, True)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
