@@ -22,14 +22,14 @@
 //
 // Measured on one GB300, calls in a row (peaks: 6702 GB/s copy, 1903 TFLOP/s cuBLAS bf16, 1728 when the power cap sets
 // the clock):
-//   prompts of 4096..16384 tokens, Hq=32 Hkv=8 D=128     3.18 ms, 1300 TFLOP/s: the chain scores, softmax, products of a
+//   prompts of 4096..16384 tokens, Hq=32 Hkv=8 D=128     3.0-3.1 ms, 1350 TFLOP/s: the chain scores, softmax, products of a
 //     stream (a pair of tiles in 1.9 us) at the power cap
-//   512 tokens behind 65536, Hq=32 Hkv=8 D=128           413 us, 1340 TFLOP/s: the same chain (359 with half of the
+//   512 tokens behind 65536, Hq=32 Hkv=8 D=128           387-411 us, 1340-1430 TFLOP/s: the same chain (14 % less with half of the
 //     softmax left out).  Its 64 items read the same keys at different times, 2.2 GB from HBM where 0.28 would do; reading
 //     them together (stretches dealt in rounds) gave 408, and 130 for 119 behind 16384
-//   13 prompts of 1..901 tokens behind 1531 shared and 0..333 own, f16 Hq=24 Hkv=4 D=64   113 us, 640 TFLOP/s: the warp
+//   13 prompts of 1..901 tokens behind 1531 shared and 0..333 own, f16 Hq=24 Hkv=4 D=64   110 us, 660 TFLOP/s: the warp
 //     that issues the products, a pair of tiles in 1.4 us; start, ends of segments and join 20 us
-//   24 prompts of 3..448 tokens over 400..1500 states, Hq=Hkv=16 D=64   59 us: start, ends of 4.6 segments a CTA, join
+//   24 prompts of 3..448 tokens over 400..1500 states, Hq=Hkv=16 D=64   57.5 us: start, ends of 4.6 segments a CTA, join
 //   64 single tokens over 1..1500 states, f16 Hq=Hkv=16 D=64   45 us, 4.4 TB/s (few rows)
 //   one prompt of 37 tokens   14 us: the host's two launches and its four tensor maps
 #include <atomic>
