@@ -225,10 +225,19 @@ gdn_status gdn_attn_rope(const gdn_kv_dims* dims, const gdn_rope* rope, const ui
  * gdn_kv_commit: a sequence that gets no pages (GDN_DEVERR_KV_FULL), whose last page is shared
  * (GDN_DEVERR_KV_SHARED) or whose n_new is out of range (GDN_DEVERR_KV_LEN) is left unchanged.
  * dims: K, Hq and the strides are checked as by gdn_kv_fork; the workspace is gdn_kv_workspace_size's.
+ *
+ * Which sequences were left unchanged is known on the device alone, and the last tokens of such a slot are not the
+ * ones that were to follow.  gdn_kv_reserve_marked notes them for the calls that come after it, the _marked ones:
+ *   refused    [n_slots] int32, or NULL: entry slot0 + b becomes -1 if the sequence got its tokens (or n_new[b] is 0),
+ *              else the slot's length.  The other slots' entries are left as they are; -1 to begin with.
+ * A slot whose length is still its entry of refused has not grown since.
  */
 gdn_status gdn_kv_reserve(const gdn_kv_dims* dims, const int32_t* n_new, const int32_t* table_in, int32_t* table_out,
                           const int32_t* len_in, int32_t* len_out, const int32_t* ref_in, int32_t* ref_out,
                           void* workspace, uint64_t workspace_bytes, gdn_stream_t stream);
+gdn_status gdn_kv_reserve_marked(const gdn_kv_dims* dims, const int32_t* n_new, const int32_t* table_in, int32_t* table_out,
+                                 const int32_t* len_in, int32_t* len_out, const int32_t* ref_in, int32_t* ref_out,
+                                 int32_t* refused, void* workspace, uint64_t workspace_bytes, gdn_stream_t stream);
 
 /*
  * Append: one layer's packed new tokens.  Tokens cu_seqlens[b] .. cu_seqlens[b+1] - 1 are the last ones of
@@ -242,12 +251,21 @@ gdn_status gdn_kv_reserve(const gdn_kv_dims* dims, const int32_t* n_new, const i
  *   k_cache, v_cache  written, as described above; q_out may be q as in gdn_attn_rope
  * A sequence with more tokens than its slot holds is not written (GDN_DEVERR_KV_LEN), nor are keys and values of
  * a token on a page outside the pool (GDN_DEVERR_KV_PAGE).  dims: K and win_token_stride are not read.
+ * gdn_kv_append takes the slots' last tokens as they are: the caller knows that each sequence has got its room, or it
+ * overwrites tokens that are cached, also for the sequences that share their pages.  gdn_kv_append_marked does not
+ * rely on it: a sequence whose slot's length is refused[slot0 + b] is not written, q_out neither (GDN_DEVERR_KV_LEN).
  */
 gdn_status gdn_kv_append(const gdn_kv_dims* dims, int32_t layer, const gdn_rope* rope, const uint64_t* turns,
                          const float* q_weight, const float* k_weight, int64_t n_tokens, const int32_t* cu_seqlens,
                          const void* q, const void* k, const void* v, const int32_t* positions, void* k_cache,
                          void* v_cache, const int32_t* page_table, const int32_t* seq_len, const int32_t* prefix_of,
                          void* q_out, gdn_stream_t stream);
+gdn_status gdn_kv_append_marked(const gdn_kv_dims* dims, int32_t layer, const gdn_rope* rope, const uint64_t* turns,
+                                const float* q_weight, const float* k_weight, int64_t n_tokens,
+                                const int32_t* cu_seqlens, const void* q, const void* k, const void* v,
+                                const int32_t* positions, void* k_cache, void* v_cache, const int32_t* page_table,
+                                const int32_t* seq_len, const int32_t* refused, const int32_t* prefix_of, void* q_out,
+                                gdn_stream_t stream);
 
 /*
  * Attention of packed queries over the cache, one layer.  Row (token j of the n of sequence b, h) attends to
@@ -265,11 +283,18 @@ gdn_status gdn_kv_append(const gdn_kv_dims* dims, int32_t layer, const gdn_rope*
  * Rounding as in gdn_attn_verify.  What the cache holds beyond a slot's tokens reaches no output; a value
  * that is not finite at a token of a slot may reach every row with keys of the sequences that read the slot.
  * Results do not depend on the order in which CTAs run.  dims: K and win_token_stride are not read.
+ * gdn_attn_prefill_marked, where causal != 0: rows of a sequence whose slot's length is refused[slot0 + b] see nothing,
+ * not its prefix either, and get out 0 and lse -inf (GDN_DEVERR_KV_LEN).
  */
 gdn_status gdn_attn_prefill(const gdn_kv_dims* dims, int32_t layer, int64_t n_tokens, const int32_t* cu_seqlens,
                             const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
                             const int32_t* seq_len, const int32_t* prefix_of, int32_t causal, float scale, void* out,
                             float* lse, void* workspace, uint64_t workspace_bytes, gdn_stream_t stream);
+gdn_status gdn_attn_prefill_marked(const gdn_kv_dims* dims, int32_t layer, int64_t n_tokens,
+                                   const int32_t* cu_seqlens, const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* page_table, const int32_t* seq_len, const int32_t* refused,
+                                   const int32_t* prefix_of, int32_t causal, float scale, void* out, float* lse,
+                                   void* workspace, uint64_t workspace_bytes, gdn_stream_t stream);
 
 /* Bytes of workspace gdn_attn_prefill needs for `dims` and n_tokens rows (any lengths). */
 gdn_status gdn_attn_prefill_workspace_size(const gdn_kv_dims* dims, int64_t n_tokens, uint64_t* bytes);

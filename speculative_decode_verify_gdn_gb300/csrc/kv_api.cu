@@ -359,9 +359,9 @@ gdn_status gdn_kv_commit(const gdn_kv_dims* dims, const int32_t* accept_len, con
   return gdn::report_ok();
 }
 
-gdn_status gdn_kv_reserve(const gdn_kv_dims* dims, const int32_t* n_new, const int32_t* table_in, int32_t* table_out,
-                          const int32_t* len_in, int32_t* len_out, const int32_t* ref_in, int32_t* ref_out,
-                          void* workspace, uint64_t workspace_bytes, gdn_stream_t stream) {
+gdn_status gdn_kv_reserve_marked(const gdn_kv_dims* dims, const int32_t* n_new, const int32_t* table_in, int32_t* table_out,
+                                 const int32_t* len_in, int32_t* len_out, const int32_t* ref_in, int32_t* ref_out,
+                                 int32_t* refused, void* workspace, uint64_t workspace_bytes, gdn_stream_t stream) {
   GDN_RETURN_IF(check_dims(dims, kSlots, false));
   const gdn_kv_dims d = normal(*dims);
   const Buf bufs[] = {
@@ -372,6 +372,7 @@ gdn_status gdn_kv_reserve(const gdn_kv_dims* dims, const int32_t* n_new, const i
       {"table_out", table_out, 4ull * d.n_slots * d.max_pages, 4, true, false, bufs[1].name},
       {"len_out", len_out, 4ull * d.n_slots, 4, true, false, bufs[2].name},
       {"ref_out", ref_out, 4ull * d.n_pages, 4, true, false, bufs[3].name},
+      {"refused", refused, 4ull * d.n_slots, 4, true, true, nullptr},
       {"workspace", workspace, gdn::pages_workspace_bytes(d, d.B), 256, true, false, nullptr},
   };
   gdn::PagesParams p = pool_params(d, nullptr, nullptr, table_in, table_out, ref_in, ref_out, workspace);
@@ -379,9 +380,17 @@ gdn_status gdn_kv_reserve(const gdn_kv_dims* dims, const int32_t* n_new, const i
   p.accept = n_new;
   p.len_in = len_in;
   p.len_out = len_out;
+  p.refused = refused;
   const cudaError_t e = gdn::launch_reserve(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "reserve launch: %s", cudaGetErrorString(e));
   return gdn::report_ok();
+}
+
+gdn_status gdn_kv_reserve(const gdn_kv_dims* dims, const int32_t* n_new, const int32_t* table_in, int32_t* table_out,
+                          const int32_t* len_in, int32_t* len_out, const int32_t* ref_in, int32_t* ref_out,
+                          void* workspace, uint64_t workspace_bytes, gdn_stream_t stream) {
+  return gdn_kv_reserve_marked(dims, n_new, table_in, table_out, len_in, len_out, ref_in, ref_out, nullptr, workspace,
+                               workspace_bytes, stream);
 }
 
 gdn_status gdn_kv_fork(const gdn_kv_dims* dims, const int32_t* src, void* k_cache, void* v_cache,
@@ -502,11 +511,12 @@ gdn_status gdn_attn_rope(const gdn_kv_dims* dims, const gdn_rope* rope, const ui
   return gdn::report_ok();
 }
 
-gdn_status gdn_kv_append(const gdn_kv_dims* dims, int32_t layer, const gdn_rope* rope, const uint64_t* turns,
-                         const float* q_weight, const float* k_weight, int64_t n_tokens, const int32_t* cu_seqlens,
-                         const void* q, const void* k, const void* v, const int32_t* positions, void* k_cache,
-                         void* v_cache, const int32_t* page_table, const int32_t* seq_len, const int32_t* prefix_of,
-                         void* q_out, gdn_stream_t stream) {
+gdn_status gdn_kv_append_marked(const gdn_kv_dims* dims, int32_t layer, const gdn_rope* rope, const uint64_t* turns,
+                                const float* q_weight, const float* k_weight, int64_t n_tokens,
+                                const int32_t* cu_seqlens, const void* q, const void* k, const void* v,
+                                const int32_t* positions, void* k_cache, void* v_cache, const int32_t* page_table,
+                                const int32_t* seq_len, const int32_t* refused, const int32_t* prefix_of, void* q_out,
+                                gdn_stream_t stream) {
   GDN_RETURN_IF(check_dims(dims, kPacked, false));
   const gdn_kv_dims d = normal(*dims);
   GDN_RETURN_IF(check_cache_strides(d));
@@ -532,6 +542,7 @@ gdn_status gdn_kv_append(const gdn_kv_dims* dims, int32_t layer, const gdn_rope*
       {"cu_seqlens", cu_seqlens, 4ull * (d.B + 1), 4, false, false, nullptr},
       {"page_table", page_table, 4ull * d.n_slots * d.max_pages, 4, false, false, nullptr},
       {"seq_len", seq_len, 4ull * d.n_slots, 4, false, false, nullptr},
+      {"refused", refused, 4ull * d.n_slots, 4, false, true, nullptr},
       {"prefix_of", prefix_of, 4ull * d.B, 4, false, true, nullptr},
       {"positions", positions, 4ull * n, 4, false, true, nullptr},
       {"k_cache", k_cache, cache_bytes(d), 16, true, false, kInterleaved},
@@ -547,10 +558,20 @@ gdn_status gdn_kv_append(const gdn_kv_dims* dims, int32_t layer, const gdn_rope*
   p.k_out = static_cast<uint16_t*>(k_cache) + layer * d.cache_layer_stride;
   p.v_out = static_cast<uint16_t*>(v_cache) + layer * d.cache_layer_stride;
   p.seq_len = seq_len, p.prefix_of = prefix_of, p.positions = positions, p.cu = cu_seqlens, p.table = page_table;
+  p.refused = refused;
   p.n_tokens = int32_t(n), p.hq = q ? d.Hq : 0, p.hk = d.Hkv, p.hv = d.Hkv;
   const cudaError_t e = gdn::launch_append(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
   return gdn::report_ok();
+}
+
+gdn_status gdn_kv_append(const gdn_kv_dims* dims, int32_t layer, const gdn_rope* rope, const uint64_t* turns,
+                         const float* q_weight, const float* k_weight, int64_t n_tokens, const int32_t* cu_seqlens,
+                         const void* q, const void* k, const void* v, const int32_t* positions, void* k_cache,
+                         void* v_cache, const int32_t* page_table, const int32_t* seq_len, const int32_t* prefix_of,
+                         void* q_out, gdn_stream_t stream) {
+  return gdn_kv_append_marked(dims, layer, rope, turns, q_weight, k_weight, n_tokens, cu_seqlens, q, k, v, positions,
+                              k_cache, v_cache, page_table, seq_len, nullptr, prefix_of, q_out, stream);
 }
 
 gdn_status gdn_attn_prefill_workspace_size(const gdn_kv_dims* dims, int64_t n_tokens, uint64_t* bytes) {
@@ -561,10 +582,11 @@ gdn_status gdn_attn_prefill_workspace_size(const gdn_kv_dims* dims, int64_t n_to
   return gdn::report_ok();
 }
 
-gdn_status gdn_attn_prefill(const gdn_kv_dims* dims, int32_t layer, int64_t n_tokens, const int32_t* cu_seqlens,
-                            const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
-                            const int32_t* seq_len, const int32_t* prefix_of, int32_t causal, float scale, void* out,
-                            float* lse, void* workspace, uint64_t workspace_bytes, gdn_stream_t stream) {
+gdn_status gdn_attn_prefill_marked(const gdn_kv_dims* dims, int32_t layer, int64_t n_tokens,
+                                   const int32_t* cu_seqlens, const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* page_table, const int32_t* seq_len, const int32_t* refused,
+                                   const int32_t* prefix_of, int32_t causal, float scale, void* out, float* lse,
+                                   void* workspace, uint64_t workspace_bytes, gdn_stream_t stream) {
   GDN_RETURN_IF(check_dims(dims, kPacked, false));
   const gdn_kv_dims d = normal(*dims);
   GDN_RETURN_IF(check_cache_strides(d));
@@ -583,6 +605,7 @@ gdn_status gdn_attn_prefill(const gdn_kv_dims* dims, int32_t layer, int64_t n_to
       {"cu_seqlens", cu_seqlens, 4ull * (d.B + 1), 4, false, false, nullptr},
       {"page_table", page_table, 4ull * d.n_slots * d.max_pages, 4, false, false, nullptr},
       {"seq_len", seq_len, 4ull * d.n_slots, 4, false, false, nullptr},
+      {"refused", refused, 4ull * d.n_slots, 4, false, true, nullptr},
       {"prefix_of", prefix_of, 4ull * d.B, 4, false, true, nullptr},
       {"out", out, 2ull * n * d.Hq * d.D, 16, true, false, nullptr},
       {"lse", lse, 4ull * n * d.Hq, 4, true, true, nullptr},
@@ -595,11 +618,19 @@ gdn_status gdn_attn_prefill(const gdn_kv_dims* dims, int32_t layer, int64_t n_to
   p.q = static_cast<const uint16_t*>(q);
   p.k_cache = static_cast<const uint16_t*>(k_cache) + layer * d.cache_layer_stride;
   p.v_cache = static_cast<const uint16_t*>(v_cache) + layer * d.cache_layer_stride;
-  p.table = page_table, p.seq_len = seq_len, p.prefix_of = prefix_of, p.causal = causal != 0, p.scale = scale;
+  p.table = page_table, p.seq_len = seq_len, p.prefix_of = prefix_of, p.refused = refused, p.causal = causal != 0, p.scale = scale;
   p.out = static_cast<uint16_t*>(out), p.lse = lse, p.ws = workspace;
   const cudaError_t e = gdn::launch_packed_attn(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "prefill attention launch: %s", cudaGetErrorString(e));
   return gdn::report_ok();
+}
+
+gdn_status gdn_attn_prefill(const gdn_kv_dims* dims, int32_t layer, int64_t n_tokens, const int32_t* cu_seqlens,
+                            const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                            const int32_t* seq_len, const int32_t* prefix_of, int32_t causal, float scale, void* out,
+                            float* lse, void* workspace, uint64_t workspace_bytes, gdn_stream_t stream) {
+  return gdn_attn_prefill_marked(dims, layer, n_tokens, cu_seqlens, q, k_cache, v_cache, page_table, seq_len, nullptr,
+                                 prefix_of, causal, scale, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -53,6 +53,7 @@ struct PagesParams {
   int32_t* len_out;
   const int32_t* ref_in;
   int32_t* ref_out;
+  int32_t* refused;          // reserve: [n_slots] or null
   int32_t* n_live;           // compact
   void* ws;
   uint32_t* err;
@@ -78,6 +79,7 @@ struct RopeParams {
   const int32_t* parent;
   const int32_t* cu;         // packed tokens
   const int32_t* table;
+  const int32_t* refused;    // [n_slots] or null
   uint32_t* err;
   int32_t n_tokens;
   int32_t hq, hk, hv;        // heads of each kind that the call handles
@@ -97,6 +99,7 @@ struct PackedAttnParams {
   const int32_t* table;
   const int32_t* seq_len;
   const int32_t* prefix_of;
+  const int32_t* refused;    // [n_slots] or null
   int32_t causal;
   float scale;
   uint16_t* out;

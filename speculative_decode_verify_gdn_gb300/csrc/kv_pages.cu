@@ -322,8 +322,8 @@ struct ReserveRec {
   long long first;  // rank of the sequence's first new page
   int32_t need;     // new pages
   int32_t have;     // pages before
-  int32_t len;      // tokens after
-  int32_t pad;
+  int32_t len;      // tokens after (-1: as before)
+  int32_t asked;    // n_new was not 0
 };
 
 __device__ __forceinline__ long long block_scan64(long long v, long long* sums, long long& total) {  // exclusive, kPlanThreads
@@ -411,6 +411,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const __grid_c
       const int slot = d.slot0 + b;
       int n = p.accept[b], len = p.len_in[slot];
       uint32_t bad = 0;
+      r.asked = n != 0;
       if (len < 0 || (long long)len > (long long)d.max_pages * d.page_size) bad |= GDN_DEVERR_KV_LEN;
       if (n < 0 || n > (1 << 30)) bad |= GDN_DEVERR_KV_LEN;
       if (bad) n = 0;
@@ -425,7 +426,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const __grid_c
       if (!bad && (long long)len + n > (long long)d.max_pages * d.page_size) bad |= GDN_DEVERR_KV_FULL;
       if (bad) n = 0;
       if (bad && rank == 0) atomicOr(p.err, bad);
-      r.len = n > 0 ? len + n : -1;  // (-1: as before)
+      r.len = n > 0 ? len + n : -1;
       r.need = n > 0 ? pages_of(len + n, d.page_size) - r.have : 0;
     }
     long long total;
@@ -447,11 +448,11 @@ __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const __grid_c
   if (rank == 0) {
     for (int b = tid; b < d.B; b += kPlanThreads) {
       const ReserveRec r = rec[b];
-      if (r.len < 0) continue;
-      if (r.need > 0 && r.first + r.need > found)
-        atomicOr(p.err, GDN_DEVERR_KV_FULL);
-      else
-        p.len_out[d.slot0 + b] = r.len;
+      const int slot = d.slot0 + b;
+      const bool full = r.need > 0 && r.first + r.need > found, got = r.len >= 0 && !full;
+      if (full) atomicOr(p.err, GDN_DEVERR_KV_FULL);
+      if (p.refused) p.refused[slot] = r.asked && !got ? p.len_in[slot] : -1;
+      if (got) p.len_out[slot] = r.len;
     }
   }
   for (int i0 = lo; i0 < hi && at < wanted; i0 += step) {

@@ -139,6 +139,7 @@ __device__ __forceinline__ SeqRows load_sequence(const PackedAttnParams& p, int 
   const gdn_kv_dims& d = p.d;
   SeqRows s;
   const int lo = p.cu[b], hi = p.cu[b + 1], len = p.seq_len[d.slot0 + b], slot = p.prefix_of ? p.prefix_of[b] : -1;
+  const int refused = p.refused && p.causal ? p.refused[d.slot0 + b] : -1;
   uint32_t bad = 0;
   s.lo = lo, s.n = hi > lo ? hi - lo : 0;
   s.len = len;
@@ -150,6 +151,8 @@ __device__ __forceinline__ SeqRows load_sequence(const PackedAttnParams& p, int 
     s.pre_keys = p.seq_len[s.pre_slot];
     if (s.pre_keys < 0 || (long long)s.pre_keys > (long long)d.max_pages * d.page_size) s.pre_keys = 0, bad |= GDN_DEVERR_KV_LEN;
   }
+  // a slot that is as long as when room for its tokens was refused: its last tokens are others than the rows, which see nothing
+  if (refused >= 0 && refused == len && s.n > 0) s.len = 0, s.pre_slot = -1, s.pre_keys = 0, bad |= GDN_DEVERR_KV_LEN;
   if (bad && report) atomicOr(p.err, bad);
   return s;
 }

@@ -89,9 +89,11 @@ __device__ __forceinline__ Tok packed_token(const RopeParams& p, int token, int 
   const int b = find_sequence(p.cu, d.B, token, lane);
   const int lo = p.cu[b], hi = p.cu[b + 1];
   if (token < lo || token >= hi) return x;  // behind the last sequence (or bounds out of order)
+  const int refused = p.refused ? p.refused[d.slot0 + b] : -1;
   const int len = checked_slot_len(p.seq_len[d.slot0 + b], d, p.err);
   const int slot = checked_prefix(p.prefix_of, b, d, p.err);
-  if ((long long)hi - lo > len) {
+  // (a slot that is as long as when room for its tokens was refused: its last tokens are others)
+  if ((long long)hi - lo > len || refused == len) {
     atomicOr(p.err, GDN_DEVERR_KV_LEN);
     return x;
   }

@@ -22,7 +22,8 @@ from .gdn import _check
 
 EXPORTED = ("gdn_attn_verify", "gdn_attn_workspace_size", "gdn_kv_commit", "gdn_kv_fork", "gdn_kv_compact",
             "gdn_kv_workspace_size", "gdn_rope_turns", "gdn_attn_rope", "gdn_kv_reserve", "gdn_kv_append",
-            "gdn_attn_prefill", "gdn_attn_prefill_workspace_size")
+            "gdn_attn_prefill", "gdn_attn_prefill_workspace_size", "gdn_kv_reserve_marked", "gdn_kv_append_marked",
+            "gdn_attn_prefill_marked")
 
 DEVERR_KV_LEN, DEVERR_KV_PAGE, DEVERR_KV_SLOT, DEVERR_KV_FULL, DEVERR_KV_SHARED, DEVERR_KV_WINDOW = 32, 64, 128, 256, 512, 1024
 
@@ -87,6 +88,9 @@ def load_library() -> ctypes.CDLL:
         lib.gdn_kv_reserve.argtypes = [D] + [P] * 8 + [U, P]
         lib.gdn_kv_append.argtypes = [D, I, R, P, P, P, L] + [P] * 12
         lib.gdn_attn_prefill.argtypes = [D, I, L] + [P] * 7 + [I, ctypes.c_float, P, P, P, U, P]
+        lib.gdn_kv_reserve_marked.argtypes = [D] + [P] * 9 + [U, P]
+        lib.gdn_kv_append_marked.argtypes = [D, I, R, P, P, P, L] + [P] * 13
+        lib.gdn_attn_prefill_marked.argtypes = [D, I, L] + [P] * 8 + [I, ctypes.c_float, P, P, P, U, P]
         lib.gdn_attn_prefill_workspace_size.argtypes = [D, L, ctypes.POINTER(U)]
         for f in EXPORTED:
             getattr(lib, f).restype = ctypes.c_int
@@ -307,6 +311,14 @@ def _arg(t, name, dtype, shape, dev, optional=False):
     return p
 
 
+def _lengths(t, name, n_slots, dev):
+    """Addresses of lengths and, where they are one of a pair, of the refused entries beside them."""
+    if not isinstance(t, tuple):
+        return _arg(t, name, _I32, (n_slots,), dev), None
+    lens, refused = t
+    return _arg(lens, name, _I32, (n_slots,), dev), _arg(refused, "refused", _I32, (n_slots,), dev)
+
+
 def _on_device(t, name, dev):
     if t.get_device() != dev:
         raise ValueError(f"{name} is on device {t.get_device()}, the current one is {dev}")
@@ -411,24 +423,27 @@ def gdn_attn_rope(dims: KvDims, rope: Rope, q, k, v, seq_len, prefix_of, win_len
 
 
 def gdn_kv_reserve(dims: KvDims, n_new, table_in, table_out, len_in, len_out, ref_in, ref_out, workspace, stream=None) -> None:
-    """Pages for n_new [B] more tokens of each sequence, whose lengths grow by them.  Each *_out may be its *_in."""
+    """Pages for n_new [B] more tokens of each sequence, whose lengths grow by them.  Each *_out may be its *_in.
+    len_out may be a pair of the lengths and of refused [n_slots] int32, -1 to begin with, in which the call notes the
+    sequences that it had no room for; as a pair with seq_len, gdn_kv_append and gdn_attn_prefill leave those out."""
     d = dims
     lib = load_library()
     dev, st = _place(stream)
     table, slots, pages = (d.n_slots, d.max_pages), (d.n_slots,), (d.n_pages,)
     wp, wb = _workspace(workspace)
     _on_device(workspace, "workspace", dev)
-    _check(lib.gdn_kv_reserve(
+    lens, refused = _lengths(len_out, "len_out", d.n_slots, dev)
+    _check(lib.gdn_kv_reserve_marked(
         ctypes.byref(d), _arg(n_new, "n_new", _I32, (d.B,), dev), _arg(table_in, "table_in", _I32, table, dev),
         _arg(table_out, "table_out", _I32, table, dev), _arg(len_in, "len_in", _I32, slots, dev),
-        _arg(len_out, "len_out", _I32, slots, dev), _arg(ref_in, "ref_in", _I32, pages, dev),
-        _arg(ref_out, "ref_out", _I32, pages, dev), wp, wb, st))
+        lens, _arg(ref_in, "ref_in", _I32, pages, dev), _arg(ref_out, "ref_out", _I32, pages, dev), refused, wp, wb, st))
 
 
 def gdn_kv_append(dims: KvDims, layer, rope: Rope, cu_seqlens, q, k, v, positions, k_cache, v_cache, page_table, seq_len,
                   prefix_of, q_out, stream=None) -> None:
     """One layer's packed tokens into place (see include/gdn_kv.h): q [N, Hq, D] to q_out (or both None), k, v
-    [N, Hkv, D] to the last tokens of the slots.  cu_seqlens [B + 1]; positions [N] int32 or None."""
+    [N, Hkv, D] to the last tokens of the slots.  cu_seqlens [B + 1]; positions [N] int32 or None.  seq_len may be a
+    pair with what reserve refused: without it every sequence has to have got its room."""
     d = dims
     lib = load_library()
     Hq, Hkv, D = d.Hq, d.Hkv, d.D
@@ -444,10 +459,11 @@ def gdn_kv_append(dims: KvDims, layer, rope: Rope, cu_seqlens, q, k, v, position
     kp, kt, kh = _heads(k, "k", dt, (N, Hkv, D), dev)
     vp, kt, kh = _beside(k, kt, kh, v, dt, (N, Hkv, D), dev)
     q_to = None if q_out is None else _out_rows(q_out, "q_out", dt, (N, Hq, D), d.q_token_stride, dev)
-    _check(lib.gdn_kv_append(
+    lens, refused = _lengths(seq_len, "seq_len", d.n_slots, dev)
+    _check(lib.gdn_kv_append_marked(
         ctypes.byref(d), layer, rope._args((qt, qh, kt, kh)), *rope._at, N, _arg(cu_seqlens, "cu_seqlens", _I32, (d.B + 1,), dev),
         qp, kp, vp, _arg(positions, "positions", _I32, (N,), dev, True), kc, vc,
-        _arg(page_table, "page_table", _I32, (d.n_slots, d.max_pages), dev), _arg(seq_len, "seq_len", _I32, (d.n_slots,), dev),
+        _arg(page_table, "page_table", _I32, (d.n_slots, d.max_pages), dev), lens, refused,
         _arg(prefix_of, "prefix_of", _I32, (d.B,), dev, True), q_to, st))
 
 
@@ -466,7 +482,7 @@ def gdn_attn_prefill(dims: KvDims, layer, cu_seqlens, q, k_cache, v_cache, page_
                      out, lse, workspace, stream=None) -> None:
     """Attention of packed queries over the cache (see include/gdn_kv.h): q [N, Hq, D], out [N, Hq, D], lse [N, Hq]
     f32 or None; cu_seqlens [B + 1].  causal: a sequence's rows are its slot's last tokens; else every row
-    sees the whole slot."""
+    sees the whole slot.  seq_len may be a pair with what reserve refused."""
     d = dims
     lib = load_library()
     Hq, D = d.Hq, d.D
@@ -479,9 +495,10 @@ def gdn_attn_prefill(dims: KvDims, layer, cu_seqlens, q, k_cache, v_cache, page_
     wp, wb = _workspace(workspace)
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache"), (workspace, "workspace")):
         _on_device(t, name, dev)
-    _check(lib.gdn_attn_prefill(
+    lens, refused = _lengths(seq_len, "seq_len", d.n_slots, dev)
+    _check(lib.gdn_attn_prefill_marked(
         ctypes.byref(d), layer, N, _arg(cu_seqlens, "cu_seqlens", _I32, (d.B + 1,), dev),
         _out_rows(q, "q", dt, (N, Hq, D), d.q_token_stride, dev), kc, vc,
-        _arg(page_table, "page_table", _I32, (d.n_slots, d.max_pages), dev), _arg(seq_len, "seq_len", _I32, (d.n_slots,), dev),
+        _arg(page_table, "page_table", _I32, (d.n_slots, d.max_pages), dev), lens, refused,
         _arg(prefix_of, "prefix_of", _I32, (d.B,), dev, True), 1 if causal else 0, scale,
         _arg(out, "out", dt, (N, Hq, D), dev), _arg(lse, "lse", torch.float32, (N, Hq), dev, True), wp, wb, st))

@@ -45,7 +45,9 @@ class PagedCache:
     pool_workspace: torch.Tensor
     fork_scratch: tuple
     prefill_workspace: torch.Tensor
+    refused: torch.Tensor     # [n_slots] int32: length of a slot that reserve had no room for, else -1
     cur: int = 0
+    reserved: bool = False    # some reserve has written refused
 
     @classmethod
     def create(cls, B, K, Hq, Hkv, D, page_size, n_pages, max_pages, n_prefixes=0, n_layers=1, dtype=torch.bfloat16,
@@ -65,7 +67,7 @@ class PagedCache:
                                                          dtype), device),  # (reserve takes any of the slots)
                    (ints(B), torch.empty(B, dtype=torch.bool, device=device), ints(B),
                     torch.arange(B, dtype=torch.int32, device=device), ints(n_slots, fill=-1)),
-                   kv.alloc_attn_prefill_workspace(dims, 0, device))
+                   kv.alloc_attn_prefill_workspace(dims, 0, device), ints(n_slots, fill=-1))
 
     @property
     def table(self) -> torch.Tensor:
@@ -95,9 +97,11 @@ class PagedCache:
 
     def reserve(self, n_new, slot0=0, stream=None) -> None:
         """Pages for n_new (int32) more tokens of the sequences from slot0 on, in all layers, which grow by them;
-        append_layer fills them."""
-        kv.gdn_kv_reserve(self._dims(n_new.shape[0], slot0), n_new, self.table, self.table, self.seq_len, self.seq_len, self.ref,
-                          self.ref, self.pool_workspace, stream)
+        append_layer fills them.  A sequence that there is no room for (gdn_device_status) stays as it is, and
+        append_layer and causal attend_prefill leave it out until its slot has grown or has been asked for again."""
+        self.reserved = True
+        kv.gdn_kv_reserve(self._dims(n_new.shape[0], slot0), n_new, self.table, self.table, self.seq_len,
+                          (self.seq_len, self.refused), self.ref, self.ref, self.pool_workspace, stream)
 
     def append_layer(self, layer, rope, cu_seqlens, q, k, v, q_out, slot0=0, positions=None, stream=None) -> None:
         """One layer's packed tokens of the sequences from slot0 on, with bounds cu_seqlens (int32), to the places
@@ -105,14 +109,14 @@ class PagedCache:
         rotated, and v, [N, Hkv, D], to the pages."""
         n = cu_seqlens.shape[0] - 1
         kv.gdn_kv_append(self._dims(n, slot0, q=q_out), layer, rope, cu_seqlens, q, k, v, positions, self.k, self.v, self.table,
-                         self.seq_len, self._prefixes(slot0, n), q_out, stream)
+                         (self.seq_len, self.refused), self._prefixes(slot0, n), q_out, stream)
 
     def attend_prefill(self, layer, cu_seqlens, q, out, lse=None, slot0=0, causal=True, scale=None, stream=None) -> None:
         """Packed queries [N, Hq, D] of the sequences from slot0 on attend to prefix and slot: causally, a
         sequence's queries being those of its last tokens, or to all of the slot (cross attention)."""
         n = cu_seqlens.shape[0] - 1
-        kv.gdn_attn_prefill(self._dims(n, slot0, q=q), layer, cu_seqlens, q, self.k, self.v, self.table, self.seq_len,
-                            self._prefixes(slot0, n), causal, 1.0 / math.sqrt(self.D) if scale is None else scale, out, lse,
+        kv.gdn_attn_prefill(self._dims(n, slot0, q=q), layer, cu_seqlens, q, self.k, self.v, self.table,
+                            (self.seq_len, self.refused), self._prefixes(slot0, n), causal, 1.0 / math.sqrt(self.D) if scale is None else scale, out, lse,
                             self.prefill_workspace, stream)
 
     def _dims(self, n, slot0=0, q=None, win=None) -> kv.KvDims:
@@ -147,9 +151,12 @@ class PagedCache:
         kv.gdn_kv_fork(self.dims, src, self.k, self.v, self.tables[i], self.tables[o], self.lens[i], self.lens[o],
                        self.ref, self.ref, self.pool_workspace, stream)
         self.cur = o
-        if self.n_prefixes:
+        if self.n_prefixes or self.reserved:
             with torch.cuda.stream(stream):
-                self._take_prefixes(src[:self.B])
+                if self.reserved:
+                    self.refused.fill_(-1)  # (its slots hold other sequences now)
+                if self.n_prefixes:
+                    self._take_prefixes(src[:self.B])
 
     def _take_prefixes(self, src) -> None:
         """prefix_of of the slots that src names.  Five small kernels into buffers of the cache: 80 us of the
