@@ -40,7 +40,10 @@ def frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", fact
     else:
         def index(turns):  # of the pair that turns so many times in the trained tokens
             return rot_dim * math.log(trained / (2 * math.pi * turns)) / (2 * math.log(base))
-        lo, hi = max(0.0, math.floor(index(fast))), min(rot_dim / 2 - 1.0, math.ceil(index(slow)))
+        # (the end may lie behind the last pair, which then keeps a part; the published method ends at rot_dim - 1)
+        lo, hi = max(0.0, math.floor(index(fast))), min(rot_dim - 1.0, math.ceil(index(slow)))
+        if hi <= 0.0:  # every pair turns at most `slow` times
+            return f / factor
         keep = 1.0 - (pair / 2 - lo) / max(hi - lo, 1e-3)
     keep = keep.clamp(0.0, 1.0)
     return f * keep + f / factor * (1.0 - keep)
