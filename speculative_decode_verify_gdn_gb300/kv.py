@@ -137,6 +137,14 @@ def _stream(stream):
     return _current_stream(_current_device()) if stream is None else stream.cuda_stream
 
 
+def stream_state(stream):
+    """Handle of `stream`, or of the current one, and whether work on it is being captured into a graph."""
+    if stream is None:
+        return _current_stream(_current_device()), torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return stream.cuda_stream, torch.cuda.is_current_stream_capturing()
+
+
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 

@@ -8,12 +8,14 @@ reference counts are updated in place except by a fork, which writes the other o
 
 Every method takes the stream that it runs on (None: the current one).  What it allocates for
 itself belongs to that stream; the caller's tensors and the cache have to be ready there, as for the
-C calls.
+C calls.  The two attentions only read the cache, and may run on several streams at once: each stream has a workspace for
+them, made by its first call, and a captured call has one in its graph's own memory.  What changes the cache
+runs alone.
 """
 from __future__ import annotations
 
 import math
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 
 import torch
 
@@ -41,13 +43,12 @@ class PagedCache:
     prefix_of: torch.Tensor   # [B] int32: slot of the sequence's prefix, -1 without
     n_live: torch.Tensor      # [1] int32, set by compact
     dims: kv.KvDims
-    attn_workspace: torch.Tensor
     pool_workspace: torch.Tensor
     fork_scratch: tuple
-    prefill_workspace: torch.Tensor
     refused: torch.Tensor     # [n_slots] int32: length of a slot that reserve had no room for, else -1
     cur: int = 0
     reserved: bool = False    # some reserve has written refused
+    workspaces: dict = field(default_factory=dict)  # of the attentions: (which, stream) -> tensor
 
     @classmethod
     def create(cls, B, K, Hq, Hkv, D, page_size, n_pages, max_pages, n_prefixes=0, n_layers=1, dtype=torch.bfloat16,
@@ -62,12 +63,12 @@ class PagedCache:
         return cls(B, K, Hq, Hkv, D, page_size, n_pages, max_pages, n_prefixes, n_layers, dtype,
                    torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device),
                    [ints(n_slots, max_pages, fill=-1) for _ in range(2)], [ints(n_slots) for _ in range(2)],
-                   ints(n_pages), ints(B, fill=-1), ints(1), dims, kv.alloc_attn_workspace(dims, device),
+                   ints(n_pages), ints(B, fill=-1), ints(1), dims,
                    kv.alloc_kv_workspace(kv.make_kv_dims(n_slots, K, Hq, Hkv, D, page_size, n_pages, max_pages, n_slots, 0, n_layers,
                                                          dtype), device),  # (reserve takes any of the slots)
                    (ints(B), torch.empty(B, dtype=torch.bool, device=device), ints(B),
                     torch.arange(B, dtype=torch.int32, device=device), ints(n_slots, fill=-1)),
-                   kv.alloc_attn_prefill_workspace(dims, 0, device), ints(n_slots, fill=-1))
+                   ints(n_slots, fill=-1))
 
     @property
     def table(self) -> torch.Tensor:
@@ -116,8 +117,23 @@ class PagedCache:
         sequence's queries being those of its last tokens, or to all of the slot (cross attention)."""
         n = cu_seqlens.shape[0] - 1
         kv.gdn_attn_prefill(self._dims(n, slot0, q=q), layer, cu_seqlens, q, self.k, self.v, self.table,
-                            (self.seq_len, self.refused), self._prefixes(slot0, n), causal, 1.0 / math.sqrt(self.D) if scale is None else scale, out, lse,
-                            self.prefill_workspace, stream)
+                            (self.seq_len, self.refused), self._prefixes(slot0, n), causal,
+                            1.0 / math.sqrt(self.D) if scale is None else scale, out, lse,
+                            self._workspace(kv.alloc_attn_prefill_workspace, 0, stream=stream), stream)
+
+    def _workspace(self, alloc, *args, stream=None) -> torch.Tensor:
+        """Scratch of an attention that runs on this stream.  Eager calls on one stream come one after the other and share
+        theirs; graphs that were captured on one stream may be replayed on two at once, so each has its own."""
+        if not self.k.is_cuda:
+            return alloc(self.dims, *args, self.k.device)
+        handle, captured = kv.stream_state(stream)
+        ws = None if captured else self.workspaces.get((alloc.__name__, handle))
+        if ws is None:
+            with torch.cuda.stream(stream):
+                ws = alloc(self.dims, *args, self.k.device)
+            if not captured:
+                self.workspaces[alloc.__name__, handle] = ws
+        return ws
 
     def _dims(self, n, slot0=0, q=None, win=None) -> kv.KvDims:
         """The dims of a call on n sequences from slot0 on, with these queries' and windows' strides."""
@@ -136,7 +152,8 @@ class PagedCache:
         """The window's attention in one layer (a chain, or a token tree given by parent [B, K])."""
         kv.gdn_attn_verify(self.dims, layer, q, k_win, v_win, self.k, self.v, self.table, self.seq_len,
                            self.prefix_of if self.n_prefixes else None, win_len, parent,
-                           1.0 / math.sqrt(self.D) if scale is None else scale, out, lse, self.attn_workspace, stream)
+                           1.0 / math.sqrt(self.D) if scale is None else scale, out, lse,
+                           self._workspace(kv.alloc_attn_workspace, stream=stream), stream)
 
     def commit(self, accept_len, k_win, v_win, parent=None, stream=None) -> None:
         """Keeps each sequence's accepted window tokens, all layers: k_win, v_win [n_layers, B, K, Hkv, D]."""
