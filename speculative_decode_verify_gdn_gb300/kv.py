@@ -25,6 +25,8 @@ EXPORTED = ("gdn_attn_verify", "gdn_attn_workspace_size", "gdn_kv_commit", "gdn_
             "gdn_attn_prefill", "gdn_attn_prefill_workspace_size", "gdn_kv_reserve_marked", "gdn_kv_append_marked",
             "gdn_attn_prefill_marked")
 
+MAX_BATCH = 65535  # sequences of a call
+
 DEVERR_KV_LEN, DEVERR_KV_PAGE, DEVERR_KV_SLOT, DEVERR_KV_FULL, DEVERR_KV_SHARED, DEVERR_KV_WINDOW = 32, 64, 128, 256, 512, 1024
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}

@@ -64,8 +64,8 @@ class PagedCache:
                    torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device),
                    [ints(n_slots, max_pages, fill=-1) for _ in range(2)], [ints(n_slots) for _ in range(2)],
                    ints(n_pages), ints(B, fill=-1), ints(1), dims,
-                   kv.alloc_kv_workspace(kv.make_kv_dims(n_slots, K, Hq, Hkv, D, page_size, n_pages, max_pages, n_slots, 0, n_layers,
-                                                         dtype), device),  # (reserve takes any of the slots)
+                   kv.alloc_kv_workspace(kv.make_kv_dims(min(n_slots, kv.MAX_BATCH), K, Hq, Hkv, D, page_size, n_pages, max_pages,
+                                                         n_slots, 0, n_layers, dtype), device),  # (reserve takes any of the slots)
                    (ints(B), torch.empty(B, dtype=torch.bool, device=device), ints(B),
                     torch.arange(B, dtype=torch.int32, device=device), ints(n_slots, fill=-1)),
                    ints(n_slots, fill=-1))

@@ -68,3 +68,14 @@ def test_a_workspace_for_each_stream_and_each_capture(world):
     assert all(a is b for a, b in zip(calls(None), side))
     for t, size in zip(main, (kv.gdn_attn_workspace_size(c.dims), kv.gdn_attn_prefill_workspace_size(c.dims, 1000))):
         assert t.numel() >= size
+
+
+@pytest.mark.parametrize("B,n_prefixes", [(65535, 0), (65535, 1), (3, 65533), (1000, 70000)])
+def test_the_pool_has_room_for_the_largest_call(B, n_prefixes):
+    """More slots than a call may name sequences: the workspace serves a commit of all B and a reserve of as many slots as
+    a call takes."""
+    build.build_library()
+    c = PagedCache.create(B, 1, 1, 1, 64, 16, n_pages=4, max_pages=1, n_prefixes=n_prefixes, device="cpu")
+    assert c.pool_workspace.numel() >= kv.gdn_kv_workspace_size(c.dims)
+    assert c.pool_workspace.numel() >= kv.gdn_kv_workspace_size(c._dims(min(65535, B + n_prefixes)))
+    assert kv.gdn_kv_workspace_size(c._dims(65535 if B + n_prefixes > 65535 else 1)) > kv.gdn_kv_workspace_size(c._dims(0))
