@@ -55,6 +55,7 @@ class PagedCache:
                device="cuda") -> "PagedCache":
         n_slots = B + n_prefixes
         dims = kv.make_kv_dims(B, K, Hq, Hkv, D, page_size, n_pages, max_pages, n_slots, 0, n_layers, dtype)
+        kv.gdn_attn_workspace_size(dims)  # (refuses here what the attention would refuse later)
         shape = (n_layers, n_pages, page_size, Hkv, D)
 
         def ints(*s, fill=0):

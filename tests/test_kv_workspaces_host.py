@@ -4,7 +4,7 @@ import types
 
 import pytest
 
-from speculative_decode_verify_gdn_gb300 import build, kv
+from speculative_decode_verify_gdn_gb300 import build, gdn, kv
 from speculative_decode_verify_gdn_gb300.kv_runtime import PagedCache
 
 torch = pytest.importorskip("torch")
@@ -79,3 +79,11 @@ def test_the_pool_has_room_for_the_largest_call(B, n_prefixes):
     assert c.pool_workspace.numel() >= kv.gdn_kv_workspace_size(c.dims)
     assert c.pool_workspace.numel() >= kv.gdn_kv_workspace_size(c._dims(min(65535, B + n_prefixes)))
     assert kv.gdn_kv_workspace_size(c._dims(65535 if B + n_prefixes > 65535 else 1)) > kv.gdn_kv_workspace_size(c._dims(0))
+
+
+@pytest.mark.parametrize("over", [dict(K=17), dict(B=65536), dict(Hq=3, Hkv=2), dict(D=96), dict(page_size=24), dict(Hq=129)])
+def test_a_cache_that_no_attention_takes_is_refused_at_once(over):
+    build.build_library()
+    args = dict(B=2, K=1, Hq=1, Hkv=1, D=64, page_size=16, n_pages=4, max_pages=1, device="cpu")
+    with pytest.raises(gdn.GdnError):
+        PagedCache.create(**dict(args, **over))
