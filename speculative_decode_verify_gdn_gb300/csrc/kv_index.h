@@ -24,4 +24,7 @@ GDN_HD int32_t page_column(int32_t token, uint32_t inv) {
   return int32_t(inv ? uint32_t((uint64_t(n) * inv) >> 32) : n);
 }
 
+// CTAs of `each` tokens for n tokens, 0 <= n < 2^31 (n + each - 1 may be above 2^31).
+GDN_HD uint32_t ctas_of(int32_t n, int32_t each) { return (uint32_t(n) + uint32_t(each) - 1) / uint32_t(each); }
+
 }  // namespace gdn

@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(PACKED)) rope_kernel(c
 template <bool PACKED>
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
   const int toks = p.n_tokens <= rope_ctas(PACKED) * 152 ? 1 : kRopeToks;
-  const unsigned grid = unsigned((p.n_tokens + toks - 1) / toks);
+  const unsigned grid = ctas_of(p.n_tokens, toks);
   const bool f16 = p.d.dtype != 0;
   auto kernel = [&]() -> void (*)(RopeParams, int) {
     if (p.d.D == 128)
