@@ -14,7 +14,7 @@
 // the lengths alone, and no sum is formed by atomics, so results repeat bit for bit.
 //
 // Kernels: tiles (persistent, tcgen05; every CTA plans for itself) or, for few rows to a sequence, a kernel of warps that
-// work by themselves (below); join.
+// work by themselves (below); join.  A batch of both kinds of sequences has both, one after the other in the same workspace.
 //
 // A block of more than 128 rows gives each stream half of them, on the same keys; a smaller one gives the
 // streams alternate tiles of the same rows, and at its end the two sums are joined in tensor memory, each
@@ -33,6 +33,7 @@
 //   64 single tokens over 1..1500 states, f16 Hq=Hkv=16 D=64   45 us, 4.4 TB/s (few rows)
 //   one prompt of 37 tokens   14 us: the host's two launches and its four tensor maps
 #include <atomic>
+#include <climits>
 
 #include "kv_device.cuh"
 #include "kv_index.h"
@@ -85,6 +86,7 @@ struct Cut {
   int period_log;       // after so many (2^period_log) blocks, their keys are a whole number of tiles more
   int causal;
   int workers;          // that the tiles are dealt to
+  int least, most;      // sequences of so many tokens are taken; the others count for none here
   __host__ __device__ __forceinline__ long long tiles_of(long long keys) const { return (keys + (1 << key_log) - 1) >> key_log; }
 };
 
@@ -135,7 +137,7 @@ struct SeqRows {
   }
 };
 
-__device__ __forceinline__ SeqRows load_sequence(const PackedAttnParams& p, int b, bool report) {
+__device__ __forceinline__ SeqRows load_sequence(const PackedAttnParams& p, const Cut& cut, int b, bool report) {
   const gdn_kv_dims& d = p.d;
   SeqRows s;
   const int lo = p.cu[b], hi = p.cu[b + 1], len = p.seq_len[d.slot0 + b], slot = p.prefix_of ? p.prefix_of[b] : -1;
@@ -154,6 +156,7 @@ __device__ __forceinline__ SeqRows load_sequence(const PackedAttnParams& p, int 
   // a slot that is as long as when room for its tokens was refused: its last tokens are others than the rows, which see nothing
   if (refused >= 0 && refused == len && s.n > 0) s.len = 0, s.pre_slot = -1, s.pre_keys = 0, bad |= GDN_DEVERR_KV_LEN;
   if (bad && report) atomicOr(p.err, bad);
+  if (s.n < cut.least || s.n > cut.most) s.n = 0;
   return s;
 }
 
@@ -185,7 +188,7 @@ __device__ __forceinline__ void make_plan(const PackedAttnParams& p, const Cut& 
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     bad |= p.cu[b] > p.cu[b + 1];
-    const SeqRows s = load_sequence(p, b, cta == 0);
+    const SeqRows s = load_sequence(p, cut, b, cta == 0);
     mine += s.tiles(cut, s.blocks(cut));
     empty |= s.without_keys(cut) > 0;
   }
@@ -221,7 +224,7 @@ __device__ __forceinline__ void make_plan(const PackedAttnParams& p, const Cut& 
 __device__ __noinline__ void write_empty(const PackedAttnParams& p, const Cut& cut) {
   const gdn_kv_dims& d = p.d;
   for (int b = int(blockIdx.x); b < d.B; b += int(gridDim.x)) {
-    const SeqRows s = load_sequence(p, b, false);
+    const SeqRows s = load_sequence(p, cut, b, false);
     const long long rows = (long long)s.without_keys(cut) * d.Hq, first = (long long)s.lo * d.Hq;
     uint4* const out = reinterpret_cast<uint4*>(p.out + first * d.D);
     for (long long k = threadIdx.x; k < rows * (d.D / 8); k += blockDim.x) out[k] = make_uint4(0u, 0u, 0u, 0u);
@@ -270,7 +273,7 @@ struct SegWalk {
     if (i < from || i >= from + 32) {
       from = i;
       const int at = i + lane < p.d.B ? i + lane : p.d.B - 1;
-      mine = load_sequence(p, at, false);
+      mine = load_sequence(p, cut, at, false);
     }
     const int l = i - from;
     SeqRows s;
@@ -1203,7 +1206,19 @@ cudaError_t launch(const PackedAttnParams& p, const PackedWs& w, const Cut& cut,
 
 template <int D, bool F16>
 cudaError_t launch_few(const PackedAttnParams& p, const PackedWs& w, const Cut& cut, cudaStream_t stream) {
-  const cudaError_t e = launch_dependent(packed_few_kernel<D, F16>, unsigned(kCtas * few_ctas(D)), kFewThreads, 0, stream, p, w, cut, page_units_inv(p.d.page_size));
+  // Loads in flight need room in L1, which a kernel with all of the shared memory leaves little of, and a kernel that can do
+  // with what it finds does not have it changed: 64 tokens behind 4000 157 us by themselves, 245 next to the tiles, 167 there
+  // when asked for (10 % is room for all CTAs; with 0 a part of them waits at D = 64: 50 -> 73 us).
+  static std::atomic<uint64_t> asked{0};  // a bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(asked.load() >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(packed_few_kernel<D, F16>, cudaFuncAttributePreferredSharedMemoryCarveout, 10);
+    if (e != cudaSuccess) return e;
+    asked.fetch_or(1ull << (dev & 63));
+  }
+  e = launch_dependent(packed_few_kernel<D, F16>, unsigned(kCtas * few_ctas(D)), kFewThreads, 0, stream, p, w, cut, page_units_inv(p.d.page_size));
   if (e != cudaSuccess) return e;
   // A token's items by wide CTAs for four workers, where they are few and in hundreds of pieces each, or by a small one for each
   // worker: 8 items behind 65536 keys 54 and 59 us, one 35 and 79, but 16 (D = 64) 57 and 54, and 1024 of 1..1500 keys 49 and 45.
@@ -1213,8 +1228,8 @@ cudaError_t launch_few(const PackedAttnParams& p, const PackedWs& w, const Cut& 
 }
 
 // How rows are cut into blocks of `toks` tokens, and keys into tiles of 2^key_log, dealt to so many workers.
-Cut make_cut(int tile_toks, int toks, int key_log, int causal, int workers) {
-  Cut c{tile_toks, toks, key_log, 0, causal, workers};
+Cut make_cut(int tile_toks, int toks, int key_log, int causal, int workers, int least, int most) {
+  Cut c{tile_toks, toks, key_log, 0, causal, workers, least, most};
   while ((c.toks << c.period_log) % (1 << key_log)) ++c.period_log;
   return c;
 }
@@ -1231,16 +1246,31 @@ cudaError_t launch_packed_attn(const PackedAttnParams& p, cudaStream_t stream) {
   const gdn_kv_dims& d = p.d;
   const int G = d.Hq / d.Hkv, toks = kTileRows / G;
   const PackedWs w = carve_packed(p.ws, d, nullptr);
-  // Few rows or tiles, by the rows that a sequence has for a kv head on average; their distribution is known on the
-  // device alone.  Us with one and the other, 64 sequences of 1..1500 keys: f16 Hkv=16 D=64, 1 row 45 and 71, 8 rows 47 and
-  // 72; bf16 Hkv=8 D=128 causal, 4 rows 45 and 52, 8 rows 45 and 52, 12 rows 67 and 52; Hkv=4, 8 rows 31 and 33, 16 rows 40
-  // and 33.  Should all tokens be one sequence's, few rows cost 24 us for 512 tokens where tiles cost 17, and 138 for
-  // 2048 where they cost 35 (Hkv=16 D=64): more than 512 have to be one a sequence on average.
+  // Few rows or tiles: the host knows how many rows and sequences there are and how long a slot can be, the device alone how
+  // the rows are distributed.  The kernel for few rows reads a sequence's keys once for every 8 rows, so it is for sequences
+  // of that many: us with it and with tiles, 64 sequences of 1..1500 keys f16 Hkv=16 D=64 1 row 44 and 64, 8 rows 43 and 65;
+  // bf16 Hkv=8 D=128 4 rows 39 and 46, 8 rows 40 and 48, 12 rows 67 and 52; 8 such sequences 15 and 19.  But 200 tokens of one
+  // sequence behind 30000 1235 and 112, 16 behind 65536 218 and 55, 16 behind 1000 20 and 15.
+  //  - It takes all that has at most 8 rows a sequence and kv head on average (of more than 512 tokens, a token), if what it
+  //    would read should all tokens be one sequence's costs no more than it saves, a few us.  That they are as many as
+  //    the sequences makes a token each likely, and more can be risked.
+  //  - Else each kernel takes its sequences, one after the other: 255 tokens of as many sequences behind 1000 and 257 of one
+  //    behind 65536 412 us (3790 with few rows alone).  The second pair of launches costs 7 us where it has nothing to do.
+  //    Both and tiles alone: 64 x 8 rows D=64 51 and 65, 128 x 8 rows D=128 81 and 85, 32 x 8 rows 36 and 33, 16 x 8 rows 30 and
+  //    23: below 32 sequences tiles take all.
+  int least = 0;  // tokens of the sequences that the tiles take
   if (G <= kFewRows && (long long)p.n_tokens * G <= (long long)kFewRows * d.B && (p.n_tokens <= 512 || p.n_tokens <= d.B)) {
     const int few = kFewRows / G;
-    const Cut cut = make_cut(few, few, 5, p.causal, few_workers(d.D));
-    if (d.D == 128) return d.dtype ? launch_few<128, true>(p, w, cut, stream) : launch_few<128, false>(p, w, cut, stream);
-    return d.dtype ? launch_few<64, true>(p, w, cut, stream) : launch_few<64, false>(p, w, cut, stream);
+    const double slot = double(d.max_pages) * d.page_size * (p.prefix_of ? 2 : 1);
+    const double read = ctas_of(p.n_tokens, few) * slot * d.Hkv * d.D * 4.0;  // bytes, at 10 TB/s
+    const bool alone = p.n_tokens <= few || read <= (p.n_tokens == d.B ? 1e9 : 64e6);
+    if (alone || (p.n_tokens >= 32 && d.B >= 32)) {
+      const Cut cut = make_cut(few, few, 5, p.causal, few_workers(d.D), 0, alone ? INT_MAX : few);
+      const cudaError_t e = d.D == 128 ? (d.dtype ? launch_few<128, true>(p, w, cut, stream) : launch_few<128, false>(p, w, cut, stream))
+                                       : (d.dtype ? launch_few<64, true>(p, w, cut, stream) : launch_few<64, false>(p, w, cut, stream));
+      if (e != cudaSuccess || alone) return e;
+      least = few + 1;
+    }
   }
   const EncodeTiled encode = encoder();
   if (!encode) return cudaErrorNotSupported;
@@ -1271,7 +1301,7 @@ cudaError_t launch_packed_attn(const PackedAttnParams& p, cudaStream_t stream) {
   const cuuint32_t bt[3] = {64, cuuint32_t(G), cuuint32_t(toks)};
   map(&maps.queries, p.q, 3, qd, qst, bt);
   if (!ok) return cudaErrorInvalidValue;
-  const Cut cut = make_cut(toks, 2 * toks, 7, p.causal, kCtas);
+  const Cut cut = make_cut(toks, 2 * toks, 7, p.causal, kCtas, least, INT_MAX);
   if (d.D == 128) return d.dtype ? launch<128, true>(p, w, cut, box, maps, stream) : launch<128, false>(p, w, cut, box, maps, stream);
   return d.dtype ? launch<64, true>(p, w, cut, box, maps, stream) : launch<64, false>(p, w, cut, box, maps, stream);
 }
