@@ -27,8 +27,8 @@ namespace gdn {
 namespace {
 
 constexpr int kRopeThreads = 128;
-// CTAs to an SM: windows 7 (72 registers: 18.6 us, 21.3 with 8, at 256 trees of 16 tokens), packed tokens 8 (149.5 us, 152.7 with 7,
-// at 36864 tokens).
+// CTAs to an SM: windows 7 (72 registers, 24 to 28 bytes a thread spilled: 18.6 us, 21.3 with 8, at 256 trees of 16 tokens), packed
+// tokens 8 (64 registers, 52 to 68 bytes spilled: 149.5 us, 152.7 with 7, at 36864 tokens).
 constexpr int rope_ctas(bool packed) { return packed ? 8 : 7; }
 constexpr int kRopeToks = 4;   // tokens of a CTA, at most (a warp each looks them up)
 constexpr int kRopeAhead = 4;  // heads that a group of lanes has in flight
@@ -292,7 +292,12 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(PACKED)) rope_kernel(c
 
 template <bool PACKED>
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
-  const int toks = p.n_tokens <= rope_ctas(PACKED) * 152 ? 1 : kRopeToks;
+  // Tokens of a CTA: 1 while all CTAs are on the card at once, 2 up to three times as many tokens, then 4.  Us with 1, 2 and 4 in
+  // a graph, windows of Hq=32 Hkv=8 and Hq=16 Hkv=2, D=128: 1024 tokens 5.5 8.0 10.8 and 4.6 5.1 6.1; 1072 7.2 8.3 9.4 and
+  // 6.1 5.2 5.1; 2048 10.7 10.2 13.4 and 7.9 5.6 7.2; 3072 13.8 13.6 15.8 and 11.1 8.2 8.1; 4096 19.8 18.5 17.2 and 14.3 9.7 8.3.
+  // Packed tokens: 1216 6.1 6.9 9.0 and 5.0 4.7 5.4; 2048 10.0 11.0 16.8 and 8.1 6.3 8.7; 3000 13.5 14.4 17.8 and 10.9 8.6 9.3;
+  // 4096 19.3 19.1 19.4 and 14.1 9.9 9.6; 16384 69 70 71 and 50 36 33.
+  const int wave = rope_ctas(PACKED) * 152, toks = p.n_tokens <= wave ? 1 : p.n_tokens <= 3 * wave ? 2 : kRopeToks;
   const unsigned grid = ctas_of(p.n_tokens, toks);
   const bool f16 = p.d.dtype != 0;
   auto kernel = [&]() -> void (*)(RopeParams, int) {
