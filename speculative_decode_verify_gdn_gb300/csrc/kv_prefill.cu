@@ -20,18 +20,18 @@
 // streams alternate tiles of the same rows, and at its end the two sums are joined in tensor memory, each
 // softmax group taking half of the columns.
 //
-// Measured on one GB300, calls in a row (peaks: 6702 GB/s copy, 1903 TFLOP/s cuBLAS bf16, 1728 when the power cap sets
+// Measured on one GB300, calls in a row and, where it differs, in turn with other work (peaks: 6702 GB/s copy, 1903 TFLOP/s cuBLAS bf16, 1728 when the power cap sets
 // the clock):
-//   prompts of 4096..16384 tokens, Hq=32 Hkv=8 D=128     3.0-3.1 ms, 1350 TFLOP/s: the chain scores, softmax, products of a
+//   prompts of 4096..16384 tokens, Hq=32 Hkv=8 D=128     3.0-3.3 ms, 1250-1350 TFLOP/s: the chain scores, softmax, products of a
 //     stream (a pair of tiles in 1.9 us) at the power cap
-//   512 tokens behind 65536, Hq=32 Hkv=8 D=128           387-411 us, 1340-1430 TFLOP/s: the same chain (14 % less with half of the
+//   512 tokens behind 65536, Hq=32 Hkv=8 D=128           387-413 us, 1340-1430 TFLOP/s, in turn 444-453, 1220-1250: the same chain (14 % less with half of the
 //     softmax left out).  Its 64 items read the same keys at different times, 2.2 GB from HBM where 0.28 would do; reading
 //     them together (stretches dealt in rounds) gave 408, and 130 for 119 behind 16384
 //   13 prompts of 1..901 tokens behind 1531 shared and 0..333 own, f16 Hq=24 Hkv=4 D=64   110 us, 660 TFLOP/s: the warp
 //     that issues the products, a pair of tiles in 1.4 us; start, ends of segments and join 20 us
-//   24 prompts of 3..448 tokens over 400..1500 states, Hq=Hkv=16 D=64   57.5 us: start, ends of 4.6 segments a CTA, join
-//   64 single tokens over 1..1500 states, f16 Hq=Hkv=16 D=64   45 us, 4.4 TB/s (few rows)
-//   one prompt of 37 tokens   14 us: the host's two launches and its four tensor maps
+//   24 prompts of 3..448 tokens over 400..1500 states, Hq=Hkv=16 D=64   57.5 us, in turn 62: start, ends of 4.6 segments a CTA, join
+//   64 single tokens over 1..1500 states, f16 Hq=Hkv=16 D=64   45-49 us, 4.0-4.4 TB/s (few rows)
+//   one prompt of 37 tokens   14 us: the host's two launches and its tensor maps (three, five where 32 tokens of a page lie together)
 #include <atomic>
 #include <climits>
 
@@ -874,9 +874,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 //   S = Q K^T: lane (n, j) = (lane / 4, lane % 4) holds elements 32 c + 8 j .. + 7 of query n and of key n (and n + 8);
 //   O^T = V^T P^T: it holds elements 64 c + 8 n .. + 7 of keys 2 j, 2 j + 1, 2 j + 8, 2 j + 9 - the keys whose scores of
 //   row n it has from S - and gets elements 64 c + 8 n .. + 7 of rows 2 j and 2 j + 1.
+// P is rounded to the type of V, as in the tiles.
 // Keys of the round to come are fetched as soon as the products have read the ones before, and values likewise, so that
 // one or the other is always on its way.  Bound: HBM (4000 keys at Hkv=8 D=128 5.9 TB/s), at short lengths the trips to
-// memory that a segment begins with, one behind the other: bounds, page numbers, keys.  Four CTAs to an SM at D = 64 (120
+// memory that a segment begins with, one behind the other: bounds, page numbers, keys.  Four CTAs to an SM at D = 64 (122
 // registers; 5 spill and are as fast, 3 take 53 us for 45), three at D = 128 (89 us at 4000 keys, 98 with two or four).
 template <bool F16>
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {

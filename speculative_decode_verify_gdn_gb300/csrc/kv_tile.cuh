@@ -417,7 +417,10 @@ __device__ __forceinline__ void softmax_tile(const uint32_t ts, const uint32_t t
   // 64 scores at a time, in a loop (all 128 unrolled hold up the other warps' instruction fetches, 32
   // at a time wait longer for their loads).  The exponentials take the maximum that is known; only if
   // a row's next 64 lie more than kLag above it are O, its sum and the tile's P so far rescaled.
-  // P goes over scores that have been read.
+  // P goes over scores that have been read, rounded to the type of V: the product takes both of one 16-bit type, and a second
+  // product for what the rounding drops would make its part of the tensor core's time twice as long.  Each weight is off
+  // by half a step at most, the sum l is of the f32 weights: against float64 2.2e-3 of the output's norm in bf16 and 2.9e-4 in f16,
+  // of which rounding the output alone is 1.7e-3 and 2.1e-4.
   float2 sum = make_float2(0.f, 0.f);
   const float2 c2 = make_float2(c, c);
 #pragma unroll 1
