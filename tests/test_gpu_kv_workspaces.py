@@ -81,6 +81,29 @@ def test_streams_at_once(cache, attend):
     assert all(torch.equal(a, b) for a, b in zip(want, copies(made)))
 
 
+def test_whether_a_stream_is_captured():
+    """The capture's stream and one that joined it, but none beside; the current stream stays what it was."""
+    main, side, other = torch.cuda.current_stream(), torch.cuda.Stream(), torch.cuda.Stream()
+    x = torch.zeros(4, device="cuda")
+
+    def look():
+        before = torch.cuda.current_stream()
+        seen = [kv.stream_state(s) for s in (None, side, other)]
+        assert torch.cuda.current_stream() == before
+        assert [h for h, _ in seen] == [before.cuda_stream, side.cuda_stream, other.cuda_stream]
+        return [c for _, c in seen]
+
+    assert look() == [False, False, False]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.add_(1)
+        assert look() == [True, False, False]
+        side.wait_stream(torch.cuda.current_stream())
+        assert look() == [True, True, False]
+        torch.cuda.current_stream().wait_stream(side)
+    assert look() == [False, False, False] and torch.cuda.current_stream() == main
+
+
 @pytest.mark.parametrize("attend", [False, True])
 def test_graphs_at_once(cache, attend):
     made = jobs(cache, attend)

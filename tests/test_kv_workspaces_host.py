@@ -24,6 +24,7 @@ def world(monkeypatch):
 
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: w.current[-1] in w.captured)
+    monkeypatch.setattr(kv, "_capturing", lambda s: s.cuda_stream in w.captured)
     monkeypatch.setattr(kv, "_current_device", lambda: 0)
     monkeypatch.setattr(kv, "_current_stream", lambda device: w.current[-1])
     for name in ("alloc_attn_workspace", "alloc_attn_prefill_workspace"):
