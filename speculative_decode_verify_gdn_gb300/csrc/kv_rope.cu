@@ -294,7 +294,7 @@ template <bool PACKED>
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
   // Tokens of a CTA: 1 while all CTAs are on the card at once, 2 up to three times as many tokens, then 4.  Us with 1, 2 and 4 in
   // a graph, windows of Hq=32 Hkv=8 and Hq=16 Hkv=2, D=128: 1024 tokens 5.5 8.0 10.8 and 4.6 5.1 6.1; 1072 7.2 8.3 9.4 and
-  // 6.1 5.2 5.1; 2048 10.7 10.2 13.4 and 7.9 5.6 7.2; 3072 13.8 13.6 15.8 and 11.1 8.2 8.1; 4096 19.8 18.5 17.2 and 14.3 9.7 8.3.
+  // 6.1 5.2 5.1; 2048 10.7 10.2 13.4 and 7.9 5.6 7.2; 2992 13.7 13.8 15.8 and 10.9 8.2 8.0; 4096 19.8 18.5 17.2 and 14.3 9.7 8.3.
   // Packed tokens: 1216 6.1 6.9 9.0 and 5.0 4.7 5.4; 2048 10.0 11.0 16.8 and 8.1 6.3 8.7; 3000 13.5 14.4 17.8 and 10.9 8.6 9.3;
   // 4096 19.3 19.1 19.4 and 14.1 9.9 9.6; 16384 69 70 71 and 50 36 33.
   const int wave = rope_ctas(PACKED) * 152, toks = p.n_tokens <= wave ? 1 : p.n_tokens <= 3 * wave ? 2 : kRopeToks;
