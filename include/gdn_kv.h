@@ -280,6 +280,7 @@ gdn_status gdn_kv_append_marked(const gdn_kv_dims* dims, int32_t layer, const gd
  *   q          [n_tokens, Hq, D], tokens q_token_stride apart
  *   out        [n_tokens, Hq, D] contiguous, dtype; lse [n_tokens, Hq] f32 or NULL
  *   workspace  at least gdn_attn_prefill_workspace_size() bytes, no initialisation needed, dead after the call
+ *              (calls that may run at once, on two streams or in two graphs, need one each)
  * Rounding as in gdn_attn_verify.  What the cache holds beyond a slot's tokens reaches no output; a value
  * that is not finite at a token of a slot may reach every row with keys of the sequences that read the slot.
  * Results do not depend on the order in which CTAs run.  dims: K and win_token_stride are not read.
