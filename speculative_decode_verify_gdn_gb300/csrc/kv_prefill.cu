@@ -24,7 +24,7 @@
 // the clock):
 //   prompts of 4096..16384 tokens, Hq=32 Hkv=8 D=128     3.0-3.3 ms, 1250-1350 TFLOP/s: the chain scores, softmax, products of a
 //     stream (a pair of tiles in 1.9 us) at the power cap
-//   512 tokens behind 65536, Hq=32 Hkv=8 D=128           387-413 us, 1340-1430 TFLOP/s, in turn 444-453, 1220-1250: the same chain (14 % less with half of the
+//   512 tokens behind 65536, Hq=32 Hkv=8 D=128           387-413 us, 1340-1430 TFLOP/s, in turn 444-458, 1210-1250: the same chain (14 % less with half of the
 //     softmax left out).  Its 64 items read the same keys at different times, 2.2 GB from HBM where 0.28 would do; reading
 //     them together (stretches dealt in rounds) gave 408, and 130 for 119 behind 16384
 //   13 prompts of 1..901 tokens behind 1531 shared and 0..333 own, f16 Hq=24 Hkv=4 D=64   110 us, 660 TFLOP/s: the warp
